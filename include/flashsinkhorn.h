@@ -391,6 +391,141 @@ FS_API fs_status fs_solve_host(const fs_desc *desc, const void *X_host, const vo
 FS_API fs_status fs_update_f_noalloc(int n, int m, int d, float eps, const float *X, const float *Y,
                                      const float *b, const float *g, float *f, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Row-softmax operators of a model that trains on, or reads from, point sets:
+ * cross attention (the row-normalised plan between two sets, applied to
+ * values) and softmax cross entropy over many classes (the same streamed
+ * LogSumExp, with a label per row).  No counterpart on the pages; they share
+ * the library's streamed-score kernels and never store a score matrix.
+ *
+ * Conventions of these calls: no handle; every tensor is a device pointer on
+ * the current device; work is enqueued on `stream` (a cudaStream_t, NULL =
+ * legacy default) and the call returns without waiting, allocates nothing and
+ * may be captured into a CUDA graph.  `workspace` is device scratch of at
+ * least the size that the matching query returns, 256-byte aligned; it may be
+ * NULL when that size is 0.  Its contents matter only while the call's work
+ * runs, so calls ordered on one stream may share it; calls (or replays of two
+ * graphs) that can overlap need one each.  Outputs must not overlap inputs,
+ * the workspace or one another.  Argument errors are returned before any
+ * work is enqueued, with a message in fs_last_error(NULL).
+ * Results do not depend on timing: every sum has a fixed order.
+ * ------------------------------------------------------------------------ */
+
+/* Element strides of a [batch][token][head][width] tensor; width is contiguous. */
+typedef struct {
+    long long batch, token, head;
+} fs_view;
+
+/*
+ * Cross attention of n queries to m keys of another sequence:
+ *   S_ij = scale q_i.k_j + bias_j,   L_i = log sum_j e^{S_ij},
+ *   out_i = sum_j e^{S_ij - L_i} v_j,   lse_i = L_i
+ * for every problem and head; query head h reads key head h / (heads / kv_heads).
+ * q [batch][n][heads][d], k [batch][m][kv_heads][d], v [batch][m][kv_heads][dv],
+ * out [batch][n][heads][dv], all of `dtype` with the strides below; the
+ * gradient's dout and dq, dk, dv have the shapes of out and q, k, v.
+ */
+typedef struct {
+    int batch, n, m;          /* problems, queries and keys of each (0 allowed)       */
+    int heads, kv_heads;      /* heads is a multiple of kv_heads                      */
+    int d, dv;                /* widths of q and k, and of v and out (1 to 256)       */
+    fs_dtype dtype;           /* FS_F32 (plain fp32 products) or FS_BF16              */
+    float scale;              /* score scale, finite and > 0                          */
+    fs_view q, k, v, out;     /* strides                                              */
+    fs_view dout, dq, dk, dvw; /* strides of the gradient's tensors (dvw: of dv);
+                                 read by fs_cross_attn_grad only                      */
+} fs_attn_desc;
+
+/* Bytes of workspace of fs_cross_attn (grad = 0) or fs_cross_attn_grad (grad = 1)
+ * for this problem on the current device; 0 if the descriptor is not valid. */
+FS_API size_t fs_cross_attn_workspace(const fs_attn_desc *desc, int grad);
+
+/*
+ * Forward.  k_len: device int [batch], the valid keys of each problem (clamped
+ * to 0..m), or NULL for m.  bias: device fp32 [batch][m], or NULL; a value of
+ * -1e30 or less masks its key.  Keys past the length or masked take no part:
+ * their k and v may hold anything, NaN included.  A row without a key gives
+ * out = 0 and lse = -inf.  lse: device fp32 [batch][heads][n], natural log; may
+ * be NULL.  bf16 on the tensor cores: scores and sums in fp32, the weights
+ * e^{S - max} rounded to bf16 for their product with v.  Where few rows face
+ * many keys (single tokens) the keys are split over the SMs and joined in order.
+ * Non-finite inputs that take part give non-finite outputs.  Asynchronous.
+ * Errors: FS_ERR_INVALID_ARG (sizes, scale, strides, null pointers, output
+ * strides that overlap, a workspace that is too small), FS_ERR_UNSUPPORTED (device not
+ * compute capability 10.x; batch * heads over 65535; n * heads or m of 2^30 or more).
+ */
+FS_API fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const void *k, const void *v,
+                               const int *k_len, const float *bias, void *out, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient, from the forward's out and lse and the gradient dout of out:
+ *   P_ij = e^{S_ij - lse_i},  D_i = dout_i.out_i,  dS_ij = P_ij (dout_i.v_j - D_i)
+ *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
+ * (dk and dv summed over the heads that share a key head).  Keys that take no
+ * part get zeros.  k_len and bias as in the forward; no gradient of bias.  On
+ * the tensor cores P and dS are rounded to bf16 for their products.
+ * Asynchronous.  Errors as fs_cross_attn.
+ */
+FS_API fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void *k, const void *v,
+                                    const int *k_len, const float *bias, const void *out, const float *lse,
+                                    const void *dout, void *dq, void *dk, void *dv, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/*
+ * Softmax cross entropy of n rows over v classes, without keeping the logits:
+ *   z_ij = scale x_i.w_j,   lse_i = log sum_j e^{z_ij},   loss_i = lse_i - z_{i, target_i}
+ * x [n][d] and w [v][d] of `dtype` with row strides ldx and ldw (elements).
+ */
+typedef struct {
+    int n, v, d;              /* rows (0 allowed), classes, width                      */
+    fs_dtype dtype;           /* FS_F32 (plain fp32 products) or FS_BF16               */
+    float scale;              /* logit scale (inverse temperature), finite and > 0     */
+    long long ldx, ldw;       /* row strides of x and w                                */
+    long long lddx, lddw;     /* row strides of dx and dw; read by the gradient only   */
+    long long ignore_index;   /* target value of rows that are not counted             */
+} fs_xent_desc;
+
+/* Bytes of workspace of fs_cross_entropy (grad = 0) or fs_cross_entropy_grad
+ * (grad = 1) on the current device; 0 if the descriptor is not valid.  The
+ * gradient's holds the logit gradients of one piece of the classes (up to
+ * 256 MiB, or 256 classes if those take more) and partial sums of dx. */
+FS_API size_t fs_cross_entropy_workspace(const fs_xent_desc *desc, int grad);
+
+/*
+ * Forward: loss and lse, device fp32 [n] (natural log).  target: device int64
+ * [n].  A row whose target is ignore_index has loss 0 (its lse is computed);
+ * any other target outside 0..v-1 gives loss NaN, without a read out of range.
+ * Asynchronous.  Errors: FS_ERR_INVALID_ARG (sizes, scale, strides, null
+ * pointers, a workspace that is too small), FS_ERR_UNSUPPORTED (device not
+ * compute capability 10.x; v over 2^22 or d over 65536; n of 2^30 or more).
+ */
+FS_API fs_status fs_cross_entropy(const fs_xent_desc *desc, const void *x, const void *w, const long long *target,
+                                  float *loss, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient, from the forward's lse and the gradients dloss (device fp32 [n])
+ * and dlse (device fp32 [n], or NULL for 0) of the two outputs:
+ *   dz_ij = e^{z_ij - lse_i} (dloss_i + dlse_i) - [j = target_i] dloss_i
+ *   dx_i = scale sum_j dz_ij w_j,   dw_j = scale sum_i dz_ij x_i
+ * dx [n][d] and dw [v][d] of `dtype`.  dloss of ignored rows is not used.
+ * Taken in pieces of the classes: the logits of a piece again, dz of the piece
+ * (bf16 for bf16 inputs), its share of dx (summed in fp32) and its rows of dw.
+ * A target outside 0..v-1 that is not ignore_index makes the gradients NaN.
+ * Asynchronous.  Errors as fs_cross_entropy.
+ */
+FS_API fs_status fs_cross_entropy_grad(const fs_xent_desc *desc, const void *x, const void *w,
+                                       const long long *target, const float *lse, const float *dloss,
+                                       const float *dlse, void *dx, void *dw, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+/*
+ * Wait for `stream` and report what the handle-less calls above raised on the
+ * current device since the last check: FS_ERR_TIMEOUT if a bounded device-side
+ * wait ran out (the outputs of that call are then not valid).  Synchronises.
+ */
+FS_API fs_status fs_check(void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,7 +27,9 @@ STATUS_NAMES = {0: "FS_OK", 1: "FS_ERR_INVALID_ARG", 2: "FS_ERR_CUDA", 3: "FS_ER
 EXPORTS = ["fs_create", "fs_update_f", "fs_update_g", "fs_solve", "fs_marginal_err", "fs_ot_cost",
            "fs_sync", "fs_get_info", "fs_destroy", "fs_last_error", "fs_solve_host", "fs_kernel_launches",
            "fs_update_f_noalloc", "fs_transport_apply", "fs_barycentric_map", "fs_grad_x",
-           "fs_transport_apply_t", "fs_grad_y", "fs_hvp_x", "fs_selftest_wait"]
+           "fs_transport_apply_t", "fs_grad_y", "fs_hvp_x", "fs_selftest_wait", "fs_cross_attn", "fs_cross_attn_grad",
+           "fs_cross_attn_workspace", "fs_cross_entropy", "fs_cross_entropy_grad", "fs_cross_entropy_workspace",
+           "fs_check"]
 
 
 class FsDesc(ctypes.Structure):
@@ -51,6 +53,23 @@ class FsInfo(ctypes.Structure):
                                                                                d["last_apply_path"])
         d["last_solve_graph"] = {0: None, 1: "graph", 2: "direct"}.get(d["last_solve_graph"], d["last_solve_graph"])
         return d
+
+
+class FsView(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_longlong), ("token", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
+class FsAttnDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("n", ctypes.c_int), ("m", ctypes.c_int), ("heads", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("d", ctypes.c_int), ("dv", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("scale", ctypes.c_float), ("q", FsView), ("k", FsView), ("v", FsView), ("out", FsView),
+                ("dout", FsView), ("dq", FsView), ("dk", FsView), ("dvw", FsView)]
+
+
+class FsXentDesc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("v", ctypes.c_int), ("d", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("scale", ctypes.c_float), ("ldx", ctypes.c_longlong), ("ldw", ctypes.c_longlong),
+                ("lddx", ctypes.c_longlong), ("lddw", ctypes.c_longlong), ("ignore_index", ctypes.c_longlong)]
 
 
 class FsError(RuntimeError):
@@ -94,8 +113,18 @@ def lib():
         L.fs_selftest_wait.argtypes = [vp, ctypes.c_int]
         L.fs_kernel_launches.argtypes = []
         L.fs_kernel_launches.restype = ctypes.c_ulonglong
+        szt, ad, xd = ctypes.c_size_t, ctypes.POINTER(FsAttnDesc), ctypes.POINTER(FsXentDesc)
+        L.fs_cross_attn_workspace.argtypes = [ad, ctypes.c_int]
+        L.fs_cross_attn.argtypes = [ad] + [vp] * 8 + [szt, vp]
+        L.fs_cross_attn_grad.argtypes = [ad] + [vp] * 12 + [szt, vp]
+        L.fs_cross_entropy_workspace.argtypes = [xd, ctypes.c_int]
+        L.fs_cross_entropy.argtypes = [xd] + [vp] * 6 + [szt, vp]
+        L.fs_cross_entropy_grad.argtypes = [xd] + [vp] * 9 + [szt, vp]
+        L.fs_check.argtypes = [vp]
+        L.fs_cross_attn_workspace.restype = L.fs_cross_entropy_workspace.restype = szt
         for name in EXPORTS:
-            if name not in ("fs_last_error", "fs_kernel_launches"):
+            if name not in ("fs_last_error", "fs_kernel_launches", "fs_cross_attn_workspace",
+                            "fs_cross_entropy_workspace"):
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -328,3 +357,212 @@ def fs_hvp_x(h: Handle, f, g, X, Y, V, out, max_cg_iters=200, cg_rtol=1e-6) -> i
 def fs_selftest_wait(h: Handle, timeout_ms=50) -> int:
     """Run the failure-path self test; returns the library status (FS_ERR_TIMEOUT = 5 expected)."""
     return int(lib().fs_selftest_wait(h.ptr, int(timeout_ms)))
+
+
+# ---- row-softmax operators without a handle ----
+_OP_DTYPES = {"torch.float32": FS_F32, "torch.bfloat16": FS_BF16}
+
+
+def _same(what, cond):
+    if not cond:
+        raise ValueError(what)
+
+
+def _op_dtype(first, *others):
+    """The operators' dtype code; every tensor must share it and the device."""
+    dt = _OP_DTYPES.get(str(first.dtype))
+    if dt is None:
+        raise ValueError("tensors must be float32 or bfloat16")
+    if not first.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    for t in others:
+        if t.dtype != first.dtype:
+            raise ValueError("tensors must share a dtype")
+        if t.device != first.device:
+            raise ValueError("tensors must be on one device")
+    return dt
+
+
+def _side(t, dtype, shape, device, what):
+    """A contiguous side array (lengths, bias, statistics, targets), or None."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != getattr(torch, dtype) or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+    return t.data_ptr()
+
+
+def _view(t, what):
+    if t.dim() != 4:
+        raise ValueError(f"{what} must be [batch, token, head, width]")
+    s, w = t.stride(), t.shape[3]
+    if w > 1 and s[3] != 1:
+        raise ValueError(f"the last dimension of {what} must be contiguous")
+    return FsView(s[0], s[1], s[2])
+
+
+def _op_call(device, stream, query, grad, desc, workspace, call):
+    """Run `call(workspace pointer, bytes, stream)` on the tensors' device: a given stream or
+    that device's current one, and a given workspace or one from torch's allocator (in that
+    stream's order; under graph capture, of the capture's own pool)."""
+    import contextlib
+    import torch
+    here = torch.cuda.current_device() == device.index
+    with contextlib.nullcontext() if here else torch.cuda.device(device):
+        s = torch.cuda.current_stream(device) if stream is None else stream
+        if s.device != device:
+            raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
+        need = query(ctypes.byref(desc), grad)
+        if workspace is None and need:
+            if stream is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            else:
+                with torch.cuda.stream(s):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        size = 0
+        if workspace is not None:
+            if workspace.device != device or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be a contiguous tensor on {device}")
+            size = workspace.numel() * workspace.element_size()
+        _check(call(workspace.data_ptr() if size else None, size, s.cuda_stream))
+
+
+def _attn_desc(q, k, v, out, scale):
+    dt = _op_dtype(q, k, v, out)
+    views = [_view(t, w) for t, w in ((q, "q"), (k, "k"), (v, "v"), (out, "out"))]
+    B, n, H, d = q.shape
+    m, Hk, dv = k.shape[1], k.shape[2], v.shape[3]
+    _same("k must be [batch, m, kv_heads, d]", k.shape[0] == B and k.shape[3] == d)
+    _same("v must be [batch, m, kv_heads, dv]", tuple(v.shape[:3]) == (B, m, Hk))
+    _same("out must be [batch, n, heads, dv]", tuple(out.shape) == (B, n, H, dv))
+    return FsAttnDesc(B, n, m, H, Hk, d, dv, dt, float(d ** -0.5 if scale is None else scale), *views)
+
+
+def fs_cross_attn(q, k, v, out, lse=None, k_len=None, bias=None, scale=None, stream=None, workspace=None):
+    """Cross attention: out[b, i, h] = sum_j softmax_j(scale q_i.k_j + bias_j) v_j.
+
+    q [batch, n, heads, d], k [batch, m, kv_heads, d], v [batch, m, kv_heads, dv], out [batch, n,
+    heads, dv]: CUDA float32 or bfloat16 with any strides whose last one is 1 (slices of a fused
+    projection, inputs expanded over the batch).  heads is a multiple of kv_heads.  lse (written
+    if given): float32 [batch, heads, n].  k_len: int32 [batch] valid keys, or None for all; bias:
+    float32 [batch, m] added to the scores, -1e30 or less masking the key.  Masked keys may hold
+    anything; a row without a key gives 0 and lse -inf.  scale: 1/sqrt(d) if None.  stream: the
+    device's current one if None (tensors used on another stream must be kept alive by the
+    caller).  workspace: uint8 tensor of fs_cross_attn_workspace bytes; allocated if None."""
+    desc = _attn_desc(q, k, v, out, scale)
+    dev = q.device
+    kl = _side(k_len, "int32", (desc.batch,), dev, "k_len")
+    bp = _side(bias, "float32", (desc.batch, desc.m), dev, "bias")
+    lp = _side(lse, "float32", (desc.batch, desc.heads, desc.n), dev, "lse")
+    L = lib()
+    _op_call(dev, stream, L.fs_cross_attn_workspace, 0, desc, workspace,
+             lambda ws, size, s: L.fs_cross_attn(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), kl, bp,
+                                                 out.data_ptr(), lp, ws, size, s))
+
+
+def _attn_grad_desc(q, k, v, out, dout, dq, dk, dv, scale):
+    desc = _attn_desc(q, k, v, out, scale)
+    _op_dtype(q, dout, dq, dk, dv)
+    for t, like, what in ((dout, out, "dout"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        _same(f"{what} has the wrong shape", t.shape == like.shape)
+    desc.dout, desc.dq, desc.dk, desc.dvw = (_view(t, w) for t, w in ((dout, "dout"), (dq, "dq"), (dk, "dk"),
+                                                                     (dv, "dv")))
+    return desc
+
+
+def fs_cross_attn_grad(q, k, v, out, lse, dout, dq, dk, dv, k_len=None, bias=None, scale=None, stream=None,
+                       workspace=None):
+    """Gradients dq, dk, dv of fs_cross_attn from its out and lse and the gradient dout of out
+    (shapes of q, k, v and out; the other arguments as in the forward)."""
+    desc = _attn_grad_desc(q, k, v, out, dout, dq, dk, dv, scale)
+    dev = q.device
+    kl = _side(k_len, "int32", (desc.batch,), dev, "k_len")
+    bp = _side(bias, "float32", (desc.batch, desc.m), dev, "bias")
+    lp = _side(lse, "float32", (desc.batch, desc.heads, desc.n), dev, "lse")
+    _same("lse is needed", lse is not None)
+    L = lib()
+    _op_call(dev, stream, L.fs_cross_attn_workspace, 1, desc, workspace,
+             lambda ws, size, s: L.fs_cross_attn_grad(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), kl,
+                                                      bp, out.data_ptr(), lp, dout.data_ptr(), dq.data_ptr(),
+                                                      dk.data_ptr(), dv.data_ptr(), ws, size, s))
+
+
+def fs_cross_attn_workspace(q, k, v, out, dout=None, dq=None, dk=None, dv=None) -> int:
+    """Workspace bytes of fs_cross_attn, or (with dout, dq, dk and dv) of fs_cross_attn_grad."""
+    import torch
+    grad = dout is not None
+    desc = _attn_grad_desc(q, k, v, out, dout, dq, dk, dv, None) if grad else _attn_desc(q, k, v, out, None)
+    with torch.cuda.device(q.device):
+        return int(lib().fs_cross_attn_workspace(ctypes.byref(desc), int(grad)))
+
+
+def _rows(t, what):
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be a matrix")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {what} must be contiguous")
+    return t.stride(0)
+
+
+def _xent_desc(x, w, scale, ignore_index):
+    dt = _op_dtype(x, w)
+    ldx, ldw = _rows(x, "x"), _rows(w, "w")
+    _same("x [n, d] and w [v, d] must share d", x.shape[1] == w.shape[1])
+    return FsXentDesc(x.shape[0], w.shape[0], x.shape[1], dt, float(scale), ldx, ldw, 0, 0, int(ignore_index))
+
+
+def fs_cross_entropy(x, w, target, loss, lse, scale=1.0, ignore_index=-100, stream=None, workspace=None):
+    """Softmax cross entropy of logits scale x w^T without storing them: x [n, d], w [v, d] (CUDA
+    float32 or bfloat16, rows contiguous, any row stride), target int64 [n]; writes loss and lse,
+    float32 [n].  loss_i = lse_i - z_{i, target_i}, 0 where the target is ignore_index, NaN where it
+    is anything else outside the classes.  stream, workspace: as in fs_cross_attn."""
+    desc = _xent_desc(x, w, scale, ignore_index)
+    dev = x.device
+    tp = _side(target, "int64", (desc.n,), dev, "target")
+    lo, le = (_side(t, "float32", (desc.n,), dev, what) for t, what in ((loss, "loss"), (lse, "lse")))
+    L = lib()
+    _op_call(dev, stream, L.fs_cross_entropy_workspace, 0, desc, workspace,
+             lambda ws, size, s: L.fs_cross_entropy(ctypes.byref(desc), x.data_ptr(), w.data_ptr(), tp, lo, le, ws,
+                                                    size, s))
+
+
+def _xent_grad_desc(x, w, dx, dw, scale, ignore_index):
+    desc = _xent_desc(x, w, scale, ignore_index)
+    _op_dtype(x, dx, dw)
+    _same("dx and dw have the shapes of x and w", dx.shape == x.shape and dw.shape == w.shape)
+    desc.lddx, desc.lddw = _rows(dx, "dx"), _rows(dw, "dw")
+    return desc
+
+
+def fs_cross_entropy_grad(x, w, target, lse, dloss, dx, dw, dlse=None, scale=1.0, ignore_index=-100, stream=None,
+                          workspace=None):
+    """Gradients dx and dw (shapes of x and w) from the forward's lse and the gradients dloss and
+    dlse (float32 [n]; dlse None for 0) of its outputs.  Other arguments as in the forward."""
+    desc = _xent_grad_desc(x, w, dx, dw, scale, ignore_index)
+    dev = x.device
+    tp = _side(target, "int64", (desc.n,), dev, "target")
+    le, dl, dz = (_side(t, "float32", (desc.n,), dev, what)
+                  for t, what in ((lse, "lse"), (dloss, "dloss"), (dlse, "dlse")))
+    L = lib()
+    _op_call(dev, stream, L.fs_cross_entropy_workspace, 1, desc, workspace,
+             lambda ws, size, s: L.fs_cross_entropy_grad(ctypes.byref(desc), x.data_ptr(), w.data_ptr(), tp, le, dl, dz,
+                                                         dx.data_ptr(), dw.data_ptr(), ws, size, s))
+
+
+def fs_cross_entropy_workspace(x, w, dx=None, dw=None) -> int:
+    """Workspace bytes of fs_cross_entropy, or (with dx and dw) of fs_cross_entropy_grad."""
+    import torch
+    grad = dx is not None
+    desc = _xent_grad_desc(x, w, dx, dw, 1.0, -100) if grad else _xent_desc(x, w, 1.0, -100)
+    with torch.cuda.device(x.device):
+        return int(lib().fs_cross_entropy_workspace(ctypes.byref(desc), int(grad)))
+
+
+def fs_check(stream=None):
+    """Wait for the stream and raise FsError if a handle-less call on its device reported a
+    bounded wait that ran out since the last check."""
+    import torch
+    s = torch.cuda.current_stream() if stream is None else stream
+    with torch.cuda.device(s.device):
+        _check(lib().fs_check(ctypes.c_void_p(s.cuda_stream)))

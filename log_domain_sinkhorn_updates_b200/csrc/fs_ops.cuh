@@ -1,0 +1,89 @@
+// Internal declarations of the row-softmax operators beside the Sinkhorn
+// passes: cross attention and softmax cross entropy, with their gradients.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "flashsinkhorn.h"
+#include "fs_internal.cuh"
+
+namespace fs {
+
+// A bias at or below this masks its key (it counts as -inf).  Masks written as
+// the type's lowest value then leave an empty row empty instead of making all
+// of its keys equally likely, and times log2(e) no kept bias leaves fp32.
+constexpr float kBiasMask = -1e30f;
+
+struct AttnParams {
+    int batch, n, m, heads, kv_heads, group, d, dv;
+    float scale, scale2;  // score scale, and times log2(e)
+    fs_view qs, ks, vs, os, dos, dqs, dks, dvs;  // element strides (batch, token, head)
+    const void *q, *k, *v, *dout;
+    const int *k_len;     // [batch] or null
+    const float *bias;    // [batch][m] or null
+    void *out, *dq, *dk, *dv_out;
+    float *lse;           // [batch][heads][n], natural log (out of the forward, into the gradient); may be null forward
+    float *dot;           // gradient: [batch][heads][n], D_i = dout_i.out_i
+    int splits;           // parts of the key axis (forward)
+    int split_keys;       // keys of a part
+    float *part_o;        // [splits][batch][kv_heads][n group][dv], relative to part_ml's maximum
+    float2 *part_ml;      // [splits][batch][kv_heads][n group]: running max (base 2) and sum
+    unsigned long long timeout_ns;
+    int *err;
+};
+
+// Valid keys of problem b.
+__device__ __forceinline__ int attn_keys(const AttnParams &p, int b) {
+    return p.k_len ? min(max(__ldg(p.k_len + b), 0), p.m) : p.m;
+}
+// Base-2 bias of key j (valid or not): -inf where it is masked.
+__device__ __forceinline__ float attn_bias2(const AttnParams &p, int b, int j, int keys) {
+    if (j >= keys) return -INFINITY;
+    if (!p.bias) return 0.f;
+    const float v = __ldg(p.bias + (size_t)b * p.m + j);
+    return v <= kBiasMask ? -INFINITY : v * kLog2e;
+}
+
+cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, cudaStream_t s);  // two launches
+
+// Softmax cross entropy: rows x [n][d] against classes w [v][d].
+struct XentParams {
+    int n, v, d;
+    float scale, scale2;           // logit scale, and times log2(e)
+    const void *x, *w;
+    long long ldx, ldw;            // row strides in elements
+    const long long *target;       // [n]
+    long long ignore;
+    float *loss, *lse;             // [n]
+    const float *dloss, *dlse;     // [n] ([n] or null)
+    void *dx, *dw;
+    long long lddx, lddw;
+    // one product's launch
+    int c0, c1;                    // class range of the launch
+    float2 *part;                  // [column tiles][n]: (max, sum) in base 2
+    float *hit;                    // [n] scaled logit of the target
+    void *dl;                      // [n][ld_dl] gradient of the logits of classes c0..c1
+    long long ld_dl;
+    float *acc;                    // [parts][n][d] partial sums of dx
+    int parts;                     // parts of the class range (dx)
+    int acc_add;                   // 1: add to acc, 0: overwrite
+    unsigned long long timeout_ns;
+    int *err;
+};
+
+// Column-tile width of the partial statistics on each path.
+constexpr int kXentSimtCols = 128;
+
+cudaError_t launch_xent_lse_simt(const XentParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_xent_finish(const XentParams &p, int tiles, cudaStream_t s);
+cudaError_t launch_xent_dl_simt(const XentParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_xent_dx_simt(const XentParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_xent_dw_simt(const XentParams &p, bool bf16, cudaStream_t s);
+// dx = sum over the parts of acc, rounded to the output type.
+cudaError_t launch_xent_reduce(const XentParams &p, bool bf16, cudaStream_t s);
+
+}  // namespace fs

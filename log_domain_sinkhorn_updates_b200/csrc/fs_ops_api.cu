@@ -1,0 +1,398 @@
+// C entry points of the row-softmax operators: cross attention and softmax
+// cross entropy.  Host code only: argument checks, the choice between the
+// tensor-core and the CUDA-core kernels, the plan of splits and pieces, the
+// layout of the caller's workspace, and the launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <mutex>
+
+#include "fs_ops.cuh"
+
+namespace {
+
+__device__ int g_ops_err;  // error bits of the handle-less calls on this device
+
+constexpr int kMaxDevices = 64;
+constexpr unsigned long long kTimeoutNs = 2000000000ull;
+
+fs_status reject(fs_status st, const char *fmt, ...) {
+    char buf[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    fs::set_thread_error(buf);
+    return st;
+}
+
+#define OPS_LAUNCH(call, kernels)                                                                \
+    do {                                                                                         \
+        cudaError_t e_ = (call);                                                                 \
+        if (e_ != cudaSuccess) return reject(FS_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_)); \
+        fs::count_launches(kernels);                                                             \
+    } while (0)
+
+struct Device {
+    bool ready = false;
+    int sms = 0;
+    int *err = nullptr;
+};
+
+// The current device's properties and error word, looked up once per device.
+fs_status current_device(Device *out) {
+    static std::mutex mu;
+    static Device known[kMaxDevices];
+    int dev = 0, major = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return reject(FS_ERR_CUDA, "no CUDA device: %s", cudaGetErrorString(e));
+    if (dev >= kMaxDevices) return reject(FS_ERR_UNSUPPORTED, "device index beyond 63");
+    std::lock_guard<std::mutex> lock(mu);
+    Device &d = known[dev];
+    if (!d.ready) {
+        void *addr = nullptr;
+        e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+        if (e == cudaSuccess && major != 10) return reject(FS_ERR_UNSUPPORTED, "this library is built for sm_100a");
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) e = cudaGetSymbolAddress(&addr, g_ops_err);
+        if (e != cudaSuccess) return reject(FS_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
+        d.err = static_cast<int *>(addr);
+        d.ready = true;
+    }
+    *out = d;
+    return FS_OK;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+int up(int a, int b) { return (a + b - 1) / b; }
+
+// Whether a [batch][token][head][w] tensor with these strides holds every element at its own address.
+bool distinct(const fs_view &s, int batch, int tokens, int heads, int w) {
+    struct Dim {
+        long long stride, size;
+    } dims[3] = {{s.batch, batch}, {s.token, tokens}, {s.head, heads}};
+    std::sort(dims, dims + 3, [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
+    long long extent = w;  // elements spanned so far
+    for (const Dim &x : dims) {
+        if (x.size <= 1) continue;
+        if (x.stride < extent) return false;
+        extent = x.stride * (x.size - 1) + extent;
+    }
+    return true;
+}
+bool nonneg(const fs_view &s) { return s.batch >= 0 && s.token >= 0 && s.head >= 0; }
+
+// ------------------------------------------------------------------ cross attention
+fs_status check_attn(const fs_attn_desc *D, bool grad) {
+    if (!D) return reject(FS_ERR_INVALID_ARG, "null descriptor");
+    if (D->batch < 0 || D->n < 0 || D->m < 0) return reject(FS_ERR_INVALID_ARG, "batch, n and m must be >= 0");
+    if (D->heads < 1 || D->kv_heads < 1 || D->heads % D->kv_heads)
+        return reject(FS_ERR_INVALID_ARG, "heads must be a positive multiple of kv_heads");
+    if (D->d < 1 || D->dv < 1 || D->d > 256 || D->dv > 256)
+        return reject(FS_ERR_INVALID_ARG, "d and dv must be 1 to 256");
+    if (D->dtype != FS_F32 && D->dtype != FS_BF16) return reject(FS_ERR_INVALID_ARG, "unknown dtype");
+    if (!(D->scale > 0.f) || !std::isfinite(D->scale))
+        return reject(FS_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (!nonneg(D->q) || !nonneg(D->k) || !nonneg(D->v) || !nonneg(D->out) ||
+        (grad && (!nonneg(D->dout) || !nonneg(D->dq) || !nonneg(D->dk) || !nonneg(D->dvw))))
+        return reject(FS_ERR_INVALID_ARG, "strides must be >= 0");
+    if ((long long)D->batch * D->heads > 65535)
+        return reject(FS_ERR_UNSUPPORTED, "batch * heads exceeds 65535");
+    if ((long long)D->n * D->heads >= 1ll << 30 || D->m >= 1 << 30)
+        return reject(FS_ERR_UNSUPPORTED, "n * heads or m is 2^30 or more");
+    const bool ok = grad ? distinct(D->dq, D->batch, D->n, D->heads, D->d) &&
+                               distinct(D->dk, D->batch, D->m, D->kv_heads, D->d) &&
+                               distinct(D->dvw, D->batch, D->m, D->kv_heads, D->dv)
+                         : distinct(D->out, D->batch, D->n, D->heads, D->dv);
+    if (!ok) return reject(FS_ERR_INVALID_ARG, "an output's strides make elements overlap");
+    return FS_OK;
+}
+
+struct AttnPlan {
+    int splits = 1, split_keys = 0;
+    size_t part_ml = 0, part_o = 0, dot = 0, total = 0;  // workspace offsets, and its size
+};
+
+AttnPlan plan_attn(const fs_attn_desc &D, bool grad, int sms) {
+    AttnPlan L;
+    const size_t rows = (size_t)D.n * (D.heads / D.kv_heads), heads = (size_t)D.batch * D.kv_heads;
+    L.split_keys = std::max(D.m, 1);
+    if (grad) {
+        L.total = align256((size_t)D.batch * D.heads * D.n * 4);
+        return L;
+    }
+    // Few rows: enough parts of at least 256 keys that two CTAs' worth of work reach every SM.
+    const size_t ctas = (rows + 15) / 16 * heads;
+    if (ctas > 0 && ctas < (size_t)sms) {
+        const int want = (int)((2 * sms + ctas - 1) / ctas);
+        const int parts = std::max(1, std::min(want, up(D.m, 256)));
+        L.split_keys = std::max(64, up(up(std::max(D.m, 1), parts), 64) * 64);
+        L.splits = std::max(1, up(D.m, L.split_keys));
+    }
+    if (L.splits > 1) {
+        L.part_ml = 0;
+        L.part_o = align256(rows * heads * L.splits * sizeof(float2));
+        L.total = L.part_o + align256(rows * heads * L.splits * D.dv * sizeof(float));
+    }
+    return L;
+}
+
+fs::AttnParams attn_params(const fs_attn_desc &D, const AttnPlan &L, const Device &dev, void *ws) {
+    fs::AttnParams p{};
+    p.batch = D.batch;
+    p.n = D.n;
+    p.m = D.m;
+    p.heads = D.heads;
+    p.kv_heads = D.kv_heads;
+    p.group = D.heads / D.kv_heads;
+    p.d = D.d;
+    p.dv = D.dv;
+    p.scale = D.scale;
+    p.scale2 = (float)((double)D.scale * fs::kLog2ed);
+    p.qs = D.q;
+    p.ks = D.k;
+    p.vs = D.v;
+    p.os = D.out;
+    p.dos = D.dout;
+    p.dqs = D.dq;
+    p.dks = D.dk;
+    p.dvs = D.dvw;
+    p.splits = L.splits;
+    p.split_keys = L.split_keys;
+    char *w = static_cast<char *>(ws);
+    p.part_ml = reinterpret_cast<float2 *>(w + L.part_ml);
+    p.part_o = reinterpret_cast<float *>(w + L.part_o);
+    p.dot = reinterpret_cast<float *>(w + L.dot);
+    p.timeout_ns = kTimeoutNs;
+    p.err = dev.err;
+    return p;
+}
+
+fs_status check_workspace(const void *ws, size_t have, size_t need) {
+    if (need == 0) return FS_OK;
+    if (!ws || have < need)
+        return reject(FS_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", ws ? have : (size_t)0, need);
+    if (reinterpret_cast<uintptr_t>(ws) & 255) return reject(FS_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+    return FS_OK;
+}
+
+// ------------------------------------------------------------------ cross entropy
+fs_status check_xent(const fs_xent_desc *D, bool grad) {
+    if (!D) return reject(FS_ERR_INVALID_ARG, "null descriptor");
+    if (D->n < 0 || D->v < 1 || D->d < 1) return reject(FS_ERR_INVALID_ARG, "n must be >= 0, v and d >= 1");
+    if (D->dtype != FS_F32 && D->dtype != FS_BF16) return reject(FS_ERR_INVALID_ARG, "unknown dtype");
+    if (!(D->scale > 0.f) || !std::isfinite(D->scale))
+        return reject(FS_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (D->ldx < 0 || D->ldw < 0) return reject(FS_ERR_INVALID_ARG, "row strides must be >= 0");
+    if (grad && ((D->n > 1 && D->lddx < D->d) || (D->v > 1 && D->lddw < D->d)))
+        return reject(FS_ERR_INVALID_ARG, "an output's row stride is below d");
+    if (D->v > 1 << 22 || D->d > 65536 || D->n >= 1 << 30)
+        return reject(FS_ERR_UNSUPPORTED, "v over 2^22, d over 65536 or n of 2^30 or more");
+    return FS_OK;
+}
+
+struct XentPlan {
+    int tiles = 0;            // column tiles of the forward
+    int piece = 0, parts = 1;  // classes of a piece; parts of it in the dx product
+    long long ld_dl = 0;
+    size_t part = 0, hit = 0, dl = 0, acc = 0, total = 0;
+};
+
+XentPlan plan_xent(const fs_xent_desc &D, bool grad, int sms) {
+    XentPlan L;
+    if (!grad) {
+        L.tiles = up(D.v, fs::kXentSimtCols);
+        L.hit = align256((size_t)L.tiles * D.n * sizeof(float2));
+        L.total = L.hit + align256((size_t)D.n * sizeof(float));
+        return L;
+    }
+    // Pieces of the classes whose logit gradients stay within 256 MiB.
+    const size_t elem = 4, budget = (size_t)256 << 20;
+    const size_t fit = budget / (elem * std::max(D.n, 1)) / 256 * 256;
+    L.piece = (int)std::max<size_t>(256, std::min<size_t>(fit, (size_t)up(D.v, 256) * 256));
+    L.ld_dl = L.piece;
+    // dx: few tiles of a long sum are split over the classes too.
+    const long long tiles = (long long)up(std::max(D.n, 1), 128) * up(D.d, 128);
+    L.parts = (int)std::max(1ll, std::min<long long>(std::min(32ll, 2 * sms / tiles), L.piece / 512));
+    L.acc = align256((size_t)D.n * L.ld_dl * elem);
+    L.total = L.acc + align256((size_t)L.parts * D.n * D.d * sizeof(float));
+    return L;
+}
+
+fs::XentParams xent_params(const fs_xent_desc &D, const XentPlan &L, const Device &dev, void *ws) {
+    fs::XentParams p{};
+    p.n = D.n;
+    p.v = D.v;
+    p.d = D.d;
+    p.scale = D.scale;
+    p.scale2 = (float)((double)D.scale * fs::kLog2ed);
+    p.ldx = D.ldx;
+    p.ldw = D.ldw;
+    p.lddx = D.lddx;
+    p.lddw = D.lddw;
+    p.ignore = D.ignore_index;
+    char *w = static_cast<char *>(ws);
+    p.part = reinterpret_cast<float2 *>(w + L.part);
+    p.hit = reinterpret_cast<float *>(w + L.hit);
+    p.dl = w + L.dl;
+    p.ld_dl = L.ld_dl;
+    p.acc = reinterpret_cast<float *>(w + L.acc);
+    p.parts = L.parts;
+    p.timeout_ns = kTimeoutNs;
+    p.err = dev.err;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fs_cross_attn_workspace(const fs_attn_desc *desc, int grad) {
+    Device dev;
+    if (check_attn(desc, grad != 0) != FS_OK || current_device(&dev) != FS_OK) return 0;
+    return plan_attn(*desc, grad != 0, dev.sms).total;
+}
+
+fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const void *k, const void *v, const int *k_len,
+                        const float *bias, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                        void *stream) {
+    fs_status st = check_attn(desc, false);
+    if (st != FS_OK) return st;
+    const fs_attn_desc &D = *desc;
+    if (D.batch == 0 || D.n == 0) return FS_OK;
+    if (!q || !out || (D.m > 0 && (!k || !v))) return reject(FS_ERR_INVALID_ARG, "null argument");
+    Device dev;
+    if ((st = current_device(&dev)) != FS_OK) return st;
+    const AttnPlan L = plan_attn(D, false, dev.sms);
+    if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
+    fs::AttnParams p = attn_params(D, L, dev, workspace);
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.k_len = k_len;
+    p.bias = bias;
+    p.out = out;
+    p.lse = lse;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf16 = D.dtype == FS_BF16;
+    OPS_LAUNCH(fs::launch_xattn_simt(p, bf16, s), 1);
+    if (p.splits > 1) OPS_LAUNCH(fs::launch_xattn_combine(p, bf16, s), 1);
+    return FS_OK;
+}
+
+fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void *k, const void *v, const int *k_len,
+                             const float *bias, const void *out, const float *lse, const void *dout, void *dq,
+                             void *dk, void *dv, void *workspace, size_t workspace_bytes, void *stream) {
+    fs_status st = check_attn(desc, true);
+    if (st != FS_OK) return st;
+    const fs_attn_desc &D = *desc;
+    if (D.batch == 0 || (D.n == 0 && D.m == 0)) return FS_OK;
+    if ((D.n > 0 && (!q || !out || !lse || !dout || !dq)) || (D.m > 0 && (!k || !v || !dk || !dv)))
+        return reject(FS_ERR_INVALID_ARG, "null argument");
+    Device dev;
+    if ((st = current_device(&dev)) != FS_OK) return st;
+    const AttnPlan L = plan_attn(D, true, dev.sms);
+    if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
+    fs::AttnParams p = attn_params(D, L, dev, workspace);
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.k_len = k_len;
+    p.bias = bias;
+    p.out = const_cast<void *>(out);
+    p.lse = const_cast<float *>(lse);
+    p.dout = dout;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv_out = dv;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf16 = D.dtype == FS_BF16;
+    if (D.n > 0) OPS_LAUNCH(fs::launch_xattn_dot(p, bf16, s), 1);
+    OPS_LAUNCH(fs::launch_xattn_grad_simt(p, bf16, s), (D.m > 0) + (D.n > 0));
+    return FS_OK;
+}
+
+size_t fs_cross_entropy_workspace(const fs_xent_desc *desc, int grad) {
+    Device dev;
+    if (check_xent(desc, grad != 0) != FS_OK || current_device(&dev) != FS_OK) return 0;
+    return plan_xent(*desc, grad != 0, dev.sms).total;
+}
+
+fs_status fs_cross_entropy(const fs_xent_desc *desc, const void *x, const void *w, const long long *target,
+                           float *loss, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    fs_status st = check_xent(desc, false);
+    if (st != FS_OK) return st;
+    const fs_xent_desc &D = *desc;
+    if (D.n == 0) return FS_OK;
+    if (!x || !w || !target || !loss || !lse) return reject(FS_ERR_INVALID_ARG, "null argument");
+    Device dev;
+    if ((st = current_device(&dev)) != FS_OK) return st;
+    const XentPlan L = plan_xent(D, false, dev.sms);
+    if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
+    fs::XentParams p = xent_params(D, L, dev, workspace);
+    p.x = x;
+    p.w = w;
+    p.target = target;
+    p.loss = loss;
+    p.lse = lse;
+    p.c1 = D.v;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf16 = D.dtype == FS_BF16;
+    OPS_LAUNCH(fs::launch_xent_lse_simt(p, bf16, s), 1);
+    OPS_LAUNCH(fs::launch_xent_finish(p, L.tiles, s), 1);
+    return FS_OK;
+}
+
+fs_status fs_cross_entropy_grad(const fs_xent_desc *desc, const void *x, const void *w, const long long *target,
+                                const float *lse, const float *dloss, const float *dlse, void *dx, void *dw,
+                                void *workspace, size_t workspace_bytes, void *stream) {
+    fs_status st = check_xent(desc, true);
+    if (st != FS_OK) return st;
+    const fs_xent_desc &D = *desc;
+    if (!w || !dw || (D.n > 0 && (!x || !target || !lse || !dloss || !dx)))
+        return reject(FS_ERR_INVALID_ARG, "null argument");
+    Device dev;
+    if ((st = current_device(&dev)) != FS_OK) return st;
+    const XentPlan L = plan_xent(D, true, dev.sms);
+    if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
+    fs::XentParams p = xent_params(D, L, dev, workspace);
+    p.x = x;
+    p.w = w;
+    p.target = target;
+    p.lse = const_cast<float *>(lse);
+    p.dloss = dloss;
+    p.dlse = dlse;
+    p.dx = dx;
+    p.dw = dw;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf16 = D.dtype == FS_BF16;
+    for (int c0 = 0; c0 < D.v; c0 += L.piece) {
+        p.c0 = c0;
+        p.c1 = std::min(D.v, c0 + L.piece);
+        p.acc_add = c0 > 0;
+        if (D.n > 0) {
+            OPS_LAUNCH(fs::launch_xent_dl_simt(p, bf16, s), 1);
+            OPS_LAUNCH(fs::launch_xent_dx_simt(p, bf16, s), 1);
+        }
+        OPS_LAUNCH(fs::launch_xent_dw_simt(p, bf16, s), 1);
+    }
+    if (D.n > 0) OPS_LAUNCH(fs::launch_xent_reduce(p, bf16, s), 1);
+    return FS_OK;
+}
+
+fs_status fs_check(void *stream) {
+    Device dev;
+    fs_status st = current_device(&dev);
+    if (st != FS_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int bits = 0;
+    cudaError_t e = cudaMemcpyAsync(&bits, dev.err, sizeof(int), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dev.err, 0, sizeof(int), s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return reject(FS_ERR_CUDA, "fs_check: %s", cudaGetErrorString(e));
+    if (bits & fs::kDevErrTimeout) return reject(FS_ERR_TIMEOUT, "a bounded device wait timed out");
+    return FS_OK;
+}
+
+}  // extern "C"
