@@ -20,6 +20,7 @@
 
 #include "flashsinkhorn.h"
 #include "fs_internal.cuh"
+#include "fs_ops.cuh"
 #include "fs_prep.cuh"
 
 using fs::kBlockCols;
@@ -337,6 +338,23 @@ fs_status measure(fs_handle *h, const float *f, const float *g, bool fdir, int s
 }  // namespace
 
 void fs::set_thread_error(const char *msg) { g_last_error = msg; }
+
+bool fs::encode_bf16_map(CUtensorMap *map, const void *base, int dims, const long long *size, const long long *stride,
+                         const int *box) {
+    auto fn = encode_fn();
+    if (!fn || dims > 5) return false;
+    cuuint64_t gdim[5], gstride[5];
+    cuuint32_t gbox[5], estr[5];
+    for (int i = 0; i < dims; ++i) {
+        gdim[i] = (cuuint64_t)size[i];
+        gbox[i] = (cuuint32_t)box[i];
+        estr[i] = 1;
+        if (i) gstride[i - 1] = (cuuint64_t)stride[i - 1] * 2;
+    }
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, const_cast<void *>(base), gdim, gstride, gbox, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 namespace {
 // Whether (f, g) are still the last alternating solve's output, bit for bit

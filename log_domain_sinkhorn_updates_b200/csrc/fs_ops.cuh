@@ -2,6 +2,7 @@
 // passes: cross attention and softmax cross entropy, with their gradients.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -45,6 +46,11 @@ __device__ __forceinline__ float attn_bias2(const AttnParams &p, int b, int j, i
     return v <= kBiasMask ? -INFINITY : v * kLog2e;
 }
 
+// TMA map of a bf16 tensor of `dims` axes (innermost first, contiguous), 128-byte swizzle; strides in elements
+// of the axes but the first.  False if the driver refuses it.
+bool encode_bf16_map(CUtensorMap *map, const void *base, int dims, const long long *size, const long long *stride,
+                     const int *box);
+
 cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s);
@@ -68,7 +74,8 @@ struct XentParams {
     float *hit;                    // [n] scaled logit of the target
     void *dl;                      // [n][ld_dl] gradient of the logits of classes c0..c1
     long long ld_dl;
-    float *acc;                    // [parts][n][d] partial sums of dx
+    float *acc;                    // [parts][n][ld_acc] partial sums of dx
+    long long ld_acc;
     int parts;                     // parts of the class range (dx)
     int acc_add;                   // 1: add to acc, 0: overwrite
     unsigned long long timeout_ns;
@@ -76,13 +83,30 @@ struct XentParams {
 };
 
 // Column-tile width of the partial statistics on each path.
-constexpr int kXentSimtCols = 128;
+constexpr int kXentSimtCols = 128, kXentTcCols = 256;
+
+// One product C [M][N] of the tensor-core kernel.
+struct XentGemm {
+    int M, N, K, mt, nt;  // sizes, and 256-row and 256-column tiles
+    int parts, k_part;    // parts of K, and the length of one
+    int a_off, b_off;     // offset of the operands' first row in their maps
+    int pairs;            // CTA pairs of the grid
+    int vec;              // out's rows can be written 16 bytes at a time
+    void *out;
+    long long ldo;
+};
 
 cudaError_t launch_xent_lse_simt(const XentParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xent_finish(const XentParams &p, int tiles, cudaStream_t s);
 cudaError_t launch_xent_dl_simt(const XentParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xent_dx_simt(const XentParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xent_dw_simt(const XentParams &p, bool bf16, cudaStream_t s);
+bool xent_tc_ok(const void *x, long long ldx, const void *w, long long ldw, int n, int v);
+cudaError_t xent_tc_pairs(int *pairs);
+cudaError_t launch_xent_lse_tc(const XentParams &p, int pairs, cudaStream_t s);
+cudaError_t launch_xent_dl_tc(const XentParams &p, int pairs, cudaStream_t s);
+cudaError_t launch_xent_dx_tc(const XentParams &p, bool direct, int pairs, cudaStream_t s);
+cudaError_t launch_xent_dw_tc(const XentParams &p, int pairs, cudaStream_t s);
 // dx = sum over the parts of acc, rounded to the output type.
 cudaError_t launch_xent_reduce(const XentParams &p, bool bf16, cudaStream_t s);
 

@@ -36,7 +36,7 @@ fs_status reject(fs_status st, const char *fmt, ...) {
 
 struct Device {
     bool ready = false;
-    int sms = 0;
+    int sms = 0, pairs = 0;  // SMs; CTA pairs of the cross-entropy kernel that run at once
     int *err = nullptr;
 };
 
@@ -56,6 +56,7 @@ fs_status current_device(Device *out) {
         if (e == cudaSuccess && major != 10) return reject(FS_ERR_UNSUPPORTED, "this library is built for sm_100a");
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess) e = cudaGetSymbolAddress(&addr, g_ops_err);
+        if (e == cudaSuccess) e = fs::xent_tc_pairs(&d.pairs);
         if (e != cudaSuccess) return reject(FS_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
         d.err = static_cast<int *>(addr);
         d.ready = true;
@@ -193,31 +194,42 @@ fs_status check_xent(const fs_xent_desc *D, bool grad) {
 }
 
 struct XentPlan {
-    int tiles = 0;            // column tiles of the forward
+    int tiles = 0;             // column tiles of the forward
     int piece = 0, parts = 1;  // classes of a piece; parts of it in the dx product
-    long long ld_dl = 0;
+    bool direct = false;       // one product is all of dx: written at once
+    long long ld_dl = 0, ld_acc = 0;
     size_t part = 0, hit = 0, dl = 0, acc = 0, total = 0;
 };
 
-XentPlan plan_xent(const fs_xent_desc &D, bool grad, int sms) {
+// Whether the pointers can be on the tensor-core path is known only at the
+// call, so both paths fit the workspace of the larger one.
+XentPlan plan_xent(const fs_xent_desc &D, bool grad, bool tc, const Device &dev) {
     XentPlan L;
     if (!grad) {
-        L.tiles = up(D.v, fs::kXentSimtCols);
+        L.tiles = up(D.v, tc ? fs::kXentTcCols : fs::kXentSimtCols);
         L.hit = align256((size_t)L.tiles * D.n * sizeof(float2));
         L.total = L.hit + align256((size_t)D.n * sizeof(float));
         return L;
     }
     // Pieces of the classes whose logit gradients stay within 256 MiB.
-    const size_t elem = 4, budget = (size_t)256 << 20;
+    const size_t elem = tc ? 2 : 4, budget = (size_t)256 << 20;
     const size_t fit = budget / (elem * std::max(D.n, 1)) / 256 * 256;
     L.piece = (int)std::max<size_t>(256, std::min<size_t>(fit, (size_t)up(D.v, 256) * 256));
     L.ld_dl = L.piece;
-    // dx: few tiles of a long sum are split over the classes too.
-    const long long tiles = (long long)up(std::max(D.n, 1), 128) * up(D.d, 128);
-    L.parts = (int)std::max(1ll, std::min<long long>(std::min(32ll, 2 * sms / tiles), L.piece / 512));
+    L.ld_acc = (D.d + 7) / 8 * 8;
+    // dx: where the tiles of the product are fewer than what runs at once, the sum over the classes is split.
+    const int side = tc ? 256 : 128;
+    const long long tiles = (long long)up(std::max(D.n, 1), side) * up(D.d, side);
+    const long long want = (tc ? dev.pairs : 2 * dev.sms) / tiles;
+    L.parts = (int)std::max(1ll, std::min<long long>(std::min(32ll, want), L.piece / 512));
+    L.direct = tc && L.piece >= D.v && L.parts == 1;
     L.acc = align256((size_t)D.n * L.ld_dl * elem);
-    L.total = L.acc + align256((size_t)L.parts * D.n * D.d * sizeof(float));
+    L.total = L.acc + (L.direct ? 0 : align256((size_t)L.parts * D.n * L.ld_acc * sizeof(float)));
     return L;
+}
+size_t xent_workspace(const fs_xent_desc &D, bool grad, const Device &dev) {
+    const size_t simt = plan_xent(D, grad, false, dev).total;
+    return D.dtype == FS_BF16 ? std::max(simt, plan_xent(D, grad, true, dev).total) : simt;
 }
 
 fs::XentParams xent_params(const fs_xent_desc &D, const XentPlan &L, const Device &dev, void *ws) {
@@ -238,6 +250,7 @@ fs::XentParams xent_params(const fs_xent_desc &D, const XentPlan &L, const Devic
     p.dl = w + L.dl;
     p.ld_dl = L.ld_dl;
     p.acc = reinterpret_cast<float *>(w + L.acc);
+    p.ld_acc = L.ld_acc;
     p.parts = L.parts;
     p.timeout_ns = kTimeoutNs;
     p.err = dev.err;
@@ -316,7 +329,7 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
 size_t fs_cross_entropy_workspace(const fs_xent_desc *desc, int grad) {
     Device dev;
     if (check_xent(desc, grad != 0) != FS_OK || current_device(&dev) != FS_OK) return 0;
-    return plan_xent(*desc, grad != 0, dev.sms).total;
+    return xent_workspace(*desc, grad != 0, dev);
 }
 
 fs_status fs_cross_entropy(const fs_xent_desc *desc, const void *x, const void *w, const long long *target,
@@ -328,7 +341,9 @@ fs_status fs_cross_entropy(const fs_xent_desc *desc, const void *x, const void *
     if (!x || !w || !target || !loss || !lse) return reject(FS_ERR_INVALID_ARG, "null argument");
     Device dev;
     if ((st = current_device(&dev)) != FS_OK) return st;
-    const XentPlan L = plan_xent(D, false, dev.sms);
+    const bool bf16 = D.dtype == FS_BF16;
+    const bool tc = bf16 && fs::xent_tc_ok(x, D.ldx, w, D.ldw, D.n, D.v);
+    const XentPlan L = plan_xent(D, false, tc, dev);
     if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
     fs::XentParams p = xent_params(D, L, dev, workspace);
     p.x = x;
@@ -338,8 +353,10 @@ fs_status fs_cross_entropy(const fs_xent_desc *desc, const void *x, const void *
     p.lse = lse;
     p.c1 = D.v;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool bf16 = D.dtype == FS_BF16;
-    OPS_LAUNCH(fs::launch_xent_lse_simt(p, bf16, s), 1);
+    if (tc)
+        OPS_LAUNCH(fs::launch_xent_lse_tc(p, dev.pairs, s), 1);
+    else
+        OPS_LAUNCH(fs::launch_xent_lse_simt(p, bf16, s), 1);
     OPS_LAUNCH(fs::launch_xent_finish(p, L.tiles, s), 1);
     return FS_OK;
 }
@@ -354,7 +371,9 @@ fs_status fs_cross_entropy_grad(const fs_xent_desc *desc, const void *x, const v
         return reject(FS_ERR_INVALID_ARG, "null argument");
     Device dev;
     if ((st = current_device(&dev)) != FS_OK) return st;
-    const XentPlan L = plan_xent(D, true, dev.sms);
+    const bool bf16 = D.dtype == FS_BF16;
+    const bool tc = bf16 && fs::xent_tc_ok(x, D.ldx, w, D.ldw, D.n, D.v);
+    const XentPlan L = plan_xent(D, true, tc, dev);
     if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
     fs::XentParams p = xent_params(D, L, dev, workspace);
     p.x = x;
@@ -366,18 +385,23 @@ fs_status fs_cross_entropy_grad(const fs_xent_desc *desc, const void *x, const v
     p.dx = dx;
     p.dw = dw;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool bf16 = D.dtype == FS_BF16;
     for (int c0 = 0; c0 < D.v; c0 += L.piece) {
         p.c0 = c0;
         p.c1 = std::min(D.v, c0 + L.piece);
         p.acc_add = c0 > 0;
+        if (tc && D.n > 0) {
+            OPS_LAUNCH(fs::launch_xent_dl_tc(p, dev.pairs, s), 1);
+            OPS_LAUNCH(fs::launch_xent_dx_tc(p, L.direct, dev.pairs, s), 1);
+            OPS_LAUNCH(fs::launch_xent_dw_tc(p, dev.pairs, s), 1);
+            continue;
+        }
         if (D.n > 0) {
             OPS_LAUNCH(fs::launch_xent_dl_simt(p, bf16, s), 1);
             OPS_LAUNCH(fs::launch_xent_dx_simt(p, bf16, s), 1);
         }
         OPS_LAUNCH(fs::launch_xent_dw_simt(p, bf16, s), 1);
     }
-    if (D.n > 0) OPS_LAUNCH(fs::launch_xent_reduce(p, bf16, s), 1);
+    if (D.n > 0 && !L.direct) OPS_LAUNCH(fs::launch_xent_reduce(p, bf16, s), 1);
     return FS_OK;
 }
 

@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads)
                 const int j = j0 + tj * 4 + (w / 4) * 64 + w % 4;
                 if (j >= nj) continue;
                 if constexpr (EPI == kAcc) {
-                    float *o = p.acc + ((size_t)blockIdx.z * ni + i) * nj + j;
+                    float *o = p.acc + ((size_t)blockIdx.z * ni + i) * p.ld_acc + j;
                     *o = p.acc_add ? *o + c[u][w] : c[u][w];
                 } else {
                     from_f(c[u][w] * factor, out + ldo * i + j);
@@ -138,10 +138,11 @@ __global__ void __launch_bounds__(256) xent_finish_kernel(const XentParams p, in
         mx = mn;
     }
     if (!live || sub) return;
-    const float lse = (float)(((double)mx + log2((double)l)) * kLn2d);
-    p.lse[i] = lse;
+    // no sum at all: every logit was NaN
+    const double lse = l == 0.f ? (double)NAN : ((double)mx + log2((double)l)) * kLn2d;
+    p.lse[i] = (float)lse;
     const long long t = p.target[i];
-    p.loss[i] = t == p.ignore ? 0.f : (t < 0 || t >= p.v ? NAN : (float)(((double)mx + log2((double)l)) * kLn2d - (double)p.hit[i]));
+    p.loss[i] = t == p.ignore ? 0.f : (t < 0 || t >= p.v ? NAN : (float)(lse - (double)p.hit[i]));
 }
 
 template <class T>
@@ -149,8 +150,9 @@ __global__ void __launch_bounds__(256) xent_reduce_kernel(const XentParams p) {
     const size_t all = (size_t)p.n * p.d;
     for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < all; e += (size_t)gridDim.x * 256) {
         float s = 0.f;
-        for (int k = 0; k < p.parts; ++k) s += p.acc[(size_t)k * all + e];
-        from_f(s, (T *)p.dx + p.lddx * (long long)(e / p.d) + (long long)(e % p.d));
+        const size_t i = e / p.d, j = e % p.d;
+        for (int k = 0; k < p.parts; ++k) s += p.acc[((size_t)k * p.n + i) * p.ld_acc + j];
+        from_f(s, (T *)p.dx + p.lddx * (long long)i + (long long)j);
     }
 }
 

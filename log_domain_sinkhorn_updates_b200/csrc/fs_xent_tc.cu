@@ -1,0 +1,463 @@
+// Softmax cross entropy on the sm_100a tensor cores: the three products of the
+// operator (logits, dx, dw) as one persistent kernel on CTA pairs with an
+// epilogue each, so that logits live in TMEM only and what leaves a tile is
+// two numbers a row (forward) or the bf16 logit gradients of one piece of the
+// classes (gradient).
+//
+//   LSE  C = x w^T          rows: (max, sum 2^(z - max)) per 256 columns, the target's logit
+//   DL   C = x w^T          dz = scale (e^{z - lse} (dloss + dlse) - onehot dloss) -> bf16
+//   ACC  C = dz w           fp32 partial sums of dx (per part of the classes)
+//   OUT  C = dz^T x or dz w  bf16 rows of dw, or of dx where one product is all of it
+//
+// One tcgen05.mma.cta_group::2 covers a 256 x 256 tile of the pair (each CTA
+// holds 128 rows of A and 128 rows of B, and its own 128 x 256 accumulator, two
+// of them in TMEM's 512 columns): per 64 columns of K a CTA reads 32 KB for 512
+// cycles of MMA, where a 128 x 256 tile of one CTA would read 48 KB.  dz^T and
+// w as the right factor are read as they lie: an operand whose M or N axis is
+// contiguous is staged as 64-element columns by the same 128-byte swizzle and
+// told apart by the descriptor (no transposed copy of x, w or dz is made).
+// Warp 0 loads, warp 1 issues, two groups of four warps take alternate tiles
+// out of TMEM, so an epilogue has two tiles' time before the MMAs wait for it.
+#include <cuda.h>
+
+#include "fs_ops.cuh"
+#include "fs_tc_common.cuh"
+
+namespace fs {
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 256, kBK = 64, kStages = 6;
+constexpr int kOperand = 128 * kBK * 2;      // bytes of a CTA's share of one operand of a stage
+constexpr int kStageBytes = 2 * kOperand;
+constexpr int kThreads = 320;
+constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
+constexpr int kGroupRows = 8;  // row tiles that share a column tile while it is in L2
+
+enum { kLse = 0, kDl = 1, kAcc = 2, kOut = 3 };
+
+// M or N axis contiguous, 128-byte swizzle: 64-element columns of `krows` rows of K, 8192 bytes
+// apart; groups of 8 rows of K 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr) {
+    uint64_t desc = (uint64_t)((addr >> 4) & 0x3FFFu);
+    desc |= (uint64_t)(8192u >> 4) << 16;
+    desc |= (uint64_t)(1024u >> 4) << 32;
+    desc |= (uint64_t)1u << 46;
+    desc |= 2ull << 61;
+    return desc;
+}
+
+__device__ __forceinline__ void st_v8(void *p, const uint32_t *r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void ld_v8(const void *p, uint32_t *r) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+struct Tile {
+    int m0, n0, k0, kb, part;  // first row and column, first K element, K blocks, part
+};
+__device__ __forceinline__ Tile tile_of(const XentGemm &g, int t) {
+    const int per_part = g.mt * g.nt;
+    Tile o;
+    o.part = t / per_part;
+    const int r = t % per_part;
+    const int band = r / (kGroupRows * g.nt), rows = min(kGroupRows, g.mt - band * kGroupRows);
+    const int in = r - band * kGroupRows * g.nt;
+    o.m0 = (band * kGroupRows + in % rows) * kTile;
+    o.n0 = in / rows * kTile;
+    o.k0 = o.part * g.k_part;
+    o.kb = max(0, (min(g.K - o.k0, g.k_part) + kBK - 1) / kBK);
+    return o;
+}
+
+// 128 columns [c, c + 128) of a row from TMEM.
+__device__ __forceinline__ void load128(uint32_t ta, uint32_t (&r)[128]) {
+    tmem_ld32(ta + 0u, &r[0]);
+    tmem_ld32(ta + 32u, &r[32]);
+    tmem_ld32(ta + 64u, &r[64]);
+    tmem_ld32(ta + 96u, &r[96]);
+    tmem_ld_wait();
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kThreads, 1)
+    xent_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const XentParams p, const XentGemm g) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes);  // used in the first CTA
+    uint64_t *empty = full + kStages;                                             // both CTAs
+    uint64_t *sfull = empty + kStages;                                            // [2] both CTAs
+    uint64_t *sempty = sfull + 2;                                                 // [2] first CTA (8 arrivals)
+    uint64_t *drain = sempty + 2;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(drain + 2);
+
+    const uint32_t rank = cluster_rank();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int tiles = g.mt * g.nt * g.parts;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(sfull + b, 1);
+            mbar_init(sempty + b, 8);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_holder)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            int i = 0;  // stages filled so far
+            for (int t = pair; ok && t < tiles; t += pairs) {
+                const Tile T = tile_of(g, t);
+                const int ra = T.m0 + (int)rank * 128, rb = T.n0 + (int)rank * 128;
+                if (*abort_flag) break;
+                for (int kb = 0; kb < T.kb; ++kb, ++i) {
+                    const int s = i % kStages, k = T.k0 + kb * kBK;
+                    if (i >= kStages && !mbar_wait(empty + s, ((uint32_t)(i / kStages) & 1u) ^ 1u, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_expect_tx(full + s, 2u * kStageBytes);
+                    const uint32_t bar = cluster_addr(saddr(full + s), 0);
+                    const uint32_t a = saddr(smem + s * kStageBytes), b = a + kOperand;
+                    if (A_MN) {
+                        tma_load_2d_pair(a, &map_a, bar, ra, g.a_off + k);
+                        tma_load_2d_pair(a + 8192u, &map_a, bar, ra + 64, g.a_off + k);
+                    } else {
+                        tma_load_2d_pair(a, &map_a, bar, k, g.a_off + ra);
+                    }
+                    if (B_MN) {
+                        tma_load_2d_pair(b, &map_b, bar, rb, g.b_off + k);
+                        tma_load_2d_pair(b + 8192u, &map_b, bar, rb + 64, g.b_off + k);
+                    } else {
+                        tma_load_2d_pair(b, &map_b, bar, k, g.b_off + rb);
+                    }
+                }
+            }
+            if (!ok) {
+                atomicOr(p.err, kDevErrTimeout);
+                *abort_flag = 1;
+            }
+            // never leave with copies in flight: both CTAs' copies count on the first one's barriers
+            if (rank == 0)
+                for (int j = max(0, i - kStages); j < i; ++j)
+                    mbar_wait(full + (j % kStages), (uint32_t)(j / kStages) & 1u, p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = make_idesc<0, 256, 256>() | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+            constexpr uint32_t ka = A_MN ? 128u : 2u, kb16 = B_MN ? 128u : 2u;  // 16 of K, in 16-byte units
+            bool ok = true;
+            int i = 0, n = 0;
+            for (int t = pair; ok && t < tiles; t += pairs, ++n) {
+                const Tile T = tile_of(g, t);
+                const int b = n & 1;
+                if (n >= 2 && !mbar_wait_cluster(sempty + b, ((uint32_t)(n >> 1) & 1u) ^ 1u, p.timeout_ns)) ok = false;
+                const uint32_t dt = tmem_base + (uint32_t)(b * 256);
+                for (int kb = 0; ok && kb < T.kb; ++kb, ++i) {
+                    const int s = i % kStages;
+                    if (!mbar_wait(full + s, (uint32_t)(i / kStages) & 1u, p.timeout_ns) || *abort_flag) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = saddr(smem + s * kStageBytes);
+                    const uint64_t ad = A_MN ? sdesc_mn(a) : make_sdesc(a, 128u);
+                    const uint64_t bd = B_MN ? sdesc_mn(a + kOperand) : make_sdesc(a + kOperand, 128u);
+#pragma unroll
+                    for (int k = 0; k < kBK / 16; ++k)
+                        tc_mma_pair<0>(dt, ad + k * ka, bd + k * kb16, idesc, kb > 0 || k > 0 ? 1u : 0u);
+                    tc_commit_pair(saddr(empty + s), (uint16_t)3);
+                }
+                if (ok) tc_commit_pair(saddr(sfull + b), (uint16_t)3);
+            }
+            if (!ok) {
+                atomicOr(p.err, kDevErrTimeout);
+                *abort_flag = 1;
+            }
+            tc_commit_pair(saddr(drain), (uint16_t)1);
+            mbar_wait(drain, 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3, grp = (warp - 2) >> 2;
+        const int rl = (int)rank * 128 + q * 32 + lane;
+        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(grp * 256);
+        const uint32_t sempty0 = cluster_addr(saddr(sempty + grp), 0);
+        bool ok = true;
+        int n = grp;
+        for (int t = pair + grp * pairs; t < tiles; t += 2 * pairs, n += 2) {
+            const Tile T = tile_of(g, t);
+            const int row = T.m0 + rl;
+            const bool live = row < g.M;
+            // what the row needs, fetched while the MMAs run
+            long long target = -1;
+            float gl = 0.f, gs = 0.f, l2 = 0.f;
+            if (EPI <= kDl && live) {
+                target = __ldg(p.target + row);
+                if (EPI == kDl) {
+                    const bool ign = target == p.ignore;
+                    gl = ign ? 0.f : (target < 0 || target >= p.v ? NAN : __ldg(p.dloss + row));
+                    gs = gl + (p.dlse ? __ldg(p.dlse + row) : 0.f);
+                    l2 = __ldg(p.lse + row) * kLog2e;
+                    if (ign) target = -1;
+                }
+            }
+            if (!mbar_wait(sfull + grp, (uint32_t)(n >> 1) & 1u, p.timeout_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            float mx = -INFINITY, l = 0.f;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const int c0 = T.n0 + 128 * half;  // first column of the half
+                uint32_t r[128];
+                if (T.kb > 0) {
+                    load128(taddr + 128u * half, r);
+                } else {  // an empty sum: nothing was multiplied
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) r[k] = 0u;
+                }
+                if (half == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(sempty0);
+                }
+                if (c0 >= g.N) continue;
+                if constexpr (EPI == kLse) {
+                    const long long at = target - c0;
+                    if (__any_sync(~0u, at >= 0 && at < 128)) {
+                        float hit = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 128; ++k)
+                            if (k == at) hit = __uint_as_float(r[k]);
+                        if (at >= 0 && at < 128) p.hit[row] = hit * p.scale;
+                    }
+                    if (c0 + 128 > g.N) {
+#pragma unroll
+                        for (int k = 0; k < 128; ++k)
+                            if (c0 + k >= g.N) r[k] = 0xff800000u;  // -inf
+                    }
+                    consume128_folded(r, p.scale2, mx, l);
+                } else if constexpr (EPI == kDl) {
+                    const long long at = target - p.c0 - c0;
+                    const bool any = __any_sync(~0u, at >= 0 && at < 128);
+                    uint8_t *dst = (uint8_t *)p.dl + ((size_t)row * p.ld_dl + c0) * 2;
+#pragma unroll
+                    for (int k = 0; k < 128; k += 16) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int u = 0; u < 16; u += 2) {
+                            // a row without a gradient stays out even if its logits are not finite
+                            float d0 = gs == 0.f ? 0.f
+                                                 : ex2_approx(fmaf(__uint_as_float(r[k + u]), p.scale2, -l2)) * gs;
+                            float d1 = gs == 0.f ? 0.f
+                                                 : ex2_approx(fmaf(__uint_as_float(r[k + u + 1]), p.scale2, -l2)) * gs;
+                            if (any) {
+                                if (at == k + u) d0 -= gl;
+                                if (at == k + u + 1) d1 -= gl;
+                            }
+                            w[u / 2] = bf16x2(d0 * p.scale, d1 * p.scale);
+                        }
+                        // the row's padding beyond the last class (up to ld_dl, a multiple of 256) may be written
+                        if (live && c0 + k < g.N) st_v8(dst + 2 * k, w);
+                    }
+                } else if constexpr (EPI == kAcc) {
+                    float *dst = p.acc + ((size_t)T.part * g.M + row) * p.ld_acc + c0;
+#pragma unroll
+                    for (int k = 0; k < 128; k += 8) {
+                        if (!live || c0 + k >= g.N) break;  // ld_acc is a multiple of 8
+                        if (p.acc_add) {
+                            uint32_t o[8];
+                            ld_v8(dst + k, o);
+#pragma unroll
+                            for (int u = 0; u < 8; ++u)
+                                r[k + u] = __float_as_uint(__uint_as_float(r[k + u]) + __uint_as_float(o[u]));
+                        }
+                        st_v8(dst + k, &r[k]);
+                    }
+                } else {
+                    __nv_bfloat16 *dst = (__nv_bfloat16 *)g.out + g.ldo * row + c0;
+                    if (live) {
+#pragma unroll
+                        for (int k = 0; k < 128; k += 8) {
+                            uint4 w;
+                            w.x = bf16x2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+                            w.y = bf16x2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
+                            w.z = bf16x2(__uint_as_float(r[k + 4]), __uint_as_float(r[k + 5]));
+                            w.w = bf16x2(__uint_as_float(r[k + 6]), __uint_as_float(r[k + 7]));
+                            if (g.vec && c0 + k + 8 <= g.N) {
+                                *reinterpret_cast<uint4 *>(dst + k) = w;
+                            } else {
+#pragma unroll
+                                for (int u = 0; u < 8; ++u)
+                                    if (c0 + k + u < g.N) dst[k + u] = __float2bfloat16_rn(__uint_as_float(r[k + u]));
+                            }
+                        }
+                    }
+                }
+            }
+            if (EPI == kLse && live) p.part[(size_t)(T.n0 / kTile) * g.M + row] = make_float2(mx, l);
+            if (*abort_flag) break;
+        }
+        if (!ok) {
+            atomicOr(p.err, kDevErrTimeout);
+            *abort_flag = 1;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u) : "memory");
+    }
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+cudaError_t launch(const XentParams &p, const XentGemm &g, const CUtensorMap &a, const CUtensorMap &b,
+                   cudaStream_t s) {
+    auto kern = xent_tc_kernel<EPI, A_MN, B_MN>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    const int tiles = g.mt * g.nt * g.parts;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (tiles < g.pairs ? tiles : g.pairs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, a, b, p, g);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+int up(int a, int b) { return (a + b - 1) / b; }
+
+XentGemm shape(int M, int N, int K, int parts, int pairs) {
+    XentGemm g{};
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.mt = up(M, kTile);
+    g.nt = up(N, kTile);
+    g.parts = parts;
+    g.k_part = parts > 1 ? up(up(K, parts), kBK) * kBK : up(K > 0 ? K : 1, kBK) * kBK;
+    g.pairs = pairs;
+    return g;
+}
+
+// A map of a row-major [rows][width] bf16 matrix: boxes of 64 x box_rows.
+bool encode(CUtensorMap *m, const void *base, long long width, long long rows, long long ld, int box_rows) {
+    const long long size[2] = {width, rows}, stride[1] = {rows > 1 ? ld : (width + 7) / 8 * 8};
+    const int box[2] = {64, box_rows};
+    return encode_bf16_map(m, base, 2, size, stride, box);
+}
+
+}  // namespace
+
+// The rows a TMA box can start on: base and row stride multiples of 16 bytes.
+bool xent_tc_ok(const void *x, long long ldx, const void *w, long long ldw, int n, int v) {
+    auto al = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    auto ld = [](long long s, int rows) { return rows <= 1 || (s > 0 && s % 8 == 0 && s < 1ll << 36); };
+    return al(x) && al(w) && ld(ldx, n) && ld(ldw, v);
+}
+
+cudaError_t launch_xent_lse_tc(const XentParams &p, int pairs, cudaStream_t s) {
+    CUtensorMap a, b;
+    if (!encode(&a, p.x, p.d, p.n, p.ldx, 128) || !encode(&b, p.w, p.d, p.v, p.ldw, 128)) return cudaErrorInvalidValue;
+    return launch<kLse, false, false>(p, shape(p.n, p.v, p.d, 1, pairs), a, b, s);
+}
+cudaError_t launch_xent_dl_tc(const XentParams &p, int pairs, cudaStream_t s) {
+    CUtensorMap a, b;
+    if (!encode(&a, p.x, p.d, p.n, p.ldx, 128) || !encode(&b, p.w, p.d, p.v, p.ldw, 128)) return cudaErrorInvalidValue;
+    XentGemm g = shape(p.n, p.c1 - p.c0, p.d, 1, pairs);
+    g.b_off = p.c0;
+    return launch<kDl, false, false>(p, g, a, b, s);
+}
+// dx (direct: the whole of it, written in bf16; otherwise partial sums in acc)
+cudaError_t launch_xent_dx_tc(const XentParams &p, bool direct, int pairs, cudaStream_t s) {
+    CUtensorMap a, b;
+    const int nc = p.c1 - p.c0;
+    if (!encode(&a, p.dl, nc, p.n, p.ld_dl, 128) || !encode(&b, p.w, p.d, p.v, p.ldw, 64)) return cudaErrorInvalidValue;
+    XentGemm g = shape(p.n, p.d, nc, p.parts, pairs);
+    g.b_off = p.c0;
+    if (!direct) return launch<kAcc, false, true>(p, g, a, b, s);
+    g.out = p.dx;
+    g.ldo = p.lddx;
+    g.vec = p.lddx % 8 == 0 && (reinterpret_cast<uintptr_t>(p.dx) & 15) == 0;
+    return launch<kOut, false, true>(p, g, a, b, s);
+}
+cudaError_t launch_xent_dw_tc(const XentParams &p, int pairs, cudaStream_t s) {
+    CUtensorMap a, b;
+    const int nc = p.c1 - p.c0;
+    if (!encode(&a, p.dl, nc, p.n, p.ld_dl, 64) || !encode(&b, p.x, p.d, p.n, p.ldx, 64)) return cudaErrorInvalidValue;
+    XentGemm g = shape(nc, p.d, p.n, 1, pairs);
+    g.out = (__nv_bfloat16 *)p.dw + p.lddw * p.c0;
+    g.ldo = p.lddw;
+    g.vec = p.lddw % 8 == 0 && (reinterpret_cast<uintptr_t>(p.dw) & 15) == 0;
+    return launch<kOut, true, true>(p, g, a, b, s);
+}
+
+// CTA pairs that are resident at once on the current device.
+cudaError_t xent_tc_pairs(int *pairs) {
+    auto kern = xent_tc_kernel<kLse, false, false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(148);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(pairs, kern, &cfg);
+    if (e == cudaSuccess && *pairs < 1) e = cudaErrorInvalidConfiguration;
+    return e;
+}
+
+}  // namespace fs
