@@ -51,6 +51,18 @@ __device__ __forceinline__ float attn_bias2(const AttnParams &p, int b, int j, i
 bool encode_bf16_map(CUtensorMap *map, const void *base, int dims, const long long *size, const long long *stride,
                      const int *box);
 
+// Geometry of the tensor-core attention kernels.
+struct AttnTc {
+    int datoms, vatoms;  // 64-element columns of d and dv
+    int dv_pad;          // dv rounded up to 16
+    int slots;           // ring of K and V tiles
+    int k_head, k_batch, v_head, v_batch;  // 0: that axis of the map has one element
+};
+bool attn_tc_view(const void *base, const fs_view &s, int tokens, int heads, int batch, bool map);
+bool attn_map(CUtensorMap *map, const void *base, const fs_view &s, int w, int tokens, int heads, int batch,
+              int box_rows, int *hm, int *bm);
+cudaError_t launch_xattn_tc(const AttnParams &p, bool two_blocks, cudaStream_t s);
+
 cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s);

@@ -112,10 +112,11 @@ fs_status check_attn(const fs_attn_desc *D, bool grad) {
 
 struct AttnPlan {
     int splits = 1, split_keys = 0;
+    bool two_blocks = false;  // tensor cores: 256 rows a CTA
     size_t part_ml = 0, part_o = 0, dot = 0, total = 0;  // workspace offsets, and its size
 };
 
-AttnPlan plan_attn(const fs_attn_desc &D, bool grad, int sms) {
+AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, const Device &dev) {
     AttnPlan L;
     const size_t rows = (size_t)D.n * (D.heads / D.kv_heads), heads = (size_t)D.batch * D.kv_heads;
     L.split_keys = std::max(D.m, 1);
@@ -123,20 +124,42 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, int sms) {
         L.total = align256((size_t)D.batch * D.heads * D.n * 4);
         return L;
     }
-    // Few rows: enough parts of at least 256 keys that two CTAs' worth of work reach every SM.
-    const size_t ctas = (rows + 15) / 16 * heads;
-    if (ctas > 0 && ctas < (size_t)sms) {
-        const int want = (int)((2 * sms + ctas - 1) / ctas);
-        const int parts = std::max(1, std::min(want, up(D.m, 256)));
-        L.split_keys = std::max(64, up(up(std::max(D.m, 1), parts), 64) * 64);
-        L.splits = std::max(1, up(D.m, L.split_keys));
+    if (rows == 0 || heads == 0) return L;
+    // Parts of the keys: as many as cost least, in waves of CTAs (one an SM on the tensor cores, two otherwise) times
+    // the tiles of a part plus its start and end; more than one part costs the joining pass too.
+    const int tile = tc ? 128 : 64, side = tc ? 128 : 16, slots = tc ? dev.sms : 2 * dev.sms;
+    const size_t ctas = (rows + side - 1) / side * heads;
+    const int tiles = up(std::max(D.m, 1), tile);
+    double best = 1e300;
+    for (int s = 1; s <= std::min(tiles, 128) && (s == 1 || ctas < 2 * (size_t)slots); ++s) {
+        const int t = up(tiles, s), parts = up(tiles, t);
+        const double cost = (double)((ctas * parts + slots - 1) / slots) * (t + 3.0) + (parts > 1 ? 3.0 + 0.02 * parts : 0.0);
+        if (cost < best - 1e-9) {
+            best = cost;
+            L.splits = parts;
+            L.split_keys = t * tile;
+        }
     }
+    L.two_blocks = tc && L.splits == 1 && (rows + 255) / 256 * heads >= (size_t)dev.sms;
     if (L.splits > 1) {
-        L.part_ml = 0;
         L.part_o = align256(rows * heads * L.splits * sizeof(float2));
         L.total = L.part_o + align256(rows * heads * L.splits * D.dv * sizeof(float));
     }
     return L;
+}
+size_t attn_workspace(const fs_attn_desc &D, bool grad, const Device &dev) {
+    const size_t simt = plan_attn(D, grad, false, dev).total;
+    return D.dtype == FS_BF16 ? std::max(simt, plan_attn(D, grad, true, dev).total) : simt;
+}
+
+// Whether the tensor-core kernels take the call: bf16, widths up to 128 and multiples of 8, keys to load, and
+// bases and strides that 16-byte loads and TMA boxes can start on.
+bool attn_tc(const fs_attn_desc &D, const void *q, const void *k, const void *v, const void *out) {
+    return D.dtype == FS_BF16 && D.d <= 128 && D.dv <= 128 && D.d % 8 == 0 && D.dv % 8 == 0 && D.m > 0 &&
+           fs::attn_tc_view(q, D.q, D.n, D.heads, D.batch, false) &&
+           fs::attn_tc_view(k, D.k, D.m, D.kv_heads, D.batch, true) &&
+           fs::attn_tc_view(v, D.v, D.m, D.kv_heads, D.batch, true) &&
+           fs::attn_tc_view(out, D.out, D.n, D.heads, D.batch, false);
 }
 
 fs::AttnParams attn_params(const fs_attn_desc &D, const AttnPlan &L, const Device &dev, void *ws) {
@@ -264,7 +287,7 @@ extern "C" {
 size_t fs_cross_attn_workspace(const fs_attn_desc *desc, int grad) {
     Device dev;
     if (check_attn(desc, grad != 0) != FS_OK || current_device(&dev) != FS_OK) return 0;
-    return plan_attn(*desc, grad != 0, dev.sms).total;
+    return attn_workspace(*desc, grad != 0, dev);
 }
 
 fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const void *k, const void *v, const int *k_len,
@@ -277,7 +300,8 @@ fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const void *k, 
     if (!q || !out || (D.m > 0 && (!k || !v))) return reject(FS_ERR_INVALID_ARG, "null argument");
     Device dev;
     if ((st = current_device(&dev)) != FS_OK) return st;
-    const AttnPlan L = plan_attn(D, false, dev.sms);
+    const bool bf16 = D.dtype == FS_BF16, tc = attn_tc(D, q, k, v, out);
+    const AttnPlan L = plan_attn(D, false, tc, dev);
     if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
     fs::AttnParams p = attn_params(D, L, dev, workspace);
     p.q = q;
@@ -288,8 +312,10 @@ fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const void *k, 
     p.out = out;
     p.lse = lse;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool bf16 = D.dtype == FS_BF16;
-    OPS_LAUNCH(fs::launch_xattn_simt(p, bf16, s), 1);
+    if (tc)
+        OPS_LAUNCH(fs::launch_xattn_tc(p, L.two_blocks, s), 1);
+    else
+        OPS_LAUNCH(fs::launch_xattn_simt(p, bf16, s), 1);
     if (p.splits > 1) OPS_LAUNCH(fs::launch_xattn_combine(p, bf16, s), 1);
     return FS_OK;
 }
@@ -305,7 +331,7 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
         return reject(FS_ERR_INVALID_ARG, "null argument");
     Device dev;
     if ((st = current_device(&dev)) != FS_OK) return st;
-    const AttnPlan L = plan_attn(D, true, dev.sms);
+    const AttnPlan L = plan_attn(D, true, false, dev);
     if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
     fs::AttnParams p = attn_params(D, L, dev, workspace);
     p.q = q;

@@ -1,0 +1,576 @@
+// Cross attention forward on the sm_100a tensor cores: S = Q K^T and O += P V
+// per 128-key tile with S, P and O in TMEM, one pass over the keys with a
+// running maximum and sum a row.
+//
+// A CTA has 128-row blocks of Q (rows r = query x heads that share the key
+// head) and two softmax groups of 128 threads, a thread a row:
+//  * QT = 2: two row blocks, each group its own, every K and V tile serves both
+//    (whole sequences: half the stream of K and V a score);
+//  * QT = 1: one row block, the groups take alternate key tiles into their own
+//    S and O and are joined at the end (few rows; the loads of one tile run
+//    under the softmax of the other).
+// TMEM (512 columns): S_g / P_g in [128 g, 128 g + 128), O_g behind them in
+// [256 + 128 g, ...).  P (bf16) is written over the S it came from and is the
+// A operand of the P V product there; V is its right factor as it lies in
+// memory (width contiguous), by the descriptor.
+//
+// The maximum is lazy: weights are taken against the running maximum until a
+// score exceeds it by 2^8, and only then are O and the sum rescaled (by the
+// row's own thread, between two products), so P stays below 2^8, exact to
+// bf16's relative rounding as ever, and most tiles touch O from the tensor
+// core alone.
+//
+// Keys past the length or masked by the bias: one warp reads the bias ahead,
+// and where a tile has such keys it clears their rows of K and V in shared
+// memory before the products read them, so that whatever stood there (NaN
+// included) is a zero score plus -inf and a zero weight times zero.
+//
+// Warps: 0 loads K and V by TMA; 1 allocates TMEM; 1 and 2 issue the MMAs of
+// groups 0 and 1; 3 bias and masks; 4..7 and 8..11 are the softmax groups.
+#include <cuda.h>
+
+#include "fs_ops.cuh"
+#include "fs_tc_common.cuh"
+
+namespace fs {
+namespace {
+
+using namespace tc;
+
+constexpr int kTS = 128;        // keys of a tile
+constexpr int kThreads = 384;
+constexpr int kBiasSlots = 4;
+constexpr float kLazy = 8.f;
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// The P V product's right factor: rows = keys (K axis), 64-element columns of
+// the width `lbo` bytes apart, 128-byte swizzle.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, uint32_t lbo) {
+    uint64_t desc = (uint64_t)((addr >> 4) & 0x3FFFu);
+    desc |= (uint64_t)(lbo >> 4) << 16;
+    desc |= (uint64_t)(1024u >> 4) << 32;
+    desc |= (uint64_t)1u << 46;
+    desc |= 2ull << 61;
+    return desc;
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *map, uint32_t bar, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void group_bar(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+struct Layout {
+    uint32_t q, ring, slot, bias, ml, bars, total;
+};
+__host__ __device__ inline Layout layout(int qt, int datoms, int vatoms, int slots) {
+    Layout L;
+    L.q = 0;
+    L.ring = L.q + (uint32_t)qt * datoms * 16384u;
+    L.slot = (uint32_t)(datoms > vatoms ? datoms : vatoms) * 16384u;
+    L.bias = L.ring + (uint32_t)slots * L.slot;
+    L.ml = L.bias + kBiasSlots * kTS * 4;
+    L.bars = L.ml + 128 * 8;
+    L.total = L.bars + (3 * slots + 2 * kBiasSlots + 1 + 2 + 4 + 2 + 2) * 8 + 32;
+    return L;
+}
+
+// KS: steps of 16 along d, fixed at compile time (descriptor offsets are then
+// immediates); what lies beyond d is zero in shared memory.
+template <int QT, int KS>
+__global__ void __launch_bounds__(kThreads, 1)
+    xattn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                    const AttnParams p, const AttnTc g) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+    const int NS = g.slots;
+    const Layout L = layout(QT, g.datoms, g.vatoms, NS);
+    uint8_t *sQ = smem + L.q, *ring = smem + L.ring;
+    float *sBias = reinterpret_cast<float *>(smem + L.bias);
+    float2 *sML = reinterpret_cast<float2 *>(smem + L.ml);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L.bars);  // [NS] tile loaded
+    uint64_t *ready = full + NS;                                   // [NS] masked rows cleared
+    uint64_t *empty = ready + NS;                                  // [NS] products that read it are complete
+    uint64_t *bfull = empty + NS;                                  // [kBiasSlots]
+    uint64_t *bempty = bfull + kBiasSlots;                         // [kBiasSlots]
+    uint64_t *qfull = bempty + kBiasSlots;
+    uint64_t *sfull = qfull + 1;    // [2]
+    uint64_t *pready = sfull + 2;   // [2][2] P of group g, half h
+    uint64_t *pvdone = pready + 4;  // [2]
+    uint64_t *drain = pvdone + 2;   // [2] every MMA of issuer g is complete
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    volatile int *tile_masked = reinterpret_cast<volatile int *>(tmem_holder + 2);  // [kBiasSlots]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = p.n * p.group;
+    const int blocks = (rows + QT * 128 - 1) / (QT * 128);
+    const int rb = blockIdx.x % blocks, sp = blockIdx.x / blocks;
+    const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads;
+    const int keys = attn_keys(p, b);
+    const int j_beg = sp * p.split_keys, j_end = min(keys, j_beg + p.split_keys);
+    const int nt = j_end > j_beg ? (j_end - j_beg + kTS - 1) / kTS : 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(ready + s, 1);
+            mbar_init(empty + s, QT);
+        }
+        for (int s = 0; s < kBiasSlots; ++s) {
+            mbar_init(bfull + s, 1);
+            mbar_init(bempty + s, 4 * QT);
+        }
+        mbar_init(qfull, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sfull + i, 1);
+            mbar_init(pready + 2 * i, 4);
+            mbar_init(pready + 2 * i + 1, 4);
+            mbar_init(pvdone + i, 1);
+            mbar_init(drain + i, 1);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_holder)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+
+    if (warp == 0) {
+        // ---------------- K and V tiles: slot 2 t holds K(t), slot 2 t + 1 V(t) ----------------
+        if (lane == 0) {
+            bool ok = true;
+            int i = 0;
+            for (; ok && i < 2 * nt; ++i) {
+                const int s = i % NS, t = i >> 1;
+                if (*abort_flag) break;
+                if (i >= NS && !mbar_wait(empty + s, ((uint32_t)(i / NS) & 1u) ^ 1u, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                const int atoms = i & 1 ? g.vatoms : g.datoms;
+                const CUtensorMap *map = i & 1 ? &map_v : &map_k;
+                const int hm = i & 1 ? g.v_head : g.k_head, bm = i & 1 ? g.v_batch : g.k_batch;
+                const uint32_t dst = saddr(ring + (size_t)s * L.slot);
+                mbar_expect_tx(full + s, (uint32_t)atoms * 16384u);
+                for (int a = 0; a < atoms; ++a)
+                    tma_load_4d(dst + a * 16384u, map, saddr(full + s), a * 64, j_beg + t * kTS, c * hm, b * bm);
+            }
+            if (!ok) {
+                atomicOr(p.err, kDevErrTimeout);
+                *abort_flag = 1;
+            }
+            for (int k = max(0, i - NS); k < i; ++k) mbar_wait(full + (k % NS), (uint32_t)(k / NS) & 1u, p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        // ---------------- bias slices and masked rows ----------------
+        bool ok = true;
+        for (int t = 0; ok && t < nt; ++t) {
+            const int j = t % kBiasSlots;
+            float bv[4];
+            unsigned dead[4];
+            bool any = p.bias != nullptr;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                bv[u] = attn_bias2(p, b, j_beg + t * kTS + 32 * u + lane, j_end);
+                dead[u] = __ballot_sync(~0u, bv[u] == -INFINITY);
+                any = any || dead[u];
+            }
+            if (t >= kBiasSlots && !mbar_wait(bempty + j, ((uint32_t)(t / kBiasSlots) & 1u) ^ 1u, p.timeout_ns))
+                ok = false;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) sBias[j * kTS + 32 * u + lane] = bv[u];
+            if (lane == 0) tile_masked[j] = any;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bfull + j);
+            const bool clear = dead[0] | dead[1] | dead[2] | dead[3];
+            for (int kv = 0; kv < 2; ++kv) {
+                const int i = 2 * t + kv, s = i % NS;
+                if (!mbar_wait(full + s, (uint32_t)(i / NS) & 1u, p.timeout_ns)) ok = false;
+                if (clear) {
+                    uint8_t *tile = ring + (size_t)s * L.slot;
+                    const int atoms = kv ? g.vatoms : g.datoms;
+                    for (int e = lane; e < kTS * 8; e += 32) {  // 16-byte pieces of the 128-byte rows of an atom
+                        const int row = e >> 3;
+                        const unsigned word = row < 64 ? (row < 32 ? dead[0] : dead[1]) : (row < 96 ? dead[2] : dead[3]);
+                        if (word >> (row & 31) & 1u)
+                            for (int a = 0; a < atoms; ++a)
+                                *reinterpret_cast<uint4 *>(tile + a * 16384 + row * 128 + (e & 7) * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_async();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(ready + s);
+            }
+            if (*abort_flag) break;
+        }
+        if (!ok && lane == 0) {
+            atomicOr(p.err, kDevErrTimeout);
+            *abort_flag = 1;
+        }
+        __syncwarp();
+    } else if (warp == 1 || warp == 2) {
+        // ---------------- MMA issuers ----------------
+        if (lane == 0) {
+            const int grp = warp - 1;
+            const int t0 = QT == 2 ? 0 : grp, step = QT == 2 ? 1 : 2;
+            const uint32_t idesc_s = make_idesc<0, 128, kTS>();
+            const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
+                                     ((uint32_t)(g.dv_pad >> 3) << 17) | ((128u >> 4) << 24);
+            const uint32_t ts = tmem_base + (uint32_t)(grp * 128), to = tmem_base + 256u + (uint32_t)(grp * 128);
+            const uint64_t qd = make_sdesc(saddr(sQ) + (QT == 2 ? grp : 0) * g.datoms * 16384u, 128u);
+            auto slot_ready = [&](int i) {
+                const uint32_t ph = (uint32_t)(i / NS) & 1u;
+                return mbar_wait(full + i % NS, ph, p.timeout_ns) && mbar_wait(ready + i % NS, ph, p.timeout_ns);
+            };
+            auto s_product = [&](int t) {
+                if (!slot_ready(2 * t)) return false;
+                tc_fence_after();
+                const uint64_t kd = make_sdesc(saddr(ring + (size_t)(2 * t % NS) * L.slot), 128u);
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    tc_mma<0>(ts, qd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
+                              kd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
+                tc_commit(saddr(sfull + grp));
+                tc_commit(saddr(empty + 2 * t % NS));
+                return true;
+            };
+            bool ok = mbar_wait(qfull, 0, p.timeout_ns);
+            tc_fence_after();
+            if (ok && t0 < nt) ok = s_product(t0);
+            int n = 0;
+            for (int t = t0; ok && t < nt; t += step, ++n) {
+                const int i = 2 * t + 1;
+                for (int h = 0; ok && h < 2; ++h) {
+                    if (!mbar_wait(pready + 2 * grp + h, (uint32_t)n & 1u, p.timeout_ns) || (h == 0 && !slot_ready(i)) ||
+                        *abort_flag) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t vd = sdesc_mn(saddr(ring + (size_t)(i % NS) * L.slot), 16384u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)  // 16 keys: 8 TMEM columns of P, 2048 bytes of V
+                        tc_mma_ts(to, ts + 32u * h + 8u * k, vd + (4 * h + k) * 128u, idesc_o,
+                                  n > 0 || h > 0 || k > 0 ? 1u : 0u);
+                }
+                if (!ok) break;
+                tc_commit(saddr(pvdone + grp));
+                tc_commit(saddr(empty + i % NS));
+                // the next S takes the columns of P: not before the products that read it are complete
+                if (t + step < nt) ok = mbar_wait(pvdone + grp, (uint32_t)n & 1u, p.timeout_ns) && s_product(t + step);
+            }
+            if (!ok) {
+                atomicOr(p.err, kDevErrTimeout);
+                *abort_flag = 1;
+            }
+            tc_commit(saddr(drain + grp));
+            mbar_wait(drain + grp, 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- softmax groups ----------------
+        const int q = warp & 3, grp = (warp - 4) >> 2;
+        const int rl = q * 32 + lane;
+        const int blk = QT == 2 ? grp : 0;
+        const int r = (rb * QT + blk) * 128 + rl;  // packed row
+        const bool warp_live = (rb * QT + blk) * 128 + q * 32 < rows;
+        // Q into shared memory, 16 bytes at a time, as the 128-byte swizzle lays it
+        {
+            const int per = g.datoms * 8;
+            for (int e = (int)threadIdx.x - 128; e < QT * 128 * per; e += 256) {
+                const int row = e / per, ch = e % per, at = rb * QT * 128 + row;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (at < rows && ch * 8 < p.d)
+                    v = *reinterpret_cast<const uint4 *>(
+                        (const __nv_bfloat16 *)p.q + p.qs.batch * b + p.qs.token * (at / p.group) +
+                        p.qs.head * (c * p.group + at % p.group) + ch * 8);
+                *reinterpret_cast<uint4 *>(sQ + (row >> 7) * g.datoms * 16384 + (ch >> 3) * 16384 + (row & 127) * 128 +
+                                           (((ch & 7) ^ (row & 7)) << 4)) = v;
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull);
+        }
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        const uint32_t ts = tmem_base + lanes + (uint32_t)(grp * 128);
+        const uint32_t to = tmem_base + lanes + 256u + (uint32_t)(grp * 128);
+        const float c2 = p.scale2;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        int n = 0;
+        for (int t = QT == 2 ? 0 : grp; t < nt; t += QT == 2 ? 1 : 2, ++n) {
+            const int j = t % kBiasSlots;
+            if (!mbar_wait(sfull + grp, (uint32_t)n & 1u, p.timeout_ns) ||
+                !mbar_wait(bfull + j, (uint32_t)(t / kBiasSlots) & 1u, p.timeout_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (warp_live) {
+                uint32_t s[128];
+                tmem_ld32(ts + 0u, &s[0]);
+                tmem_ld32(ts + 32u, &s[32]);
+                tmem_ld32(ts + 64u, &s[64]);
+                tmem_ld32(ts + 96u, &s[96]);
+                tmem_ld_wait();
+                float mul = c2;
+                if (tile_masked[j]) {  // scores in base 2 with the bias; otherwise they stay as they are
+                    const float4 *bq = reinterpret_cast<const float4 *>(sBias + j * kTS);
+                    const uint64_t cc = pack2(c2, c2);
+#pragma unroll
+                    for (int k = 0; k < 128; k += 4) {
+                        const float4 bb = bq[k / 4];
+                        float z0, z1, z2, z3;
+                        unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, pack2(bb.x, bb.y)),
+                                z0, z1);
+                        unpack2(fma2(pack2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), cc,
+                                     pack2(bb.z, bb.w)),
+                                z2, z3);
+                        s[k] = __float_as_uint(z0);
+                        s[k + 1] = __float_as_uint(z1);
+                        s[k + 2] = __float_as_uint(z2);
+                        s[k + 3] = __float_as_uint(z3);
+                    }
+                    mul = 1.f;
+                }
+                float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 128; k += 8) {
+                    t0 = max3(t0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                    t1 = max3(t1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+                    t2 = max3(t2, __uint_as_float(s[k + 4]), __uint_as_float(s[k + 5]));
+                    t3 = max3(t3, __uint_as_float(s[k + 6]), __uint_as_float(s[k + 7]));
+                }
+                const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * mul;
+                const bool grow = top > m + kLazy;  // also the first key that counts (m = -inf)
+                const float mn = grow ? top : m;
+                if (n > 0 && __any_sync(~0u, grow)) {
+                    // O and the sum move to the new maximum; the products so far have to be in
+                    if (!mbar_wait(pvdone + grp, (uint32_t)(n - 1) & 1u, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const float f = grow && m != -INFINITY ? ex2_approx(m - mn) : (grow ? 0.f : 1.f);
+                    l *= f;
+                    for (int k = 0; k < g.dv_pad; k += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(to + k, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+                        tmem_st16(to + k, o);
+                    }
+                    tmem_st_wait();
+                }
+                m = mn;
+                const float ref = m == -INFINITY ? 0.f : m;
+                const uint64_t cc = pack2(mul, mul), rn = pack2(-ref, -ref);
+                uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int k = 0; k < 64; k += 2) {
+                        float d0, d1;
+                        unpack2(fma2(pack2(__uint_as_float(s[64 * h + k]), __uint_as_float(s[64 * h + k + 1])), cc, rn),
+                                d0, d1);
+                        d0 = ex2_approx(d0);
+                        d1 = ex2_approx(d1);
+                        acc[(k / 2) & 1] = add2(acc[(k / 2) & 1], pack2(d0, d1));
+                        w[k / 2] = bf16x2(d0, d1);
+                    }
+                    tmem_st32(ts + 32u * h, w);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pready + 2 * grp + h);
+                }
+                float a0, a1, a2, a3;
+                unpack2(acc[0], a0, a1);
+                unpack2(acc[1], a2, a3);
+                l += (a0 + a1) + (a2 + a3);
+            } else if (lane == 0) {  // no row of this warp exists: its lanes of P may hold anything
+                mbar_arrive(pready + 2 * grp);
+                mbar_arrive(pready + 2 * grp + 1);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bempty + j);
+            if (*abort_flag) break;
+        }
+        if (ok && n > 0 && !mbar_wait(pvdone + grp, (uint32_t)(n - 1) & 1u, p.timeout_ns)) ok = false;
+        if (!ok) {
+            atomicOr(p.err, kDevErrTimeout);
+            *abort_flag = 1;
+        }
+        tc_fence_after();
+        float f0 = 1.f, f1 = 0.f;  // weights of this group's and the other group's sums
+        float *xo = reinterpret_cast<float *>(ring);  // QT = 1: group 1's O, [column][row]
+        if (QT == 1) {
+            // every product has read the ring by now: each group has waited for its last one
+            group_bar(1, 256);
+            if (grp == 1) {
+                sML[rl] = make_float2(m, l);
+                if (warp_live && n > 0)
+                    for (int k = 0; k < g.dv_pad; k += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(to + k, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) xo[(k + u) * 128 + rl] = __uint_as_float(o[u]);
+                    }
+            }
+            group_bar(1, 256);
+            if (grp == 0) {
+                const float2 other = sML[rl];
+                if (nt > 1) {
+                    const float mn = fmaxf(m, other.x), ref = mn == -INFINITY ? 0.f : mn;
+                    f0 = ex2_approx(m - ref);
+                    f1 = ex2_approx(other.x - ref);
+                    l = l * f0 + other.y * f1;
+                    m = mn;
+                }
+            }
+        }
+        if (warp_live && (QT == 2 || grp == 0)) {
+            const bool live = r < rows;
+            if (p.splits > 1) {
+                const size_t at = ((size_t)(sp * p.batch + b) * p.kv_heads + c) * rows + r;
+                if (live) p.part_ml[at] = make_float2(m, l);
+                if (nt > 0)
+                    for (int k = 0; k < p.dv; k += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(to + k, o);
+                        tmem_ld_wait();
+                        float v[16];
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) {
+                            v[u] = __uint_as_float(o[u]) * f0;
+                            if (QT == 1 && nt > 1) v[u] = fmaf(xo[(k + u) * 128 + rl], f1, v[u]);
+                        }
+#pragma unroll
+                        for (int u = 0; u < 16; u += 4)
+                            if (live && k + u < p.dv)  // dv is a multiple of 8
+                                *reinterpret_cast<float4 *>(p.part_o + at * p.dv + k + u) =
+                                    make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+                    }
+            } else {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const int h = c * p.group + r % p.group, i = r / p.group;
+                __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out + p.os.batch * b + p.os.token * i + p.os.head * h;
+                for (int k = 0; k < p.dv; k += 16) {
+                    uint32_t o[16];
+                    if (nt > 0) {
+                        tmem_ld16(to + k, o);
+                        tmem_ld_wait();
+                    }
+                    uint32_t w[8];
+#pragma unroll
+                    for (int u = 0; u < 16; u += 2) {
+                        float v0 = 0.f, v1 = 0.f;
+                        if (nt > 0) {
+                            v0 = __uint_as_float(o[u]) * f0;
+                            v1 = __uint_as_float(o[u + 1]) * f0;
+                            if (QT == 1 && nt > 1) {
+                                v0 = fmaf(xo[(k + u) * 128 + rl], f1, v0);
+                                v1 = fmaf(xo[(k + u + 1) * 128 + rl], f1, v1);
+                            }
+                        }
+                        w[u / 2] = bf16x2(v0 * inv, v1 * inv);
+                    }
+                    if (live) *reinterpret_cast<uint4 *>(dst + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (live && k + 8 < p.dv)
+                        *reinterpret_cast<uint4 *>(dst + k + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+                if (p.lse && live)
+                    p.lse[((size_t)b * p.heads + h) * p.n + i] =
+                        l == 0.f ? -INFINITY : (float)(((double)m + log2((double)l)) * kLn2d);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u) : "memory");
+    }
+}
+
+template <int QT, int KS>
+cudaError_t launch(const AttnParams &p, AttnTc g, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
+    const uint32_t limit = 227u * 1024u;
+    g.slots = 8;
+    while (layout(QT, g.datoms, g.vatoms, g.slots).total + 1024u > limit) --g.slots;
+    const uint32_t smem = layout(QT, g.datoms, g.vatoms, g.slots).total + 1024u;
+    cudaError_t e = cudaFuncSetAttribute(xattn_tc_kernel<QT, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
+    if (e != cudaSuccess) return e;
+    const int blocks = (p.n * p.group + QT * 128 - 1) / (QT * 128);
+    // at least half the shared memory: a CTA holds all of TMEM, so two on one SM would wait for each other
+    xattn_tc_kernel<QT, KS><<<dim3(blocks * p.splits, p.batch * p.kv_heads), kThreads,
+                          smem > limit / 2 + 1024u ? smem : limit / 2 + 1024u, s>>>(mk, mv, p, g);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// A [batch][token][head][w] bf16 tensor as a 4-D map (boxes of 64 x box_rows of one head); a head or batch axis of
+// stride 0 or of one element is left out (*hm, *bm: what to multiply its index with).
+bool attn_map(CUtensorMap *map, const void *base, const fs_view &s, int w, int tokens, int heads, int batch,
+              int box_rows, int *hm, int *bm) {
+    const long long unit = (w + 7) / 8 * 8;
+    *hm = heads > 1 && s.head > 0 ? 1 : 0;
+    *bm = batch > 1 && s.batch > 0 ? 1 : 0;
+    const long long size[4] = {w, tokens, *hm ? heads : 1, *bm ? batch : 1};
+    const long long stride[3] = {tokens > 1 ? s.token : unit, *hm ? s.head : unit, *bm ? s.batch : unit};
+    const int box[4] = {64, box_rows, 1, 1};
+    return encode_bf16_map(map, base, 4, size, stride, box);
+}
+
+// What the vector loads and the TMA boxes of the tensor-core kernels need of a tensor.
+bool attn_tc_view(const void *base, const fs_view &s, int tokens, int heads, int batch, bool map) {
+    const long long big = 1ll << 36;
+    if (reinterpret_cast<uintptr_t>(base) & 15) return false;
+    if (tokens > 1 && (s.token % 8 || s.token >= big || (map && s.token == 0))) return false;
+    if (heads > 1 && (s.head % 8 || s.head >= big)) return false;
+    return !(batch > 1 && (s.batch % 8 || s.batch >= big));
+}
+
+// two_blocks: 256 rows a CTA (p.splits = 1)
+cudaError_t launch_xattn_tc(const AttnParams &p, bool two_blocks, cudaStream_t s) {
+    AttnTc g{};
+    g.datoms = (p.d + 63) / 64;
+    g.vatoms = (p.dv + 63) / 64;
+    g.dv_pad = (p.dv + 15) / 16 * 16;
+    CUtensorMap mk, mv;
+    if (!attn_map(&mk, p.k, p.ks, p.d, p.m, p.kv_heads, p.batch, kTS, &g.k_head, &g.k_batch) ||
+        !attn_map(&mv, p.v, p.vs, p.dv, p.m, p.kv_heads, p.batch, kTS, &g.v_head, &g.v_batch))
+        return cudaErrorInvalidValue;
+    const int ks = (p.d + 31) / 32 * 2;
+    if (two_blocks)
+        return ks == 2 ? launch<2, 2>(p, g, mk, mv, s) : ks == 4 ? launch<2, 4>(p, g, mk, mv, s)
+               : ks == 6 ? launch<2, 6>(p, g, mk, mv, s) : launch<2, 8>(p, g, mk, mv, s);
+    return ks == 2 ? launch<1, 2>(p, g, mk, mv, s) : ks == 4 ? launch<1, 4>(p, g, mk, mv, s)
+           : ks == 6 ? launch<1, 6>(p, g, mk, mv, s) : launch<1, 8>(p, g, mk, mv, s);
+}
+
+}  // namespace fs

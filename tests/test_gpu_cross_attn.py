@@ -68,6 +68,11 @@ SIZES = [
     (1, 20, 70, 2, 1, 256, 256),
     (1, 400, 20, 2, 2, 128, 96),
     (1, 513, 384, 7, 7, 72, 72),
+    # enough heads that one CTA walks many tiles: one row block a CTA, and two
+    (1, 128, 650, 100, 100, 32, 32),
+    (2, 40, 900, 60, 60, 128, 128),
+    (2, 150, 1300, 80, 80, 128, 64),
+    (3, 260, 700, 64, 32, 96, 96),
 ]
 
 
