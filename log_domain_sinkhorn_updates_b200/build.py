@@ -21,8 +21,9 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 SOURCES = ["fs_api.cu", "fs_prep.cu", "fs_lse_tc.cu", "fs_lse_tc2.cu", "fs_lse_simt.cu", "fs_apply.cu", "fs_apply_tc.cu",
            "fs_apply_tc2.cu", "fs_apply_tc_q2.cu", "fs_hvp_tc.cu",
-           "fs_hvp.cu", "fs_cosine.cu", "fs_selftest.cu", "fs_noalloc.cu", "fs_ops_api.cu", "fs_xattn.cu", "fs_xattn_tc.cu", "fs_xent.cu", "fs_xent_tc.cu"]
-HEADERS = ["fs_internal.cuh", "fs_finish.cuh", "fs_prep.cuh", "fs_tc_common.cuh", "fs_ops.cuh"]
+           "fs_hvp.cu", "fs_cosine.cu", "fs_selftest.cu", "fs_noalloc.cu", "fs_ops_api.cu", "fs_xattn.cu", "fs_xattn_tc.cu", "fs_xattn_grad_tc.cu", "fs_xent.cu", "fs_xent_tc.cu"]
+HEADERS = ["fs_internal.cuh", "fs_finish.cuh", "fs_prep.cuh", "fs_tc_common.cuh", "fs_ops.cuh",
+           "fs_attn_tc.cuh"]
 
 FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",

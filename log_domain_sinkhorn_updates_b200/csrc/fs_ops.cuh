@@ -58,10 +58,17 @@ struct AttnTc {
     int slots;           // ring of K and V tiles
     int k_head, k_batch, v_head, v_batch;  // 0: that axis of the map has one element
 };
+struct AttnGradTc {
+    int d_pad, dv_pad;  // rounded up to 16
+    int slots;          // ring of streamed tiles
+    int s1_head, s1_batch, s2_head, s2_batch, k_head, k_batch, v_head, v_batch;  // as above, streamed and kept maps
+};
 bool attn_tc_view(const void *base, const fs_view &s, int tokens, int heads, int batch, bool map);
 bool attn_map(CUtensorMap *map, const void *base, const fs_view &s, int w, int tokens, int heads, int batch,
               int box_rows, int *hm, int *bm);
 cudaError_t launch_xattn_tc(const AttnParams &p, bool two_blocks, cudaStream_t s);
+
+cudaError_t launch_xattn_grad_tc(const AttnParams &p, cudaStream_t s);  // two launches
 
 cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s);

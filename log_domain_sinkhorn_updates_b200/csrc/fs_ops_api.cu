@@ -154,12 +154,22 @@ size_t attn_workspace(const fs_attn_desc &D, bool grad, const Device &dev) {
 
 // Whether the tensor-core kernels take the call: bf16, widths up to 128 and multiples of 8, keys to load, and
 // bases and strides that 16-byte loads and TMA boxes can start on.
-bool attn_tc(const fs_attn_desc &D, const void *q, const void *k, const void *v, const void *out) {
+bool attn_tc_operands(const fs_attn_desc &D, const void *q, const void *k, const void *v) {
     return D.dtype == FS_BF16 && D.d <= 128 && D.dv <= 128 && D.d % 8 == 0 && D.dv % 8 == 0 && D.m > 0 &&
            fs::attn_tc_view(q, D.q, D.n, D.heads, D.batch, false) &&
            fs::attn_tc_view(k, D.k, D.m, D.kv_heads, D.batch, true) &&
-           fs::attn_tc_view(v, D.v, D.m, D.kv_heads, D.batch, true) &&
-           fs::attn_tc_view(out, D.out, D.n, D.heads, D.batch, false);
+           fs::attn_tc_view(v, D.v, D.m, D.kv_heads, D.batch, true);
+}
+bool attn_tc(const fs_attn_desc &D, const void *q, const void *k, const void *v, const void *out) {
+    return attn_tc_operands(D, q, k, v) && fs::attn_tc_view(out, D.out, D.n, D.heads, D.batch, false);
+}
+bool attn_grad_tc(const fs_attn_desc &D, const void *q, const void *k, const void *v, const void *dout, const void *dq,
+                  const void *dk, const void *dv) {
+    return D.n > 0 && attn_tc_operands(D, q, k, v) && fs::attn_tc_view(q, D.q, D.n, D.heads, D.batch, true) &&
+           fs::attn_tc_view(dout, D.dout, D.n, D.heads, D.batch, true) &&
+           fs::attn_tc_view(dq, D.dq, D.n, D.heads, D.batch, false) &&
+           fs::attn_tc_view(dk, D.dk, D.m, D.kv_heads, D.batch, false) &&
+           fs::attn_tc_view(dv, D.dvw, D.m, D.kv_heads, D.batch, false);
 }
 
 fs::AttnParams attn_params(const fs_attn_desc &D, const AttnPlan &L, const Device &dev, void *ws) {
@@ -348,7 +358,10 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = D.dtype == FS_BF16;
     if (D.n > 0) OPS_LAUNCH(fs::launch_xattn_dot(p, bf16, s), 1);
-    OPS_LAUNCH(fs::launch_xattn_grad_simt(p, bf16, s), (D.m > 0) + (D.n > 0));
+    if (attn_grad_tc(D, q, k, v, dout, dq, dk, dv))
+        OPS_LAUNCH(fs::launch_xattn_grad_tc(p, s), 2);
+    else
+        OPS_LAUNCH(fs::launch_xattn_grad_simt(p, bf16, s), (D.m > 0) + (D.n > 0));
     return FS_OK;
 }
 

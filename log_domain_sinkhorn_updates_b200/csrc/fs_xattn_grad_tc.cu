@@ -1,0 +1,483 @@
+// Gradient of cross attention on the sm_100a tensor cores, in two passes that
+// each keep what they sum in TMEM (no atomics: the order of every sum is fixed):
+//
+//   KEYS  a CTA keeps 128 keys (K and V) and streams Q and dO in tiles of 64
+//         queries over the heads that share the key head:
+//           S^T = K Q^T, dP^T = V dO^T, P^T = 2^(S^T c + b_j - L_i), dS^T = P^T (dP^T - D_i)
+//           dV += P^T dO, dK += dS^T Q
+//   ROWS  a CTA keeps 128 packed rows (Q and dO) and streams K and V in tiles of 64 keys:
+//           S = Q K^T, dP = dO V^T, P, dS as above, dQ += dS K
+//
+// In both the kept side is the left factor, so S, dP and with them P and dS
+// come out with the kept rows in TMEM's lanes: they are written back as bf16
+// over the scores they came from and are the left factor of the next products
+// there.  The streamed tile is the right factor of both kinds of product, once
+// with its width and once with its rows as the K axis: the same shared-memory
+// tile under two descriptors.  Seven products instead of the five of one
+// combined pass, in exchange for sums that never leave the SM.
+//
+// TMEM (512 columns): S / P of tile t in [64 (t & 1), +64), dP / dS in [128 + 64 (t & 1), +64),
+// dV or dQ in [256, ...), dK in [384, ...).  Warps: 0 loads by TMA, 1 issues the MMAs and allocates
+// TMEM, 2 statistics, bias and masks, 4..7 and 8..11 turn scores into P and dS for even and odd tiles.
+#include <cuda.h>
+
+#include "fs_attn_tc.cuh"
+
+namespace fs {
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 64;  // streamed rows of a tile
+constexpr int kThreads = 384;
+constexpr int kColSlots = 4;
+
+struct Layout {
+    uint32_t st2, ring, half, cols, bars, total;
+};
+__host__ __device__ inline Layout layout(int atoms, int slots) {
+    Layout L;
+    L.st2 = (uint32_t)atoms * 16384u;
+    L.ring = 2 * L.st2;
+    L.half = (uint32_t)atoms * 8192u;
+    L.cols = L.ring + (uint32_t)slots * 2u * L.half;
+    L.bars = L.cols + kColSlots * 2 * kTile * 4;
+    L.total = L.bars + (3 * slots + 2 * kColSlots + 2 + 2 + 2 + 2 + 1) * 8 + 32;
+    return L;
+}
+
+// KS: steps of 16 along the widths (d and dv, the larger of the two), zeros beyond each.
+template <bool KEYS, int KS>
+__global__ void __launch_bounds__(kThreads, 1)
+    xattn_grad_tc_kernel(const __grid_constant__ CUtensorMap map_s1, const __grid_constant__ CUtensorMap map_s2,
+                         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                         const AttnParams p, const AttnGradTc g) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+    constexpr int kAtoms = (KS + 3) / 4;
+    const int NS = g.slots;
+    const Layout L = layout(kAtoms, NS);
+    uint8_t *st1 = smem, *st2 = smem + L.st2, *ring = smem + L.ring;
+    float *sCols = reinterpret_cast<float *>(smem + L.cols);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L.bars);  // [NS] streamed tiles loaded
+    uint64_t *ready = full + NS;                                   // [NS] masked rows cleared (ROWS)
+    uint64_t *empty = ready + NS;                                  // [NS]
+    uint64_t *cfull = empty + NS;                                  // [kColSlots]
+    uint64_t *cempty = cfull + kColSlots;                          // [kColSlots]
+    uint64_t *stfull = cempty + kColSlots;                         // kept side loaded
+    uint64_t *stready = stfull + 1;                                // kept side usable
+    uint64_t *sfull = stready + 1;                                 // [2]
+    uint64_t *pready = sfull + 2;                                  // [2]
+    uint64_t *pfree = pready + 2;                                  // [2]
+    uint64_t *done = pfree + 2;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    volatile int *tile_masked = reinterpret_cast<volatile int *>(tmem_holder + 2);  // [kColSlots]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads;
+    const int r0 = blockIdx.x * 128;  // first kept row (key, or packed query row)
+    const int keys = attn_keys(p, b), rows = p.n * p.group;
+    const int head_tiles = (p.n + kTile - 1) / kTile;
+    const int nt = KEYS ? (r0 < keys ? p.group * head_tiles : 0) : (keys + kTile - 1) / kTile;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(ready + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int s = 0; s < kColSlots; ++s) {
+            mbar_init(cfull + s, 1);
+            mbar_init(cempty + s, 4);
+        }
+        mbar_init(stfull, 1);
+        mbar_init(stready, KEYS ? 1 : 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sfull + i, 1);
+            mbar_init(pready + i, 4);
+            mbar_init(pfree + i, 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_holder)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+
+    if (warp == 0) {
+        // ---------------- loads ----------------
+        if (lane == 0) {
+            bool ok = true;
+            if (KEYS && nt > 0) {  // the kept 128 keys, as two boxes of 64
+                mbar_expect_tx(stfull, 2u * kAtoms * 16384u);
+                for (int a = 0; a < kAtoms; ++a)
+                    for (int u = 0; u < 2; ++u) {
+                        tma_load_4d(saddr(st1) + a * 16384u + u * 8192u, &map_k, saddr(stfull), a * 64, r0 + 64 * u,
+                                    c * g.k_head, b * g.k_batch);
+                        tma_load_4d(saddr(st2) + a * 16384u + u * 8192u, &map_v, saddr(stfull), a * 64, r0 + 64 * u,
+                                    c * g.v_head, b * g.v_batch);
+                    }
+            }
+            int t = 0;
+            for (; ok && t < nt; ++t) {
+                const int s = t % NS;
+                if (*abort_flag) break;
+                if (t >= NS && !mbar_wait(empty + s, ((uint32_t)(t / NS) & 1u) ^ 1u, p.timeout_ns)) {
+                    ok = false;
+                    break;
+                }
+                const int y = (KEYS ? t % head_tiles : t) * kTile;
+                const int h = KEYS ? c * p.group + t / head_tiles : c;
+                const uint32_t dst = saddr(ring + (size_t)s * 2 * L.half);
+                mbar_expect_tx(full + s, 2u * L.half);
+                for (int a = 0; a < kAtoms; ++a) {
+                    tma_load_4d(dst + a * 8192u, &map_s1, saddr(full + s), a * 64, y, h * g.s1_head, b * g.s1_batch);
+                    tma_load_4d(dst + L.half + a * 8192u, &map_s2, saddr(full + s), a * 64, y, h * g.s2_head,
+                                b * g.s2_batch);
+                }
+            }
+            if (!ok) {
+                atomicOr(p.err, kDevErrTimeout);
+                *abort_flag = 1;
+            }
+            if (KEYS && nt > 0) mbar_wait(stfull, 0, p.timeout_ns);
+            for (int k = max(0, t - NS); k < t; ++k) mbar_wait(full + (k % NS), (uint32_t)(k / NS) & 1u, p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ---------------- per-column terms of the streamed tiles, and masked keys ----------------
+        bool ok = true;
+        if (KEYS && nt > 0) {
+            unsigned dead[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                dead[u] = __ballot_sync(~0u, attn_bias2(p, b, r0 + 32 * u + lane, keys) == -INFINITY);
+            if (!mbar_wait(stfull, 0, p.timeout_ns)) ok = false;
+            if (dead[0] | dead[1] | dead[2] | dead[3]) {
+                clear_rows(st1, 128, kAtoms, dead, lane);
+                clear_rows(st2, 128, kAtoms, dead, lane);
+                fence_async();
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(stready);
+        }
+        for (int t = 0; ok && t < nt; ++t) {
+            const int j = t % kColSlots;
+            float *col = sCols + j * 2 * kTile;
+            float v0[2], v1[2] = {0.f, 0.f};
+            unsigned dead[2] = {0u, 0u};
+            bool any = !KEYS && p.bias != nullptr;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (KEYS) {  // -L (base 2) and -D; a row without a key, or past the end, gives P = 0
+                    const int i = (t % head_tiles) * kTile + 32 * u + lane;
+                    v0[u] = -INFINITY;
+                    if (i < p.n) {
+                        const size_t at = ((size_t)b * p.heads + c * p.group + t / head_tiles) * p.n + i;
+                        const float l = __ldg(p.lse + at);
+                        v0[u] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+                        v1[u] = -__ldg(p.dot + at);
+                    }
+                } else {
+                    v0[u] = attn_bias2(p, b, t * kTile + 32 * u + lane, keys);
+                    dead[u] = __ballot_sync(~0u, v0[u] == -INFINITY);
+                    any = any || dead[u];
+                }
+            }
+            if (t >= kColSlots && !mbar_wait(cempty + j, ((uint32_t)(t / kColSlots) & 1u) ^ 1u, p.timeout_ns)) ok = false;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                col[32 * u + lane] = v0[u];
+                col[kTile + 32 * u + lane] = v1[u];
+            }
+            if (lane == 0) tile_masked[j] = any;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cfull + j);
+            if (!KEYS) {
+                const int s = t % NS;
+                if (!mbar_wait(full + s, (uint32_t)(t / NS) & 1u, p.timeout_ns)) ok = false;
+                if (dead[0] | dead[1]) {
+                    uint8_t *tile = ring + (size_t)s * 2 * L.half;
+                    clear_rows(tile, kTile, kAtoms, dead, lane);
+                    clear_rows(tile + L.half, kTile, kAtoms, dead, lane);
+                    fence_async();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(ready + s);
+            }
+            if (*abort_flag) break;
+        }
+        if (!ok && lane == 0) {
+            atomicOr(p.err, kDevErrTimeout);
+            *abort_flag = 1;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0) {
+            const uint32_t idesc_s = make_idesc<0, 128, kTile>();
+            const uint32_t idesc_1 = idesc_mn(KEYS ? g.dv_pad : g.d_pad), idesc_2 = idesc_mn(g.d_pad);
+            const uint64_t a1 = make_sdesc(saddr(st1), 128u), a2 = make_sdesc(saddr(st2), 128u);
+            bool ok = nt == 0 || mbar_wait(stready, 0, p.timeout_ns);
+            tc_fence_after();
+            // S and dP of tile t into its buffers, once the products that read them last are complete
+            auto scores = [&](int t) {
+                const int s = t % NS, u = t & 1;
+                if (t >= 2 && !mbar_wait(pfree + u, ((uint32_t)(t >> 1) & 1u) ^ 1u, p.timeout_ns)) return false;
+                if (!mbar_wait(full + s, (uint32_t)(t / NS) & 1u, p.timeout_ns)) return false;
+                if (!KEYS && !mbar_wait(ready + s, (uint32_t)(t / NS) & 1u, p.timeout_ns)) return false;
+                tc_fence_after();
+                const uint32_t at = saddr(ring + (size_t)s * 2 * L.half);
+                const uint64_t b1 = make_sdesc(at, 128u), b2 = make_sdesc(at + L.half, 128u);
+                const uint32_t ts = tmem_base + 64u * u;
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    tc_mma<0>(ts, a1 + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
+                              b1 + (uint64_t)((k / 4) * 512 + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    tc_mma<0>(ts + 128u, a2 + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
+                              b2 + (uint64_t)((k / 4) * 512 + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
+                tc_commit(saddr(sfull + u));
+                return true;
+            };
+            // the sums over tile t's streamed rows, once its P and dS are written
+            auto sums = [&](int t, uint32_t first) {
+                const int s = t % NS, u = t & 1;
+                if (!mbar_wait(pready + u, (uint32_t)(t >> 1) & 1u, p.timeout_ns) || *abort_flag) return false;
+                tc_fence_after();
+                const uint32_t at = saddr(ring + (size_t)s * 2 * L.half);
+                const uint64_t m1 = sdesc_mn(at, 8192u), m2 = sdesc_mn(at + L.half, 8192u);
+                const uint32_t ts = tmem_base + 64u * u;
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k) {
+                    const uint32_t acc = k > 0 ? 1u : first;
+                    if (KEYS)
+                        tc_mma_ts(tmem_base + 256u, ts + 8u * k, m2 + (uint64_t)(k * 128), idesc_1, acc);
+                    else
+                        tc_mma_ts(tmem_base + 256u, ts + 128u + 8u * k, m1 + (uint64_t)(k * 128), idesc_1, acc);
+                }
+                if (KEYS) {
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        tc_mma_ts(tmem_base + 384u, ts + 128u + 8u * k, m1 + (uint64_t)(k * 128), idesc_2,
+                                  k > 0 ? 1u : first);
+                }
+                tc_commit(saddr(pfree + u));
+                tc_commit(saddr(empty + s));
+                return true;
+            };
+            for (int t = 0; ok && t < nt; t += 2) {
+                ok = scores(t);
+                if (ok && t + 1 < nt) ok = scores(t + 1);
+                if (ok) ok = sums(t, t > 0 ? 1u : 0u);
+                if (ok && t + 1 < nt) ok = sums(t + 1, 1u);
+            }
+            if (!ok) {
+                atomicOr(p.err, kDevErrTimeout);
+                *abort_flag = 1;
+            }
+            tc_commit(saddr(done));
+            mbar_wait(done, 0, p.timeout_ns);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---------------- P and dS ----------------
+        const int q = warp & 3, grp = (warp - 4) >> 2;
+        const int row = r0 + q * 32 + lane;
+        float nl = 0.f, nd = 0.f;  // KEYS: the key's bias; ROWS: -L (base 2) and -D of the row
+        if (KEYS) {
+            nl = attn_bias2(p, b, row, keys);
+        } else {
+            const int tid = (int)threadIdx.x - 128;
+            stage_packed(st1, p.q, p.qs, p, b, c, r0, 128, p.d, kAtoms, tid, 256);
+            stage_packed(st2, p.dout, p.dos, p, b, c, r0, 128, p.dv, kAtoms, tid, 256);
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(stready);
+            nl = -INFINITY;
+            if (row < rows) {
+                const size_t at = ((size_t)b * p.heads + c * p.group + row % p.group) * p.n + row / p.group;
+                const float l = p.lse[at];
+                nl = l == -INFINITY ? -INFINITY : -l * kLog2e;
+                nd = -p.dot[at];
+            }
+        }
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        const uint32_t ts = tmem_base + lanes + (uint32_t)(grp * 64), td = ts + 128u;
+        const uint64_t cc = pack2(p.scale2, p.scale2), nl2 = pack2(nl, nl), nd2 = pack2(nd, nd);
+        bool ok = true;
+        int n = 0;
+        for (int t = grp; t < nt; t += 2, ++n) {
+            const int j = t % kColSlots;
+            if (!mbar_wait(sfull + grp, (uint32_t)n & 1u, p.timeout_ns) ||
+                !mbar_wait(cfull + j, (uint32_t)(t / kColSlots) & 1u, p.timeout_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float4 *c0 = reinterpret_cast<const float4 *>(sCols + j * 2 * kTile);
+            const bool masked = KEYS || tile_masked[j];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t s[32], d[32], wp[16], ws[16];
+                tmem_ld32(ts + 32u * h, s);
+                tmem_ld32(td + 32u * h, d);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    uint64_t z0 = nl2, z1 = nl2, e0 = nd2, e1 = nd2;
+                    if (masked) {
+                        const float4 v = c0[8 * h + k / 4];
+                        z0 = add2(z0, pack2(v.x, v.y));
+                        z1 = add2(z1, pack2(v.z, v.w));
+                    }
+                    if (KEYS) {
+                        const float4 v = c0[kTile / 4 + 8 * h + k / 4];
+                        e0 = pack2(v.x, v.y);
+                        e1 = pack2(v.z, v.w);
+                    }
+                    float p0, p1, p2, p3, g0, g1, g2, g3;
+                    unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, z0), p0, p1);
+                    unpack2(fma2(pack2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), cc, z1), p2, p3);
+                    p0 = ex2_approx(p0);
+                    p1 = ex2_approx(p1);
+                    p2 = ex2_approx(p2);
+                    p3 = ex2_approx(p3);
+                    unpack2(add2(pack2(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), e0), g0, g1);
+                    unpack2(add2(pack2(__uint_as_float(d[k + 2]), __uint_as_float(d[k + 3])), e1), g2, g3);
+                    wp[k / 2] = bf16x2(p0, p1);
+                    wp[k / 2 + 1] = bf16x2(p2, p3);
+                    ws[k / 2] = bf16x2(p0 * g0, p1 * g1);
+                    ws[k / 2 + 1] = bf16x2(p2 * g2, p3 * g3);
+                }
+                if (KEYS) tmem_st16(ts + 16u * h, wp);
+                tmem_st16(td + 16u * h, ws);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(pready + grp);
+                mbar_arrive(cempty + j);
+            }
+            if (*abort_flag) break;
+        }
+        if (ok && nt > 0 && !mbar_wait(done, 0, p.timeout_ns)) ok = false;
+        if (!ok) {
+            atomicOr(p.err, kDevErrTimeout);
+            *abort_flag = 1;
+        }
+        tc_fence_after();
+        // KEYS: group 0 writes dv, group 1 dk.  ROWS: alternate 32-column pieces of dq.
+        const bool second = KEYS && grp == 1;
+        const int width = KEYS && grp == 0 ? p.dv : p.d;
+        const float mul = KEYS && grp == 0 ? 1.f : p.scale;
+        __nv_bfloat16 *dst;
+        bool live;
+        if (KEYS) {
+            live = row < p.m;
+            const fs_view &v = second ? p.dks : p.dvs;
+            dst = (__nv_bfloat16 *)(second ? p.dk : p.dv_out) + v.batch * b + v.token * row + v.head * c;
+        } else {
+            live = row < rows;
+            dst = (__nv_bfloat16 *)p.dq + p.dqs.batch * b + p.dqs.token * (row / p.group) +
+                  p.dqs.head * (c * p.group + row % p.group);
+        }
+        const uint32_t to = tmem_base + lanes + (second ? 384u : 256u);
+        for (int k = KEYS ? 0 : 32 * grp; k < width; k += KEYS ? 32 : 64) {
+            uint32_t o[32];
+            if (nt > 0) {
+                tmem_ld32(to + k, o);
+                tmem_ld_wait();
+            }
+#pragma unroll
+            for (int u = 0; u < 32; u += 8) {
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (nt > 0) {
+                    w.x = bf16x2(__uint_as_float(o[u]) * mul, __uint_as_float(o[u + 1]) * mul);
+                    w.y = bf16x2(__uint_as_float(o[u + 2]) * mul, __uint_as_float(o[u + 3]) * mul);
+                    w.z = bf16x2(__uint_as_float(o[u + 4]) * mul, __uint_as_float(o[u + 5]) * mul);
+                    w.w = bf16x2(__uint_as_float(o[u + 6]) * mul, __uint_as_float(o[u + 7]) * mul);
+                }
+                if (live && k + u < width) *reinterpret_cast<uint4 *>(dst + k + u) = w;  // widths: multiples of 8
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u) : "memory");
+    }
+}
+
+template <bool KEYS, int KS>
+cudaError_t launch(const AttnParams &p, AttnGradTc g, const CUtensorMap &s1, const CUtensorMap &s2,
+                   const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
+    constexpr int atoms = (KS + 3) / 4;
+    const uint32_t limit = 227u * 1024u;
+    g.slots = 8;
+    while (layout(atoms, g.slots).total + 1024u > limit) --g.slots;
+    const uint32_t need = layout(atoms, g.slots).total + 1024u;
+    // at least half the shared memory: a CTA holds all of TMEM, so two on one SM would wait for each other
+    const uint32_t smem = need > limit / 2 + 1024u ? need : limit / 2 + 1024u;
+    auto kern = xattn_grad_tc_kernel<KEYS, KS>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
+    if (e != cudaSuccess) return e;
+    const int blocks = ((KEYS ? p.m : p.n * p.group) + 127) / 128;
+    kern<<<dim3(blocks, p.batch * p.kv_heads), kThreads, smem, s>>>(s1, s2, mk, mv, p, g);
+    return cudaGetLastError();
+}
+
+template <int KS>
+cudaError_t both(const AttnParams &p, AttnGradTc g, const CUtensorMap &mq, const CUtensorMap &mg,
+                 const CUtensorMap &mk, const CUtensorMap &mv, const int *hb, cudaStream_t s) {
+    g.k_head = hb[4];
+    g.k_batch = hb[5];
+    g.v_head = hb[6];
+    g.v_batch = hb[7];
+    g.s1_head = hb[0];
+    g.s1_batch = hb[1];
+    g.s2_head = hb[2];
+    g.s2_batch = hb[3];
+    cudaError_t e = launch<true, KS>(p, g, mq, mg, mk, mv, s);
+    if (e != cudaSuccess) return e;
+    g.s1_head = hb[4];
+    g.s1_batch = hb[5];
+    g.s2_head = hb[6];
+    g.s2_batch = hb[7];
+    return launch<false, KS>(p, g, mk, mv, mk, mv, s);
+}
+
+}  // namespace
+
+cudaError_t launch_xattn_grad_tc(const AttnParams &p, cudaStream_t s) {
+    AttnGradTc g{};
+    g.d_pad = (p.d + 15) / 16 * 16;
+    g.dv_pad = (p.dv + 15) / 16 * 16;
+    CUtensorMap mq, mg, mk, mv;
+    int hb[8];
+    if (!attn_map(&mq, p.q, p.qs, p.d, p.n, p.heads, p.batch, kTile, hb, hb + 1) ||
+        !attn_map(&mg, p.dout, p.dos, p.dv, p.n, p.heads, p.batch, kTile, hb + 2, hb + 3) ||
+        !attn_map(&mk, p.k, p.ks, p.d, p.m, p.kv_heads, p.batch, kTile, hb + 4, hb + 5) ||
+        !attn_map(&mv, p.v, p.vs, p.dv, p.m, p.kv_heads, p.batch, kTile, hb + 6, hb + 7))
+        return cudaErrorInvalidValue;
+    const int w = p.d > p.dv ? p.d : p.dv;
+    if (w <= 32) return both<2>(p, g, mq, mg, mk, mv, hb, s);
+    if (w <= 64) return both<4>(p, g, mq, mg, mk, mv, hb, s);
+    if (w <= 96) return both<6>(p, g, mq, mg, mk, mv, hb, s);
+    return both<8>(p, g, mq, mg, mk, mv, hb, s);
+}
+
+}  // namespace fs

@@ -29,8 +29,7 @@
 // groups 0 and 1; 3 bias and masks; 4..7 and 8..11 are the softmax groups.
 #include <cuda.h>
 
-#include "fs_ops.cuh"
-#include "fs_tc_common.cuh"
+#include "fs_attn_tc.cuh"
 
 namespace fs {
 namespace {
@@ -41,33 +40,6 @@ constexpr int kTS = 128;        // keys of a tile
 constexpr int kThreads = 384;
 constexpr int kBiasSlots = 4;
 constexpr float kLazy = 8.f;
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// The P V product's right factor: rows = keys (K axis), 64-element columns of
-// the width `lbo` bytes apart, 128-byte swizzle.
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, uint32_t lbo) {
-    uint64_t desc = (uint64_t)((addr >> 4) & 0x3FFFu);
-    desc |= (uint64_t)(lbo >> 4) << 16;
-    desc |= (uint64_t)(1024u >> 4) << 32;
-    desc |= (uint64_t)1u << 46;
-    desc |= 2ull << 61;
-    return desc;
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *map, uint32_t bar, int x, int y, int z, int w) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void group_bar(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 
 struct Layout {
     uint32_t q, ring, slot, bias, ml, bars, total;
@@ -206,15 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!mbar_wait(full + s, (uint32_t)(i / NS) & 1u, p.timeout_ns)) ok = false;
                 if (clear) {
                     uint8_t *tile = ring + (size_t)s * L.slot;
-                    const int atoms = kv ? g.vatoms : g.datoms;
-                    for (int e = lane; e < kTS * 8; e += 32) {  // 16-byte pieces of the 128-byte rows of an atom
-                        const int row = e >> 3;
-                        const unsigned word = row < 64 ? (row < 32 ? dead[0] : dead[1]) : (row < 96 ? dead[2] : dead[3]);
-                        if (word >> (row & 31) & 1u)
-                            for (int a = 0; a < atoms; ++a)
-                                *reinterpret_cast<uint4 *>(tile + a * 16384 + row * 128 + (e & 7) * 16) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                    }
+                    clear_rows(tile, kTS, kv ? g.vatoms : g.datoms, dead, lane);
                     fence_async();
                     __syncwarp();
                 }
@@ -233,8 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int grp = warp - 1;
             const int t0 = QT == 2 ? 0 : grp, step = QT == 2 ? 1 : 2;
             const uint32_t idesc_s = make_idesc<0, 128, kTS>();
-            const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
-                                     ((uint32_t)(g.dv_pad >> 3) << 17) | ((128u >> 4) << 24);
+            const uint32_t idesc_o = idesc_mn(g.dv_pad);
             const uint32_t ts = tmem_base + (uint32_t)(grp * 128), to = tmem_base + 256u + (uint32_t)(grp * 128);
             const uint64_t qd = make_sdesc(saddr(sQ) + (QT == 2 ? grp : 0) * g.datoms * 16384u, 128u);
             auto slot_ready = [&](int i) {
@@ -294,22 +257,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = (rb * QT + blk) * 128 + rl;  // packed row
         const bool warp_live = (rb * QT + blk) * 128 + q * 32 < rows;
         // Q into shared memory, 16 bytes at a time, as the 128-byte swizzle lays it
-        {
-            const int per = g.datoms * 8;
-            for (int e = (int)threadIdx.x - 128; e < QT * 128 * per; e += 256) {
-                const int row = e / per, ch = e % per, at = rb * QT * 128 + row;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (at < rows && ch * 8 < p.d)
-                    v = *reinterpret_cast<const uint4 *>(
-                        (const __nv_bfloat16 *)p.q + p.qs.batch * b + p.qs.token * (at / p.group) +
-                        p.qs.head * (c * p.group + at % p.group) + ch * 8);
-                *reinterpret_cast<uint4 *>(sQ + (row >> 7) * g.datoms * 16384 + (ch >> 3) * 16384 + (row & 127) * 128 +
-                                           (((ch & 7) ^ (row & 7)) << 4)) = v;
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(qfull);
-        }
+        stage_packed(sQ, p.q, p.qs, p, b, c, rb * QT * 128, QT * 128, p.d, g.datoms, (int)threadIdx.x - 128, 256);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qfull);
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         const uint32_t ts = tmem_base + lanes + (uint32_t)(grp * 128);
         const uint32_t to = tmem_base + lanes + 256u + (uint32_t)(grp * 128);

@@ -7,6 +7,11 @@ The bounds follow the library's arithmetic on the same inputs, term by term:
 - exponentials by 2^-21 relative, a stored fp32 statistic by 2^-23 of its size;
 - bf16 inputs: P, dS and dz are rounded to bf16 for their products (half a
   step, 2^-8 relative), and so are the outputs.
+- underflow: a weight, or a weight times its gradient factor, below the least
+  normal number 2^-126 (fp32 and bf16 alike) may become zero or lose bits, an
+  absolute error of at most 2^-126 for the weight (so 2^-126 of the factor it
+  multiplies) and 2^-126 for the product.  Relative bounds alone would ask for
+  weights like 1e-206 that no such number holds.
 First-order errors are added up in absolute value; a factor 1.05 covers the
 products of errors.
 """
@@ -19,6 +24,7 @@ EXP = 2.0 ** -21
 BF = torch.finfo(torch.bfloat16).eps / 2
 SLACK = 1.05
 MASK = -1e30
+TINY = 2.0 ** -126
 
 
 def _half(dtype):
@@ -67,7 +73,7 @@ def attention(q, k, v, k_len=None, bias=None, scale=None, dout=None, out=None):
     O = torch.einsum("bhij,bhjd->bhid", P, V)
     sumerr = (m + 64) * U
     w = torch.einsum("bhij->bhi", P * eP)
-    eO = torch.einsum("bhij,bhjd->bhid", P * eP, V.abs()) + (w + 2 * sumerr + 4 * U)[..., None] * aPV + rnd * aPV \
+    eO = torch.einsum("bhij,bhjd->bhid", P * eP + TINY, V.abs()) + (w + 2 * sumerr + 4 * U)[..., None] * aPV + rnd * aPV \
         + rout * O.abs()
     elog = w + sumerr + 3 * U * torch.where(empty, torch.zeros_like(lse), lse).abs() + 4 * U
     res = {"out": (O.permute(0, 2, 1, 3), SLACK * eO.permute(0, 2, 1, 3)), "lse": (lse, SLACK * elog)}
@@ -85,7 +91,7 @@ def attention(q, k, v, k_len=None, bias=None, scale=None, dout=None, out=None):
     dS = P * (dP - D[..., None])
     edS = P * ((dP - D[..., None]).abs() * eP + (dv + 4) * U * adP + eD[..., None]
                + 2 * U * (dP.abs() + D.abs()[..., None]))
-    edS = edS + rnd * (dS.abs() + edS)
+    edS = edS + rnd * (dS.abs() + edS) + TINY * (1 + (dP - D[..., None]).abs())
 
     def fold(t):  # heads that share a key head
         return t.reshape(B, Hk, H // Hk, m, t.shape[-1]).sum(dim=2).permute(0, 2, 1, 3)
@@ -98,7 +104,7 @@ def attention(q, k, v, k_len=None, bias=None, scale=None, dout=None, out=None):
     edK = fold(scale * (torch.einsum("bhij,bhid->bhjd", edS, Q.abs())
                         + rows * torch.einsum("bhij,bhid->bhjd", dS.abs(), Q.abs()))) + rout * dK.abs()
     dV = fold(torch.einsum("bhij,bhid->bhjd", P, G))
-    edV = fold(torch.einsum("bhij,bhid->bhjd", P * eP, G.abs())
+    edV = fold(torch.einsum("bhij,bhid->bhjd", P * eP + TINY, G.abs())
                + (rnd * (1 + BF) + rows) * torch.einsum("bhij,bhid->bhjd", P, G.abs())) + rout * dV.abs()
     res["dq"] = (dQ.permute(0, 2, 1, 3), SLACK * edQ.permute(0, 2, 1, 3))
     res["dk"], res["dv"] = (dK, SLACK * edK), (dV, SLACK * edV)
@@ -133,7 +139,7 @@ def cross_entropy(x, w, target, scale=1.0, ignore=-100, dloss=None, dlse=None):
     dz = p * gs[:, None] - hot
     edz = p * gs.abs()[:, None] * (ez + elog[:, None] + 3 * U * (lse.abs()[:, None] + z.abs()) + EXP) \
         + 3 * U * (p * gs.abs()[:, None] + hot.abs())
-    edz = edz + rnd * (dz.abs() + edz)
+    edz = edz + rnd * (dz.abs() + edz) + TINY * (1 + gs.abs()[:, None])
     dx = scale * dz @ W
     edx = scale * (edz @ W.abs() + (V + 64) * U * (dz.abs() @ W.abs())) + rout * dx.abs()
     dw = scale * dz.t() @ X
