@@ -21,5 +21,6 @@ def __getattr__(name):
     if name in __all__:
         mod = importlib.import_module(".binding", __name__)
         mod.lib()  # fail loudly here if the CUDA extension is missing
-        return getattr(mod, name)
+        value = globals()[name] = getattr(mod, name)  # later accesses find it without this call
+        return value
     raise AttributeError(name)

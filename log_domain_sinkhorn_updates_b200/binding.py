@@ -360,12 +360,22 @@ def fs_selftest_wait(h: Handle, timeout_ms=50) -> int:
 
 
 # ---- row-softmax operators without a handle ----
+# A call's descriptor and workspace size follow from the tensors' shapes, strides, types and
+# device alone, so they are checked and built once for each such combination and kept (at most
+# _PLAN_LIMIT of them; no data, address or tensor is kept).
+_plans = {}
+_PLAN_LIMIT = 4096
 _OP_DTYPES = {"torch.float32": FS_F32, "torch.bfloat16": FS_BF16}
 
 
 def _same(what, cond):
     if not cond:
         raise ValueError(what)
+
+
+def _geometry(*tensors):
+    """What a plan depends on, as a dictionary key."""
+    return tuple([x for t in tensors for x in (t.shape, t.stride(), t.dtype, t.get_device())])
 
 
 def _op_dtype(first, *others):
@@ -384,12 +394,11 @@ def _op_dtype(first, *others):
 
 
 def _side(t, dtype, shape, device, what):
-    """A contiguous side array (lengths, bias, statistics, targets), or None."""
-    import torch
+    """Address of a contiguous side array (lengths, bias, statistics, targets), or None."""
     if t is None:
         return None
-    if t.dtype != getattr(torch, dtype) or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on the tensors' device")
     return t.data_ptr()
 
 
@@ -402,30 +411,49 @@ def _view(t, what):
     return FsView(s[0], s[1], s[2])
 
 
-def _op_call(device, stream, query, grad, desc, workspace, call):
-    """Run `call(workspace pointer, bytes, stream)` on the tensors' device: a given stream or
-    that device's current one, and a given workspace or one from torch's allocator (in that
+def _plan(key, build, query, grad):
+    """(descriptor, reference to it, workspace bytes) of `key`, built on its first use."""
+    plan = _plans.get(key)
+    if plan is None:
+        import torch
+        desc, device = build()
+        with torch.cuda.device(device):
+            plan = (desc, ctypes.byref(desc), int(query(ctypes.byref(desc), grad)))
+        if len(_plans) >= _PLAN_LIMIT:
+            _plans.clear()
+        _plans[key] = plan
+    return plan
+
+
+def _op_call(device, need, stream, workspace, call):
+    """Run `call(workspace address, bytes, stream)` on device number `device`: on the given stream
+    or that device's current one, with the given workspace or one from torch's allocator (in that
     stream's order; under graph capture, of the capture's own pool)."""
-    import contextlib
     import torch
-    here = torch.cuda.current_device() == device.index
-    with contextlib.nullcontext() if here else torch.cuda.device(device):
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        if s.device != device:
-            raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
-        need = query(ctypes.byref(desc), grad)
-        if workspace is None and need:
-            if stream is None:
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _op_call(device, need, stream, workspace, call)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        if stream.device.index != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
+        raw = stream.cuda_stream
+    size, address = 0, None
+    if workspace is not None:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the tensors' device")
+        size, address = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    elif need:
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            with torch.cuda.stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=device)
-            else:
-                with torch.cuda.stream(s):
-                    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        size = 0
-        if workspace is not None:
-            if workspace.device != device or not workspace.is_contiguous():
-                raise ValueError(f"workspace must be a contiguous tensor on {device}")
-            size = workspace.numel() * workspace.element_size()
-        _check(call(workspace.data_ptr() if size else None, size, s.cuda_stream))
+        size, address = need, workspace.data_ptr()
+    status = call(address, size, raw)
+    if status != FS_OK:
+        _check(status)
 
 
 def _attn_desc(q, k, v, out, scale):
@@ -439,6 +467,23 @@ def _attn_desc(q, k, v, out, scale):
     return FsAttnDesc(B, n, m, H, Hk, d, dv, dt, float(d ** -0.5 if scale is None else scale), *views)
 
 
+def _attn_grad_desc(q, k, v, out, dout, dq, dk, dv, scale):
+    desc = _attn_desc(q, k, v, out, scale)
+    _op_dtype(q, dout, dq, dk, dv)
+    for t, like, what in ((dout, out, "dout"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        _same(f"{what} has the wrong shape", t.shape == like.shape)
+    desc.dout, desc.dq, desc.dk, desc.dvw = (_view(t, w) for t, w in ((dout, "dout"), (dq, "dq"), (dk, "dk"),
+                                                                     (dv, "dv")))
+    return desc
+
+
+def _attn_sides(desc, device, k_len, bias, lse):
+    import torch
+    return (_side(k_len, torch.int32, (desc.batch,), device, "k_len"),
+            _side(bias, torch.float32, (desc.batch, desc.m), device, "bias"),
+            _side(lse, torch.float32, (desc.batch, desc.heads, desc.n), device, "lse"))
+
+
 def fs_cross_attn(q, k, v, out, lse=None, k_len=None, bias=None, scale=None, stream=None, workspace=None):
     """Cross attention: out[b, i, h] = sum_j softmax_j(scale q_i.k_j + bias_j) v_j.
 
@@ -450,41 +495,30 @@ def fs_cross_attn(q, k, v, out, lse=None, k_len=None, bias=None, scale=None, str
     anything; a row without a key gives 0 and lse -inf.  scale: 1/sqrt(d) if None.  stream: the
     device's current one if None (tensors used on another stream must be kept alive by the
     caller).  workspace: uint8 tensor of fs_cross_attn_workspace bytes; allocated if None."""
-    desc = _attn_desc(q, k, v, out, scale)
-    dev = q.device
-    kl = _side(k_len, "int32", (desc.batch,), dev, "k_len")
-    bp = _side(bias, "float32", (desc.batch, desc.m), dev, "bias")
-    lp = _side(lse, "float32", (desc.batch, desc.heads, desc.n), dev, "lse")
     L = lib()
-    _op_call(dev, stream, L.fs_cross_attn_workspace, 0, desc, workspace,
-             lambda ws, size, s: L.fs_cross_attn(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), kl, bp,
-                                                 out.data_ptr(), lp, ws, size, s))
-
-
-def _attn_grad_desc(q, k, v, out, dout, dq, dk, dv, scale):
-    desc = _attn_desc(q, k, v, out, scale)
-    _op_dtype(q, dout, dq, dk, dv)
-    for t, like, what in ((dout, out, "dout"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
-        _same(f"{what} has the wrong shape", t.shape == like.shape)
-    desc.dout, desc.dq, desc.dk, desc.dvw = (_view(t, w) for t, w in ((dout, "dout"), (dq, "dq"), (dk, "dk"),
-                                                                     (dv, "dv")))
-    return desc
+    desc, ref, need = _plan(("attn", scale, *_geometry(q, k, v, out)),
+                            lambda: (_attn_desc(q, k, v, out, scale), q.device), L.fs_cross_attn_workspace, 0)
+    dev = q.get_device()
+    kl, bp, lp = _attn_sides(desc, dev, k_len, bias, lse)
+    _op_call(dev, need, stream, workspace,
+             lambda ws, size, s: L.fs_cross_attn(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), kl, bp, out.data_ptr(),
+                                                 lp, ws, size, s))
 
 
 def fs_cross_attn_grad(q, k, v, out, lse, dout, dq, dk, dv, k_len=None, bias=None, scale=None, stream=None,
                        workspace=None):
     """Gradients dq, dk, dv of fs_cross_attn from its out and lse and the gradient dout of out
     (shapes of q, k, v and out; the other arguments as in the forward)."""
-    desc = _attn_grad_desc(q, k, v, out, dout, dq, dk, dv, scale)
-    dev = q.device
-    kl = _side(k_len, "int32", (desc.batch,), dev, "k_len")
-    bp = _side(bias, "float32", (desc.batch, desc.m), dev, "bias")
-    lp = _side(lse, "float32", (desc.batch, desc.heads, desc.n), dev, "lse")
-    _same("lse is needed", lse is not None)
     L = lib()
-    _op_call(dev, stream, L.fs_cross_attn_workspace, 1, desc, workspace,
-             lambda ws, size, s: L.fs_cross_attn_grad(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), kl,
-                                                      bp, out.data_ptr(), lp, dout.data_ptr(), dq.data_ptr(),
+    desc, ref, need = _plan(("attn_grad", scale, *_geometry(q, k, v, out, dout, dq, dk, dv)),
+                            lambda: (_attn_grad_desc(q, k, v, out, dout, dq, dk, dv, scale), q.device),
+                            L.fs_cross_attn_workspace, 1)
+    dev = q.get_device()
+    _same("lse is needed", lse is not None)
+    kl, bp, lp = _attn_sides(desc, dev, k_len, bias, lse)
+    _op_call(dev, need, stream, workspace,
+             lambda ws, size, s: L.fs_cross_attn_grad(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), kl, bp,
+                                                      out.data_ptr(), lp, dout.data_ptr(), dq.data_ptr(),
                                                       dk.data_ptr(), dv.data_ptr(), ws, size, s))
 
 
@@ -512,21 +546,6 @@ def _xent_desc(x, w, scale, ignore_index):
     return FsXentDesc(x.shape[0], w.shape[0], x.shape[1], dt, float(scale), ldx, ldw, 0, 0, int(ignore_index))
 
 
-def fs_cross_entropy(x, w, target, loss, lse, scale=1.0, ignore_index=-100, stream=None, workspace=None):
-    """Softmax cross entropy of logits scale x w^T without storing them: x [n, d], w [v, d] (CUDA
-    float32 or bfloat16, rows contiguous, any row stride), target int64 [n]; writes loss and lse,
-    float32 [n].  loss_i = lse_i - z_{i, target_i}, 0 where the target is ignore_index, NaN where it
-    is anything else outside the classes.  stream, workspace: as in fs_cross_attn."""
-    desc = _xent_desc(x, w, scale, ignore_index)
-    dev = x.device
-    tp = _side(target, "int64", (desc.n,), dev, "target")
-    lo, le = (_side(t, "float32", (desc.n,), dev, what) for t, what in ((loss, "loss"), (lse, "lse")))
-    L = lib()
-    _op_call(dev, stream, L.fs_cross_entropy_workspace, 0, desc, workspace,
-             lambda ws, size, s: L.fs_cross_entropy(ctypes.byref(desc), x.data_ptr(), w.data_ptr(), tp, lo, le, ws,
-                                                    size, s))
-
-
 def _xent_grad_desc(x, w, dx, dw, scale, ignore_index):
     desc = _xent_desc(x, w, scale, ignore_index)
     _op_dtype(x, dx, dw)
@@ -535,19 +554,38 @@ def _xent_grad_desc(x, w, dx, dw, scale, ignore_index):
     return desc
 
 
+def fs_cross_entropy(x, w, target, loss, lse, scale=1.0, ignore_index=-100, stream=None, workspace=None):
+    """Softmax cross entropy of logits scale x w^T without storing them: x [n, d], w [v, d] (CUDA
+    float32 or bfloat16, rows contiguous, any row stride), target int64 [n]; writes loss and lse,
+    float32 [n].  loss_i = lse_i - z_{i, target_i}, 0 where the target is ignore_index, NaN where it
+    is anything else outside the classes.  stream, workspace: as in fs_cross_attn."""
+    import torch
+    L = lib()
+    desc, ref, need = _plan(("xent", scale, ignore_index, *_geometry(x, w)),
+                            lambda: (_xent_desc(x, w, scale, ignore_index), x.device), L.fs_cross_entropy_workspace, 0)
+    dev, shape = x.get_device(), (desc.n,)
+    tp = _side(target, torch.int64, shape, dev, "target")
+    lo, le = _side(loss, torch.float32, shape, dev, "loss"), _side(lse, torch.float32, shape, dev, "lse")
+    _op_call(dev, need, stream, workspace,
+             lambda ws, size, s: L.fs_cross_entropy(ref, x.data_ptr(), w.data_ptr(), tp, lo, le, ws, size, s))
+
+
 def fs_cross_entropy_grad(x, w, target, lse, dloss, dx, dw, dlse=None, scale=1.0, ignore_index=-100, stream=None,
                           workspace=None):
     """Gradients dx and dw (shapes of x and w) from the forward's lse and the gradients dloss and
     dlse (float32 [n]; dlse None for 0) of its outputs.  Other arguments as in the forward."""
-    desc = _xent_grad_desc(x, w, dx, dw, scale, ignore_index)
-    dev = x.device
-    tp = _side(target, "int64", (desc.n,), dev, "target")
-    le, dl, dz = (_side(t, "float32", (desc.n,), dev, what)
-                  for t, what in ((lse, "lse"), (dloss, "dloss"), (dlse, "dlse")))
+    import torch
     L = lib()
-    _op_call(dev, stream, L.fs_cross_entropy_workspace, 1, desc, workspace,
-             lambda ws, size, s: L.fs_cross_entropy_grad(ctypes.byref(desc), x.data_ptr(), w.data_ptr(), tp, le, dl, dz,
-                                                         dx.data_ptr(), dw.data_ptr(), ws, size, s))
+    desc, ref, need = _plan(("xent_grad", scale, ignore_index, *_geometry(x, w, dx, dw)),
+                            lambda: (_xent_grad_desc(x, w, dx, dw, scale, ignore_index), x.device),
+                            L.fs_cross_entropy_workspace, 1)
+    dev, shape = x.get_device(), (desc.n,)
+    tp = _side(target, torch.int64, shape, dev, "target")
+    le, dl, dz = (_side(t, torch.float32, shape, dev, what)
+                  for t, what in ((lse, "lse"), (dloss, "dloss"), (dlse, "dlse")))
+    _op_call(dev, need, stream, workspace,
+             lambda ws, size, s: L.fs_cross_entropy_grad(ref, x.data_ptr(), w.data_ptr(), tp, le, dl, dz, dx.data_ptr(),
+                                                         dw.data_ptr(), ws, size, s))
 
 
 def fs_cross_entropy_workspace(x, w, dx=None, dw=None) -> int:

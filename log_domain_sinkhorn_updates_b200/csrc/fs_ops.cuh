@@ -34,6 +34,24 @@ struct AttnParams {
     int *err;
 };
 
+// A kernel launched by launch_dependent may start before the stream's last one has ended (its launch then costs no
+// gap); nothing that one wrote may be read before this wait.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class... A, class... B>
+cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s, B... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Valid keys of problem b.
 __device__ __forceinline__ int attn_keys(const AttnParams &p, int b) {
     return p.k_len ? min(max(__ldg(p.k_len + b), 0), p.m) : p.m;

@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParam
     if (at >= all) return;
     const int lane = threadIdx.x % 32;
     const int r = (int)(at % rows), c = (int)(at / rows % p.kv_heads), b = (int)(at / rows / p.kv_heads);
+    grid_dependency_wait();
     float mx = -INFINITY;
     for (int s = lane; s < p.splits; s += 32) mx = fmaxf(mx, p.part_ml[s * all + at].x);
     for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, w));
@@ -149,20 +150,53 @@ __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParam
     float l = 0.f, o[kMaxD / 32];
 #pragma unroll
     for (int k = 0; k < kMaxD / 32; ++k) o[k] = 0.f;
-    for (int s = 0; s < p.splits; ++s) {
-        const float2 ml = p.part_ml[s * all + at];
-        if (ml.y == 0.f) continue;  // a part without a key: its sums were not written
-        const float f = exp2f(ml.x - ref);
-        l = fmaf(ml.y, f, l);
+    for (int s0 = 0; s0 < p.splits; s0 += 32) {
+        // a lane's part: its weight; 0 where it has no key (its sums were not written)
+        const float2 ml = s0 + lane < p.splits ? p.part_ml[(s0 + lane) * all + at] : make_float2(-INFINITY, 0.f);
+        const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - ref);
+        const unsigned has = __ballot_sync(~0u, ml.y != 0.f);
+        float lw = ml.y * f;
+        for (int w = 16; w; w >>= 1) lw += __shfl_xor_sync(~0u, lw, w);
+        l += lw;
+        const int cnt = min(32, p.splits - s0);
+        if (p.dv % 4 == 0 && p.dv <= 128) {
+            // four consecutive values a lane, kept in o[0..3]
+            for (int j = 0; j < cnt; j += 4) {
+                float4 v[4];
+                float fj[4];
 #pragma unroll
-        for (int k = 0; k < kMaxD / 32; ++k)
-            if (lane + 32 * k < p.dv) o[k] = fmaf(p.part_o[(s * all + at) * p.dv + lane + 32 * k], f, o[k]);
+                for (int u = 0; u < 4; ++u) {
+                    fj[u] = __shfl_sync(~0u, f, (j + u) & 31);
+                    v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (j + u < cnt && (has >> (j + u) & 1u) && 4 * lane < p.dv)
+                        v[u] = *reinterpret_cast<const float4 *>(p.part_o + ((s0 + j + u) * all + at) * p.dv + 4 * lane);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    o[0] = fmaf(v[u].x, fj[u], o[0]);
+                    o[1] = fmaf(v[u].y, fj[u], o[1]);
+                    o[2] = fmaf(v[u].z, fj[u], o[2]);
+                    o[3] = fmaf(v[u].w, fj[u], o[3]);
+                }
+            }
+        } else {
+            for (int j = 0; j < cnt; ++j) {
+                const float fj = __shfl_sync(~0u, f, j);
+                if (!(has >> j & 1u)) continue;
+#pragma unroll
+                for (int k = 0; k < kMaxD / 32; ++k)
+                    if (lane + 32 * k < p.dv) o[k] = fmaf(p.part_o[((s0 + j) * all + at) * p.dv + lane + 32 * k], fj, o[k]);
+            }
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;  // 0: no key is left (a NaN row stays NaN)
     T *dst = (T *)p.out + row_off(p.os, p, b, c, r);
+    const bool four = p.dv % 4 == 0 && p.dv <= 128;
 #pragma unroll
-    for (int k = 0; k < kMaxD / 32; ++k)
-        if (lane + 32 * k < p.dv) from_f(o[k] * inv, dst + lane + 32 * k);
+    for (int k = 0; k < kMaxD / 32; ++k) {
+        const int e = four ? (k < 4 ? 4 * lane + k : p.dv) : lane + 32 * k;
+        if (e < p.dv) from_f(o[k] * inv, dst + e);
+    }
     if (p.lse && lane == 0)
         p.lse[row_stat(p, b, c, r)] = l == 0.f ? -INFINITY : (float)(((double)mx + log2((double)l)) * kLn2d);
 }
@@ -326,11 +360,8 @@ cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s) {
 cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s) {
     const size_t rows = (size_t)p.n * p.group * p.batch * p.kv_heads;
     const unsigned grid = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
-    if (bf16)
-        xattn_combine_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-    else
-        xattn_combine_kernel<float><<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return bf16 ? launch_dependent(xattn_combine_kernel<__nv_bfloat16>, grid, kThreads, 0, s, p)
+                : launch_dependent(xattn_combine_kernel<float>, grid, kThreads, 0, s, p);
 }
 cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s) {
     const size_t rows = (size_t)p.batch * p.n * p.heads;
