@@ -69,6 +69,9 @@ __device__ __forceinline__ float attn_bias2(const AttnParams &p, int b, int j, i
 bool encode_bf16_map(CUtensorMap *map, const void *base, int dims, const long long *size, const long long *stride,
                      const int *box);
 
+// Packed rows up to which the CUDA-core forward takes 16 rows a CTA instead of 64.
+constexpr int kXattnFewRows = 16;
+
 // Geometry of the tensor-core attention kernels.
 struct AttnTc {
     int datoms, vatoms;  // 64-element columns of d and dv

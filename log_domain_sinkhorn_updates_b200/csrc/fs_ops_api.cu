@@ -127,7 +127,7 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, const Device &dev)
     if (rows == 0 || heads == 0) return L;
     // Parts of the keys: as many as cost least, in waves of CTAs (one an SM on the tensor cores, two otherwise) times
     // the tiles of a part plus its start and end; more than one part costs the joining pass too.
-    const int tile = tc ? 128 : 64, side = tc ? 128 : 16, slots = tc ? dev.sms : 2 * dev.sms;
+    const int tile = tc ? 128 : 64, side = tc ? 128 : (rows <= fs::kXattnFewRows ? 16 : 64), slots = tc ? dev.sms : 2 * dev.sms;
     const size_t ctas = (rows + side - 1) / side * heads;
     const int tiles = up(std::max(D.m, 1), tile);
     double best = 1e300;

@@ -16,9 +16,10 @@
 namespace fs {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kRows = 16, kKeys = 64;  // forward tile
-constexpr int kGT = 32;                // gradient tile (rows and keys)
+constexpr int kThreads = 128;  // of the joining pass and the row products
+constexpr int kTileThreads = 256;
+constexpr int kKeys = 64;      // keys of a forward tile
+constexpr int kKept = 64, kStream = 32;  // gradient tile
 constexpr int kMaxD = 256;
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -34,104 +35,207 @@ __device__ __forceinline__ size_t row_stat(const AttnParams &p, int b, int c, in
     return ((size_t)b * p.heads + c * p.group + r % p.group) * p.n + r / p.group;
 }
 
-// rows [r0, r0 + cnt) of a query-side tensor into sm[cnt][w + 1] (zeros beyond the last row)
-template <class T>
-__device__ void stage_rows(float *sm, const T *src, const fs_view &s, const AttnParams &p, int b, int c, int r0, int cnt,
-                           int w) {
-    const int rows = p.n * p.group;
-    for (int e = threadIdx.x; e < cnt * w; e += blockDim.x) {
-        const int r = e / w, k = e % w;
-        sm[r * (w + 1) + k] = r0 + r < rows ? to_f(src[row_off(s, p, b, c, r0 + r) + k]) : 0.f;
+// Row stride in shared memory of a tile of width w: an odd number of 16-byte pieces, so that eight rows' pieces at
+// one column lie in different banks.
+__host__ __device__ inline int smem_stride(int w) { return ((w + 3) / 4 | 1) * 4; }
+
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+}
+// `cnt` rows of width w into sm (stride smem_stride(w), zeros up to a multiple of 4); row(r) is a row's address, or
+// null for a row of zeros.  vec: every row is aligned to four elements.
+template <class T, class Row>
+__device__ void stage(float *sm, int cnt, int w, bool vec, Row row) {
+    const int ld = smem_stride(w), pieces = (w + 3) / 4;
+    int per = 1;
+    while (per < pieces) per *= 2;
+    const int k = (int)threadIdx.x % per * 4, step = kTileThreads / per;
+    for (int r0 = (int)threadIdx.x / per; r0 < cnt; r0 += 4 * step) {
+        float4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int r = r0 + u * step;
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r >= cnt || k >= w) continue;
+            const T *p = row(r);
+            if (!p) continue;
+            if (vec && k + 4 <= w) {
+                v[u] = load4(p + k);
+            } else {
+                v[u].x = to_f(p[k]);
+                if (k + 1 < w) v[u].y = to_f(p[k + 1]);
+                if (k + 2 < w) v[u].z = to_f(p[k + 2]);
+                if (k + 3 < w) v[u].w = to_f(p[k + 3]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (r0 + u * step < cnt && k < w) *reinterpret_cast<float4 *>(sm + (r0 + u * step) * ld + k) = v[u];
     }
 }
-// keys [j0, j0 + cnt) of a key-side tensor (zeros where bias2 says the key is masked)
+// packed query rows [r0, ...), and keys [j0, ...) (zeros where bias2 says the key is masked)
 template <class T>
-__device__ void stage_keys(float *sm, const T *src, const fs_view &s, int b, int c, int j0, int cnt, int w,
-                           const float *bias2) {
-    for (int e = threadIdx.x; e < cnt * w; e += blockDim.x) {
-        const int j = e / w, k = e % w;
-        sm[j * (w + 1) + k] =
-            bias2[j] == -INFINITY ? 0.f : to_f(src[s.batch * b + s.token * (j0 + j) + s.head * c + k]);
-    }
+__device__ void stage_rows(float *sm, const void *src, const fs_view &s, const AttnParams &p, int b, int c, int r0,
+                           int cnt, int w, bool vec) {
+    const int rows = p.n * p.group;
+    stage<T>(sm, cnt, w, vec, [&](int r) -> const T * {
+        return r0 + r < rows ? (const T *)src + row_off(s, p, b, c, r0 + r) : nullptr;
+    });
+}
+template <class T>
+__device__ void stage_keys(float *sm, const void *src, const fs_view &s, int b, int c, int j0, int cnt, int w,
+                           const float *bias2, bool vec) {
+    const T *base = (const T *)src + s.batch * b + s.head * c;
+    stage<T>(sm, cnt, w, vec,
+             [&](int j) -> const T * { return bias2[j] == -INFINITY ? nullptr : base + s.token * (j0 + j); });
 }
 
-// One CTA: 16 packed rows of a key head over one part of the keys.
+// acc[u][w] += sum_k a[ia + u][k] b[ib + 16 w][k] over rows of the tiles (strides la and lb)
+template <int U, int W, int BSTEP>
+__device__ __forceinline__ void dots(float (&acc)[U][W], const float *a, int la, const float *b, int lb, int width) {
+    for (int k = 0; k < width; k += 4) {
+        float4 x[U], y[W];
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = *reinterpret_cast<const float4 *>(a + u * la + k);
+#pragma unroll
+        for (int w = 0; w < W; ++w) y[w] = *reinterpret_cast<const float4 *>(b + w * BSTEP * lb + k);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                acc[u][w] = fmaf(x[u].x, y[w].x, acc[u][w]);
+                acc[u][w] = fmaf(x[u].y, y[w].y, acc[u][w]);
+                acc[u][w] = fmaf(x[u].z, y[w].z, acc[u][w]);
+                acc[u][w] = fmaf(x[u].w, y[w].w, acc[u][w]);
+            }
+    }
+}
+// o[u][k] += sum_j wt[u][j] val[j][col + 64 k .. + 3] over `cnt` rows of val
+template <int U, int C>
+__device__ __forceinline__ void weigh(float4 (&o)[U][C], const float *wt, int lw, const float *val, int lv, int cnt,
+                                      int col, int width) {
+    for (int j = 0; j < cnt; j += 4) {
+        float4 f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) f[u] = *reinterpret_cast<const float4 *>(wt + u * lw + j);
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            if (col + 64 * k >= width) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 v = *reinterpret_cast<const float4 *>(val + (j + i) * lv + col + 64 * k);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float g = i == 0 ? f[u].x : i == 1 ? f[u].y : i == 2 ? f[u].z : f[u].w;
+                    o[u][k].x = fmaf(g, v.x, o[u][k].x);
+                    o[u][k].y = fmaf(g, v.y, o[u][k].y);
+                    o[u][k].z = fmaf(g, v.z, o[u][k].z);
+                    o[u][k].w = fmaf(g, v.w, o[u][k].w);
+                }
+            }
+        }
+    }
+}
 template <class T>
-__global__ void __launch_bounds__(kThreads) xattn_simt_kernel(const AttnParams p) {
-    extern __shared__ float sm[];
-    const int tiles = (p.n * p.group + kRows - 1) / kRows;
-    const int r0 = (blockIdx.x % tiles) * kRows, sp = blockIdx.x / tiles;
+__device__ __forceinline__ void put4(T *dst, float4 v, int k, int width, float mul) {
+    if (k < width) from_f(v.x * mul, dst + k);
+    if (k + 1 < width) from_f(v.y * mul, dst + k + 1);
+    if (k + 2 < width) from_f(v.z * mul, dst + k + 2);
+    if (k + 3 < width) from_f(v.w * mul, dst + k + 3);
+}
+
+// One CTA: 16 RPT packed rows of a key head over one part of the keys, 16 x 16 threads of RPT rows x 4 keys.  C:
+// 64-column pieces of dv.
+template <class T, int RPT, int C>
+__global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnParams p, bool vec) {
+    extern __shared__ __align__(16) float sm[];
+    constexpr int R = 16 * RPT, LP = kKeys + 4;
+    const int tiles = (p.n * p.group + R - 1) / R;
+    const int r0 = (blockIdx.x % tiles) * R, sp = blockIdx.x / tiles;
     const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads;
-    float *sQ = sm, *sK = sQ + kRows * (p.d + 1), *sV = sK + kKeys * (p.d + 1);
-    float *sP = sV + kKeys * (p.dv + 1), *sB = sP + kRows * (kKeys + 1);
+    const int ld = smem_stride(p.d), lv = smem_stride(p.dv);
+    float *sQ = sm, *sK = sQ + R * ld, *sV = sK + kKeys * ld, *sP = sV + kKeys * lv, *sB = sP + R * LP;
     const int keys = attn_keys(p, b);
     const int j_beg = sp * p.split_keys, j_end = min(keys, j_beg + p.split_keys);
-    stage_rows(sQ, (const T *)p.q, p.qs, p, b, c, r0, kRows, p.d);
-    const int row = threadIdx.x / 8, t8 = threadIdx.x % 8;
-    float o[kMaxD / 8];
+    stage_rows<T>(sQ, p.q, p.qs, p, b, c, r0, R, p.d, vec);
+    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
+    float4 o[RPT][C];
+    float mx[RPT], l[RPT];
 #pragma unroll
-    for (int k = 0; k < kMaxD / 8; ++k) o[k] = 0.f;
-    float mx = -INFINITY, l = 0.f;
+    for (int u = 0; u < RPT; ++u) {
+        mx[u] = -INFINITY;
+        l[u] = 0.f;
+#pragma unroll
+        for (int k = 0; k < C; ++k) o[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     for (int j0 = j_beg; j0 < j_end; j0 += kKeys) {
         __syncthreads();
         if (threadIdx.x < kKeys) sB[threadIdx.x] = attn_bias2(p, b, j0 + threadIdx.x, j_end);
         __syncthreads();
-        stage_keys(sK, (const T *)p.k, p.ks, b, c, j0, kKeys, p.d, sB);
-        stage_keys(sV, (const T *)p.v, p.vs, b, c, j0, kKeys, p.dv, sB);
+        stage_keys<T>(sK, p.k, p.ks, b, c, j0, kKeys, p.d, sB, vec);
+        stage_keys<T>(sV, p.v, p.vs, b, c, j0, kKeys, p.dv, sB, vec);
         __syncthreads();
-        float z[8], top = -INFINITY;
+        float z[RPT][4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) z[u] = 0.f;
-        for (int k = 0; k < p.d; ++k) {
-            const float qv = sQ[row * (p.d + 1) + k];
+        for (int u = 0; u < RPT; ++u)
 #pragma unroll
-            for (int u = 0; u < 8; ++u) z[u] = fmaf(qv, sK[(t8 + 8 * u) * (p.d + 1) + k], z[u]);
-        }
+            for (int w = 0; w < 4; ++w) z[u][w] = 0.f;
+        dots<RPT, 4, 16>(z, sQ + ti * RPT * ld, ld, sK + tj * ld, ld, p.d);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            z[u] = fmaf(z[u], p.scale2, sB[t8 + 8 * u]);
-            top = fmaxf(top, z[u]);
-        }
-        for (int w = 4; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
-        const float mn = fmaxf(mx, top);
-        const float ref = mn == -INFINITY ? 0.f : mn;  // nothing but masked keys so far: every term below is 0
-        const float cor = exp2f(mx - ref);
-        float sum = 0.f;
+        for (int u = 0; u < RPT; ++u) {
+            float top = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const float e = exp2f(z[u] - ref);
-            sP[row * (kKeys + 1) + t8 + 8 * u] = e;
-            sum += e;
-        }
-        for (int w = 4; w; w >>= 1) sum += __shfl_xor_sync(~0u, sum, w);
-        l = l * cor + sum;
-        mx = mn;
-        __syncwarp();
+            for (int w = 0; w < 4; ++w) {
+                z[u][w] = fmaf(z[u][w], p.scale2, sB[tj + 16 * w]);
+                top = fmaxf(top, z[u][w]);
+            }
+            for (int w = 8; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+            const float mn = fmaxf(mx[u], top);
+            const float ref = mn == -INFINITY ? 0.f : mn;  // nothing but masked keys so far: every term below is 0
+            const float cor = exp2f(mx[u] - ref);
+            float sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < kMaxD / 8; ++k) {
-            const int e = t8 + 8 * k;
-            if (e < p.dv) {
-                float a = o[k] * cor;
-                for (int j = 0; j < kKeys; ++j) a = fmaf(sP[row * (kKeys + 1) + j], sV[j * (p.dv + 1) + e], a);
-                o[k] = a;
+            for (int w = 0; w < 4; ++w) {
+                const float e = exp2f(z[u][w] - ref);
+                sP[(ti * RPT + u) * LP + tj + 16 * w] = e;
+                sum += e;
+            }
+            for (int w = 8; w; w >>= 1) sum += __shfl_xor_sync(~0u, sum, w);
+            l[u] = l[u] * cor + sum;
+            mx[u] = mn;
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                o[u][k].x *= cor;
+                o[u][k].y *= cor;
+                o[u][k].z *= cor;
+                o[u][k].w *= cor;
             }
         }
+        __syncwarp();  // a row's weights are written and read by its 16 threads, of one warp
+        weigh<RPT, C>(o, sP + ti * RPT * LP, LP, sV, lv, kKeys, 4 * tj, p.dv);
     }
-    const int r = r0 + row;
-    if (r >= p.n * p.group) return;
-    if (p.splits > 1) {
-        const size_t at = ((size_t)(sp * p.batch + b) * p.kv_heads + c) * p.n * p.group + r;
-        if (t8 == 0) p.part_ml[at] = make_float2(mx, l);
-        for (int k = 0; t8 + 8 * k < p.dv; ++k) p.part_o[at * p.dv + t8 + 8 * k] = o[k];
-        return;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // 0: no key is left (a NaN row stays NaN)
-    T *dst = (T *)p.out + row_off(p.os, p, b, c, r);
 #pragma unroll
-    for (int k = 0; k < kMaxD / 8; ++k)
-        if (t8 + 8 * k < p.dv) from_f(o[k] * inv, dst + t8 + 8 * k);
-    if (p.lse && t8 == 0)
-        p.lse[row_stat(p, b, c, r)] = l == 0.f ? -INFINITY : (float)(((double)mx + log2((double)l)) * kLn2d);
+    for (int u = 0; u < RPT; ++u) {
+        const int r = r0 + ti * RPT + u;
+        if (r >= p.n * p.group) continue;
+        if (p.splits > 1) {
+            const size_t at = ((size_t)(sp * p.batch + b) * p.kv_heads + c) * p.n * p.group + r;
+            if (tj == 0) p.part_ml[at] = make_float2(mx[u], l[u]);
+#pragma unroll
+            for (int k = 0; k < C; ++k) put4(p.part_o + at * p.dv, o[u][k], 4 * tj + 64 * k, p.dv, 1.f);
+            continue;
+        }
+        const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];  // 0: no key is left (a NaN row stays NaN)
+        T *dst = (T *)p.out + row_off(p.os, p, b, c, r);
+#pragma unroll
+        for (int k = 0; k < C; ++k) put4(dst, o[u][k], 4 * tj + 64 * k, p.dv, inv);
+        if (p.lse && tj == 0)
+            p.lse[row_stat(p, b, c, r)] =
+                l[u] == 0.f ? -INFINITY : (float)(((double)mx[u] + log2((double)l[u])) * kLn2d);
+    }
 }
 
 // Joins the parts of a row, in the parts' order.  One warp per packed row.
@@ -216,110 +320,104 @@ __global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p)
     if (lane == 0) p.dot[((size_t)b * p.heads + h) * p.n + i] = s;
 }
 
-// The 32 x 32 tile of P and of dS: sP, sS [key][row] (rows past the end and masked keys: zero).
-__device__ void grad_tile(const AttnParams &p, const float *sQ, const float *sG, const float *sK, const float *sV,
-                          const float *sB, const float *sL, const float *sD, float *sP, float *sS) {
-    for (int e = threadIdx.x; e < kGT * kGT; e += kThreads) {
-        const int j = e / kGT, r = e % kGT;
-        float s = 0.f, g = 0.f;
-        for (int k = 0; k < p.d; ++k) s = fmaf(sQ[r * (p.d + 1) + k], sK[j * (p.d + 1) + k], s);
-        for (int k = 0; k < p.dv; ++k) g = fmaf(sG[r * (p.dv + 1) + k], sV[j * (p.dv + 1) + k], g);
-        const bool off = sB[j] == -INFINITY || sL[r] == INFINITY;
-        const float pr = off ? 0.f : exp2f(fmaf(s, p.scale2, sB[j]) - sL[r]);
-        sP[j * (kGT + 1) + r] = pr;
-        sS[j * (kGT + 1) + r] = off ? 0.f : pr * (g - sD[r]);
-    }
-}
-// Base-2 LSE and D of rows r0.. (an empty row, or one past the end, is marked by +inf).
-__device__ void stage_stats(const AttnParams &p, int b, int c, int r0, float *sL, float *sD) {
-    if (threadIdx.x < kGT) {
-        const int r = r0 + threadIdx.x;
-        float l = INFINITY, dd = 0.f;
-        if (r < p.n * p.group) {
-            const float v = p.lse[row_stat(p, b, c, r)];
-            l = v == -INFINITY ? INFINITY : v * kLog2e;
-            dd = p.dot[row_stat(p, b, c, r)];
-        }
-        sL[threadIdx.x] = l;
-        sD[threadIdx.x] = dd;
-    }
-}
-
-// KEYS: one CTA per 32 keys of a key head, over all its rows: dk and dv.
-// Otherwise: one CTA per 32 packed rows, over all keys: dq.
-template <class T, bool KEYS>
-__global__ void __launch_bounds__(kThreads) xattn_grad_kernel(const AttnParams p) {
-    extern __shared__ float sm[];
-    const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads, t0 = blockIdx.x * kGT;
-    float *sQ = sm, *sG = sQ + kGT * (p.d + 1), *sK = sG + kGT * (p.dv + 1), *sV = sK + kGT * (p.d + 1);
-    float *sP = sV + kGT * (p.dv + 1), *sS = sP + kGT * (kGT + 1), *sB = sS + kGT * (kGT + 1), *sL = sB + kGT,
-          *sD = sL + kGT;
+// KEYS: one CTA keeps 64 keys of a key head (K, V) and streams its packed rows (Q, dO) in tiles of 32: dk and dv.
+// Otherwise: 64 packed rows (Q, dO) against streamed keys (K, V): dq.  16 x 16 threads: 4 kept rows x 2 streamed ones
+// of the scores, 4 kept rows x 4 columns a piece of the sums.
+template <class T, bool KEYS, int C>
+__global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnParams p, bool vec) {
+    extern __shared__ __align__(16) float sm[];
+    constexpr int LS = kStream + 4;
+    const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads, t0 = blockIdx.x * kKept;
+    const int ld = smem_stride(p.d), lv = smem_stride(p.dv);
+    float *a1 = sm, *a2 = a1 + kKept * ld, *b1 = a2 + kKept * lv, *b2 = b1 + kStream * ld, *sP = b2 + kStream * lv;
+    float *sS = sP + kKept * LS, *kb = sS + kKept * LS;  // kept: bias, or base-2 LSE and D
+    float *kd = kb + kKept, *sb = kd + kKept, *sd = sb + kStream;
     const int keys = attn_keys(p, b), rows = p.n * p.group;
-    const int end = KEYS ? rows : keys;
-    const int own = threadIdx.x / 4, t4 = threadIdx.x % 4;
-    float a1[kMaxD / 4], a2[KEYS ? kMaxD / 4 : 1];
-#pragma unroll
-    for (int k = 0; k < kMaxD / 4; ++k) a1[k] = 0.f;
-    if (KEYS) {
-#pragma unroll
-        for (int k = 0; k < (KEYS ? kMaxD / 4 : 1); ++k) a2[k] = 0.f;
-        if (threadIdx.x < kGT) sB[threadIdx.x] = attn_bias2(p, b, t0 + threadIdx.x, keys);
-        __syncthreads();
-        stage_keys(sK, (const T *)p.k, p.ks, b, c, t0, kGT, p.d, sB);
-        stage_keys(sV, (const T *)p.v, p.vs, b, c, t0, kGT, p.dv, sB);
-    } else {
-        stage_rows(sQ, (const T *)p.q, p.qs, p, b, c, t0, kGT, p.d);
-        stage_rows(sG, (const T *)p.dout, p.dos, p, b, c, t0, kGT, p.dv);
-        stage_stats(p, b, c, t0, sL, sD);
+    const int end = KEYS ? (t0 < keys ? rows : 0) : keys;
+    // base-2 LSE (+inf: an empty row, or one past the end) and D of packed row r
+    auto stat = [&](int r, float *lse2, float *d) {
+        *lse2 = INFINITY;
+        *d = 0.f;
+        if (r < rows) {
+            const float v = p.lse[row_stat(p, b, c, r)];
+            if (v != -INFINITY) *lse2 = v * kLog2e;
+            *d = p.dot[row_stat(p, b, c, r)];
+        }
+    };
+    if (threadIdx.x < kKept) {
+        if (KEYS)
+            kb[threadIdx.x] = attn_bias2(p, b, t0 + threadIdx.x, keys);
+        else
+            stat(t0 + threadIdx.x, kb + threadIdx.x, kd + threadIdx.x);
     }
-    for (int u0 = 0; u0 < end; u0 += kGT) {
+    __syncthreads();
+    if (KEYS) {
+        stage_keys<T>(a1, p.k, p.ks, b, c, t0, kKept, p.d, kb, vec);
+        stage_keys<T>(a2, p.v, p.vs, b, c, t0, kKept, p.dv, kb, vec);
+    } else {
+        stage_rows<T>(a1, p.q, p.qs, p, b, c, t0, kKept, p.d, vec);
+        stage_rows<T>(a2, p.dout, p.dos, p, b, c, t0, kKept, p.dv, vec);
+    }
+    const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
+    float4 g1[4][C], g2[4][KEYS ? C : 1];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            g1[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (KEYS) g2[u][KEYS ? k : 0] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    for (int u0 = 0; u0 < end; u0 += kStream) {
+        __syncthreads();
+        if (threadIdx.x < kStream) {
+            if (KEYS)
+                stat(u0 + threadIdx.x, sb + threadIdx.x, sd + threadIdx.x);
+            else
+                sb[threadIdx.x] = attn_bias2(p, b, u0 + threadIdx.x, keys);
+        }
         __syncthreads();
         if (KEYS) {
-            stage_rows(sQ, (const T *)p.q, p.qs, p, b, c, u0, kGT, p.d);
-            stage_rows(sG, (const T *)p.dout, p.dos, p, b, c, u0, kGT, p.dv);
-            stage_stats(p, b, c, u0, sL, sD);
+            stage_rows<T>(b1, p.q, p.qs, p, b, c, u0, kStream, p.d, vec);
+            stage_rows<T>(b2, p.dout, p.dos, p, b, c, u0, kStream, p.dv, vec);
         } else {
-            if (threadIdx.x < kGT) sB[threadIdx.x] = attn_bias2(p, b, u0 + threadIdx.x, keys);
-            __syncthreads();
-            stage_keys(sK, (const T *)p.k, p.ks, b, c, u0, kGT, p.d, sB);
-            stage_keys(sV, (const T *)p.v, p.vs, b, c, u0, kGT, p.dv, sB);
+            stage_keys<T>(b1, p.k, p.ks, b, c, u0, kStream, p.d, sb, vec);
+            stage_keys<T>(b2, p.v, p.vs, b, c, u0, kStream, p.dv, sb, vec);
         }
         __syncthreads();
-        grad_tile(p, sQ, sG, sK, sV, sB, sL, sD, sP, sS);
-        __syncthreads();
+        float s[4][2], g[4][2];
 #pragma unroll
-        for (int k = 0; k < kMaxD / 4; ++k) {
-            const int e = t4 + 4 * k;
-            if (e < p.d) {
-                float s = a1[k];
-                for (int u = 0; u < kGT; ++u)
-                    s = KEYS ? fmaf(sS[own * (kGT + 1) + u], sQ[u * (p.d + 1) + e], s)
-                             : fmaf(sS[u * (kGT + 1) + own], sK[u * (p.d + 1) + e], s);
-                a1[k] = s;
+        for (int u = 0; u < 4; ++u) s[u][0] = s[u][1] = g[u][0] = g[u][1] = 0.f;
+        dots<4, 2, 16>(s, a1 + ti * 4 * ld, ld, b1 + tj * ld, ld, p.d);
+        dots<4, 2, 16>(g, a2 + ti * 4 * lv, lv, b2 + tj * lv, lv, p.dv);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int kept = ti * 4 + u, str = tj + 16 * w;
+                const float bias = KEYS ? kb[kept] : sb[str], lse2 = KEYS ? sb[str] : kb[kept];
+                const float dd = KEYS ? sd[str] : kd[kept];
+                const bool off = bias == -INFINITY || lse2 == INFINITY;
+                const float pr = off ? 0.f : exp2f(fmaf(s[u][w], p.scale2, bias) - lse2);
+                if (KEYS) sP[kept * LS + str] = pr;
+                sS[kept * LS + str] = off ? 0.f : pr * (g[u][w] - dd);
             }
-            if (KEYS && e < p.dv) {
-                float s = a2[KEYS ? k : 0];
-                for (int u = 0; u < kGT; ++u) s = fmaf(sP[own * (kGT + 1) + u], sG[u * (p.dv + 1) + e], s);
-                a2[KEYS ? k : 0] = s;
-            }
-        }
+        __syncwarp();  // a kept row's weights are written and read by its 16 threads, of one warp
+        weigh<4, C>(g1, sS + ti * 4 * LS, LS, b1, ld, kStream, 4 * tj, p.d);
+        if constexpr (KEYS) weigh<4, C>(g2, sP + ti * 4 * LS, LS, b2, lv, kStream, 4 * tj, p.dv);
     }
-    const int at = t0 + own;
-    if (KEYS) {
-        if (at >= p.m) return;  // keys past the length get zeros: they take no part
-        T *dk = (T *)p.dk + p.dks.batch * b + p.dks.token * at + p.dks.head * c;
-        T *dv = (T *)p.dv_out + p.dvs.batch * b + p.dvs.token * at + p.dvs.head * c;
 #pragma unroll
-        for (int k = 0; k < kMaxD / 4; ++k) {
-            if (t4 + 4 * k < p.d) from_f(a1[k] * p.scale, dk + t4 + 4 * k);
-            if (t4 + 4 * k < p.dv) from_f(a2[KEYS ? k : 0], dv + t4 + 4 * k);
+    for (int u = 0; u < 4; ++u) {
+        const int at = t0 + ti * 4 + u;
+        if (at >= (KEYS ? p.m : rows)) continue;  // keys past the length get zeros: they take no part
+        T *d1 = KEYS ? (T *)p.dk + p.dks.batch * b + p.dks.token * at + p.dks.head * c
+                     : (T *)p.dq + row_off(p.dqs, p, b, c, at);
+#pragma unroll
+        for (int k = 0; k < C; ++k) put4(d1, g1[u][k], 4 * tj + 64 * k, p.d, p.scale);
+        if (KEYS) {
+            T *d2 = (T *)p.dv_out + p.dvs.batch * b + p.dvs.token * at + p.dvs.head * c;
+#pragma unroll
+            for (int k = 0; k < C; ++k) put4(d2, g2[u][KEYS ? k : 0], 4 * tj + 64 * k, p.dv, 1.f);
         }
-    } else {
-        if (at >= rows) return;
-        T *dq = (T *)p.dq + row_off(p.dqs, p, b, c, at);
-#pragma unroll
-        for (int k = 0; k < kMaxD / 4; ++k)
-            if (t4 + 4 * k < p.d) from_f(a1[k] * p.scale, dq + t4 + 4 * k);
     }
 }
 
@@ -327,35 +425,61 @@ template <class K>
 cudaError_t with_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
-
+// Whether four elements of every row can be loaded at once.
 template <class T>
-cudaError_t fwd(const AttnParams &p, cudaStream_t s) {
-    const size_t smem =
-        sizeof(float) * ((size_t)(kRows + kKeys) * (p.d + 1) + kKeys * (p.dv + 1) + kRows * (kKeys + 1) + kKeys);
-    cudaError_t e = with_smem(xattn_simt_kernel<T>, smem);
-    if (e != cudaSuccess) return e;
-    const int tiles = (p.n * p.group + kRows - 1) / kRows;
-    xattn_simt_kernel<T><<<dim3(tiles * p.splits, p.batch * p.kv_heads), kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+bool aligned4(const void *base, const fs_view &s) {
+    return reinterpret_cast<uintptr_t>(base) % (4 * sizeof(T)) == 0 && s.batch % 4 == 0 && s.token % 4 == 0 &&
+           s.head % 4 == 0;
 }
 
-template <class T>
-cudaError_t grad(const AttnParams &p, cudaStream_t s) {
-    const size_t smem = sizeof(float) * ((size_t)2 * kGT * (p.d + 1 + p.dv + 1) + 2 * kGT * (kGT + 1) + 3 * kGT);
-    cudaError_t e = with_smem(xattn_grad_kernel<T, true>, smem);
-    if (e == cudaSuccess) e = with_smem(xattn_grad_kernel<T, false>, smem);
+template <class T, int RPT, int C>
+cudaError_t fwd(const AttnParams &p, cudaStream_t s) {
+    constexpr int R = 16 * RPT;
+    const size_t smem = sizeof(float) * ((size_t)(R + kKeys) * smem_stride(p.d) + kKeys * smem_stride(p.dv) +
+                                         R * (kKeys + 4) + kKeys);
+    cudaError_t e = with_smem(xattn_simt_kernel<T, RPT, C>, smem);
     if (e != cudaSuccess) return e;
-    if (p.m > 0)
-        xattn_grad_kernel<T, true><<<dim3((p.m + kGT - 1) / kGT, p.batch * p.kv_heads), kThreads, smem, s>>>(p);
-    if (p.n > 0)
-        xattn_grad_kernel<T, false><<<dim3((p.n * p.group + kGT - 1) / kGT, p.batch * p.kv_heads), kThreads, smem, s>>>(p);
+    const bool vec = aligned4<T>(p.q, p.qs) && aligned4<T>(p.k, p.ks) && aligned4<T>(p.v, p.vs);
+    const int tiles = (p.n * p.group + R - 1) / R;
+    xattn_simt_kernel<T, RPT, C>
+        <<<dim3(tiles * p.splits, p.batch * p.kv_heads), kTileThreads, smem, s>>>(p, vec);
     return cudaGetLastError();
+}
+template <class T, int RPT>
+cudaError_t fwd_width(const AttnParams &p, cudaStream_t s) {
+    return p.dv <= 64 ? fwd<T, RPT, 1>(p, s) : p.dv <= 128 ? fwd<T, RPT, 2>(p, s) : fwd<T, RPT, 4>(p, s);
+}
+template <class T>
+cudaError_t fwd_rows(const AttnParams &p, cudaStream_t s) {
+    return p.n * p.group <= kXattnFewRows ? fwd_width<T, 1>(p, s) : fwd_width<T, 4>(p, s);
+}
+
+template <class T, int C>
+cudaError_t grad(const AttnParams &p, cudaStream_t s) {
+    const int w = smem_stride(p.d) + smem_stride(p.dv);
+    const size_t smem = sizeof(float) * ((size_t)(kKept + kStream) * w + 2 * kKept * (kStream + 4) + 2 * kKept + 2 * kStream);
+    cudaError_t e = with_smem(xattn_grad_kernel<T, true, C>, smem);
+    if (e == cudaSuccess) e = with_smem(xattn_grad_kernel<T, false, C>, smem);
+    if (e != cudaSuccess) return e;
+    const bool vec = aligned4<T>(p.q, p.qs) && aligned4<T>(p.k, p.ks) && aligned4<T>(p.v, p.vs) &&
+                     aligned4<T>(p.dout, p.dos);
+    const int heads = p.batch * p.kv_heads, rows = p.n * p.group;
+    if (p.m > 0)
+        xattn_grad_kernel<T, true, C><<<dim3((p.m + kKept - 1) / kKept, heads), kTileThreads, smem, s>>>(p, vec);
+    if (p.n > 0)
+        xattn_grad_kernel<T, false, C><<<dim3((rows + kKept - 1) / kKept, heads), kTileThreads, smem, s>>>(p, vec);
+    return cudaGetLastError();
+}
+template <class T>
+cudaError_t grad_width(const AttnParams &p, cudaStream_t s) {
+    const int w = p.d > p.dv ? p.d : p.dv;
+    return w <= 64 ? grad<T, 1>(p, s) : w <= 128 ? grad<T, 2>(p, s) : grad<T, 4>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s) {
-    return bf16 ? fwd<__nv_bfloat16>(p, s) : fwd<float>(p, s);
+    return bf16 ? fwd_rows<__nv_bfloat16>(p, s) : fwd_rows<float>(p, s);
 }
 cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s) {
     const size_t rows = (size_t)p.n * p.group * p.batch * p.kv_heads;
@@ -373,7 +497,7 @@ cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s) {
     return cudaGetLastError();
 }
 cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, cudaStream_t s) {
-    return bf16 ? grad<__nv_bfloat16>(p, s) : grad<float>(p, s);
+    return bf16 ? grad_width<__nv_bfloat16>(p, s) : grad_width<float>(p, s);
 }
 
 }  // namespace fs
