@@ -479,7 +479,8 @@ FS_API fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, con
  */
 typedef struct {
     int n, v, d;              /* rows (0 allowed), classes, width                      */
-    fs_dtype dtype;           /* FS_F32 (plain fp32 products) or FS_BF16               */
+    fs_dtype dtype;           /* FS_F32 (products of three bf16 planes each, good to
+                                 about 2^-22 of their terms) or FS_BF16              */
     float scale;              /* logit scale (inverse temperature), finite and > 0     */
     long long ldx, ldw;       /* row strides of x and w                                */
     long long lddx, lddw;     /* row strides of dx and dw; read by the gradient only   */
@@ -487,10 +488,12 @@ typedef struct {
 } fs_xent_desc;
 
 /* Bytes of workspace of fs_cross_entropy (grad = 0) or fs_cross_entropy_grad
- * (grad = 1) on the current device; 0 if the descriptor is not valid.  The
- * gradient's holds the logit gradients of one piece of the classes (up to
- * 256 MiB, or 256 classes if those take more) and partial sums of dx. */
-FS_API size_t fs_cross_entropy_workspace(const fs_xent_desc *desc, int grad);
+ * (grad = 1) on the current device; 0 if the descriptor is not valid.  Of x and
+ * w only the address's alignment counts: bf16 rows that do not start on 16 bytes
+ * are copied to rows that do, fp32 rows to three bf16 planes.  The gradient's
+ * holds the logit gradients of one piece of the classes (up to 256 MiB, or 256
+ * classes if those take more), and partial sums of dx. */
+FS_API size_t fs_cross_entropy_workspace(const fs_xent_desc *desc, const void *x, const void *w, int grad);
 
 /*
  * Forward: loss and lse, device fp32 [n] (natural log).  target: device int64
@@ -510,7 +513,7 @@ FS_API fs_status fs_cross_entropy(const fs_xent_desc *desc, const void *x, const
  *   dx_i = scale sum_j dz_ij w_j,   dw_j = scale sum_i dz_ij x_i
  * dx [n][d] and dw [v][d] of `dtype`.  dloss of ignored rows is not used.
  * Taken in pieces of the classes: the logits of a piece again, dz of the piece
- * (bf16 for bf16 inputs), its share of dx (summed in fp32) and its rows of dw.
+ * (rounded to bf16 for bf16 inputs, in three planes for fp32), its share of dx (summed in fp32) and its rows of dw.
  * A target outside 0..v-1 that is not ignore_index makes the gradients NaN.
  * Asynchronous.  Errors as fs_cross_entropy.
  */

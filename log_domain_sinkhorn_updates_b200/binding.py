@@ -117,7 +117,7 @@ def lib():
         L.fs_cross_attn_workspace.argtypes = [ad, ctypes.c_int]
         L.fs_cross_attn.argtypes = [ad] + [vp] * 8 + [szt, vp]
         L.fs_cross_attn_grad.argtypes = [ad] + [vp] * 12 + [szt, vp]
-        L.fs_cross_entropy_workspace.argtypes = [xd, ctypes.c_int]
+        L.fs_cross_entropy_workspace.argtypes = [xd, vp, vp, ctypes.c_int]
         L.fs_cross_entropy.argtypes = [xd] + [vp] * 6 + [szt, vp]
         L.fs_cross_entropy_grad.argtypes = [xd] + [vp] * 9 + [szt, vp]
         L.fs_check.argtypes = [vp]
@@ -361,7 +361,7 @@ def fs_selftest_wait(h: Handle, timeout_ms=50) -> int:
 
 # ---- row-softmax operators without a handle ----
 # A call's descriptor and workspace size follow from the tensors' shapes, strides, types and
-# device alone, so they are checked and built once for each such combination and kept (at most
+# device (and whether they start on 16 bytes) alone, so they are checked and built once for each such combination and kept (at most
 # _PLAN_LIMIT of them; no data, address or tensor is kept).
 _plans = {}
 _PLAN_LIMIT = 4096
@@ -411,14 +411,14 @@ def _view(t, what):
     return FsView(s[0], s[1], s[2])
 
 
-def _plan(key, build, query, grad):
+def _plan(key, build, query):
     """(descriptor, reference to it, workspace bytes) of `key`, built on its first use."""
     plan = _plans.get(key)
     if plan is None:
         import torch
         desc, device = build()
         with torch.cuda.device(device):
-            plan = (desc, ctypes.byref(desc), int(query(ctypes.byref(desc), grad)))
+            plan = (desc, ctypes.byref(desc), int(query(ctypes.byref(desc))))
         if len(_plans) >= _PLAN_LIMIT:
             _plans.clear()
         _plans[key] = plan
@@ -497,7 +497,8 @@ def fs_cross_attn(q, k, v, out, lse=None, k_len=None, bias=None, scale=None, str
     caller).  workspace: uint8 tensor of fs_cross_attn_workspace bytes; allocated if None."""
     L = lib()
     desc, ref, need = _plan(("attn", scale, *_geometry(q, k, v, out)),
-                            lambda: (_attn_desc(q, k, v, out, scale), q.device), L.fs_cross_attn_workspace, 0)
+                            lambda: (_attn_desc(q, k, v, out, scale), q.device),
+                            lambda d: L.fs_cross_attn_workspace(d, 0))
     dev = q.get_device()
     kl, bp, lp = _attn_sides(desc, dev, k_len, bias, lse)
     _op_call(dev, need, stream, workspace,
@@ -512,7 +513,7 @@ def fs_cross_attn_grad(q, k, v, out, lse, dout, dq, dk, dv, k_len=None, bias=Non
     L = lib()
     desc, ref, need = _plan(("attn_grad", scale, *_geometry(q, k, v, out, dout, dq, dk, dv)),
                             lambda: (_attn_grad_desc(q, k, v, out, dout, dq, dk, dv, scale), q.device),
-                            L.fs_cross_attn_workspace, 1)
+                            lambda d: L.fs_cross_attn_workspace(d, 1))
     dev = q.get_device()
     _same("lse is needed", lse is not None)
     kl, bp, lp = _attn_sides(desc, dev, k_len, bias, lse)
@@ -561,13 +562,15 @@ def fs_cross_entropy(x, w, target, loss, lse, scale=1.0, ignore_index=-100, stre
     is anything else outside the classes.  stream, workspace: as in fs_cross_attn."""
     import torch
     L = lib()
-    desc, ref, need = _plan(("xent", scale, ignore_index, *_geometry(x, w)),
-                            lambda: (_xent_desc(x, w, scale, ignore_index), x.device), L.fs_cross_entropy_workspace, 0)
+    xp, wp = x.data_ptr(), w.data_ptr()
+    desc, ref, need = _plan(("xent", scale, ignore_index, xp & 15, wp & 15, *_geometry(x, w)),
+                            lambda: (_xent_desc(x, w, scale, ignore_index), x.device),
+                            lambda d: L.fs_cross_entropy_workspace(d, xp, wp, 0))
     dev, shape = x.get_device(), (desc.n,)
     tp = _side(target, torch.int64, shape, dev, "target")
     lo, le = _side(loss, torch.float32, shape, dev, "loss"), _side(lse, torch.float32, shape, dev, "lse")
     _op_call(dev, need, stream, workspace,
-             lambda ws, size, s: L.fs_cross_entropy(ref, x.data_ptr(), w.data_ptr(), tp, lo, le, ws, size, s))
+             lambda ws, size, s: L.fs_cross_entropy(ref, xp, wp, tp, lo, le, ws, size, s))
 
 
 def fs_cross_entropy_grad(x, w, target, lse, dloss, dx, dw, dlse=None, scale=1.0, ignore_index=-100, stream=None,
@@ -576,16 +579,17 @@ def fs_cross_entropy_grad(x, w, target, lse, dloss, dx, dw, dlse=None, scale=1.0
     dlse (float32 [n]; dlse None for 0) of its outputs.  Other arguments as in the forward."""
     import torch
     L = lib()
-    desc, ref, need = _plan(("xent_grad", scale, ignore_index, *_geometry(x, w, dx, dw)),
+    xp, wp = x.data_ptr(), w.data_ptr()
+    desc, ref, need = _plan(("xent_grad", scale, ignore_index, xp & 15, wp & 15, *_geometry(x, w, dx, dw)),
                             lambda: (_xent_grad_desc(x, w, dx, dw, scale, ignore_index), x.device),
-                            L.fs_cross_entropy_workspace, 1)
+                            lambda d: L.fs_cross_entropy_workspace(d, xp, wp, 1))
     dev, shape = x.get_device(), (desc.n,)
     tp = _side(target, torch.int64, shape, dev, "target")
     le, dl, dz = (_side(t, torch.float32, shape, dev, what)
                   for t, what in ((lse, "lse"), (dloss, "dloss"), (dlse, "dlse")))
     _op_call(dev, need, stream, workspace,
-             lambda ws, size, s: L.fs_cross_entropy_grad(ref, x.data_ptr(), w.data_ptr(), tp, le, dl, dz, dx.data_ptr(),
-                                                         dw.data_ptr(), ws, size, s))
+             lambda ws, size, s: L.fs_cross_entropy_grad(ref, xp, wp, tp, le, dl, dz, dx.data_ptr(), dw.data_ptr(),
+                                                         ws, size, s))
 
 
 def fs_cross_entropy_workspace(x, w, dx=None, dw=None) -> int:
@@ -594,7 +598,7 @@ def fs_cross_entropy_workspace(x, w, dx=None, dw=None) -> int:
     grad = dx is not None
     desc = _xent_grad_desc(x, w, dx, dw, 1.0, -100) if grad else _xent_desc(x, w, 1.0, -100)
     with torch.cuda.device(x.device):
-        return int(lib().fs_cross_entropy_workspace(ctypes.byref(desc), int(grad)))
+        return int(lib().fs_cross_entropy_workspace(ctypes.byref(desc), x.data_ptr(), w.data_ptr(), int(grad)))
 
 
 def fs_check(stream=None):

@@ -100,19 +100,22 @@ cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, cudaStream_t 
 struct XentParams {
     int n, v, d;
     float scale, scale2;           // logit scale, and times log2(e)
-    const void *x, *w;
+    // The operands as the products read them: bf16 rows of `planes` planes (1 for bf16, 3 for fp32), plane_x and
+    // plane_w elements apart.
+    const void *x, *w;             // w: of the classes from c0 on
     long long ldx, ldw;            // row strides in elements
+    int planes, plane_x, plane_w;
     const long long *target;       // [n]
     long long ignore;
     float *loss, *lse;             // [n]
     const float *dloss, *dlse;     // [n] ([n] or null)
-    void *dx, *dw;
+    void *dx, *dw;                 // dw: of the classes from c0 on
     long long lddx, lddw;
     // one product's launch
-    int c0, c1;                    // class range of the launch
+    int c0, c1;                    // classes of the piece
     float2 *part;                  // [column tiles][n]: (max, sum) in base 2
     float *hit;                    // [n] scaled logit of the target
-    void *dl;                      // [n][ld_dl] gradient of the logits of classes c0..c1
+    void *dl;                      // [n][planes][ld_dl] gradient of the logits of classes c0..c1
     long long ld_dl;
     float *acc;                    // [parts][n][ld_acc] partial sums of dx
     long long ld_acc;
@@ -122,31 +125,31 @@ struct XentParams {
     int *err;
 };
 
-// Column-tile width of the partial statistics on each path.
-constexpr int kXentSimtCols = 128, kXentTcCols = 256;
+// Columns of the products' tiles, one partial statistic of a row each.
+constexpr int kXentCols = 256;
 
 // One product C [M][N] of the tensor-core kernel.
 struct XentGemm {
-    int M, N, K, mt, nt;  // sizes, and 256-row and 256-column tiles
-    int parts, k_part;    // parts of K, and the length of one
-    int a_off, b_off;     // offset of the operands' first row in their maps
-    int pairs;            // CTA pairs of the grid
-    int vec;              // out's rows can be written 16 bytes at a time
+    int M, N, K, mt, nt;     // sizes, and 256-row and 256-column tiles
+    int parts, k_part;       // parts of K, and the length of one
+    int segments;            // plane pairs summed (1, or 6 of the three planes)
+    int a_plane, b_plane;    // elements from plane to plane of the operands
+    int pairs;               // CTA pairs of the grid
+    int vec;                 // out's rows can be written 16 bytes at a time
     void *out;
     long long ldo;
 };
 
-cudaError_t launch_xent_lse_simt(const XentParams &p, bool bf16, cudaStream_t s);
-cudaError_t launch_xent_finish(const XentParams &p, int tiles, cudaStream_t s);
-cudaError_t launch_xent_dl_simt(const XentParams &p, bool bf16, cudaStream_t s);
-cudaError_t launch_xent_dx_simt(const XentParams &p, bool bf16, cudaStream_t s);
-cudaError_t launch_xent_dw_simt(const XentParams &p, bool bf16, cudaStream_t s);
-bool xent_tc_ok(const void *x, long long ldx, const void *w, long long ldw, int n, int v);
+// Copies rows into aligned bf16 planes of dp elements (1 of bf16, 3 of fp32).
+cudaError_t launch_xent_pack(const void *src, long long ld, int rows, int d, int dp, bool bf16, void *dst,
+                             cudaStream_t s);
+bool xent_tc_rows(const void *p, long long ld, int rows);  // readable as they lie (bf16)
 cudaError_t xent_tc_pairs(int *pairs);
-cudaError_t launch_xent_lse_tc(const XentParams &p, int pairs, cudaStream_t s);
-cudaError_t launch_xent_dl_tc(const XentParams &p, int pairs, cudaStream_t s);
-cudaError_t launch_xent_dx_tc(const XentParams &p, bool direct, int pairs, cudaStream_t s);
-cudaError_t launch_xent_dw_tc(const XentParams &p, int pairs, cudaStream_t s);
+cudaError_t launch_xent_lse(const XentParams &p, int pairs, cudaStream_t s);
+cudaError_t launch_xent_finish(const XentParams &p, int tiles, cudaStream_t s);
+cudaError_t launch_xent_dl(const XentParams &p, int pairs, cudaStream_t s);
+cudaError_t launch_xent_dx(const XentParams &p, bool direct, int pairs, cudaStream_t s);
+cudaError_t launch_xent_dw(const XentParams &p, int pairs, cudaStream_t s);
 // dx = sum over the parts of acc, rounded to the output type.
 cudaError_t launch_xent_reduce(const XentParams &p, bool bf16, cudaStream_t s);
 

@@ -227,67 +227,96 @@ fs_status check_xent(const fs_xent_desc *D, bool grad) {
 }
 
 struct XentPlan {
+    int planes = 1;            // bf16 planes of the products' operands
+    bool pack_x = false, pack_w = false;  // copied into planes first (w piece by piece)
+    int dp = 0;                // a plane's width
     int tiles = 0;             // column tiles of the forward
     int piece = 0, parts = 1;  // classes of a piece; parts of it in the dx product
     bool direct = false;       // one product is all of dx: written at once
     long long ld_dl = 0, ld_acc = 0;
-    size_t part = 0, hit = 0, dl = 0, acc = 0, total = 0;
+    size_t px = 0, pw = 0, part = 0, hit = 0, dl = 0, acc = 0, total = 0;  // workspace offsets, and its size
 };
 
-// Whether the pointers can be on the tensor-core path is known only at the
-// call, so both paths fit the workspace of the larger one.
-XentPlan plan_xent(const fs_xent_desc &D, bool grad, bool tc, const Device &dev) {
+XentPlan plan_xent(const fs_xent_desc &D, const void *x, const void *w, bool grad, const Device &dev) {
     XentPlan L;
+    const bool f32 = D.dtype == FS_F32;
+    const size_t n = (size_t)std::max(D.n, 1), budget = (size_t)256 << 20;
+    L.planes = f32 ? 3 : 1;
+    L.pack_x = f32 || !fs::xent_tc_rows(x, D.ldx, D.n);
+    L.pack_w = f32 || !fs::xent_tc_rows(w, D.ldw, D.v);
+    L.dp = up(D.d, 64) * 64;
+    // Pieces of the classes whose logit gradients, and whose copies of w, stay within 256 MiB each.
+    size_t fit = (size_t)up(D.v, 256) * 256;
+    if (grad) fit = std::min(fit, budget / (n * L.planes * 2) / 256 * 256);
+    if (L.pack_w) fit = std::min(fit, budget / ((size_t)L.dp * L.planes * 2) / 256 * 256);
+    L.piece = (int)std::max<size_t>(256, fit);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += align256(bytes);
+        return o;
+    };
+    if (L.pack_x) L.px = take(n * L.planes * L.dp * 2);
+    if (L.pack_w) L.pw = take((size_t)std::min(L.piece, D.v) * L.planes * L.dp * 2);
     if (!grad) {
-        L.tiles = up(D.v, tc ? fs::kXentTcCols : fs::kXentSimtCols);
-        L.hit = align256((size_t)L.tiles * D.n * sizeof(float2));
-        L.total = L.hit + align256((size_t)D.n * sizeof(float));
-        return L;
+        L.tiles = up(D.v, fs::kXentCols);
+        L.part = take((size_t)L.tiles * n * sizeof(float2));
+        L.hit = take(n * sizeof(float));
+    } else {
+        L.ld_dl = L.piece;
+        L.ld_acc = (D.d + 7) / 8 * 8;
+        // dx: where the product's tiles are fewer than what runs at once, its sum over the classes is split.
+        const long long tiles = (long long)up((int)n, 256) * up(D.d, 256);
+        L.parts = (int)std::max(1ll, std::min<long long>(std::min(32ll, dev.pairs / tiles), L.piece / 512));
+        L.direct = L.piece >= D.v && L.parts == 1;
+        L.dl = take(n * L.planes * L.ld_dl * 2);
+        if (!L.direct) L.acc = take((size_t)L.parts * n * L.ld_acc * sizeof(float));
     }
-    // Pieces of the classes whose logit gradients stay within 256 MiB.
-    const size_t elem = tc ? 2 : 4, budget = (size_t)256 << 20;
-    const size_t fit = budget / (elem * std::max(D.n, 1)) / 256 * 256;
-    L.piece = (int)std::max<size_t>(256, std::min<size_t>(fit, (size_t)up(D.v, 256) * 256));
-    L.ld_dl = L.piece;
-    L.ld_acc = (D.d + 7) / 8 * 8;
-    // dx: where the tiles of the product are fewer than what runs at once, the sum over the classes is split.
-    const int side = tc ? 256 : 128;
-    const long long tiles = (long long)up(std::max(D.n, 1), side) * up(D.d, side);
-    const long long want = (tc ? dev.pairs : 2 * dev.sms) / tiles;
-    L.parts = (int)std::max(1ll, std::min<long long>(std::min(32ll, want), L.piece / 512));
-    L.direct = tc && L.piece >= D.v && L.parts == 1;
-    L.acc = align256((size_t)D.n * L.ld_dl * elem);
-    L.total = L.acc + (L.direct ? 0 : align256((size_t)L.parts * D.n * L.ld_acc * sizeof(float)));
+    L.total = at;
     return L;
 }
-size_t xent_workspace(const fs_xent_desc &D, bool grad, const Device &dev) {
-    const size_t simt = plan_xent(D, grad, false, dev).total;
-    return D.dtype == FS_BF16 ? std::max(simt, plan_xent(D, grad, true, dev).total) : simt;
-}
 
-fs::XentParams xent_params(const fs_xent_desc &D, const XentPlan &L, const Device &dev, void *ws) {
+fs::XentParams xent_params(const fs_xent_desc &D, const XentPlan &L, const Device &dev, void *ws, const void *x) {
     fs::XentParams p{};
+    char *base = static_cast<char *>(ws);
     p.n = D.n;
     p.v = D.v;
     p.d = D.d;
     p.scale = D.scale;
     p.scale2 = (float)((double)D.scale * fs::kLog2ed);
-    p.ldx = D.ldx;
-    p.ldw = D.ldw;
+    p.planes = L.planes;
+    p.plane_x = p.plane_w = L.dp;
+    p.x = L.pack_x ? base + L.px : x;
+    p.ldx = L.pack_x ? (long long)L.planes * L.dp : D.ldx;
+    p.ldw = L.pack_w ? (long long)L.planes * L.dp : D.ldw;
     p.lddx = D.lddx;
     p.lddw = D.lddw;
     p.ignore = D.ignore_index;
-    char *w = static_cast<char *>(ws);
-    p.part = reinterpret_cast<float2 *>(w + L.part);
-    p.hit = reinterpret_cast<float *>(w + L.hit);
-    p.dl = w + L.dl;
+    p.part = reinterpret_cast<float2 *>(base + L.part);
+    p.hit = reinterpret_cast<float *>(base + L.hit);
+    p.dl = base + L.dl;
     p.ld_dl = L.ld_dl;
-    p.acc = reinterpret_cast<float *>(w + L.acc);
+    p.acc = reinterpret_cast<float *>(base + L.acc);
     p.ld_acc = L.ld_acc;
     p.parts = L.parts;
     p.timeout_ns = kTimeoutNs;
     p.err = dev.err;
     return p;
+}
+
+// The piece of the classes from c0 on: its rows of w, copied into planes where the products need that.
+fs_status xent_piece(const fs_xent_desc &D, const XentPlan &L, const void *w, void *ws, int c0, fs::XentParams &p,
+                     cudaStream_t s) {
+    const bool bf16 = D.dtype == FS_BF16;
+    const char *rows = static_cast<const char *>(w) + D.ldw * c0 * (bf16 ? 2 : 4);
+    p.c0 = c0;
+    p.c1 = std::min(D.v, c0 + L.piece);
+    p.w = rows;
+    if (L.pack_w) {
+        p.w = static_cast<char *>(ws) + L.pw;
+        OPS_LAUNCH(fs::launch_xent_pack(rows, D.ldw, p.c1 - c0, D.d, L.dp, bf16, static_cast<char *>(ws) + L.pw, s), 1);
+    }
+    return FS_OK;
 }
 
 }  // namespace
@@ -365,10 +394,10 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
     return FS_OK;
 }
 
-size_t fs_cross_entropy_workspace(const fs_xent_desc *desc, int grad) {
+size_t fs_cross_entropy_workspace(const fs_xent_desc *desc, const void *x, const void *w, int grad) {
     Device dev;
     if (check_xent(desc, grad != 0) != FS_OK || current_device(&dev) != FS_OK) return 0;
-    return xent_workspace(*desc, grad != 0, dev);
+    return plan_xent(*desc, x, w, grad != 0, dev).total;
 }
 
 fs_status fs_cross_entropy(const fs_xent_desc *desc, const void *x, const void *w, const long long *target,
@@ -380,22 +409,19 @@ fs_status fs_cross_entropy(const fs_xent_desc *desc, const void *x, const void *
     if (!x || !w || !target || !loss || !lse) return reject(FS_ERR_INVALID_ARG, "null argument");
     Device dev;
     if ((st = current_device(&dev)) != FS_OK) return st;
-    const bool bf16 = D.dtype == FS_BF16;
-    const bool tc = bf16 && fs::xent_tc_ok(x, D.ldx, w, D.ldw, D.n, D.v);
-    const XentPlan L = plan_xent(D, false, tc, dev);
+    const XentPlan L = plan_xent(D, x, w, false, dev);
     if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
-    fs::XentParams p = xent_params(D, L, dev, workspace);
-    p.x = x;
-    p.w = w;
+    fs::XentParams p = xent_params(D, L, dev, workspace, x);
     p.target = target;
     p.loss = loss;
     p.lse = lse;
-    p.c1 = D.v;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (tc)
-        OPS_LAUNCH(fs::launch_xent_lse_tc(p, dev.pairs, s), 1);
-    else
-        OPS_LAUNCH(fs::launch_xent_lse_simt(p, bf16, s), 1);
+    if (L.pack_x)
+        OPS_LAUNCH(fs::launch_xent_pack(x, D.ldx, D.n, D.d, L.dp, D.dtype == FS_BF16, const_cast<void *>(p.x), s), 1);
+    for (int c0 = 0; c0 < D.v; c0 += L.piece) {
+        if ((st = xent_piece(D, L, w, workspace, c0, p, s)) != FS_OK) return st;
+        OPS_LAUNCH(fs::launch_xent_lse(p, dev.pairs, s), 1);
+    }
     OPS_LAUNCH(fs::launch_xent_finish(p, L.tiles, s), 1);
     return FS_OK;
 }
@@ -410,37 +436,32 @@ fs_status fs_cross_entropy_grad(const fs_xent_desc *desc, const void *x, const v
         return reject(FS_ERR_INVALID_ARG, "null argument");
     Device dev;
     if ((st = current_device(&dev)) != FS_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = D.dtype == FS_BF16;
-    const bool tc = bf16 && fs::xent_tc_ok(x, D.ldx, w, D.ldw, D.n, D.v);
-    const XentPlan L = plan_xent(D, true, tc, dev);
+    const size_t elem = bf16 ? 2 : 4;
+    if (D.n == 0) {
+        cudaError_t e = cudaMemset2DAsync(dw, (D.v > 1 ? (size_t)D.lddw : (size_t)D.d) * elem, 0, D.d * elem, D.v, s);
+        return e == cudaSuccess ? FS_OK : reject(FS_ERR_CUDA, "cudaMemset2DAsync: %s", cudaGetErrorString(e));
+    }
+    const XentPlan L = plan_xent(D, x, w, true, dev);
     if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
-    fs::XentParams p = xent_params(D, L, dev, workspace);
-    p.x = x;
-    p.w = w;
+    fs::XentParams p = xent_params(D, L, dev, workspace, x);
     p.target = target;
     p.lse = const_cast<float *>(lse);
     p.dloss = dloss;
     p.dlse = dlse;
     p.dx = dx;
-    p.dw = dw;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (L.pack_x)
+        OPS_LAUNCH(fs::launch_xent_pack(x, D.ldx, D.n, D.d, L.dp, bf16, const_cast<void *>(p.x), s), 1);
     for (int c0 = 0; c0 < D.v; c0 += L.piece) {
-        p.c0 = c0;
-        p.c1 = std::min(D.v, c0 + L.piece);
+        if ((st = xent_piece(D, L, w, workspace, c0, p, s)) != FS_OK) return st;
         p.acc_add = c0 > 0;
-        if (tc && D.n > 0) {
-            OPS_LAUNCH(fs::launch_xent_dl_tc(p, dev.pairs, s), 1);
-            OPS_LAUNCH(fs::launch_xent_dx_tc(p, L.direct, dev.pairs, s), 1);
-            OPS_LAUNCH(fs::launch_xent_dw_tc(p, dev.pairs, s), 1);
-            continue;
-        }
-        if (D.n > 0) {
-            OPS_LAUNCH(fs::launch_xent_dl_simt(p, bf16, s), 1);
-            OPS_LAUNCH(fs::launch_xent_dx_simt(p, bf16, s), 1);
-        }
-        OPS_LAUNCH(fs::launch_xent_dw_simt(p, bf16, s), 1);
+        p.dw = static_cast<char *>(dw) + D.lddw * c0 * (long long)elem;
+        OPS_LAUNCH(fs::launch_xent_dl(p, dev.pairs, s), 1);
+        OPS_LAUNCH(fs::launch_xent_dx(p, L.direct, dev.pairs, s), 1);
+        OPS_LAUNCH(fs::launch_xent_dw(p, dev.pairs, s), 1);
     }
-    if (D.n > 0 && !L.direct) OPS_LAUNCH(fs::launch_xent_reduce(p, bf16, s), 1);
+    if (!L.direct) OPS_LAUNCH(fs::launch_xent_reduce(p, bf16, s), 1);
     return FS_OK;
 }
 

@@ -7,7 +7,10 @@
 //   LSE  C = x w^T          rows: (max, sum 2^(z - max)) per 256 columns, the target's logit
 //   DL   C = x w^T          dz = scale (e^{z - lse} (dloss + dlse) - onehot dloss) -> bf16
 //   ACC  C = dz w           fp32 partial sums of dx (per part of the classes)
-//   OUT  C = dz^T x or dz w  bf16 rows of dw, or of dx where one product is all of it
+//   OUT  C = dz^T x or dz w  rows of dw, or of dx where one product is all of it
+//
+// fp32 operands arrive as three bf16 planes (fs_xent.cu); dz is then written
+// as three planes too, and a product's K runs over six plane pairs.
 //
 // One tcgen05.mma.cta_group::2 covers a 256 x 256 tile of the pair (each CTA
 // holds 128 rows of A and 128 rows of B, and its own 128 x 256 accumulator, two
@@ -36,6 +39,10 @@ constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
 constexpr int kGroupRows = 8;  // row tiles that share a column tile while it is in L2
 
 enum { kLse = 0, kDl = 1, kAcc = 2, kOut = 3 };
+
+// The planes of A and of B in plane pair s: (h h), (h m), (m h), (h l), (l h), (m m).
+__device__ __forceinline__ int plane_a(int s) { return 0x610 >> (2 * s) & 3; }
+__device__ __forceinline__ int plane_b(int s) { return 0x484 >> (2 * s) & 3; }
 
 // M or N axis contiguous, 128-byte swizzle: 64-element columns of `krows` rows of K, 8192 bytes
 // apart; groups of 8 rows of K 1024 bytes apart.
@@ -66,7 +73,7 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 }
 
 struct Tile {
-    int m0, n0, k0, kb, part;  // first row and column, first K element, K blocks, part
+    int m0, n0, k0, kb, part;  // first row and column, first K element, K blocks of a plane pair, part
 };
 __device__ __forceinline__ Tile tile_of(const XentGemm &g, int t) {
     const int per_part = g.mt * g.nt;
@@ -91,7 +98,8 @@ __device__ __forceinline__ void load128(uint32_t ta, uint32_t (&r)[128]) {
     tmem_ld_wait();
 }
 
-template <int EPI, bool A_MN, bool B_MN>
+// F32: three planes in, fp32 out.
+template <int EPI, bool A_MN, bool B_MN, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     xent_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const XentParams p, const XentGemm g) {
@@ -143,8 +151,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Tile T = tile_of(g, t);
                 const int ra = T.m0 + (int)rank * 128, rb = T.n0 + (int)rank * 128;
                 if (*abort_flag) break;
-                for (int kb = 0; kb < T.kb; ++kb, ++i) {
+                int seg = 0, kb = -1;
+                for (int u = 0; u < T.kb * g.segments; ++u, ++i) {
+                    if (++kb == T.kb) {
+                        kb = 0;
+                        ++seg;
+                    }
                     const int s = i % kStages, k = T.k0 + kb * kBK;
+                    const int xa = F32 ? plane_a(seg) * g.a_plane : 0, xb = F32 ? plane_b(seg) * g.b_plane : 0;
                     if (i >= kStages && !mbar_wait(empty + s, ((uint32_t)(i / kStages) & 1u) ^ 1u, p.timeout_ns)) {
                         ok = false;
                         break;
@@ -153,16 +167,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t bar = cluster_addr(saddr(full + s), 0);
                     const uint32_t a = saddr(smem + s * kStageBytes), b = a + kOperand;
                     if (A_MN) {
-                        tma_load_2d_pair(a, &map_a, bar, ra, g.a_off + k);
-                        tma_load_2d_pair(a + 8192u, &map_a, bar, ra + 64, g.a_off + k);
+                        tma_load_2d_pair(a, &map_a, bar, xa + ra, k);
+                        tma_load_2d_pair(a + 8192u, &map_a, bar, xa + ra + 64, k);
                     } else {
-                        tma_load_2d_pair(a, &map_a, bar, k, g.a_off + ra);
+                        tma_load_2d_pair(a, &map_a, bar, xa + k, ra);
                     }
                     if (B_MN) {
-                        tma_load_2d_pair(b, &map_b, bar, rb, g.b_off + k);
-                        tma_load_2d_pair(b + 8192u, &map_b, bar, rb + 64, g.b_off + k);
+                        tma_load_2d_pair(b, &map_b, bar, xb + rb, k);
+                        tma_load_2d_pair(b + 8192u, &map_b, bar, xb + rb + 64, k);
                     } else {
-                        tma_load_2d_pair(b, &map_b, bar, k, g.b_off + rb);
+                        tma_load_2d_pair(b, &map_b, bar, xb + k, rb);
                     }
                 }
             }
@@ -187,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int b = n & 1;
                 if (n >= 2 && !mbar_wait_cluster(sempty + b, ((uint32_t)(n >> 1) & 1u) ^ 1u, p.timeout_ns)) ok = false;
                 const uint32_t dt = tmem_base + (uint32_t)(b * 256);
-                for (int kb = 0; ok && kb < T.kb; ++kb, ++i) {
+                for (int kb = 0; ok && kb < T.kb * g.segments; ++kb, ++i) {
                     const int s = i % kStages;
                     if (!mbar_wait(full + s, (uint32_t)(i / kStages) & 1u, p.timeout_ns) || *abort_flag) {
                         ok = false;
@@ -257,9 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(sempty0);
                 }
-                if (c0 >= g.N) continue;
+                if (c0 >= g.N && !(EPI == kDl && F32)) continue;
                 if constexpr (EPI == kLse) {
-                    const long long at = target - c0;
+                    const long long at = target - p.c0 - c0;
                     if (__any_sync(~0u, at >= 0 && at < 128)) {
                         float hit = 0.f;
 #pragma unroll
@@ -276,25 +290,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if constexpr (EPI == kDl) {
                     const long long at = target - p.c0 - c0;
                     const bool any = __any_sync(~0u, at >= 0 && at < 128);
-                    uint8_t *dst = (uint8_t *)p.dl + ((size_t)row * p.ld_dl + c0) * 2;
+                    const int planes = F32 ? 3 : 1;
+                    uint8_t *dst = (uint8_t *)p.dl + ((size_t)row * planes * p.ld_dl + c0) * 2;
 #pragma unroll
                     for (int k = 0; k < 128; k += 16) {
-                        uint32_t w[8];
+                        float v[16];
 #pragma unroll
-                        for (int u = 0; u < 16; u += 2) {
+                        for (int u = 0; u < 16; ++u) {
                             // a row without a gradient stays out even if its logits are not finite
-                            float d0 = gs == 0.f ? 0.f
-                                                 : ex2_approx(fmaf(__uint_as_float(r[k + u]), p.scale2, -l2)) * gs;
-                            float d1 = gs == 0.f ? 0.f
-                                                 : ex2_approx(fmaf(__uint_as_float(r[k + u + 1]), p.scale2, -l2)) * gs;
-                            if (any) {
-                                if (at == k + u) d0 -= gl;
-                                if (at == k + u + 1) d1 -= gl;
-                            }
-                            w[u / 2] = bf16x2(d0 * p.scale, d1 * p.scale);
+                            v[u] = gs == 0.f ? 0.f : ex2_approx(fmaf(__uint_as_float(r[k + u]), p.scale2, -l2)) * gs;
+                            if (any && at == k + u) v[u] -= gl;
+                            v[u] *= p.scale;
                         }
-                        // the row's padding beyond the last class (up to ld_dl, a multiple of 256) may be written
-                        if (live && c0 + k < g.N) st_v8(dst + 2 * k, w);
+                        // a row's padding beyond the last class (ld_dl is a multiple of 256) is written too: zeros
+                        // where a next plane follows it, which the dx product reads
+                        if (F32) {
+                            if (c0 + 128 > g.N) {
+#pragma unroll
+                                for (int u = 0; u < 16; ++u)
+                                    if (c0 + k + u >= g.N) v[u] = 0.f;
+                            }
+#pragma unroll
+                            for (int pl = 0; pl < 3; ++pl) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int u = 0; u < 16; u += 2) {
+                                    w[u / 2] = bf16x2(v[u], v[u + 1]);
+                                    v[u] -= __uint_as_float(w[u / 2] << 16);
+                                    v[u + 1] -= __uint_as_float(w[u / 2] & 0xffff0000u);
+                                }
+                                if (live) st_v8(dst + ((size_t)pl * p.ld_dl + k) * 2, w);
+                            }
+                        } else {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int u = 0; u < 16; u += 2) w[u / 2] = bf16x2(v[u], v[u + 1]);
+                            if (live && c0 + k < g.N) st_v8(dst + 2 * k, w);
+                        }
                     }
                 } else if constexpr (EPI == kAcc) {
                     float *dst = p.acc + ((size_t)T.part * g.M + row) * p.ld_acc + c0;
@@ -309,6 +341,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 r[k + u] = __float_as_uint(__uint_as_float(r[k + u]) + __uint_as_float(o[u]));
                         }
                         st_v8(dst + k, &r[k]);
+                    }
+                } else if constexpr (F32) {
+                    float *dst = (float *)g.out + g.ldo * row + c0;
+#pragma unroll
+                    for (int k = 0; k < 128; k += 4) {
+                        if (!live) break;
+                        if (g.vec && c0 + k + 4 <= g.N) {
+                            *reinterpret_cast<uint4 *>(dst + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                if (c0 + k + u < g.N) dst[k + u] = __uint_as_float(r[k + u]);
+                        }
                     }
                 } else {
                     __nv_bfloat16 *dst = (__nv_bfloat16 *)g.out + g.ldo * row + c0;
@@ -331,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (EPI == kLse && live) p.part[(size_t)(T.n0 / kTile) * g.M + row] = make_float2(mx, l);
+            if (EPI == kLse && live) p.part[((size_t)p.c0 + T.n0) / kTile * g.M + row] = make_float2(mx, l);
             if (*abort_flag) break;
         }
         if (!ok) {
@@ -349,10 +394,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int EPI, bool A_MN, bool B_MN>
+template <int EPI, bool A_MN, bool B_MN, bool F32>
 cudaError_t launch(const XentParams &p, const XentGemm &g, const CUtensorMap &a, const CUtensorMap &b,
                    cudaStream_t s) {
-    auto kern = xent_tc_kernel<EPI, A_MN, B_MN>;
+    auto kern = xent_tc_kernel<EPI, A_MN, B_MN, F32>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int tiles = g.mt * g.nt * g.parts;
@@ -374,7 +419,7 @@ cudaError_t launch(const XentParams &p, const XentGemm &g, const CUtensorMap &a,
 
 int up(int a, int b) { return (a + b - 1) / b; }
 
-XentGemm shape(int M, int N, int K, int parts, int pairs) {
+XentGemm shape(const XentParams &p, int M, int N, int K, int parts, int pairs) {
     XentGemm g{};
     g.M = M;
     g.N = N;
@@ -382,66 +427,83 @@ XentGemm shape(int M, int N, int K, int parts, int pairs) {
     g.mt = up(M, kTile);
     g.nt = up(N, kTile);
     g.parts = parts;
-    g.k_part = parts > 1 ? up(up(K, parts), kBK) * kBK : up(K > 0 ? K : 1, kBK) * kBK;
+    g.k_part = parts > 1 ? up(up(K, parts), kBK) * kBK : up(K, kBK) * kBK;
+    g.segments = p.planes == 3 ? 6 : 1;
     g.pairs = pairs;
     return g;
 }
 
-// A map of a row-major [rows][width] bf16 matrix: boxes of 64 x box_rows.
-bool encode(CUtensorMap *m, const void *base, long long width, long long rows, long long ld, int box_rows) {
-    const long long size[2] = {width, rows}, stride[1] = {rows > 1 ? ld : (width + 7) / 8 * 8};
+// A map of a row-major bf16 matrix of `planes` planes side by side: boxes of 64 x box_rows.
+bool encode(CUtensorMap *m, const void *base, int width, int planes, long long plane, int rows, long long ld,
+            int box_rows) {
+    const long long all = planes > 1 ? planes * plane : width;
+    const long long size[2] = {all, rows}, stride[1] = {rows > 1 ? ld : (all + 7) / 8 * 8};
     const int box[2] = {64, box_rows};
     return encode_bf16_map(m, base, 2, size, stride, box);
+}
+bool encode_x(CUtensorMap *m, const XentParams &p, int box_rows) {
+    return encode(m, p.x, p.d, p.planes, p.plane_x, p.n, p.ldx, box_rows);
+}
+bool encode_w(CUtensorMap *m, const XentParams &p, int box_rows) {
+    return encode(m, p.w, p.d, p.planes, p.plane_w, p.c1 - p.c0, p.ldw, box_rows);
+}
+bool encode_dl(CUtensorMap *m, const XentParams &p, int box_rows) {
+    return encode(m, p.dl, p.c1 - p.c0, p.planes, p.ld_dl, p.n, p.planes * p.ld_dl, box_rows);
+}
+template <bool A_MN, bool B_MN>
+cudaError_t launch_out(const XentParams &p, XentGemm &g, void *out, long long ldo, const CUtensorMap &a,
+                       const CUtensorMap &b, cudaStream_t s) {
+    g.out = out;
+    g.ldo = ldo;
+    g.vec = ldo % (p.planes == 3 ? 4 : 8) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    return p.planes == 3 ? launch<kOut, A_MN, B_MN, true>(p, g, a, b, s) : launch<kOut, A_MN, B_MN, false>(p, g, a, b, s);
 }
 
 }  // namespace
 
 // The rows a TMA box can start on: base and row stride multiples of 16 bytes.
-bool xent_tc_ok(const void *x, long long ldx, const void *w, long long ldw, int n, int v) {
-    auto al = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-    auto ld = [](long long s, int rows) { return rows <= 1 || (s > 0 && s % 8 == 0 && s < 1ll << 36); };
-    return al(x) && al(w) && ld(ldx, n) && ld(ldw, v);
+bool xent_tc_rows(const void *p, long long ld, int rows) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (rows <= 1 || (ld > 0 && ld % 8 == 0 && ld < 1ll << 36));
 }
 
-cudaError_t launch_xent_lse_tc(const XentParams &p, int pairs, cudaStream_t s) {
+cudaError_t launch_xent_lse(const XentParams &p, int pairs, cudaStream_t s) {
     CUtensorMap a, b;
-    if (!encode(&a, p.x, p.d, p.n, p.ldx, 128) || !encode(&b, p.w, p.d, p.v, p.ldw, 128)) return cudaErrorInvalidValue;
-    return launch<kLse, false, false>(p, shape(p.n, p.v, p.d, 1, pairs), a, b, s);
+    if (!encode_x(&a, p, 128) || !encode_w(&b, p, 128)) return cudaErrorInvalidValue;
+    XentGemm g = shape(p, p.n, p.c1 - p.c0, p.d, 1, pairs);
+    g.a_plane = p.plane_x;
+    g.b_plane = p.plane_w;
+    return p.planes == 3 ? launch<kLse, false, false, true>(p, g, a, b, s) : launch<kLse, false, false, false>(p, g, a, b, s);
 }
-cudaError_t launch_xent_dl_tc(const XentParams &p, int pairs, cudaStream_t s) {
+cudaError_t launch_xent_dl(const XentParams &p, int pairs, cudaStream_t s) {
     CUtensorMap a, b;
-    if (!encode(&a, p.x, p.d, p.n, p.ldx, 128) || !encode(&b, p.w, p.d, p.v, p.ldw, 128)) return cudaErrorInvalidValue;
-    XentGemm g = shape(p.n, p.c1 - p.c0, p.d, 1, pairs);
-    g.b_off = p.c0;
-    return launch<kDl, false, false>(p, g, a, b, s);
+    if (!encode_x(&a, p, 128) || !encode_w(&b, p, 128)) return cudaErrorInvalidValue;
+    XentGemm g = shape(p, p.n, p.c1 - p.c0, p.d, 1, pairs);
+    g.a_plane = p.plane_x;
+    g.b_plane = p.plane_w;
+    return p.planes == 3 ? launch<kDl, false, false, true>(p, g, a, b, s) : launch<kDl, false, false, false>(p, g, a, b, s);
 }
-// dx (direct: the whole of it, written in bf16; otherwise partial sums in acc)
-cudaError_t launch_xent_dx_tc(const XentParams &p, bool direct, int pairs, cudaStream_t s) {
+// dx (direct: the whole of it, written in its type; otherwise partial sums in acc)
+cudaError_t launch_xent_dx(const XentParams &p, bool direct, int pairs, cudaStream_t s) {
     CUtensorMap a, b;
-    const int nc = p.c1 - p.c0;
-    if (!encode(&a, p.dl, nc, p.n, p.ld_dl, 128) || !encode(&b, p.w, p.d, p.v, p.ldw, 64)) return cudaErrorInvalidValue;
-    XentGemm g = shape(p.n, p.d, nc, p.parts, pairs);
-    g.b_off = p.c0;
-    if (!direct) return launch<kAcc, false, true>(p, g, a, b, s);
-    g.out = p.dx;
-    g.ldo = p.lddx;
-    g.vec = p.lddx % 8 == 0 && (reinterpret_cast<uintptr_t>(p.dx) & 15) == 0;
-    return launch<kOut, false, true>(p, g, a, b, s);
+    if (!encode_dl(&a, p, 128) || !encode_w(&b, p, 64)) return cudaErrorInvalidValue;
+    XentGemm g = shape(p, p.n, p.d, p.c1 - p.c0, p.parts, pairs);
+    g.a_plane = (int)p.ld_dl;
+    g.b_plane = p.plane_w;
+    if (direct) return launch_out<false, true>(p, g, p.dx, p.lddx, a, b, s);
+    return p.planes == 3 ? launch<kAcc, false, true, true>(p, g, a, b, s) : launch<kAcc, false, true, false>(p, g, a, b, s);
 }
-cudaError_t launch_xent_dw_tc(const XentParams &p, int pairs, cudaStream_t s) {
+cudaError_t launch_xent_dw(const XentParams &p, int pairs, cudaStream_t s) {
     CUtensorMap a, b;
-    const int nc = p.c1 - p.c0;
-    if (!encode(&a, p.dl, nc, p.n, p.ld_dl, 64) || !encode(&b, p.x, p.d, p.n, p.ldx, 64)) return cudaErrorInvalidValue;
-    XentGemm g = shape(nc, p.d, p.n, 1, pairs);
-    g.out = (__nv_bfloat16 *)p.dw + p.lddw * p.c0;
-    g.ldo = p.lddw;
-    g.vec = p.lddw % 8 == 0 && (reinterpret_cast<uintptr_t>(p.dw) & 15) == 0;
-    return launch<kOut, true, true>(p, g, a, b, s);
+    if (!encode_dl(&a, p, 64) || !encode_x(&b, p, 64)) return cudaErrorInvalidValue;
+    XentGemm g = shape(p, p.c1 - p.c0, p.d, p.n, 1, pairs);
+    g.a_plane = (int)p.ld_dl;
+    g.b_plane = p.plane_x;
+    return launch_out<true, true>(p, g, p.dw, p.lddw, a, b, s);
 }
 
 // CTA pairs that are resident at once on the current device.
 cudaError_t xent_tc_pairs(int *pairs) {
-    auto kern = xent_tc_kernel<kLse, false, false>;
+    auto kern = xent_tc_kernel<kLse, false, false, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

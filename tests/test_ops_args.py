@@ -103,7 +103,7 @@ def test_cross_entropy_descriptors(L):
                dict(scale=float("nan")), dict(scale=float("inf")), dict(ldx=-1), dict(ldw=-64)]:
         assert forward(_xent(**kw)) == FS_ERR_INVALID_ARG, kw
         assert grad(_xent(**kw)) == FS_ERR_INVALID_ARG, kw
-        assert L.fs_cross_entropy_workspace(ctypes.byref(_xent(**kw)), 1) == 0
+        assert L.fs_cross_entropy_workspace(ctypes.byref(_xent(**kw)), None, None, 1) == 0
     for kw in [dict(lddx=63), dict(lddw=0)]:
         assert grad(_xent(**kw)) == FS_ERR_INVALID_ARG, kw
     for kw in [dict(v=(1 << 22) + 1), dict(d=65537), dict(n=1 << 30)]:
