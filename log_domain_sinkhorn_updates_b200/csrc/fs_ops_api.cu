@@ -249,6 +249,7 @@ XentPlan plan_xent(const fs_xent_desc &D, const void *x, const void *w, bool gra
     size_t fit = (size_t)up(D.v, 256) * 256;
     if (grad) fit = std::min(fit, budget / (n * L.planes * 2) / 256 * 256);
     if (L.pack_w) fit = std::min(fit, budget / ((size_t)L.dp * L.planes * 2) / 256 * 256);
+    if (grad && f32) fit = std::min(fit, (size_t)8 * fs::kXentF32Terms);  // at most 8 parts of it in the dx product
     L.piece = (int)std::max<size_t>(256, fit);
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -268,6 +269,7 @@ XentPlan plan_xent(const fs_xent_desc &D, const void *x, const void *w, bool gra
         // dx: where the product's tiles are fewer than what runs at once, its sum over the classes is split.
         const long long tiles = (long long)up((int)n, 256) * up(D.d, 256);
         L.parts = (int)std::max(1ll, std::min<long long>(std::min(32ll, dev.pairs / tiles), L.piece / 512));
+        if (f32) L.parts = std::max(L.parts, up(L.piece, fs::kXentF32Terms));
         L.direct = L.piece >= D.v && L.parts == 1;
         L.dl = take(n * L.planes * L.ld_dl * 2);
         if (!L.direct) L.acc = take((size_t)L.parts * n * L.ld_acc * sizeof(float));
@@ -459,7 +461,9 @@ fs_status fs_cross_entropy_grad(const fs_xent_desc *desc, const void *x, const v
         p.dw = static_cast<char *>(dw) + D.lddw * c0 * (long long)elem;
         OPS_LAUNCH(fs::launch_xent_dl(p, dev.pairs, s), 1);
         OPS_LAUNCH(fs::launch_xent_dx(p, L.direct, dev.pairs, s), 1);
-        OPS_LAUNCH(fs::launch_xent_dw(p, dev.pairs, s), 1);
+        const int rows = bf16 ? D.n : fs::kXentF32Terms;
+        for (int r0 = 0; r0 < D.n; r0 += rows)
+            OPS_LAUNCH(fs::launch_xent_dw(p, r0, std::min(D.n, r0 + rows), r0 > 0, dev.pairs, s), 1);
     }
     if (!L.direct) OPS_LAUNCH(fs::launch_xent_reduce(p, bf16, s), 1);
     return FS_OK;

@@ -40,9 +40,11 @@ constexpr int kGroupRows = 8;  // row tiles that share a column tile while it is
 
 enum { kLse = 0, kDl = 1, kAcc = 2, kOut = 3 };
 
-// The planes of A and of B in plane pair s: (h h), (h m), (m h), (h l), (l h), (m m).
-__device__ __forceinline__ int plane_a(int s) { return 0x610 >> (2 * s) & 3; }
-__device__ __forceinline__ int plane_b(int s) { return 0x484 >> (2 * s) & 3; }
+// The planes of A and of B in plane pair s: (m m), (l h), (h l), (m h), (h m), (h h).  The accumulator truncates at
+// each step of K, by its own size: the small pairs go first, while it is small, and the steps that count are those of
+// the last pair alone.
+__device__ __forceinline__ int plane_a(int s) { return 0x049 >> (2 * s) & 3; }
+__device__ __forceinline__ int plane_b(int s) { return 0x121 >> (2 * s) & 3; }
 
 // M or N axis contiguous, 128-byte swizzle: 64-element columns of `krows` rows of K, 8192 bytes
 // apart; groups of 8 rows of K 1024 bytes apart.
@@ -239,14 +241,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool live = row < g.M;
             // what the row needs, fetched while the MMAs run
             long long target = -1;
-            float gl = 0.f, gs = 0.f, l2 = 0.f;
+            float gl = 0.f, gs = 0.f, l2 = 0.f, l2lo = 0.f;
             if (EPI <= kDl && live) {
                 target = __ldg(p.target + row);
                 if (EPI == kDl) {
                     const bool ign = target == p.ignore;
                     gl = ign ? 0.f : (target < 0 || target >= p.v ? NAN : __ldg(p.dloss + row));
                     gs = gl + (p.dlse ? __ldg(p.dlse + row) : 0.f);
-                    l2 = __ldg(p.lse + row) * kLog2e;
+                    const float lse = __ldg(p.lse + row);
+                    l2 = lse * kLog2e;
+                    if (F32)  // what the product's rounding lost, and log2(e)'s own tail
+                        l2lo = fmaf(lse, kLog2e, -l2) + lse * (float)(kLog2ed - (double)kLog2e);
                     if (ign) target = -1;
                 }
             }
@@ -298,7 +303,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int u = 0; u < 16; ++u) {
                             // a row without a gradient stays out even if its logits are not finite
-                            v[u] = gs == 0.f ? 0.f : ex2_approx(fmaf(__uint_as_float(r[k + u]), p.scale2, -l2)) * gs;
+                            float z = fmaf(__uint_as_float(r[k + u]), p.scale2, -l2);
+                            if (F32) z -= l2lo;
+                            v[u] = gs == 0.f ? 0.f : ex2_approx(z) * gs;
                             if (any && at == k + u) v[u] -= gl;
                             v[u] *= p.scale;
                         }
@@ -348,11 +355,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 128; k += 4) {
                         if (!live) break;
                         if (g.vec && c0 + k + 4 <= g.N) {
-                            *reinterpret_cast<uint4 *>(dst + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+                            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (g.add) o = *reinterpret_cast<const float4 *>(dst + k);
+                            o.x += __uint_as_float(r[k]);
+                            o.y += __uint_as_float(r[k + 1]);
+                            o.z += __uint_as_float(r[k + 2]);
+                            o.w += __uint_as_float(r[k + 3]);
+                            *reinterpret_cast<float4 *>(dst + k) = o;
                         } else {
 #pragma unroll
                             for (int u = 0; u < 4; ++u)
-                                if (c0 + k + u < g.N) dst[k + u] = __uint_as_float(r[k + u]);
+                                if (c0 + k + u < g.N)
+                                    dst[k + u] = (g.add ? dst[k + u] : 0.f) + __uint_as_float(r[k + u]);
                         }
                     }
                 } else {
@@ -492,10 +506,16 @@ cudaError_t launch_xent_dx(const XentParams &p, bool direct, int pairs, cudaStre
     if (direct) return launch_out<false, true>(p, g, p.dx, p.lddx, a, b, s);
     return p.planes == 3 ? launch<kAcc, false, true, true>(p, g, a, b, s) : launch<kAcc, false, true, false>(p, g, a, b, s);
 }
-cudaError_t launch_xent_dw(const XentParams &p, int pairs, cudaStream_t s) {
+// dw from the rows [r0, r1); add (fp32): onto what the rows before them gave
+cudaError_t launch_xent_dw(const XentParams &whole, int r0, int r1, bool add, int pairs, cudaStream_t s) {
     CUtensorMap a, b;
+    XentParams p = whole;
+    p.n = r1 - r0;
+    p.x = (const __nv_bfloat16 *)whole.x + whole.ldx * r0;
+    p.dl = (__nv_bfloat16 *)whole.dl + (size_t)whole.planes * whole.ld_dl * r0;
     if (!encode_dl(&a, p, 64) || !encode_x(&b, p, 64)) return cudaErrorInvalidValue;
     XentGemm g = shape(p, p.c1 - p.c0, p.d, p.n, 1, pairs);
+    g.add = add;
     g.a_plane = (int)p.ld_dl;
     g.b_plane = p.plane_x;
     return launch_out<true, true>(p, g, p.dw, p.lddw, a, b, s);
