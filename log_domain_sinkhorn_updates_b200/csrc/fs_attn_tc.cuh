@@ -12,6 +12,65 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// mbar_wait that sleeps: the thread is suspended until the phase completes, or for 50 us a try.  Warps that wait
+// then leave their issue slots to the softmax warp of the same SM quarter.
+__device__ __forceinline__ bool mbar_wait_near(uint64_t *b, uint32_t parity, unsigned long long limit_ns) {
+    unsigned long long t0 = 0;
+    while (true) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred P;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %3;\n\t"
+            "selp.b32 %0, 1, 0, P;\n\t}"
+            : "=r"(done)
+            : "r"(saddr(b)), "r"(parity), "r"(50000u)
+            : "memory");
+        if (done) return true;
+        const unsigned long long t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > limit_ns) return false;
+    }
+}
+// A ring position that moves without divisions: slot and the parity of its use.
+struct RingPos {
+    int slot;
+    uint32_t phase;
+    __device__ __forceinline__ void step(int by, int slots) {
+        slot += by;
+        if (slot >= slots) {
+            slot -= slots;
+            phase ^= 1u;
+        }
+    }
+};
+// One lane of a converged warp.  A warp that issues MMAs runs its loop with all lanes, so that addresses and
+// descriptors stay in uniform registers, and only the issuing instructions are one lane's: with the whole loop under
+// lane == 0, each MMA took about 80 cycles to issue and a wait on a completed barrier 170 to 240.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t lead;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(lead));
+    return lead != 0;
+}
+// The warpgroup gives up, or takes, registers: N a thread from here on.
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ float max_of64(const uint32_t *s) {
+    float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 64; k += 8) {
+        t0 = max3(t0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+        t1 = max3(t1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+        t2 = max3(t2, __uint_as_float(s[k + 4]), __uint_as_float(s[k + 5]));
+        t3 = max3(t3, __uint_as_float(s[k + 6]), __uint_as_float(s[k + 7]));
+    }
+    return fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+}
 // A right factor as it lies in memory: its rows are the K axis, 64-element
 // columns of its width `lbo` bytes apart, 128-byte swizzle.
 __device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, uint32_t lbo) {

@@ -25,8 +25,8 @@
 // memory before the products read them, so that whatever stood there (NaN
 // included) is a zero score plus -inf and a zero weight times zero.
 //
-// Warps: 0 loads K and V by TMA; 1 allocates TMEM; 1 and 2 issue the MMAs of
-// groups 0 and 1; 3 bias and masks; 4..7 and 8..11 are the softmax groups.
+// Warps: 0 loads K and V by TMA; 1 allocates TMEM and issues the MMAs; 3 bias
+// and masks; 4..7 and 8..11 are the softmax groups.
 #include <cuda.h>
 
 #include "fs_attn_tc.cuh"
@@ -52,7 +52,7 @@ __host__ __device__ inline Layout layout(int qt, int datoms, int vatoms, int slo
     L.bias = L.ring + (uint32_t)slots * L.slot;
     L.ml = L.bias + kBiasSlots * kTS * 4;
     L.bars = L.ml + 128 * 8;
-    L.total = L.bars + (3 * slots + 2 * kBiasSlots + 1 + 2 + 4 + 2 + 2) * 8 + 32;
+    L.total = L.bars + (3 * slots + 2 * kBiasSlots + 1 + 2 + 4 + 2 + 1) * 8 + 32;
     return L;
 }
 
@@ -78,12 +78,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *sfull = qfull + 1;    // [2]
     uint64_t *pready = sfull + 2;   // [2][2] P of group g, half h
     uint64_t *pvdone = pready + 4;  // [2]
-    uint64_t *drain = pvdone + 2;   // [2] every MMA of issuer g is complete
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 2);
+    uint64_t *drain = pvdone + 2;   // every MMA is complete
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile int *tile_masked = reinterpret_cast<volatile int *>(tmem_holder + 2);  // [kBiasSlots]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rows = p.n * p.group;
     const int blocks = (rows + QT * 128 - 1) / (QT * 128);
     const int rb = blockIdx.x % blocks, sp = blockIdx.x / blocks;
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < NS; ++s) {
             mbar_init(full + s, 1);
             mbar_init(ready + s, 1);
-            mbar_init(empty + s, QT);
+            mbar_init(empty + s, 1);
         }
         for (int s = 0; s < kBiasSlots; ++s) {
             mbar_init(bfull + s, 1);
@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(pready + 2 * i, 4);
             mbar_init(pready + 2 * i + 1, 4);
             mbar_init(pvdone + i, 1);
-            mbar_init(drain + i, 1);
         }
+        mbar_init(drain, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -123,16 +123,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
-
+    // 128 threads give up what the 256 of the softmax take: 128 x 88 + 256 x 208 of the launch's 384 x 168 registers
+    if (warp < 4) {
+    regs_dec<88>();
     if (warp == 0) {
         // ---------------- K and V tiles: slot 2 t holds K(t), slot 2 t + 1 V(t) ----------------
         if (lane == 0) {
             bool ok = true;
+            RingPos rp{0, 0};
             int i = 0;
             for (; ok && i < 2 * nt; ++i) {
-                const int s = i % NS, t = i >> 1;
+                const int s = rp.slot;
                 if (*abort_flag) break;
-                if (i >= NS && !mbar_wait(empty + s, ((uint32_t)(i / NS) & 1u) ^ 1u, p.timeout_ns)) {
+                if (i >= NS && !mbar_wait_near(empty + s, rp.phase ^ 1u, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
@@ -142,18 +145,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t dst = saddr(ring + (size_t)s * L.slot);
                 mbar_expect_tx(full + s, (uint32_t)atoms * 16384u);
                 for (int a = 0; a < atoms; ++a)
-                    tma_load_4d(dst + a * 16384u, map, saddr(full + s), a * 64, j_beg + t * kTS, c * hm, b * bm);
+                    tma_load_4d(dst + a * 16384u, map, saddr(full + s), a * 64, j_beg + (i >> 1) * kTS, c * hm, b * bm);
+                rp.step(1, NS);
             }
             if (!ok) {
                 atomicOr(p.err, kDevErrTimeout);
                 *abort_flag = 1;
             }
-            for (int k = max(0, i - NS); k < i; ++k) mbar_wait(full + (k % NS), (uint32_t)(k / NS) & 1u, p.timeout_ns);
+            for (int k = max(0, i - NS); k < i; ++k) mbar_wait_near(full + (k % NS), (uint32_t)(k / NS) & 1u, p.timeout_ns);
         }
         __syncwarp();
     } else if (warp == 3) {
         // ---------------- bias slices and masked rows ----------------
         bool ok = true;
+        RingPos rp{0, 0};
         for (int t = 0; ok && t < nt; ++t) {
             const int j = t % kBiasSlots;
             float bv[4];
@@ -165,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 dead[u] = __ballot_sync(~0u, bv[u] == -INFINITY);
                 any = any || dead[u];
             }
-            if (t >= kBiasSlots && !mbar_wait(bempty + j, ((uint32_t)(t / kBiasSlots) & 1u) ^ 1u, p.timeout_ns))
+            if (t >= kBiasSlots && !mbar_wait_near(bempty + j, ((uint32_t)(t / kBiasSlots) & 1u) ^ 1u, p.timeout_ns))
                 ok = false;
 #pragma unroll
             for (int u = 0; u < 4; ++u) sBias[j * kTS + 32 * u + lane] = bv[u];
@@ -174,8 +179,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bfull + j);
             const bool clear = dead[0] | dead[1] | dead[2] | dead[3];
             for (int kv = 0; kv < 2; ++kv) {
-                const int i = 2 * t + kv, s = i % NS;
-                if (!mbar_wait(full + s, (uint32_t)(i / NS) & 1u, p.timeout_ns)) ok = false;
+                const int s = rp.slot;
+                if (!mbar_wait_near(full + s, rp.phase, p.timeout_ns)) ok = false;
+                rp.step(1, NS);
                 if (clear) {
                     uint8_t *tile = ring + (size_t)s * L.slot;
                     clear_rows(tile, kTS, kv ? g.vatoms : g.datoms, dead, lane);
@@ -191,66 +197,91 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort_flag = 1;
         }
         __syncwarp();
-    } else if (warp == 1 || warp == 2) {
-        // ---------------- MMA issuers ----------------
-        if (lane == 0) {
-            const int grp = warp - 1;
-            const int t0 = QT == 2 ? 0 : grp, step = QT == 2 ? 1 : 2;
+    } else {
+        // ---------------- MMA issuer (warp 1) ----------------
+        if (warp == 1) {
+            const bool lead = elect_lane();
             const uint32_t idesc_s = make_idesc<0, 128, kTS>();
             const uint32_t idesc_o = idesc_mn(g.dv_pad);
-            const uint32_t ts = tmem_base + (uint32_t)(grp * 128), to = tmem_base + 256u + (uint32_t)(grp * 128);
-            const uint64_t qd = make_sdesc(saddr(sQ) + (QT == 2 ? grp : 0) * g.datoms * 16384u, 128u);
-            auto slot_ready = [&](int i) {
-                const uint32_t ph = (uint32_t)(i / NS) & 1u;
-                return mbar_wait(full + i % NS, ph, p.timeout_ns) && mbar_wait(ready + i % NS, ph, p.timeout_ns);
-            };
-            auto s_product = [&](int t) {
-                if (!slot_ready(2 * t)) return false;
+            const uint64_t q0 = make_sdesc(saddr(sQ), 128u), k0 = make_sdesc(saddr(ring), 128u);
+            const uint64_t v0 = sdesc_mn(saddr(ring), 16384u);
+            const uint32_t slot16 = L.slot >> 4;
+            // S of group grp from the K tile in slot; release: the last product that reads it
+            auto s_product = [&](int grp, int slot, bool release) {
                 tc_fence_after();
-                const uint64_t kd = make_sdesc(saddr(ring + (size_t)(2 * t % NS) * L.slot), 128u);
+                if (lead) {
+                    const uint32_t ts = tmem_base + (uint32_t)(grp * 128);
+                    const uint64_t qd = q0 + (uint64_t)((QT == 2 ? grp : 0) * g.datoms * 1024);
+                    const uint64_t kd = k0 + (uint64_t)(slot * slot16);
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    tc_mma<0>(ts, qd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
-                              kd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
-                tc_commit(saddr(sfull + grp));
-                tc_commit(saddr(empty + 2 * t % NS));
-                return true;
+                    for (int k = 0; k < KS; ++k)
+                        tc_mma<0>(ts, qd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
+                                  kd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
+                    tc_commit(saddr(sfull + grp));
+                    if (release) tc_commit(saddr(empty + slot));
+                }
+                __syncwarp();
             };
-            bool ok = mbar_wait(qfull, 0, p.timeout_ns);
-            tc_fence_after();
-            if (ok && t0 < nt) ok = s_product(t0);
-            int n = 0;
-            for (int t = t0; ok && t < nt; t += step, ++n) {
-                const int i = 2 * t + 1;
-                for (int h = 0; ok && h < 2; ++h) {
-                    if (!mbar_wait(pready + 2 * grp + h, (uint32_t)n & 1u, p.timeout_ns) || (h == 0 && !slot_ready(i)) ||
-                        *abort_flag) {
+            // One group after the other, each its P V products and its next S: the groups then run half a period
+            // apart, one in its softmax while the tensor core works for the other.
+            bool ok = mbar_wait_near(qfull, 0, p.timeout_ns);
+            RingPos kp{0, 0}, vp{1, 0};  // the next K and V tile
+            for (int grp = 0; ok && grp < 2; ++grp) {
+                if ((QT == 2 ? 0 : grp) >= nt) break;
+                ok = mbar_wait_near(ready + kp.slot, kp.phase, p.timeout_ns);
+                if (ok) s_product(grp, kp.slot, QT == 1 || grp == 1);
+                if (QT == 1 || grp == 1) kp.step(2, NS);
+            }
+            for (int u = 0; ok && u < (QT == 2 ? 2 * nt : nt); ++u) {
+                const int grp = u & 1, n = u >> 1;
+                const bool more = (QT == 2 ? n + 1 : u + 2) < nt, last = QT == 1 || grp == 1;
+                const uint32_t ts = tmem_base + (uint32_t)(grp * 128), to = ts + 256u;
+                ok = mbar_wait_near(ready + vp.slot, vp.phase, p.timeout_ns) &&
+                     (!more || mbar_wait_near(ready + kp.slot, kp.phase, p.timeout_ns));
+                const uint64_t vd = v0 + (uint64_t)(vp.slot * slot16);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!ok || !mbar_wait_near(pready + 2 * grp + h, (uint32_t)n & 1u, p.timeout_ns) || *abort_flag) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t vd = sdesc_mn(saddr(ring + (size_t)(i % NS) * L.slot), 16384u);
+                    if (lead) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)  // 16 keys: 8 TMEM columns of P, 2048 bytes of V
-                        tc_mma_ts(to, ts + 32u * h + 8u * k, vd + (4 * h + k) * 128u, idesc_o,
-                                  n > 0 || h > 0 || k > 0 ? 1u : 0u);
+                        for (int k = 0; k < 4; ++k)  // 16 keys: 8 TMEM columns of P, 2048 bytes of V
+                            tc_mma_ts(to, ts + 32u * h + 8u * k, vd + (uint64_t)((4 * h + k) * 128), idesc_o,
+                                      n > 0 || h > 0 || k > 0 ? 1u : 0u);
+                        if (h == 1) {
+                            tc_commit(saddr(pvdone + grp));
+                            if (last) tc_commit(saddr(empty + vp.slot));
+                        }
+                    }
+                    __syncwarp();
                 }
                 if (!ok) break;
-                tc_commit(saddr(pvdone + grp));
-                tc_commit(saddr(empty + i % NS));
+                if (last) vp.step(2, NS);
                 // the next S takes the columns of P: not before the products that read it are complete
-                if (t + step < nt) ok = mbar_wait(pvdone + grp, (uint32_t)n & 1u, p.timeout_ns) && s_product(t + step);
+                if (more) {
+                    ok = mbar_wait_near(pvdone + grp, (uint32_t)n & 1u, p.timeout_ns);
+                    if (ok) s_product(grp, kp.slot, last);
+                    if (last) kp.step(2, NS);
+                }
             }
-            if (!ok) {
-                atomicOr(p.err, kDevErrTimeout);
-                *abort_flag = 1;
+            if (lead) {
+                if (!ok) {
+                    atomicOr(p.err, kDevErrTimeout);
+                    *abort_flag = 1;
+                }
+                tc_commit(saddr(drain));
             }
-            tc_commit(saddr(drain + grp));
-            mbar_wait(drain + grp, 0, p.timeout_ns);
+            __syncwarp();
+            mbar_wait_near(drain, 0, p.timeout_ns);
         }
         __syncwarp();
+    }
     } else {
         // ---------------- softmax groups ----------------
+        regs_inc<208>();
         const int q = warp & 3, grp = (warp - 4) >> 2;
         const int rl = q * 32 + lane;
         const int blk = QT == 2 ? grp : 0;
@@ -270,8 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = 0;
         for (int t = QT == 2 ? 0 : grp; t < nt; t += QT == 2 ? 1 : 2, ++n) {
             const int j = t % kBiasSlots;
-            if (!mbar_wait(sfull + grp, (uint32_t)n & 1u, p.timeout_ns) ||
-                !mbar_wait(bfull + j, (uint32_t)(t / kBiasSlots) & 1u, p.timeout_ns)) {
+            if (!mbar_wait_near(sfull + grp, (uint32_t)n & 1u, p.timeout_ns) ||
+                !mbar_wait_near(bfull + j, (uint32_t)(t / kBiasSlots) & 1u, p.timeout_ns)) {
                 ok = false;
                 break;
             }
@@ -280,11 +311,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t s[128];
                 tmem_ld32(ts + 0u, &s[0]);
                 tmem_ld32(ts + 32u, &s[32]);
-                tmem_ld32(ts + 64u, &s[64]);
-                tmem_ld32(ts + 96u, &s[96]);
                 tmem_ld_wait();
-                float mul = c2;
-                if (tile_masked[j]) {  // scores in base 2 with the bias; otherwise they stay as they are
+                tmem_ld32(ts + 64u, &s[64]);  // the second half arrives under the first one's maximum
+                tmem_ld32(ts + 96u, &s[96]);
+                float mul = c2, top;
+                if (!tile_masked[j]) {
+                    top = max_of64(s);
+                    tmem_ld_wait();
+                    top = fmaxf(top, max_of64(s + 64)) * c2;
+                } else {  // scores in base 2 with the bias
+                    tmem_ld_wait();
                     const float4 *bq = reinterpret_cast<const float4 *>(sBias + j * kTS);
                     const uint64_t cc = pack2(c2, c2);
 #pragma unroll
@@ -302,21 +338,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s[k + 3] = __float_as_uint(z3);
                     }
                     mul = 1.f;
+                    top = fmaxf(max_of64(s), max_of64(s + 64));
                 }
-                float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < 128; k += 8) {
-                    t0 = max3(t0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-                    t1 = max3(t1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
-                    t2 = max3(t2, __uint_as_float(s[k + 4]), __uint_as_float(s[k + 5]));
-                    t3 = max3(t3, __uint_as_float(s[k + 6]), __uint_as_float(s[k + 7]));
-                }
-                const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * mul;
                 const bool grow = top > m + kLazy;  // also the first key that counts (m = -inf)
                 const float mn = grow ? top : m;
                 if (n > 0 && __any_sync(~0u, grow)) {
                     // O and the sum move to the new maximum; the products so far have to be in
-                    if (!mbar_wait(pvdone + grp, (uint32_t)(n - 1) & 1u, p.timeout_ns)) {
+                    if (!mbar_wait_near(pvdone + grp, (uint32_t)(n - 1) & 1u, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -368,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bempty + j);
             if (*abort_flag) break;
         }
-        if (ok && n > 0 && !mbar_wait(pvdone + grp, (uint32_t)(n - 1) & 1u, p.timeout_ns)) ok = false;
+        if (ok && n > 0 && !mbar_wait_near(pvdone + grp, (uint32_t)(n - 1) & 1u, p.timeout_ns)) ok = false;
         if (!ok) {
             atomicOr(p.err, kDevErrTimeout);
             *abort_flag = 1;
