@@ -9,24 +9,29 @@
 //  * QT = 1: one row block, the groups take alternate key tiles into their own
 //    S and O and are joined at the end (few rows; the loads of one tile run
 //    under the softmax of the other).
-// TMEM (512 columns): S_g / P_g in [128 g, 128 g + 128), O_g behind them in
-// [256 + 128 g, ...).  P (bf16) is written over the S it came from and is the
-// A operand of the P V product there; V is its right factor as it lies in
+// TMEM (512 columns): two buffers of 64 keys' scores a group, S_g / P_g in
+// [128 g + 64 h, +64), O_g behind them in [256 + 128 g, ...).  While a group
+// turns one buffer into weights, the products of the other and its next scores
+// run: with one 128-key buffer, softmax, P V and the next S were a chain.
+// P (bf16) is written over the S it came from and is the A operand of the P V
+// product there; V is its right factor as it lies in
 // memory (width contiguous), by the descriptor.
 //
-// The maximum is lazy: weights are taken against the running maximum until a
-// score exceeds it by 2^8, and only then are O and the sum rescaled (by the
-// row's own thread, between two products), so P stays below 2^8, exact to
-// bf16's relative rounding as ever, and most tiles touch O from the tensor
-// core alone.
+// The maximum is lazy: the weights of 64 keys are taken against the running
+// reference as it stands, and only where their sum passes 2^12 (which any score
+// more than 12 above it forces, and infinity or NaN too), or at a row's first
+// key, does the row move to those keys' maximum, O and the sum with it (by the
+// row's own thread, between two products).  P stays below 2^12, exact to bf16's
+// relative rounding as ever, and the common case spends nothing on the maximum
+// and touches O from the tensor core alone.
 //
 // Keys past the length or masked by the bias: one warp reads the bias ahead,
 // and where a tile has such keys it clears their rows of K and V in shared
 // memory before the products read them, so that whatever stood there (NaN
 // included) is a zero score plus -inf and a zero weight times zero.
 //
-// Warps: 0 loads K and V by TMA; 1 allocates TMEM and issues the MMAs; 3 bias
-// and masks; 4..7 and 8..11 are the softmax groups.
+// Warps: 0 loads K and V by TMA; 1 allocates TMEM; 1 and 2 issue the MMAs of
+// groups 0 and 1; 3 bias and masks; 4..7 and 8..11 are the softmax groups.
 #include <cuda.h>
 
 #include "fs_attn_tc.cuh"
@@ -36,10 +41,45 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTS = 128;        // keys of a tile
+constexpr int kTS = 128;        // keys of a loaded tile
+constexpr int kStep = 64;       // keys of a score buffer: two steps a tile
 constexpr int kThreads = 384;
 constexpr int kBiasSlots = 4;
-constexpr float kLazy = 8.f;
+
+// s = s c + bias over 64 scores (base 2)
+__device__ __forceinline__ void add_bias(uint32_t (&s)[64], const float *bias, float c) {
+    const float4 *bq = reinterpret_cast<const float4 *>(bias);
+    const uint64_t cc = pack2(c, c);
+#pragma unroll
+    for (int k = 0; k < 64; k += 4) {
+        const float4 bb = bq[k / 4];
+        float z0, z1, z2, z3;
+        unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, pack2(bb.x, bb.y)), z0, z1);
+        unpack2(fma2(pack2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), cc, pack2(bb.z, bb.w)), z2, z3);
+        s[k] = __float_as_uint(z0);
+        s[k + 1] = __float_as_uint(z1);
+        s[k + 2] = __float_as_uint(z2);
+        s[k + 3] = __float_as_uint(z3);
+    }
+}
+// w = 2^(s mul - ref) as pairs of bf16, and the sum of the unrounded weights
+__device__ __forceinline__ float weights(const uint32_t (&s)[64], float mul, float ref, uint32_t (&w)[32]) {
+    const uint64_t cc = pack2(mul, mul), rn = pack2(-ref, -ref);
+    uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+    for (int k = 0; k < 64; k += 2) {
+        float d0, d1;
+        unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, rn), d0, d1);
+        d0 = ex2_approx(d0);
+        d1 = ex2_approx(d1);
+        acc[(k / 2) & 1] = add2(acc[(k / 2) & 1], pack2(d0, d1));
+        w[k / 2] = bf16x2(d0, d1);
+    }
+    float a0, a1, a2, a3;
+    unpack2(acc[0], a0, a1);
+    unpack2(acc[1], a2, a3);
+    return (a0 + a1) + (a2 + a3);
+}
 
 struct Layout {
     uint32_t q, ring, slot, bias, ml, bars, total;
@@ -52,7 +92,7 @@ __host__ __device__ inline Layout layout(int qt, int datoms, int vatoms, int slo
     L.bias = L.ring + (uint32_t)slots * L.slot;
     L.ml = L.bias + kBiasSlots * kTS * 4;
     L.bars = L.ml + 128 * 8;
-    L.total = L.bars + (3 * slots + 2 * kBiasSlots + 1 + 2 + 4 + 2 + 1) * 8 + 32;
+    L.total = L.bars + (3 * slots + 2 * kBiasSlots + 1 + 4 + 4 + 4 + 2) * 8 + 32;
     return L;
 }
 
@@ -75,11 +115,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *bfull = empty + NS;                                  // [kBiasSlots]
     uint64_t *bempty = bfull + kBiasSlots;                         // [kBiasSlots]
     uint64_t *qfull = bempty + kBiasSlots;
-    uint64_t *sfull = qfull + 1;    // [2]
-    uint64_t *pready = sfull + 2;   // [2][2] P of group g, half h
-    uint64_t *pvdone = pready + 4;  // [2]
-    uint64_t *drain = pvdone + 2;   // every MMA is complete
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *sfull = qfull + 1;    // [2][2] S of group g, buffer h
+    uint64_t *pready = sfull + 4;   // [2][2] P is written over it
+    uint64_t *pvdone = pready + 4;  // [2][2] the products that read P are complete
+    uint64_t *drain = pvdone + 4;   // [2] every MMA of issuer g is complete
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile int *tile_masked = reinterpret_cast<volatile int *>(tmem_holder + 2);  // [kBiasSlots]
 
@@ -96,20 +136,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < NS; ++s) {
             mbar_init(full + s, 1);
             mbar_init(ready + s, 1);
-            mbar_init(empty + s, 1);
+            mbar_init(empty + s, QT);
         }
         for (int s = 0; s < kBiasSlots; ++s) {
             mbar_init(bfull + s, 1);
             mbar_init(bempty + s, 4 * QT);
         }
         mbar_init(qfull, 8);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(sfull + i, 1);
-            mbar_init(pready + 2 * i, 4);
-            mbar_init(pready + 2 * i + 1, 4);
+            mbar_init(pready + i, 4);
             mbar_init(pvdone + i, 1);
         }
         mbar_init(drain, 1);
+        mbar_init(drain + 1, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -198,85 +238,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---------------- MMA issuer (warp 1) ----------------
-        if (warp == 1) {
-            const bool lead = elect_lane();
-            const uint32_t idesc_s = make_idesc<0, 128, kTS>();
-            const uint32_t idesc_o = idesc_mn(g.dv_pad);
-            const uint64_t q0 = make_sdesc(saddr(sQ), 128u), k0 = make_sdesc(saddr(ring), 128u);
-            const uint64_t v0 = sdesc_mn(saddr(ring), 16384u);
-            const uint32_t slot16 = L.slot >> 4;
-            // S of group grp from the K tile in slot; release: the last product that reads it
-            auto s_product = [&](int grp, int slot, bool release) {
-                tc_fence_after();
-                if (lead) {
-                    const uint32_t ts = tmem_base + (uint32_t)(grp * 128);
-                    const uint64_t qd = q0 + (uint64_t)((QT == 2 ? grp : 0) * g.datoms * 1024);
-                    const uint64_t kd = k0 + (uint64_t)(slot * slot16);
-#pragma unroll
-                    for (int k = 0; k < KS; ++k)
-                        tc_mma<0>(ts, qd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
-                                  kd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
-                    tc_commit(saddr(sfull + grp));
-                    if (release) tc_commit(saddr(empty + slot));
-                }
-                __syncwarp();
-            };
-            // One group after the other, each its P V products and its next S: the groups then run half a period
-            // apart, one in its softmax while the tensor core works for the other.
-            bool ok = mbar_wait_near(qfull, 0, p.timeout_ns);
-            RingPos kp{0, 0}, vp{1, 0};  // the next K and V tile
-            for (int grp = 0; ok && grp < 2; ++grp) {
-                if ((QT == 2 ? 0 : grp) >= nt) break;
-                ok = mbar_wait_near(ready + kp.slot, kp.phase, p.timeout_ns);
-                if (ok) s_product(grp, kp.slot, QT == 1 || grp == 1);
-                if (QT == 1 || grp == 1) kp.step(2, NS);
-            }
-            for (int u = 0; ok && u < (QT == 2 ? 2 * nt : nt); ++u) {
-                const int grp = u & 1, n = u >> 1;
-                const bool more = (QT == 2 ? n + 1 : u + 2) < nt, last = QT == 1 || grp == 1;
-                const uint32_t ts = tmem_base + (uint32_t)(grp * 128), to = ts + 256u;
-                ok = mbar_wait_near(ready + vp.slot, vp.phase, p.timeout_ns) &&
-                     (!more || mbar_wait_near(ready + kp.slot, kp.phase, p.timeout_ns));
-                const uint64_t vd = v0 + (uint64_t)(vp.slot * slot16);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!ok || !mbar_wait_near(pready + 2 * grp + h, (uint32_t)n & 1u, p.timeout_ns) || *abort_flag) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (lead) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)  // 16 keys: 8 TMEM columns of P, 2048 bytes of V
-                            tc_mma_ts(to, ts + 32u * h + 8u * k, vd + (uint64_t)((4 * h + k) * 128), idesc_o,
-                                      n > 0 || h > 0 || k > 0 ? 1u : 0u);
-                        if (h == 1) {
-                            tc_commit(saddr(pvdone + grp));
-                            if (last) tc_commit(saddr(empty + vp.slot));
-                        }
-                    }
-                    __syncwarp();
-                }
-                if (!ok) break;
-                if (last) vp.step(2, NS);
-                // the next S takes the columns of P: not before the products that read it are complete
-                if (more) {
-                    ok = mbar_wait_near(pvdone + grp, (uint32_t)n & 1u, p.timeout_ns);
-                    if (ok) s_product(grp, kp.slot, last);
-                    if (last) kp.step(2, NS);
-                }
-            }
+        // ---------------- MMA issuers (warps 1 and 2, one a group) ----------------
+        const bool lead = elect_lane();
+        const int grp = warp - 1;
+        const uint32_t idesc_s = make_idesc<0, 128, kStep>();
+        const uint32_t idesc_o = idesc_mn(g.dv_pad);
+        const uint64_t qd = make_sdesc(saddr(sQ) + (QT == 2 ? grp : 0) * g.datoms * 16384u, 128u);
+        const uint64_t k0 = make_sdesc(saddr(ring), 128u), v0 = sdesc_mn(saddr(ring), 16384u);
+        const uint32_t slot16 = L.slot >> 4;
+        const uint32_t ts = tmem_base + (uint32_t)(grp * 128), to = ts + 256u;
+        // this group's tiles: all of them, or those of its parity; two steps a tile
+        const int mine = QT == 2 ? nt : (nt - grp + 1) / 2, steps = 2 * mine;
+        RingPos kp{QT == 2 ? 0 : 2 * grp, 0}, vp{QT == 2 ? 1 : 2 * grp + 1, 0};
+        // S of step i (its tile's half i & 1) into its buffer
+        auto s_product = [&](int i) {
+            const int h = i & 1;
+            if (h == 0 && !mbar_wait_near(ready + kp.slot, kp.phase, p.timeout_ns)) return false;
+            tc_fence_after();
             if (lead) {
-                if (!ok) {
-                    atomicOr(p.err, kDevErrTimeout);
-                    *abort_flag = 1;
-                }
-                tc_commit(saddr(drain));
+                const uint64_t kd = k0 + (uint64_t)(kp.slot * slot16 + h * 512);
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    tc_mma<0>(ts + 64u * h, qd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
+                              kd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
+                tc_commit(saddr(sfull + 2 * grp + h));
+                if (h == 1) tc_commit(saddr(empty + kp.slot));
             }
             __syncwarp();
-            mbar_wait_near(drain, 0, p.timeout_ns);
+            if (h == 1) kp.step(QT == 2 ? 2 : 4, NS);
+            return true;
+        };
+        bool ok = steps == 0 || mbar_wait_near(qfull, 0, p.timeout_ns);
+        if (ok && steps > 0) ok = s_product(0) && s_product(1);
+        for (int i = 0; ok && i < steps; ++i) {
+            const int h = i & 1;
+            const uint32_t ph = (uint32_t)(i >> 1) & 1u;
+            if ((h == 0 && !mbar_wait_near(ready + vp.slot, vp.phase, p.timeout_ns)) ||
+                !mbar_wait_near(pready + 2 * grp + h, ph, p.timeout_ns) || *abort_flag) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (lead) {
+                const uint64_t vd = v0 + (uint64_t)(vp.slot * slot16 + h * 512);
+#pragma unroll
+                for (int k = 0; k < kStep / 16; ++k)  // 16 keys: 8 TMEM columns of P, 2048 bytes of V
+                    tc_mma_ts(to, ts + 64u * h + 8u * k, vd + (uint64_t)(k * 128), idesc_o, i > 0 || k > 0 ? 1u : 0u);
+                tc_commit(saddr(pvdone + 2 * grp + h));
+                if (h == 1) tc_commit(saddr(empty + vp.slot));
+            }
+            __syncwarp();
+            if (h == 1) vp.step(QT == 2 ? 2 : 4, NS);
+            // the S after next takes the columns of this P: not before the products that read it are complete (the
+            // softmax has the other buffer's S meanwhile)
+            if (i + 2 < steps) ok = mbar_wait_near(pvdone + 2 * grp + h, ph, p.timeout_ns) && s_product(i + 2);
         }
+        if (lead) {
+            if (!ok) {
+                atomicOr(p.err, kDevErrTimeout);
+                *abort_flag = 1;
+            }
+            tc_commit(saddr(drain + grp));
+        }
+        __syncwarp();
+        mbar_wait_near(drain + grp, 0, p.timeout_ns);
         __syncwarp();
     }
     } else {
@@ -298,105 +323,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float c2 = p.scale2;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        int n = 0;
-        for (int t = QT == 2 ? 0 : grp; t < nt; t += QT == 2 ? 1 : 2, ++n) {
+        int n = 0;  // tiles of this group done
+        for (int t = QT == 2 ? 0 : grp; ok && t < nt; t += QT == 2 ? 1 : 2, ++n) {
             const int j = t % kBiasSlots;
-            if (!mbar_wait_near(sfull + grp, (uint32_t)n & 1u, p.timeout_ns) ||
-                !mbar_wait_near(bfull + j, (uint32_t)(t / kBiasSlots) & 1u, p.timeout_ns)) {
+            const uint32_t ph = (uint32_t)n & 1u;
+            if (!mbar_wait_near(bfull + j, (uint32_t)(t / kBiasSlots) & 1u, p.timeout_ns)) {
                 ok = false;
                 break;
             }
-            tc_fence_after();
-            if (warp_live) {
-                uint32_t s[128];
-                tmem_ld32(ts + 0u, &s[0]);
-                tmem_ld32(ts + 32u, &s[32]);
-                tmem_ld_wait();
-                tmem_ld32(ts + 64u, &s[64]);  // the second half arrives under the first one's maximum
-                tmem_ld32(ts + 96u, &s[96]);
-                float mul = c2, top;
-                if (!tile_masked[j]) {
-                    top = max_of64(s);
-                    tmem_ld_wait();
-                    top = fmaxf(top, max_of64(s + 64)) * c2;
-                } else {  // scores in base 2 with the bias
-                    tmem_ld_wait();
-                    const float4 *bq = reinterpret_cast<const float4 *>(sBias + j * kTS);
-                    const uint64_t cc = pack2(c2, c2);
-#pragma unroll
-                    for (int k = 0; k < 128; k += 4) {
-                        const float4 bb = bq[k / 4];
-                        float z0, z1, z2, z3;
-                        unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, pack2(bb.x, bb.y)),
-                                z0, z1);
-                        unpack2(fma2(pack2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), cc,
-                                     pack2(bb.z, bb.w)),
-                                z2, z3);
-                        s[k] = __float_as_uint(z0);
-                        s[k + 1] = __float_as_uint(z1);
-                        s[k + 2] = __float_as_uint(z2);
-                        s[k + 3] = __float_as_uint(z3);
-                    }
-                    mul = 1.f;
-                    top = fmaxf(max_of64(s), max_of64(s + 64));
+            const bool masked = tile_masked[j];
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                if (!mbar_wait_near(sfull + 2 * grp + h, ph, p.timeout_ns)) {
+                    ok = false;
+                    break;
                 }
-                const bool grow = top > m + kLazy;  // also the first key that counts (m = -inf)
-                const float mn = grow ? top : m;
-                if (n > 0 && __any_sync(~0u, grow)) {
-                    // O and the sum move to the new maximum; the products so far have to be in
-                    if (!mbar_wait_near(pvdone + grp, (uint32_t)(n - 1) & 1u, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
+                if (warp_live) {
                     tc_fence_after();
-                    const float f = grow && m != -INFINITY ? ex2_approx(m - mn) : (grow ? 0.f : 1.f);
-                    l *= f;
-                    for (int k = 0; k < g.dv_pad; k += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(to + k, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
-                        tmem_st16(to + k, o);
+                    uint32_t s[64], w[32];
+                    tmem_ld32(ts + 64u * h, s);
+                    tmem_ld32(ts + 64u * h + 32u, s + 32);
+                    tmem_ld_wait();
+                    float mul = c2;
+                    if (masked) {  // scores in base 2 with the bias
+                        add_bias(s, sBias + j * kTS + kStep * h, c2);
+                        mul = 1.f;
                     }
-                    tmem_st_wait();
-                }
-                m = mn;
-                const float ref = m == -INFINITY ? 0.f : m;
-                const uint64_t cc = pack2(mul, mul), rn = pack2(-ref, -ref);
-                uint64_t acc[2] = {0ull, 0ull};
+                    float sum = weights(s, mul, m == -INFINITY ? 0.f : m, w);
+                    const bool over = m == -INFINITY || !(sum <= kLazySum);
+                    if (__any_sync(~0u, over)) {
+                        // a first key, or one far above: the rows concerned move to the step's own maximum, O and the
+                        // sum with them, once the products so far are complete
+                        const float mn = over ? fmaxf(m, max_of64(s) * mul) : m;
+                        if (n > 0 || h > 0) {
+                            const uint32_t before = h == 0 ? (uint32_t)(n - 1) & 1u : ph;
+                            if (!mbar_wait_near(pvdone + 2 * grp + (h ^ 1), before, p.timeout_ns)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+                            l *= f;
+                            for (int k = 0; k < g.dv_pad; k += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(to + k, o);
+                                tmem_ld_wait();
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int k = 0; k < 64; k += 2) {
-                        float d0, d1;
-                        unpack2(fma2(pack2(__uint_as_float(s[64 * h + k]), __uint_as_float(s[64 * h + k + 1])), cc, rn),
-                                d0, d1);
-                        d0 = ex2_approx(d0);
-                        d1 = ex2_approx(d1);
-                        acc[(k / 2) & 1] = add2(acc[(k / 2) & 1], pack2(d0, d1));
-                        w[k / 2] = bf16x2(d0, d1);
+                                for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+                                tmem_st16(to + k, o);
+                            }
+                        }
+                        m = mn;
+                        sum = weights(s, mul, m == -INFINITY ? 0.f : m, w);
                     }
-                    tmem_st32(ts + 32u * h, w);
+                    l += sum;
+                    tmem_st32(ts + 64u * h, w);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(pready + 2 * grp + h);
-                }
-                float a0, a1, a2, a3;
-                unpack2(acc[0], a0, a1);
-                unpack2(acc[1], a2, a3);
-                l += (a0 + a1) + (a2 + a3);
-            } else if (lane == 0) {  // no row of this warp exists: its lanes of P may hold anything
-                mbar_arrive(pready + 2 * grp);
-                mbar_arrive(pready + 2 * grp + 1);
+                }  // else no row of this warp exists: its lanes of P may hold anything
+                if (lane == 0) mbar_arrive(pready + 2 * grp + h);
             }
+            if (!ok) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(bempty + j);
             if (*abort_flag) break;
         }
-        if (ok && n > 0 && !mbar_wait_near(pvdone + grp, (uint32_t)(n - 1) & 1u, p.timeout_ns)) ok = false;
+        if (ok && n > 0 && !mbar_wait_near(pvdone + 2 * grp + 1, (uint32_t)(n - 1) & 1u, p.timeout_ns)) ok = false;
         if (!ok) {
             atomicOr(p.err, kDevErrTimeout);
             *abort_flag = 1;
