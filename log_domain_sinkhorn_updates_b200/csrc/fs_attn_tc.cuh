@@ -12,9 +12,22 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// mbar_wait that sleeps: the thread is suspended until the phase completes, or for 50 us a try.  Warps that wait
-// then leave their issue slots to the softmax warp of the same SM quarter.
+// mbar_wait that sleeps: one plain test (a phase that has completed costs no more), then the thread is suspended until
+// the phase completes, or for 50 us a try.  Warps that wait then leave their issue slots to the softmax warp of the
+// same SM quarter.
+__device__ __forceinline__ bool mbar_done(uint64_t *b, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, P;\n\t}"
+        : "=r"(done)
+        : "r"(saddr(b)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
 __device__ __forceinline__ bool mbar_wait_near(uint64_t *b, uint32_t parity, unsigned long long limit_ns) {
+    if (mbar_done(b, parity)) return true;
     unsigned long long t0 = 0;
     while (true) {
         uint32_t done;

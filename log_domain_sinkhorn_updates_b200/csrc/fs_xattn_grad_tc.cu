@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile int *tile_masked = reinterpret_cast<volatile int *>(tmem_holder + 2);  // [kColSlots]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads;
     const int r0 = blockIdx.x * 128;  // first kept row (key, or packed query row)
     const int keys = attn_keys(p, b), rows = p.n * p.group;
@@ -127,16 +127,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     c * g.v_head, b * g.v_batch);
                     }
             }
-            int t = 0;
+            int t = 0, y = 0, h = KEYS ? c * p.group : c;
+            RingPos rp{0, 0};
             for (; ok && t < nt; ++t) {
-                const int s = t % NS;
+                const int s = rp.slot;
                 if (*abort_flag) break;
-                if (t >= NS && !mbar_wait(empty + s, ((uint32_t)(t / NS) & 1u) ^ 1u, p.timeout_ns)) {
+                if (t >= NS && !mbar_wait_near(empty + s, rp.phase ^ 1u, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
-                const int y = (KEYS ? t % head_tiles : t) * kTile;
-                const int h = KEYS ? c * p.group + t / head_tiles : c;
                 const uint32_t dst = saddr(ring + (size_t)s * 2 * L.half);
                 mbar_expect_tx(full + s, 2u * L.half);
                 for (int a = 0; a < kAtoms; ++a) {
@@ -144,13 +143,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_4d(dst + L.half + a * 8192u, &map_s2, saddr(full + s), a * 64, y, h * g.s2_head,
                                 b * g.s2_batch);
                 }
+                rp.step(1, NS);
+                y += kTile;
+                if (KEYS && y >= p.n) {
+                    y = 0;
+                    ++h;
+                }
             }
             if (!ok) {
                 atomicOr(p.err, kDevErrTimeout);
                 *abort_flag = 1;
             }
-            if (KEYS && nt > 0) mbar_wait(stfull, 0, p.timeout_ns);
-            for (int k = max(0, t - NS); k < t; ++k) mbar_wait(full + (k % NS), (uint32_t)(k / NS) & 1u, p.timeout_ns);
+            if (KEYS && nt > 0) mbar_wait_near(stfull, 0, p.timeout_ns);
+            for (int k = max(0, t - NS); k < t; ++k) mbar_wait_near(full + (k % NS), (uint32_t)(k / NS) & 1u, p.timeout_ns);
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -161,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 dead[u] = __ballot_sync(~0u, attn_bias2(p, b, r0 + 32 * u + lane, keys) == -INFINITY);
-            if (!mbar_wait(stfull, 0, p.timeout_ns)) ok = false;
+            if (!mbar_wait_near(stfull, 0, p.timeout_ns)) ok = false;
             if (dead[0] | dead[1] | dead[2] | dead[3]) {
                 clear_rows(st1, 128, kAtoms, dead, lane);
                 clear_rows(st2, 128, kAtoms, dead, lane);
@@ -170,6 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0) mbar_arrive(stready);
         }
+        RingPos rp{0, 0};
+        int i0 = 0, h = c * p.group;  // KEYS: first query and head of the tile
         for (int t = 0; ok && t < nt; ++t) {
             const int j = t % kColSlots;
             float *col = sCols + j * 2 * kTile;
@@ -179,10 +186,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 if (KEYS) {  // -L (base 2) and -D; a row without a key, or past the end, gives P = 0
-                    const int i = (t % head_tiles) * kTile + 32 * u + lane;
+                    const int i = i0 + 32 * u + lane;
                     v0[u] = -INFINITY;
                     if (i < p.n) {
-                        const size_t at = ((size_t)b * p.heads + c * p.group + t / head_tiles) * p.n + i;
+                        const size_t at = ((size_t)b * p.heads + h) * p.n + i;
                         const float l = __ldg(p.lse + at);
                         v0[u] = l == -INFINITY ? -INFINITY : -l * kLog2e;
                         v1[u] = -__ldg(p.dot + at);
@@ -193,7 +200,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     any = any || dead[u];
                 }
             }
-            if (t >= kColSlots && !mbar_wait(cempty + j, ((uint32_t)(t / kColSlots) & 1u) ^ 1u, p.timeout_ns)) ok = false;
+            i0 += kTile;
+            if (KEYS && i0 >= p.n) {
+                i0 = 0;
+                ++h;
+            }
+            if (t >= kColSlots && !mbar_wait_near(cempty + j, ((uint32_t)(t / kColSlots) & 1u) ^ 1u, p.timeout_ns)) ok = false;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 col[32 * u + lane] = v0[u];
@@ -203,8 +215,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(cfull + j);
             if (!KEYS) {
-                const int s = t % NS;
-                if (!mbar_wait(full + s, (uint32_t)(t / NS) & 1u, p.timeout_ns)) ok = false;
+                const int s = rp.slot;
+                if (!mbar_wait_near(full + s, rp.phase, p.timeout_ns)) ok = false;
+                rp.step(1, NS);
                 if (dead[0] | dead[1]) {
                     uint8_t *tile = ring + (size_t)s * 2 * L.half;
                     clear_rows(tile, kTile, kAtoms, dead, lane);
@@ -222,22 +235,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
-        if (lane == 0) {
-            const uint32_t idesc_s = make_idesc<0, 128, kTile>();
-            const uint32_t idesc_1 = idesc_mn(KEYS ? g.dv_pad : g.d_pad), idesc_2 = idesc_mn(g.d_pad);
-            const uint64_t a1 = make_sdesc(saddr(st1), 128u), a2 = make_sdesc(saddr(st2), 128u);
-            bool ok = nt == 0 || mbar_wait(stready, 0, p.timeout_ns);
+        // ---------------- MMA issuer (the warp stays converged: elect_lane) ----------------
+        const bool lead = elect_lane();
+        const uint32_t idesc_s = make_idesc<0, 128, kTile>();
+        const uint32_t idesc_1 = idesc_mn(KEYS ? g.dv_pad : g.d_pad), idesc_2 = idesc_mn(g.d_pad);
+        const uint64_t a1 = make_sdesc(saddr(st1), 128u), a2 = make_sdesc(saddr(st2), 128u);
+        const uint64_t r1 = make_sdesc(saddr(ring), 128u), r2 = make_sdesc(saddr(ring) + L.half, 128u);
+        const uint64_t c1 = sdesc_mn(saddr(ring), 8192u), c2 = sdesc_mn(saddr(ring) + L.half, 8192u);
+        const uint32_t slot16 = 2 * L.half >> 4;
+        bool ok = nt == 0 || mbar_wait_near(stready, 0, p.timeout_ns);
+        RingPos sp{0, 0};  // the next tile's slot for its scores
+        int xs = 0;        // and for its sums
+        // S and dP of tile t into its buffers, once the products that read them last are complete
+        auto scores = [&](int t) {
+            const int u = t & 1;
+            if (t >= 2 && !mbar_wait_near(pfree + u, ((uint32_t)(t >> 1) & 1u) ^ 1u, p.timeout_ns)) return false;
+            if (!mbar_wait_near((KEYS ? full : ready) + sp.slot, sp.phase, p.timeout_ns)) return false;
             tc_fence_after();
-            // S and dP of tile t into its buffers, once the products that read them last are complete
-            auto scores = [&](int t) {
-                const int s = t % NS, u = t & 1;
-                if (t >= 2 && !mbar_wait(pfree + u, ((uint32_t)(t >> 1) & 1u) ^ 1u, p.timeout_ns)) return false;
-                if (!mbar_wait(full + s, (uint32_t)(t / NS) & 1u, p.timeout_ns)) return false;
-                if (!KEYS && !mbar_wait(ready + s, (uint32_t)(t / NS) & 1u, p.timeout_ns)) return false;
-                tc_fence_after();
-                const uint32_t at = saddr(ring + (size_t)s * 2 * L.half);
-                const uint64_t b1 = make_sdesc(at, 128u), b2 = make_sdesc(at + L.half, 128u);
+            if (lead) {
+                const uint64_t b1 = r1 + (uint64_t)(sp.slot * slot16), b2 = r2 + (uint64_t)(sp.slot * slot16);
                 const uint32_t ts = tmem_base + 64u * u;
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
@@ -248,48 +264,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_mma<0>(ts + 128u, a2 + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
                               b2 + (uint64_t)((k / 4) * 512 + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
                 tc_commit(saddr(sfull + u));
-                return true;
-            };
-            // the sums over tile t's streamed rows, once its P and dS are written
-            auto sums = [&](int t, uint32_t first) {
-                const int s = t % NS, u = t & 1;
-                if (!mbar_wait(pready + u, (uint32_t)(t >> 1) & 1u, p.timeout_ns) || *abort_flag) return false;
-                tc_fence_after();
-                const uint32_t at = saddr(ring + (size_t)s * 2 * L.half);
-                const uint64_t m1 = sdesc_mn(at, 8192u), m2 = sdesc_mn(at + L.half, 8192u);
+            }
+            __syncwarp();
+            sp.step(1, NS);
+            return true;
+        };
+        // the sums over tile t's streamed rows, once its P and dS are written
+        auto sums = [&](int t) {
+            const int u = t & 1;
+            if (!mbar_wait_near(pready + u, (uint32_t)(t >> 1) & 1u, p.timeout_ns) || *abort_flag) return false;
+            tc_fence_after();
+            if (lead) {
+                const uint64_t m1 = c1 + (uint64_t)(xs * slot16), m2 = c2 + (uint64_t)(xs * slot16);
                 const uint32_t ts = tmem_base + 64u * u;
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k) {
-                    const uint32_t acc = k > 0 ? 1u : first;
                     if (KEYS)
-                        tc_mma_ts(tmem_base + 256u, ts + 8u * k, m2 + (uint64_t)(k * 128), idesc_1, acc);
+                        tc_mma_ts(tmem_base + 256u, ts + 8u * k, m2 + (uint64_t)(k * 128), idesc_1,
+                                  t > 0 || k > 0 ? 1u : 0u);
                     else
-                        tc_mma_ts(tmem_base + 256u, ts + 128u + 8u * k, m1 + (uint64_t)(k * 128), idesc_1, acc);
+                        tc_mma_ts(tmem_base + 256u, ts + 128u + 8u * k, m1 + (uint64_t)(k * 128), idesc_1,
+                                  t > 0 || k > 0 ? 1u : 0u);
                 }
                 if (KEYS) {
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
                         tc_mma_ts(tmem_base + 384u, ts + 128u + 8u * k, m1 + (uint64_t)(k * 128), idesc_2,
-                                  k > 0 ? 1u : first);
+                                  t > 0 || k > 0 ? 1u : 0u);
                 }
                 tc_commit(saddr(pfree + u));
-                tc_commit(saddr(empty + s));
-                return true;
-            };
-            for (int t = 0; ok && t < nt; t += 2) {
-                ok = scores(t);
-                if (ok && t + 1 < nt) ok = scores(t + 1);
-                if (ok) ok = sums(t, t > 0 ? 1u : 0u);
-                if (ok && t + 1 < nt) ok = sums(t + 1, 1u);
+                tc_commit(saddr(empty + xs));
             }
+            __syncwarp();
+            if (++xs == NS) xs = 0;
+            return true;
+        };
+        for (int t = 0; ok && t < nt; t += 2) {
+            ok = scores(t);
+            if (ok && t + 1 < nt) ok = scores(t + 1);
+            if (ok) ok = sums(t);
+            if (ok && t + 1 < nt) ok = sums(t + 1);
+        }
+        if (lead) {
             if (!ok) {
                 atomicOr(p.err, kDevErrTimeout);
                 *abort_flag = 1;
             }
             tc_commit(saddr(done));
-            mbar_wait(done, 0, p.timeout_ns);
         }
         __syncwarp();
+        mbar_wait_near(done, 0, p.timeout_ns);
     } else if (warp >= 4) {
         // ---------------- P and dS ----------------
         const int q = warp & 3, grp = (warp - 4) >> 2;
@@ -319,8 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = 0;
         for (int t = grp; t < nt; t += 2, ++n) {
             const int j = t % kColSlots;
-            if (!mbar_wait(sfull + grp, (uint32_t)n & 1u, p.timeout_ns) ||
-                !mbar_wait(cfull + j, (uint32_t)(t / kColSlots) & 1u, p.timeout_ns)) {
+            if (!mbar_wait_near(sfull + grp, (uint32_t)n & 1u, p.timeout_ns) ||
+                !mbar_wait_near(cfull + j, (uint32_t)(t / kColSlots) & 1u, p.timeout_ns)) {
                 ok = false;
                 break;
             }
@@ -372,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (*abort_flag) break;
         }
-        if (ok && nt > 0 && !mbar_wait(done, 0, p.timeout_ns)) ok = false;
+        if (ok && nt > 0 && !mbar_wait_near(done, 0, p.timeout_ns)) ok = false;
         if (!ok) {
             atomicOr(p.err, kDevErrTimeout);
             *abort_flag = 1;
