@@ -17,8 +17,8 @@
 // combined pass, in exchange for sums that never leave the SM.
 //
 // TMEM (512 columns): S / P of tile t in [64 (t & 1), +64), dP / dS in [128 + 64 (t & 1), +64),
-// dV or dQ in [256, ...), dK in [384, ...).  Warps: 0 loads by TMA, 1 issues the MMAs and allocates
-// TMEM, 2 statistics, bias and masks, 4..7 and 8..11 turn scores into P and dS for even and odd tiles.
+// dV or dQ in [256, ...), dK in [384, ...).  Warps: 0 loads by TMA, 1 allocates TMEM, 1 and 3 issue the
+// MMAs of the scores and of the sums, 2 statistics, bias and masks, 4..7 and 8..11 turn scores into P and dS for even and odd tiles.
 #include <cuda.h>
 
 #include "fs_attn_tc.cuh"
@@ -42,7 +42,7 @@ __host__ __device__ inline Layout layout(int atoms, int slots) {
     L.half = (uint32_t)atoms * 8192u;
     L.cols = L.ring + (uint32_t)slots * 2u * L.half;
     L.bars = L.cols + kColSlots * 2 * kTile * 4;
-    L.total = L.bars + (3 * slots + 2 * kColSlots + 2 + 2 + 2 + 2 + 1) * 8 + 32;
+    L.total = L.bars + (3 * slots + 2 * kColSlots + 2 + 2 + 2 + 2 + 2) * 8 + 32;
     return L;
 }
 
@@ -69,8 +69,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *sfull = stready + 1;                                 // [2]
     uint64_t *pready = sfull + 2;                                  // [2]
     uint64_t *pfree = pready + 2;                                  // [2]
-    uint64_t *done = pfree + 2;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(done + 1);
+    uint64_t *done = pfree + 2;                                    // every sum is complete
+    uint64_t *sdone = done + 1;                                    // every score is
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sdone + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile int *tile_masked = reinterpret_cast<volatile int *>(tmem_holder + 2);  // [kColSlots]
 
@@ -99,6 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(pfree + i, 1);
         }
         mbar_init(done, 1);
+        mbar_init(sdone, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -234,8 +236,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort_flag = 1;
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ---------------- MMA issuer (the warp stays converged: elect_lane) ----------------
+    } else if (warp < 4) {
+        // ---------------- MMA issuers: warp 1 the scores, warp 3 the sums ----------------
+        // (converged warps: elect_lane; with one warp for both, a tile's scores waited behind the last tile's sums)
         const bool lead = elect_lane();
         const uint32_t idesc_s = make_idesc<0, 128, kTile>();
         const uint32_t idesc_1 = idesc_mn(KEYS ? g.dv_pad : g.d_pad), idesc_2 = idesc_mn(g.d_pad);
@@ -299,22 +302,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (++xs == NS) xs = 0;
             return true;
         };
-        for (int t = 0; ok && t < nt; t += 2) {
-            ok = scores(t);
-            if (ok && t + 1 < nt) ok = scores(t + 1);
-            if (ok) ok = sums(t);
-            if (ok && t + 1 < nt) ok = sums(t + 1);
-        }
+        if (warp == 1)
+            for (int t = 0; ok && t < nt; ++t) ok = scores(t);
+        else
+            for (int t = 0; ok && t < nt; ++t) ok = sums(t);
+        uint64_t *drain = warp == 1 ? sdone : done;
         if (lead) {
             if (!ok) {
                 atomicOr(p.err, kDevErrTimeout);
                 *abort_flag = 1;
             }
-            tc_commit(saddr(done));
+            tc_commit(saddr(drain));
         }
         __syncwarp();
-        mbar_wait_near(done, 0, p.timeout_ns);
-    } else if (warp >= 4) {
+        mbar_wait_near(drain, 0, p.timeout_ns);
+    } else {
         // ---------------- P and dS ----------------
         const int q = warp & 3, grp = (warp - 4) >> 2;
         const int row = r0 + q * 32 + lane;
@@ -351,12 +353,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const float4 *c0 = reinterpret_cast<const float4 *>(sCols + j * 2 * kTile);
             const bool masked = KEYS || tile_masked[j];
+            uint32_t sr[2][32], dr[2][32];
+            tmem_ld32(ts, sr[0]);
+            tmem_ld32(td, dr[0]);
+            tmem_ld_wait();
+            tmem_ld32(ts + 32u, sr[1]);  // the second half arrives under the first one's arithmetic
+            tmem_ld32(td + 32u, dr[1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t s[32], d[32], wp[16], ws[16];
-                tmem_ld32(ts + 32u * h, s);
-                tmem_ld32(td + 32u * h, d);
-                tmem_ld_wait();
+                if (h == 1) tmem_ld_wait();
+                const uint32_t(&s)[32] = sr[h], (&d)[32] = dr[h];
+                uint32_t wp[16], ws[16];
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
                     uint64_t z0 = nl2, z1 = nl2, e0 = nd2, e1 = nd2;
