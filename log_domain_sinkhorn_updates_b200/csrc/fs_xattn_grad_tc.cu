@@ -16,8 +16,7 @@
 // tile under two descriptors.  Seven products instead of the five of one
 // combined pass, in exchange for sums that never leave the SM.
 //
-// TMEM (512 columns): S / P of tile t in [64 (t & 1), +64), dP / dS in [128 + 64 (t & 1), +64),
-// dV or dQ in [256, ...), dK in [384, ...).  Warps: 0 loads by TMA, 1 allocates TMEM, 1 and 3 issue the
+// TMEM (512 columns): two or three buffers of S / P and dP / dS (64 columns each), the sums behind them.  Warps: 0 loads by TMA, 1 allocates TMEM, 1 and 3 issue the
 // MMAs of the scores and of the sums, 2 statistics, bias and masks, 4..7 and 8..11 turn scores into P and dS for even and odd tiles.
 #include <cuda.h>
 
@@ -42,7 +41,7 @@ __host__ __device__ inline Layout layout(int atoms, int slots) {
     L.half = (uint32_t)atoms * 8192u;
     L.cols = L.ring + (uint32_t)slots * 2u * L.half;
     L.bars = L.cols + kColSlots * 2 * kTile * 4;
-    L.total = L.bars + (3 * slots + 2 * kColSlots + 2 + 2 + 2 + 2 + 2) * 8 + 32;
+    L.total = L.bars + (3 * slots + 2 * kColSlots + 2 + 3 + 3 + 3 + 2) * 8 + 32;
     return L;
 }
 
@@ -55,6 +54,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
     constexpr int kAtoms = (KS + 3) / 4;
+    // Score buffers, 128 TMEM columns each (S / P, then dP / dS): as many as the sums leave room for.  With three, a
+    // tile's scores wait for the sums of the tile three before it, not for those of its own group's last.
+    constexpr int NB = KEYS && KS > 4 ? 2 : 3;
+    constexpr uint32_t kSum1 = 128u * NB, kSum2 = kSum1 + (KS > 4 ? 128u : 64u);  // KEYS: dV, dK; ROWS: dQ
     const int NS = g.slots;
     const Layout L = layout(kAtoms, NS);
     uint8_t *st1 = smem, *st2 = smem + L.st2, *ring = smem + L.ring;
@@ -66,10 +69,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *cempty = cfull + kColSlots;                          // [kColSlots]
     uint64_t *stfull = cempty + kColSlots;                         // kept side loaded
     uint64_t *stready = stfull + 1;                                // kept side usable
-    uint64_t *sfull = stready + 1;                                 // [2]
-    uint64_t *pready = sfull + 2;                                  // [2]
-    uint64_t *pfree = pready + 2;                                  // [2]
-    uint64_t *done = pfree + 2;                                    // every sum is complete
+    uint64_t *sfull = stready + 1;                                 // [3]
+    uint64_t *pready = sfull + 3;                                  // [3]
+    uint64_t *pfree = pready + 3;                                  // [3]
+    uint64_t *done = pfree + 3;                                    // every sum is complete
     uint64_t *sdone = done + 1;                                    // every score is
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sdone + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -94,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(stfull, 1);
         mbar_init(stready, KEYS ? 1 : 8);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(sfull + i, 1);
             mbar_init(pready + i, 4);
             mbar_init(pfree + i, 1);
@@ -247,59 +250,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t c1 = sdesc_mn(saddr(ring), 8192u), c2 = sdesc_mn(saddr(ring) + L.half, 8192u);
         const uint32_t slot16 = 2 * L.half >> 4;
         bool ok = nt == 0 || mbar_wait_near(stready, 0, p.timeout_ns);
-        RingPos sp{0, 0};  // the next tile's slot for its scores
-        int xs = 0;        // and for its sums
+        RingPos sp{0, 0}, bp{0, 0};  // the next tile's slot and buffer (each warp counts its own)
         // S and dP of tile t into its buffers, once the products that read them last are complete
         auto scores = [&](int t) {
-            const int u = t & 1;
-            if (t >= 2 && !mbar_wait_near(pfree + u, ((uint32_t)(t >> 1) & 1u) ^ 1u, p.timeout_ns)) return false;
+            const int u = bp.slot;
+            if (t >= NB && !mbar_wait_near(pfree + u, bp.phase ^ 1u, p.timeout_ns)) return false;
             if (!mbar_wait_near((KEYS ? full : ready) + sp.slot, sp.phase, p.timeout_ns)) return false;
             tc_fence_after();
             if (lead) {
                 const uint64_t b1 = r1 + (uint64_t)(sp.slot * slot16), b2 = r2 + (uint64_t)(sp.slot * slot16);
-                const uint32_t ts = tmem_base + 64u * u;
+                const uint32_t ts = tmem_base + 128u * u;
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
                     tc_mma<0>(ts, a1 + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
                               b1 + (uint64_t)((k / 4) * 512 + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
-                    tc_mma<0>(ts + 128u, a2 + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
+                    tc_mma<0>(ts + 64u, a2 + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
                               b2 + (uint64_t)((k / 4) * 512 + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
                 tc_commit(saddr(sfull + u));
             }
             __syncwarp();
             sp.step(1, NS);
+            bp.step(1, NB);
             return true;
         };
         // the sums over tile t's streamed rows, once its P and dS are written
         auto sums = [&](int t) {
-            const int u = t & 1;
-            if (!mbar_wait_near(pready + u, (uint32_t)(t >> 1) & 1u, p.timeout_ns) || *abort_flag) return false;
+            const int u = bp.slot, xs = sp.slot;
+            if (!mbar_wait_near(pready + u, bp.phase, p.timeout_ns) || *abort_flag) return false;
             tc_fence_after();
             if (lead) {
                 const uint64_t m1 = c1 + (uint64_t)(xs * slot16), m2 = c2 + (uint64_t)(xs * slot16);
-                const uint32_t ts = tmem_base + 64u * u;
+                const uint32_t ts = tmem_base + 128u * u;
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k) {
                     if (KEYS)
-                        tc_mma_ts(tmem_base + 256u, ts + 8u * k, m2 + (uint64_t)(k * 128), idesc_1,
+                        tc_mma_ts(tmem_base + kSum1, ts + 8u * k, m2 + (uint64_t)(k * 128), idesc_1,
                                   t > 0 || k > 0 ? 1u : 0u);
                     else
-                        tc_mma_ts(tmem_base + 256u, ts + 128u + 8u * k, m1 + (uint64_t)(k * 128), idesc_1,
+                        tc_mma_ts(tmem_base + kSum1, ts + 64u + 8u * k, m1 + (uint64_t)(k * 128), idesc_1,
                                   t > 0 || k > 0 ? 1u : 0u);
                 }
                 if (KEYS) {
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        tc_mma_ts(tmem_base + 384u, ts + 128u + 8u * k, m1 + (uint64_t)(k * 128), idesc_2,
+                        tc_mma_ts(tmem_base + kSum2, ts + 64u + 8u * k, m1 + (uint64_t)(k * 128), idesc_2,
                                   t > 0 || k > 0 ? 1u : 0u);
                 }
                 tc_commit(saddr(pfree + u));
                 tc_commit(saddr(empty + xs));
             }
             __syncwarp();
-            if (++xs == NS) xs = 0;
+            sp.step(1, NS);
+            bp.step(1, NB);
             return true;
         };
         if (warp == 1)
@@ -339,13 +343,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
-        const uint32_t ts = tmem_base + lanes + (uint32_t)(grp * 64), td = ts + 128u;
+        RingPos bp{grp, 0};  // this group's next buffer
         const uint64_t cc = pack2(p.scale2, p.scale2), nl2 = pack2(nl, nl), nd2 = pack2(nd, nd);
         bool ok = true;
-        int n = 0;
-        for (int t = grp; t < nt; t += 2, ++n) {
-            const int j = t % kColSlots;
-            if (!mbar_wait_near(sfull + grp, (uint32_t)n & 1u, p.timeout_ns) ||
+        for (int t = grp; t < nt; t += 2) {
+            const int j = t % kColSlots, u = bp.slot;
+            const uint32_t ts = tmem_base + lanes + 128u * u, td = ts + 64u;
+            if (!mbar_wait_near(sfull + u, bp.phase, p.timeout_ns) ||
                 !mbar_wait_near(cfull + j, (uint32_t)(t / kColSlots) & 1u, p.timeout_ns)) {
                 ok = false;
                 break;
@@ -398,9 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(pready + grp);
+                mbar_arrive(pready + u);
                 mbar_arrive(cempty + j);
             }
+            bp.step(2, NB);
             if (*abort_flag) break;
         }
         if (ok && nt > 0 && !mbar_wait_near(done, 0, p.timeout_ns)) ok = false;
@@ -424,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst = (__nv_bfloat16 *)p.dq + p.dqs.batch * b + p.dqs.token * (row / p.group) +
                   p.dqs.head * (c * p.group + row % p.group);
         }
-        const uint32_t to = tmem_base + lanes + (second ? 384u : 256u);
+        const uint32_t to = tmem_base + lanes + (second ? kSum2 : kSum1);
         for (int k = KEYS ? 0 : 32 * grp; k < width; k += KEYS ? 32 : 64) {
             uint32_t o[32];
             if (nt > 0) {
