@@ -23,7 +23,7 @@ SOURCES = ["fs_api.cu", "fs_prep.cu", "fs_lse_tc.cu", "fs_lse_tc2.cu", "fs_lse_s
            "fs_apply_tc2.cu", "fs_apply_tc_q2.cu", "fs_hvp_tc.cu",
            "fs_hvp.cu", "fs_cosine.cu", "fs_selftest.cu", "fs_noalloc.cu", "fs_ops_api.cu", "fs_xattn.cu", "fs_xattn_tc.cu", "fs_xattn_grad_tc.cu", "fs_xent.cu", "fs_xent_tc.cu"]
 HEADERS = ["fs_internal.cuh", "fs_finish.cuh", "fs_prep.cuh", "fs_tc_common.cuh", "fs_ops.cuh",
-           "fs_attn_tc.cuh"]
+           "fs_ops_tc.cuh"]
 
 FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",

@@ -1,4 +1,4 @@
-// Device helpers shared by the tensor-core cross-attention kernels.
+// Device helpers shared by the tensor-core kernels of the row-softmax operators.
 #pragma once
 
 #include "fs_ops.cuh"

@@ -20,7 +20,7 @@
 // MMAs of the scores and of the sums, 2 statistics, bias and masks, 4..7 and 8..11 turn scores into P and dS for even and odd tiles.
 #include <cuda.h>
 
-#include "fs_attn_tc.cuh"
+#include "fs_ops_tc.cuh"
 
 namespace fs {
 namespace {

@@ -34,7 +34,7 @@
 // groups 0 and 1; 3 bias and masks; 4..7 and 8..11 are the softmax groups.
 #include <cuda.h>
 
-#include "fs_attn_tc.cuh"
+#include "fs_ops_tc.cuh"
 
 namespace fs {
 namespace {

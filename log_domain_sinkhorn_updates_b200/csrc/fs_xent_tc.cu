@@ -23,8 +23,7 @@
 // out of TMEM, so an epilogue has two tiles' time before the MMAs wait for it.
 #include <cuda.h>
 
-#include "fs_ops.cuh"
-#include "fs_tc_common.cuh"
+#include "fs_ops_tc.cuh"
 
 namespace fs {
 namespace {
@@ -46,17 +45,6 @@ enum { kLse = 0, kDl = 1, kAcc = 2, kOut = 3 };
 __device__ __forceinline__ int plane_a(int s) { return 0x049 >> (2 * s) & 3; }
 __device__ __forceinline__ int plane_b(int s) { return 0x121 >> (2 * s) & 3; }
 
-// M or N axis contiguous, 128-byte swizzle: 64-element columns of `krows` rows of K, 8192 bytes
-// apart; groups of 8 rows of K 1024 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr) {
-    uint64_t desc = (uint64_t)((addr >> 4) & 0x3FFFu);
-    desc |= (uint64_t)(8192u >> 4) << 16;
-    desc |= (uint64_t)(1024u >> 4) << 32;
-    desc |= (uint64_t)1u << 46;
-    desc |= 2ull << 61;
-    return desc;
-}
-
 __device__ __forceinline__ void st_v8(void *p, const uint32_t *r) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -68,12 +56,6 @@ __device__ __forceinline__ void ld_v8(const void *p, uint32_t *r) {
                  : "l"(p)
                  : "memory");
 }
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 struct Tile {
     int m0, n0, k0, kb, part;  // first row and column, first K element, K blocks of a plane pair, part
 };
@@ -116,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(drain + 2);
 
     const uint32_t rank = cluster_rank();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int tiles = g.mt * g.nt * g.parts;
 
@@ -149,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             bool ok = true;
             int i = 0;  // stages filled so far
+            RingPos rp{0, 0};
             for (int t = pair; ok && t < tiles; t += pairs) {
                 const Tile T = tile_of(g, t);
                 const int ra = T.m0 + (int)rank * 128, rb = T.n0 + (int)rank * 128;
@@ -159,9 +142,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         kb = 0;
                         ++seg;
                     }
-                    const int s = i % kStages, k = T.k0 + kb * kBK;
+                    const int s = rp.slot, k = T.k0 + kb * kBK;
                     const int xa = F32 ? plane_a(seg) * g.a_plane : 0, xb = F32 ? plane_b(seg) * g.b_plane : 0;
-                    if (i >= kStages && !mbar_wait(empty + s, ((uint32_t)(i / kStages) & 1u) ^ 1u, p.timeout_ns)) {
+                    if (i >= kStages && !mbar_wait_near(empty + s, rp.phase ^ 1u, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
@@ -180,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         tma_load_2d_pair(b, &map_b, bar, xb + k, rb);
                     }
+                    rp.step(1, kStages);
                 }
             }
             if (!ok) {
@@ -189,43 +173,55 @@ __global__ void __launch_bounds__(kThreads, 1)
             // never leave with copies in flight: both CTAs' copies count on the first one's barriers
             if (rank == 0)
                 for (int j = max(0, i - kStages); j < i; ++j)
-                    mbar_wait(full + (j % kStages), (uint32_t)(j / kStages) & 1u, p.timeout_ns);
+                    mbar_wait_near(full + (j % kStages), (uint32_t)(j / kStages) & 1u, p.timeout_ns);
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {  // the warp stays converged: elect_lane
+            const bool lead = elect_lane();
             const uint32_t idesc = make_idesc<0, 256, 256>() | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
             constexpr uint32_t ka = A_MN ? 128u : 2u, kb16 = B_MN ? 128u : 2u;  // 16 of K, in 16-byte units
+            const uint32_t base = saddr(smem);
+            const uint64_t a0 = A_MN ? sdesc_mn(base, 8192u) : make_sdesc(base, 128u);
+            const uint64_t b0 = B_MN ? sdesc_mn(base + kOperand, 8192u) : make_sdesc(base + kOperand, 128u);
             bool ok = true;
-            int i = 0, n = 0;
+            RingPos rp{0, 0};
+            int n = 0;
             for (int t = pair; ok && t < tiles; t += pairs, ++n) {
-                const Tile T = tile_of(g, t);
+                const int blocks = tile_of(g, t).kb * g.segments;
                 const int b = n & 1;
                 if (n >= 2 && !mbar_wait_cluster(sempty + b, ((uint32_t)(n >> 1) & 1u) ^ 1u, p.timeout_ns)) ok = false;
                 const uint32_t dt = tmem_base + (uint32_t)(b * 256);
-                for (int kb = 0; ok && kb < T.kb * g.segments; ++kb, ++i) {
-                    const int s = i % kStages;
-                    if (!mbar_wait(full + s, (uint32_t)(i / kStages) & 1u, p.timeout_ns) || *abort_flag) {
+                for (int kb = 0; ok && kb < blocks; ++kb) {
+                    if (!mbar_wait_near(full + rp.slot, rp.phase, p.timeout_ns) || *abort_flag) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a = saddr(smem + s * kStageBytes);
-                    const uint64_t ad = A_MN ? sdesc_mn(a) : make_sdesc(a, 128u);
-                    const uint64_t bd = B_MN ? sdesc_mn(a + kOperand) : make_sdesc(a + kOperand, 128u);
+                    if (lead) {
+                        const uint64_t ad = a0 + (uint64_t)(rp.slot * (kStageBytes >> 4));
+                        const uint64_t bd = b0 + (uint64_t)(rp.slot * (kStageBytes >> 4));
 #pragma unroll
-                    for (int k = 0; k < kBK / 16; ++k)
-                        tc_mma_pair<0>(dt, ad + k * ka, bd + k * kb16, idesc, kb > 0 || k > 0 ? 1u : 0u);
-                    tc_commit_pair(saddr(empty + s), (uint16_t)3);
+                        for (int k = 0; k < kBK / 16; ++k)
+                            tc_mma_pair<0>(dt, ad + (uint64_t)(k * ka), bd + (uint64_t)(k * kb16), idesc,
+                                           kb > 0 || k > 0 ? 1u : 0u);
+                        tc_commit_pair(saddr(empty + rp.slot), (uint16_t)3);
+                        if (kb == blocks - 1) tc_commit_pair(saddr(sfull + b), (uint16_t)3);
+                    }
+                    __syncwarp();
+                    rp.step(1, kStages);
                 }
-                if (ok) tc_commit_pair(saddr(sfull + b), (uint16_t)3);
+                if (ok && blocks == 0 && lead) tc_commit_pair(saddr(sfull + b), (uint16_t)3);
             }
-            if (!ok) {
-                atomicOr(p.err, kDevErrTimeout);
-                *abort_flag = 1;
+            if (lead) {
+                if (!ok) {
+                    atomicOr(p.err, kDevErrTimeout);
+                    *abort_flag = 1;
+                }
+                tc_commit_pair(saddr(drain), (uint16_t)1);
             }
-            tc_commit_pair(saddr(drain), (uint16_t)1);
-            mbar_wait(drain, 0, p.timeout_ns);
+            __syncwarp();
+            mbar_wait_near(drain, 0, p.timeout_ns);
         }
         __syncwarp();
     } else {
@@ -255,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (ign) target = -1;
                 }
             }
-            if (!mbar_wait(sfull + grp, (uint32_t)(n >> 1) & 1u, p.timeout_ns)) {
+            if (!mbar_wait_near(sfull + grp, (uint32_t)(n >> 1) & 1u, p.timeout_ns)) {
                 ok = false;
                 break;
             }
