@@ -115,6 +115,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    // Few rows: only those of A are loaded (a box of zeros costs more than rows that exist: 145 us against 128 for one
+    // row and 256 at 262144 classes of 1024), over zeros that stay.
+    const int a_rows = A_MN ? 128 : g.a_rows;
+    if (!A_MN && a_rows < 128)
+        for (int e = threadIdx.x; e < kStages * kOperand / 16; e += kThreads)
+            *reinterpret_cast<uint4 *>(smem + e / (kOperand / 16) * kStageBytes + e % (kOperand / 16) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+    fence_async();
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_holder)),
                      "r"(512u)
@@ -135,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = pair; ok && t < tiles; t += pairs) {
                 const Tile T = tile_of(g, t);
                 const int ra = T.m0 + (int)rank * 128, rb = T.n0 + (int)rank * 128;
+                const bool second = a_rows == 128;  // the second CTA has rows to load
                 if (*abort_flag) break;
                 int seg = 0, kb = -1;
                 for (int u = 0; u < T.kb * g.segments; ++u, ++i) {
@@ -148,13 +157,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    if (rank == 0) mbar_expect_tx(full + s, 2u * kStageBytes);
+                    if (rank == 0)
+                        mbar_expect_tx(full + s, 2u * kOperand + (second ? 2u * kOperand : (uint32_t)a_rows * 128u));
                     const uint32_t bar = cluster_addr(saddr(full + s), 0);
                     const uint32_t a = saddr(smem + s * kStageBytes), b = a + kOperand;
                     if (A_MN) {
                         tma_load_2d_pair(a, &map_a, bar, xa + ra, k);
                         tma_load_2d_pair(a + 8192u, &map_a, bar, xa + ra + 64, k);
-                    } else {
+                    } else if (rank == 0 || second) {
                         tma_load_2d_pair(a, &map_a, bar, xa + k, ra);
                     }
                     if (B_MN) {
@@ -257,6 +267,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             float mx = -INFINITY, l = 0.f;
+            if (T.m0 + (int)rank * 128 + q * 32 >= g.M) {  // none of the warp's rows exists
+                if (lane == 0) mbar_arrive_cluster(sempty0);
+                continue;
+            }
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 const int c0 = T.n0 + 128 * half;  // first column of the half
@@ -429,6 +443,9 @@ cudaError_t launch(const XentParams &p, const XentGemm &g, const CUtensorMap &a,
 
 int up(int a, int b) { return (a + b - 1) / b; }
 
+// Rows of a box of A.
+int box_rows(int rows) { return rows < 128 ? up(rows, 8) * 8 : 128; }
+
 XentGemm shape(const XentParams &p, int M, int N, int K, int parts, int pairs) {
     XentGemm g{};
     g.M = M;
@@ -440,6 +457,7 @@ XentGemm shape(const XentParams &p, int M, int N, int K, int parts, int pairs) {
     g.k_part = parts > 1 ? up(up(K, parts), kBK) * kBK : up(K, kBK) * kBK;
     g.segments = p.planes == 3 ? 6 : 1;
     g.pairs = pairs;
+    g.a_rows = box_rows(M);
     return g;
 }
 
@@ -478,7 +496,7 @@ bool xent_tc_rows(const void *p, long long ld, int rows) {
 
 cudaError_t launch_xent_lse(const XentParams &p, int pairs, cudaStream_t s) {
     CUtensorMap a, b;
-    if (!encode_x(&a, p, 128) || !encode_w(&b, p, 128)) return cudaErrorInvalidValue;
+    if (!encode_x(&a, p, box_rows(p.n)) || !encode_w(&b, p, 128)) return cudaErrorInvalidValue;
     XentGemm g = shape(p, p.n, p.c1 - p.c0, p.d, 1, pairs);
     g.a_plane = p.plane_x;
     g.b_plane = p.plane_w;
@@ -486,7 +504,7 @@ cudaError_t launch_xent_lse(const XentParams &p, int pairs, cudaStream_t s) {
 }
 cudaError_t launch_xent_dl(const XentParams &p, int pairs, cudaStream_t s) {
     CUtensorMap a, b;
-    if (!encode_x(&a, p, 128) || !encode_w(&b, p, 128)) return cudaErrorInvalidValue;
+    if (!encode_x(&a, p, box_rows(p.n)) || !encode_w(&b, p, 128)) return cudaErrorInvalidValue;
     XentGemm g = shape(p, p.n, p.c1 - p.c0, p.d, 1, pairs);
     g.a_plane = p.plane_x;
     g.b_plane = p.plane_w;
@@ -495,7 +513,7 @@ cudaError_t launch_xent_dl(const XentParams &p, int pairs, cudaStream_t s) {
 // dx (direct: the whole of it, written in its type; otherwise partial sums in acc)
 cudaError_t launch_xent_dx(const XentParams &p, bool direct, int pairs, cudaStream_t s) {
     CUtensorMap a, b;
-    if (!encode_dl(&a, p, 128) || !encode_w(&b, p, 64)) return cudaErrorInvalidValue;
+    if (!encode_dl(&a, p, box_rows(p.n)) || !encode_w(&b, p, 64)) return cudaErrorInvalidValue;
     XentGemm g = shape(p, p.n, p.d, p.c1 - p.c0, p.parts, pairs);
     g.a_plane = (int)p.ld_dl;
     g.b_plane = p.plane_w;
