@@ -51,29 +51,42 @@ __global__ void __launch_bounds__(256) xent_pack_kernel(const T *src, long long 
     }
 }
 
-// Joins the column tiles of a row in order, and writes lse and loss.  `per`
-// threads take a row (a power of two up to 32): one where there are many rows,
-// a warp where there are few.
+// The online states (max, sum) of two disjoint parts of a row, joined.
+__device__ __forceinline__ void join(float &mx, float &l, float m2, float l2) {
+    const float mn = fmaxf(mx, m2), ref = mn == -INFINITY ? 0.f : mn;
+    l = l * exp2f(mx - ref) + l2 * exp2f(m2 - ref);
+    mx = mn;
+}
+
+// Joins the column tiles of a row and writes lse and loss.  `per` threads of a
+// warp take a row (a power of two), or the whole block takes one (per = 256):
+// few rows have many tiles each and nothing else to run beside them.  The order
+// of the sum depends on the sizes alone.
 __global__ void __launch_bounds__(256) xent_finish_kernel(const XentParams p, int tiles, int per) {
     const long long g = (long long)blockIdx.x * 256 + threadIdx.x;
     const int sub = (int)(g % per);
     const long long i = g / per;
     const bool live = i < p.n;
-    // the row's partial (max, sum) pairs: per neighbouring lanes take every per-th tile
+    grid_dependency_wait();
     float mx = -INFINITY, l = 0.f;
-    for (int t = sub; live && t < tiles; t += per) {
-        const float2 v = p.part[(size_t)t * p.n + i];
-        const float mn = fmaxf(mx, v.x);
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        l = l * exp2f(mx - ref) + v.y * exp2f(v.x - ref);
-        mx = mn;
+    for (int t0 = sub; live && t0 < tiles; t0 += 4 * per) {
+        float2 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            v[u] = t0 + u * per < tiles ? p.part[(size_t)(t0 + u * per) * p.n + i] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) join(mx, l, v[u].x, v[u].y);
     }
-    for (int s = per / 2; s; s >>= 1) {
-        const float m2 = __shfl_xor_sync(~0u, mx, s), l2 = __shfl_xor_sync(~0u, l, s);
-        const float mn = fmaxf(mx, m2), ref = mn == -INFINITY ? 0.f : mn;
-        const float la = l * exp2f(mx - ref), lb = l2 * exp2f(m2 - ref);
-        l = (sub & s) ? lb + la : la + lb;  // the same order on both lanes
-        mx = mn;
+    for (int s = min(per, 32) / 2; s; s >>= 1) {
+        const float m2 = __shfl_down_sync(~0u, mx, s, 32), l2 = __shfl_down_sync(~0u, l, s, 32);
+        join(mx, l, m2, l2);
+    }
+    if (per == 256) {
+        __shared__ float2 warps[8];
+        if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = make_float2(mx, l);
+        __syncthreads();
+        if (sub == 0)
+            for (int w = 1; w < 8; ++w) join(mx, l, warps[w].x, warps[w].y);
     }
     if (!live || sub) return;
     // no sum at all: every logit was NaN
@@ -109,11 +122,11 @@ cudaError_t launch_xent_pack(const void *src, long long ld, int rows, int d, int
     return cudaGetLastError();
 }
 cudaError_t launch_xent_finish(const XentParams &p, int tiles, cudaStream_t s) {
-    int per = 1;
-    while (per < 32 && (long long)p.n * per < 1 << 15) per *= 2;
+    int per = 256;
+    if (p.n > 512)
+        for (per = 32; per > 1 && (long long)p.n * per > 1 << 16;) per /= 2;
     const long long threads = (long long)p.n * per;
-    xent_finish_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(p, tiles, per);
-    return cudaGetLastError();
+    return launch_dependent(xent_finish_kernel, dim3((unsigned)((threads + 255) / 256)), 256, 0, s, p, tiles, per);
 }
 cudaError_t launch_xent_reduce(const XentParams &p, bool bf16, cudaStream_t s) {
     const size_t all = (size_t)p.n * p.d, blocks = (all + 255) / 256;
