@@ -41,8 +41,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTS = 128;        // keys of a loaded tile
-constexpr int kStep = 64;       // keys of a score buffer: two steps a tile
+constexpr int kStep = 64;       // keys of a score buffer
 constexpr int kThreads = 384;
 constexpr int kBiasSlots = 4;
 
@@ -84,13 +83,17 @@ __device__ __forceinline__ float weights(const uint32_t (&s)[64], float mul, flo
 struct Layout {
     uint32_t q, ring, slot, bias, ml, bars, total;
 };
+// Keys of a loaded tile: two steps where both groups read it, one where each tile is one group's (what a group works
+// on stays in the ring, and with 128 keys only a fifth of it was left for loads in flight: 111 us for 131072 keys
+// of 8 heads).
+__host__ __device__ constexpr int tile_keys(int qt) { return qt == 2 ? 128 : 64; }
 __host__ __device__ inline Layout layout(int qt, int datoms, int vatoms, int slots) {
     Layout L;
     L.q = 0;
     L.ring = L.q + (uint32_t)qt * datoms * 16384u;
-    L.slot = (uint32_t)(datoms > vatoms ? datoms : vatoms) * 16384u;
+    L.slot = (uint32_t)((datoms > vatoms ? datoms : vatoms) * tile_keys(qt) * 128);
     L.bias = L.ring + (uint32_t)slots * L.slot;
-    L.ml = L.bias + kBiasSlots * kTS * 4;
+    L.ml = L.bias + (uint32_t)(kBiasSlots * tile_keys(qt) * 4);
     L.bars = L.ml + 128 * 8;
     L.total = L.bars + (3 * slots + 2 * kBiasSlots + 1 + 4 + 4 + 4 + 2) * 8 + 32;
     return L;
@@ -104,6 +107,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const AttnParams p, const AttnTc g) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+    constexpr int kTS = tile_keys(QT), kSteps = kTS / kStep;
+    constexpr uint32_t kAtom = kTS * 128;  // bytes of a tile's 64-element column
     const int NS = g.slots;
     const Layout L = layout(QT, g.datoms, g.vatoms, NS);
     uint8_t *sQ = smem + L.q, *ring = smem + L.ring;
@@ -183,9 +188,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const CUtensorMap *map = i & 1 ? &map_v : &map_k;
                 const int hm = i & 1 ? g.v_head : g.k_head, bm = i & 1 ? g.v_batch : g.k_batch;
                 const uint32_t dst = saddr(ring + (size_t)s * L.slot);
-                mbar_expect_tx(full + s, (uint32_t)atoms * 16384u);
+                mbar_expect_tx(full + s, (uint32_t)atoms * kAtom);
                 for (int a = 0; a < atoms; ++a)
-                    tma_load_4d(dst + a * 16384u, map, saddr(full + s), a * 64, j_beg + (i >> 1) * kTS, c * hm, b * bm);
+                    tma_load_4d(dst + a * kAtom, map, saddr(full + s), a * 64, j_beg + (i >> 1) * kTS, c * hm, b * bm);
                 rp.step(1, NS);
             }
             if (!ok) {
@@ -201,28 +206,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         RingPos rp{0, 0};
         for (int t = 0; ok && t < nt; ++t) {
             const int j = t % kBiasSlots;
-            float bv[4];
-            unsigned dead[4];
+            float bv[kTS / 32];
+            unsigned dead[kTS / 32], cleared = 0;
             bool any = p.bias != nullptr;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kTS / 32; ++u) {
                 bv[u] = attn_bias2(p, b, j_beg + t * kTS + 32 * u + lane, j_end);
                 dead[u] = __ballot_sync(~0u, bv[u] == -INFINITY);
-                any = any || dead[u];
+                cleared |= dead[u];
             }
+            any = any || cleared;
             if (t >= kBiasSlots && !mbar_wait_near(bempty + j, ((uint32_t)(t / kBiasSlots) & 1u) ^ 1u, p.timeout_ns))
                 ok = false;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) sBias[j * kTS + 32 * u + lane] = bv[u];
+            for (int u = 0; u < kTS / 32; ++u) sBias[j * kTS + 32 * u + lane] = bv[u];
             if (lane == 0) tile_masked[j] = any;
             __syncwarp();
             if (lane == 0) mbar_arrive(bfull + j);
-            const bool clear = dead[0] | dead[1] | dead[2] | dead[3];
             for (int kv = 0; kv < 2; ++kv) {
                 const int s = rp.slot;
                 if (!mbar_wait_near(full + s, rp.phase, p.timeout_ns)) ok = false;
                 rp.step(1, NS);
-                if (clear) {
+                if (cleared) {
                     uint8_t *tile = ring + (size_t)s * L.slot;
                     clear_rows(tile, kTS, kv ? g.vatoms : g.datoms, dead, lane);
                     fence_async();
@@ -244,37 +249,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc_s = make_idesc<0, 128, kStep>();
         const uint32_t idesc_o = idesc_mn(g.dv_pad);
         const uint64_t qd = make_sdesc(saddr(sQ) + (QT == 2 ? grp : 0) * g.datoms * 16384u, 128u);
-        const uint64_t k0 = make_sdesc(saddr(ring), 128u), v0 = sdesc_mn(saddr(ring), 16384u);
+        const uint64_t k0 = make_sdesc(saddr(ring), 128u), v0 = sdesc_mn(saddr(ring), kAtom);
         const uint32_t slot16 = L.slot >> 4;
         const uint32_t ts = tmem_base + (uint32_t)(grp * 128), to = ts + 256u;
-        // this group's tiles: all of them, or those of its parity; two steps a tile
-        const int mine = QT == 2 ? nt : (nt - grp + 1) / 2, steps = 2 * mine;
+        // this group's tiles: all of them, or those of its parity
+        const int mine = QT == 2 ? nt : (nt - grp + 1) / 2, steps = kSteps * mine;
+        constexpr int kNext = QT == 2 ? 2 : 4;  // slots from a tile of the group to its next
         RingPos kp{QT == 2 ? 0 : 2 * grp, 0}, vp{QT == 2 ? 1 : 2 * grp + 1, 0};
-        // S of step i (its tile's half i & 1) into its buffer
+        // S of step i (part h of its tile) into buffer i & 1
         auto s_product = [&](int i) {
-            const int h = i & 1;
+            const int h = i % kSteps, u = i & 1;
             if (h == 0 && !mbar_wait_near(ready + kp.slot, kp.phase, p.timeout_ns)) return false;
             tc_fence_after();
             if (lead) {
                 const uint64_t kd = k0 + (uint64_t)(kp.slot * slot16 + h * 512);
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
-                    tc_mma<0>(ts + 64u * h, qd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
-                              kd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
-                tc_commit(saddr(sfull + 2 * grp + h));
-                if (h == 1) tc_commit(saddr(empty + kp.slot));
+                    tc_mma<0>(ts + 64u * u, qd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
+                              kd + (uint64_t)((k / 4) * (kAtom / 16) + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
+                tc_commit(saddr(sfull + 2 * grp + u));
+                if (h == kSteps - 1) tc_commit(saddr(empty + kp.slot));
             }
             __syncwarp();
-            if (h == 1) kp.step(QT == 2 ? 2 : 4, NS);
+            if (h == kSteps - 1) kp.step(kNext, NS);
             return true;
         };
         bool ok = steps == 0 || mbar_wait_near(qfull, 0, p.timeout_ns);
-        if (ok && steps > 0) ok = s_product(0) && s_product(1);
+        for (int i = 0; ok && i < min(steps, 2); ++i) ok = s_product(i);
         for (int i = 0; ok && i < steps; ++i) {
-            const int h = i & 1;
+            const int h = i % kSteps, u = i & 1;
             const uint32_t ph = (uint32_t)(i >> 1) & 1u;
             if ((h == 0 && !mbar_wait_near(ready + vp.slot, vp.phase, p.timeout_ns)) ||
-                !mbar_wait_near(pready + 2 * grp + h, ph, p.timeout_ns) || *abort_flag) {
+                !mbar_wait_near(pready + 2 * grp + u, ph, p.timeout_ns) || *abort_flag) {
                 ok = false;
                 break;
             }
@@ -283,15 +289,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t vd = v0 + (uint64_t)(vp.slot * slot16 + h * 512);
 #pragma unroll
                 for (int k = 0; k < kStep / 16; ++k)  // 16 keys: 8 TMEM columns of P, 2048 bytes of V
-                    tc_mma_ts(to, ts + 64u * h + 8u * k, vd + (uint64_t)(k * 128), idesc_o, i > 0 || k > 0 ? 1u : 0u);
-                tc_commit(saddr(pvdone + 2 * grp + h));
-                if (h == 1) tc_commit(saddr(empty + vp.slot));
+                    tc_mma_ts(to, ts + 64u * u + 8u * k, vd + (uint64_t)(k * 128), idesc_o, i > 0 || k > 0 ? 1u : 0u);
+                tc_commit(saddr(pvdone + 2 * grp + u));
+                if (h == kSteps - 1) tc_commit(saddr(empty + vp.slot));
             }
             __syncwarp();
-            if (h == 1) vp.step(QT == 2 ? 2 : 4, NS);
+            if (h == kSteps - 1) vp.step(kNext, NS);
             // the S after next takes the columns of this P: not before the products that read it are complete (the
             // softmax has the other buffer's S meanwhile)
-            if (i + 2 < steps) ok = mbar_wait_near(pvdone + 2 * grp + h, ph, p.timeout_ns) && s_product(i + 2);
+            if (i + 2 < steps) ok = mbar_wait_near(pvdone + 2 * grp + u, ph, p.timeout_ns) && s_product(i + 2);
         }
         if (lead) {
             if (!ok) {
@@ -323,26 +329,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float c2 = p.scale2;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        int n = 0;  // tiles of this group done
-        for (int t = QT == 2 ? 0 : grp; ok && t < nt; t += QT == 2 ? 1 : 2, ++n) {
+        int i = 0;  // steps of this group done
+        for (int t = QT == 2 ? 0 : grp; ok && t < nt; t += QT == 2 ? 1 : 2) {
             const int j = t % kBiasSlots;
-            const uint32_t ph = (uint32_t)n & 1u;
             if (!mbar_wait_near(bfull + j, (uint32_t)(t / kBiasSlots) & 1u, p.timeout_ns)) {
                 ok = false;
                 break;
             }
             const bool masked = tile_masked[j];
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                if (!mbar_wait_near(sfull + 2 * grp + h, ph, p.timeout_ns)) {
+            for (int h = 0; h < kSteps; ++h, ++i) {
+                const int u = i & 1;
+                if (!mbar_wait_near(sfull + 2 * grp + u, (uint32_t)(i >> 1) & 1u, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
                 if (warp_live) {
                     tc_fence_after();
                     uint32_t s[64], w[32];
-                    tmem_ld32(ts + 64u * h, s);
-                    tmem_ld32(ts + 64u * h + 32u, s + 32);
+                    tmem_ld32(ts + 64u * u, s);
+                    tmem_ld32(ts + 64u * u + 32u, s + 32);
                     tmem_ld_wait();
                     float mul = c2;
                     if (masked) {  // scores in base 2 with the bias
@@ -355,9 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // a first key, or one far above: the rows concerned move to the step's own maximum, O and the
                         // sum with them, once the products so far are complete
                         const float mn = over ? fmaxf(m, max_of64(s) * mul) : m;
-                        if (n > 0 || h > 0) {
-                            const uint32_t before = h == 0 ? (uint32_t)(n - 1) & 1u : ph;
-                            if (!mbar_wait_near(pvdone + 2 * grp + (h ^ 1), before, p.timeout_ns)) {
+                        if (i > 0) {
+                            if (!mbar_wait_near(pvdone + 2 * grp + (u ^ 1), (uint32_t)((i - 1) >> 1) & 1u, p.timeout_ns)) {
                                 ok = false;
                                 break;
                             }
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_ld16(to + k, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                                 tmem_st16(to + k, o);
                             }
                         }
@@ -377,19 +382,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum = weights(s, mul, m == -INFINITY ? 0.f : m, w);
                     }
                     l += sum;
-                    tmem_st32(ts + 64u * h, w);
+                    tmem_st32(ts + 64u * u, w);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                 }  // else no row of this warp exists: its lanes of P may hold anything
-                if (lane == 0) mbar_arrive(pready + 2 * grp + h);
+                if (lane == 0) mbar_arrive(pready + 2 * grp + u);
             }
             if (!ok) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(bempty + j);
             if (*abort_flag) break;
         }
-        if (ok && n > 0 && !mbar_wait_near(pvdone + 2 * grp + 1, (uint32_t)(n - 1) & 1u, p.timeout_ns)) ok = false;
+        if (ok && i > 0 && !mbar_wait_near(pvdone + 2 * grp + ((i - 1) & 1), (uint32_t)((i - 1) >> 1) & 1u, p.timeout_ns))
+            ok = false;
         if (!ok) {
             atomicOr(p.err, kDevErrTimeout);
             *abort_flag = 1;
@@ -402,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             group_bar(1, 256);
             if (grp == 1) {
                 sML[rl] = make_float2(m, l);
-                if (warp_live && n > 0)
+                if (warp_live && i > 0)
                     for (int k = 0; k < g.dv_pad; k += 16) {
                         uint32_t o[16];
                         tmem_ld16(to + k, o);
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int QT, int KS>
 cudaError_t launch(const AttnParams &p, AttnTc g, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
     const uint32_t limit = 227u * 1024u;
-    g.slots = 8;
+    g.slots = QT == 2 ? 8 : 12;
     while (layout(QT, g.datoms, g.vatoms, g.slots).total + 1024u > limit) --g.slots;
     const uint32_t smem = layout(QT, g.datoms, g.vatoms, g.slots).total + 1024u;
     cudaError_t e = cudaFuncSetAttribute(xattn_tc_kernel<QT, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
@@ -534,8 +540,8 @@ cudaError_t launch_xattn_tc(const AttnParams &p, bool two_blocks, cudaStream_t s
     g.vatoms = (p.dv + 63) / 64;
     g.dv_pad = (p.dv + 15) / 16 * 16;
     CUtensorMap mk, mv;
-    if (!attn_map(&mk, p.k, p.ks, p.d, p.m, p.kv_heads, p.batch, kTS, &g.k_head, &g.k_batch) ||
-        !attn_map(&mv, p.v, p.vs, p.dv, p.m, p.kv_heads, p.batch, kTS, &g.v_head, &g.v_batch))
+    if (!attn_map(&mk, p.k, p.ks, p.d, p.m, p.kv_heads, p.batch, tile_keys(two_blocks ? 2 : 1), &g.k_head, &g.k_batch) ||
+        !attn_map(&mv, p.v, p.vs, p.dv, p.m, p.kv_heads, p.batch, tile_keys(two_blocks ? 2 : 1), &g.v_head, &g.v_batch))
         return cudaErrorInvalidValue;
     const int ks = (p.d + 31) / 32 * 2;
     if (two_blocks)
