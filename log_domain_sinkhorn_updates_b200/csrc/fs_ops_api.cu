@@ -116,7 +116,7 @@ struct AttnPlan {
     size_t part_ml = 0, part_o = 0, dot = 0, total = 0;  // workspace offsets, and its size
 };
 
-AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, const Device &dev) {
+AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, bool ragged, const Device &dev) {
     AttnPlan L;
     const size_t rows = (size_t)D.n * (D.heads / D.kv_heads), heads = (size_t)D.batch * D.kv_heads;
     L.split_keys = std::max(D.m, 1);
@@ -125,22 +125,28 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, const Device &dev)
         return L;
     }
     if (rows == 0 || heads == 0) return L;
-    // Parts of the keys: as many as cost least, in waves of CTAs (one an SM on the tensor cores, two otherwise) times
-    // the tiles of a part plus its start and end; more than one part costs the joining pass too.
-    const int tile = tc ? 128 : 64, side = tc ? 128 : (rows <= fs::kXattnFewRows ? 16 : 64), slots = tc ? dev.sms : 2 * dev.sms;
-    const size_t ctas = (rows + side - 1) / side * heads;
-    const int tiles = up(std::max(D.m, 1), tile);
+    // Rows of a CTA (tensor cores: 128, or 256 in two blocks that share every tile) and parts of the keys: what costs
+    // least, in tiles of 128 keys.  A CTA takes its tiles (two blocks: 1.28 times as long each, 2.3 us against 1.8 at
+    // width 128) and 1.5 tiles' time to start and end; waves of CTAs, one an SM (CUDA cores: two); where lengths
+    // differ, CTAs fill in behind short ones, and the tail is half a CTA instead of the rest of a wave (32 requests
+    // of up to 4096 keys: 96 us in one part, 82 in two).  More than one part costs the joining pass.
+    const int slots = tc ? dev.sms : 2 * dev.sms, side = tc ? 128 : (rows <= fs::kXattnFewRows ? 16 : 64);
+    const int tile = 128, tiles = up(std::max(D.m, 1), tile);
     double best = 1e300;
-    for (int s = 1; s <= std::min(tiles, 128) && (s == 1 || ctas < 2 * (size_t)slots); ++s) {
-        const int t = up(tiles, s), parts = up(tiles, t);
-        const double cost = (double)((ctas * parts + slots - 1) / slots) * (t + 3.0) + (parts > 1 ? 3.0 + 0.02 * parts : 0.0);
-        if (cost < best - 1e-9) {
-            best = cost;
-            L.splits = parts;
-            L.split_keys = t * tile;
+    for (int two = 0; two < (tc && rows > 128 ? 2 : 1); ++two) {
+        const size_t side2 = (size_t)side << two, ctas = (rows + side2 - 1) / side2 * heads;
+        for (int s = 1; s <= std::min(tiles, 128) && (s == 1 || ctas < 3 * (size_t)slots); ++s) {
+            const int t = up(tiles, s), parts = up(tiles, t);
+            const double n = (double)(ctas * parts) / slots, waves = ragged ? std::max(1.0, n + 0.5) : std::ceil(n);
+            const double cost = waves * (t * (two ? 1.28 : 1.0) + 1.5) + (parts > 1 ? 2.0 + 0.02 * parts : 0.0);
+            if (cost < best - 1e-9) {
+                best = cost;
+                L.splits = parts;
+                L.split_keys = t * tile;
+                L.two_blocks = two != 0;
+            }
         }
     }
-    L.two_blocks = tc && L.splits == 1 && (rows + 255) / 256 * heads >= (size_t)dev.sms;
     if (L.splits > 1) {
         L.part_o = align256(rows * heads * L.splits * sizeof(float2));
         L.total = L.part_o + align256(rows * heads * L.splits * D.dv * sizeof(float));
@@ -148,8 +154,10 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, const Device &dev)
     return L;
 }
 size_t attn_workspace(const fs_attn_desc &D, bool grad, const Device &dev) {
-    const size_t simt = plan_attn(D, grad, false, dev).total;
-    return D.dtype == FS_BF16 ? std::max(simt, plan_attn(D, grad, true, dev).total) : simt;
+    size_t most = 0;  // over the kernels and the lengths that a call may bring
+    for (int k = 0; k < 4; ++k)
+        if (!(k & 1) || D.dtype == FS_BF16) most = std::max(most, plan_attn(D, grad, k & 1, k & 2, dev).total);
+    return most;
 }
 
 // Whether the tensor-core kernels take the call: bf16, widths up to 128 and multiples of 8, keys to load, and
@@ -342,7 +350,7 @@ fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const void *k, 
     Device dev;
     if ((st = current_device(&dev)) != FS_OK) return st;
     const bool bf16 = D.dtype == FS_BF16, tc = attn_tc(D, q, k, v, out);
-    const AttnPlan L = plan_attn(D, false, tc, dev);
+    const AttnPlan L = plan_attn(D, false, tc, k_len != nullptr, dev);
     if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
     fs::AttnParams p = attn_params(D, L, dev, workspace);
     p.q = q;
@@ -372,7 +380,7 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
         return reject(FS_ERR_INVALID_ARG, "null argument");
     Device dev;
     if ((st = current_device(&dev)) != FS_OK) return st;
-    const AttnPlan L = plan_attn(D, true, false, dev);
+    const AttnPlan L = plan_attn(D, true, false, false, dev);
     if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
     fs::AttnParams p = attn_params(D, L, dev, workspace);
     p.q = q;

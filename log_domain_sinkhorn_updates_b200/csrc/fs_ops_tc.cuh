@@ -110,18 +110,20 @@ __device__ __forceinline__ void group_bar(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 // Packed rows [r0, r0 + count) (row r: query r / group, head c group + r % group) of a query-side bf16
-// tensor of width w into 128-row blocks of `atoms` 64-element columns, as the 128-byte swizzle lays them; zeros
+// tensor of width w into 128-row blocks of ATOMS 64-element columns, as the 128-byte swizzle lays them; zeros
 // beyond the last row and the width.  By threads t of `threads`.
+template <int ATOMS>
 __device__ __forceinline__ void stage_packed(uint8_t *dst, const void *src, const fs_view &s, const AttnParams &p, int b,
-                                             int c, int r0, int count, int w, int atoms, int t, int threads) {
-    const int per = atoms * 8, rows = p.n * p.group;
+                                             int c, int r0, int count, int w, int t, int threads) {
+    constexpr int per = ATOMS * 8;
+    const int rows = p.n * p.group;
     for (int e = t; e < count * per; e += threads) {
         const int row = e / per, ch = e % per, at = r0 + row;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (at < rows && ch * 8 < w)
             v = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)src + s.batch * b + s.token * (at / p.group) +
                                                  s.head * (c * p.group + at % p.group) + ch * 8);
-        *reinterpret_cast<uint4 *>(dst + (row >> 7) * atoms * 16384 + (ch >> 3) * 16384 + (row & 127) * 128 +
+        *reinterpret_cast<uint4 *>(dst + (row >> 7) * ATOMS * 16384 + (ch >> 3) * 16384 + (row & 127) * 128 +
                                    (((ch & 7) ^ (row & 7)) << 4)) = v;
     }
 }

@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             nl = attn_bias2(p, b, row, keys);
         } else {
             const int tid = (int)threadIdx.x - 128;
-            stage_packed(st1, p.q, p.qs, p, b, c, r0, 128, p.d, kAtoms, tid, 256);
-            stage_packed(st2, p.dout, p.dos, p, b, c, r0, 128, p.dv, kAtoms, tid, 256);
+            stage_packed<kAtoms>(st1, p.q, p.qs, p, b, c, r0, 128, p.d, tid, 256);
+            stage_packed<kAtoms>(st2, p.dout, p.dos, p, b, c, r0, 128, p.dv, tid, 256);
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(stready);

@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = (rb * QT + blk) * 128 + rl;  // packed row
         const bool warp_live = (rb * QT + blk) * 128 + q * 32 < rows;
         // Q into shared memory, 16 bytes at a time, as the 128-byte swizzle lays it
-        stage_packed(sQ, p.q, p.qs, p, b, c, rb * QT * 128, QT * 128, p.d, g.datoms, (int)threadIdx.x - 128, 256);
+        stage_packed<(KS + 3) / 4>(sQ, p.q, p.qs, p, b, c, rb * QT * 128, QT * 128, p.d, (int)threadIdx.x - 128, 256);
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(qfull);
