@@ -69,8 +69,10 @@ __device__ __forceinline__ float attn_bias2(const AttnParams &p, int b, int j, i
 bool encode_bf16_map(CUtensorMap *map, const void *base, int dims, const long long *size, const long long *stride,
                      const int *box);
 
-// Packed rows up to which the CUDA-core forward takes 16 rows a CTA instead of 64.
-constexpr int kXattnFewRows = 16;
+// Rows of a CTA of the CUDA-core kernels: 64, or 16 where 64 would leave SMs without a CTA.
+inline int xattn_simt_rows(int rows, int heads, int sms) {
+    return rows <= 16 || (long long)((rows + 63) / 64) * heads < sms ? 16 : 64;
+}
 
 // Geometry of the tensor-core attention kernels.
 struct AttnTc {
@@ -82,19 +84,20 @@ struct AttnTc {
 struct AttnGradTc {
     int d_pad, dv_pad;  // rounded up to 16
     int slots;          // ring of streamed tiles
-    int s1_head, s1_batch, s2_head, s2_batch, k_head, k_batch, v_head, v_batch;  // as above, streamed and kept maps
+    int key_blocks;     // CTAs of the pass that keeps keys; those that keep rows follow
+    int q_head, q_batch, g_head, g_batch, k_head, k_batch, v_head, v_batch;  // as above (g: dout)
 };
 bool attn_tc_view(const void *base, const fs_view &s, int tokens, int heads, int batch, bool map);
 bool attn_map(CUtensorMap *map, const void *base, const fs_view &s, int w, int tokens, int heads, int batch,
               int box_rows, int *hm, int *bm);
 cudaError_t launch_xattn_tc(const AttnParams &p, bool two_blocks, cudaStream_t s);
 
-cudaError_t launch_xattn_grad_tc(const AttnParams &p, cudaStream_t s);  // two launches
+cudaError_t launch_xattn_grad_tc(const AttnParams &p, cudaStream_t s);
 
-cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s);
 cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s);
-cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, cudaStream_t s);  // two launches
+cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s);  // two launches
 
 // Softmax cross entropy: rows x [n][d] against classes w [v][d].
 struct XentParams {

@@ -129,16 +129,18 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, bool ragged, const
     // least, in tiles of 128 keys.  A CTA takes its tiles (two blocks: 1.28 times as long each, 2.3 us against 1.8 at
     // width 128) and 1.5 tiles' time to start and end; waves of CTAs, one an SM (CUDA cores: two); where lengths
     // differ, CTAs fill in behind short ones, and the tail is half a CTA instead of the rest of a wave (32 requests
-    // of up to 4096 keys: 96 us in one part, 82 in two).  More than one part costs the joining pass.
-    const int slots = tc ? dev.sms : 2 * dev.sms, side = tc ? 128 : (rows <= fs::kXattnFewRows ? 16 : 64);
+    // of up to 4096 keys: 96 us in one part, 82 in two).
+    const int slots = tc ? dev.sms : 2 * dev.sms, side = tc ? 128 : fs::xattn_simt_rows(D.n * (D.heads / D.kv_heads), (int)heads, dev.sms);
     const int tile = 128, tiles = up(std::max(D.m, 1), tile);
     double best = 1e300;
     for (int two = 0; two < (tc && rows > 128 ? 2 : 1); ++two) {
         const size_t side2 = (size_t)side << two, ctas = (rows + side2 - 1) / side2 * heads;
         for (int s = 1; s <= std::min(tiles, 128) && (s == 1 || ctas < 3 * (size_t)slots); ++s) {
             const int t = up(tiles, s), parts = up(tiles, t);
-            const double n = (double)(ctas * parts) / slots, waves = ragged ? std::max(1.0, n + 0.5) : std::ceil(n);
-            const double cost = waves * (t * (two ? 1.28 : 1.0) + 1.5) + (parts > 1 ? 2.0 + 0.02 * parts : 0.0);
+            // the joining pass: a launch, and the parts' sums written and read back (4 TB/s, 1.8 us a tile)
+            const double join = 2.0 + 0.02 * parts + (double)rows * heads * parts * D.dv * 8.0 / 4e6 / 1.8;
+            const double n = (double)(ctas * parts) / slots, waves = ragged && n > 1.0 ? n + 0.5 : std::ceil(n);
+            const double cost = waves * (t * (two ? 1.28 : 1.0) + 1.5) + (parts > 1 ? join : 0.0);
             if (cost < best - 1e-9) {
                 best = cost;
                 L.splits = parts;
@@ -364,7 +366,7 @@ fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const void *k, 
     if (tc)
         OPS_LAUNCH(fs::launch_xattn_tc(p, L.two_blocks, s), 1);
     else
-        OPS_LAUNCH(fs::launch_xattn_simt(p, bf16, s), 1);
+        OPS_LAUNCH(fs::launch_xattn_simt(p, bf16, dev.sms, s), 1);
     if (p.splits > 1) OPS_LAUNCH(fs::launch_xattn_combine(p, bf16, s), 1);
     return FS_OK;
 }
@@ -398,9 +400,9 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
     const bool bf16 = D.dtype == FS_BF16;
     if (D.n > 0) OPS_LAUNCH(fs::launch_xattn_dot(p, bf16, s), 1);
     if (attn_grad_tc(D, q, k, v, dout, dq, dk, dv))
-        OPS_LAUNCH(fs::launch_xattn_grad_tc(p, s), 2);
+        OPS_LAUNCH(fs::launch_xattn_grad_tc(p, s), 1);
     else
-        OPS_LAUNCH(fs::launch_xattn_grad_simt(p, bf16, s), (D.m > 0) + (D.n > 0));
+        OPS_LAUNCH(fs::launch_xattn_grad_simt(p, bf16, dev.sms, s), (D.m > 0) + (D.n > 0));
     return FS_OK;
 }
 

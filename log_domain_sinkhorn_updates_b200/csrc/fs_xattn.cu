@@ -19,7 +19,7 @@ namespace {
 constexpr int kThreads = 128;  // of the joining pass and the row products
 constexpr int kTileThreads = 256;
 constexpr int kKeys = 64;      // keys of a forward tile
-constexpr int kKept = 64, kStream = 32;  // gradient tile
+constexpr int kStream = 32;    // streamed rows of a gradient tile
 constexpr int kMaxD = 256;
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -305,28 +305,37 @@ __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParam
         p.lse[row_stat(p, b, c, r)] = l == 0.f ? -INFINITY : (float)(((double)mx + log2((double)l)) * kLn2d);
 }
 
-// D_i = dout_i.out_i, one warp per (problem, head, query).
+// D_i = dout_i.out_i of every (problem, query, head): `per` lanes take a row, four elements each at a time.
 template <class T>
-__global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p) {
-    const size_t at = (size_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-    if (at >= (size_t)p.batch * p.n * p.heads) return;
-    const int lane = threadIdx.x % 32;
+__global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p, int per, bool vec) {
+    const size_t at = ((size_t)blockIdx.x * kThreads + threadIdx.x) / per, rows = (size_t)p.batch * p.n * p.heads;
+    const int sub = threadIdx.x % per;
+    const bool live = at < rows;
     const int h = (int)(at % p.heads), i = (int)(at / p.heads % p.n), b = (int)(at / p.heads / p.n);
-    const T *o = (const T *)p.out + p.os.batch * b + p.os.token * i + p.os.head * h;
-    const T *g = (const T *)p.dout + p.dos.batch * b + p.dos.token * i + p.dos.head * h;
     float s = 0.f;
-    for (int k = lane; k < p.dv; k += 32) s = fmaf(to_f(o[k]), to_f(g[k]), s);
-    for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(~0u, s, w);
-    if (lane == 0) p.dot[((size_t)b * p.heads + h) * p.n + i] = s;
+    if (live) {
+        const T *o = (const T *)p.out + p.os.batch * b + p.os.token * i + p.os.head * h;
+        const T *g = (const T *)p.dout + p.dos.batch * b + p.dos.token * i + p.dos.head * h;
+        for (int k = 4 * sub; k < p.dv; k += 4 * per) {
+            if (vec && k + 4 <= p.dv) {
+                const float4 x = load4(o + k), y = load4(g + k);
+                s = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
+            } else {
+                for (int u = k; u < min(k + 4, p.dv); ++u) s = fmaf(to_f(o[u]), to_f(g[u]), s);
+            }
+        }
+    }
+    for (int w = per / 2; w; w >>= 1) s += __shfl_xor_sync(~0u, s, w);
+    if (live && sub == 0) p.dot[((size_t)b * p.heads + h) * p.n + i] = s;
 }
 
-// KEYS: one CTA keeps 64 keys of a key head (K, V) and streams its packed rows (Q, dO) in tiles of 32: dk and dv.
-// Otherwise: 64 packed rows (Q, dO) against streamed keys (K, V): dq.  16 x 16 threads: 4 kept rows x 2 streamed ones
-// of the scores, 4 kept rows x 4 columns a piece of the sums.
-template <class T, bool KEYS, int C>
+// KEYS: one CTA keeps 16 U keys of a key head (K, V) and streams its packed rows (Q, dO) in tiles of 32: dk and dv.
+// Otherwise: 16 U packed rows (Q, dO) against streamed keys (K, V): dq.  16 x 16 threads: U kept rows x 2 streamed
+// ones of the scores, U kept rows x 4 columns a piece of the sums.
+template <class T, bool KEYS, int U, int C>
 __global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnParams p, bool vec) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int LS = kStream + 4;
+    constexpr int LS = kStream + 4, kKept = 16 * U;
     const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads, t0 = blockIdx.x * kKept;
     const int ld = smem_stride(p.d), lv = smem_stride(p.dv);
     float *a1 = sm, *a2 = a1 + kKept * ld, *b1 = a2 + kKept * lv, *b2 = b1 + kStream * ld, *sP = b2 + kStream * lv;
@@ -359,9 +368,9 @@ __global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnPara
         stage_rows<T>(a2, p.dout, p.dos, p, b, c, t0, kKept, p.dv, vec);
     }
     const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
-    float4 g1[4][C], g2[4][KEYS ? C : 1];
+    float4 g1[U][C], g2[U][KEYS ? C : 1];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int k = 0; k < C; ++k) {
             g1[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -384,16 +393,16 @@ __global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnPara
             stage_keys<T>(b2, p.v, p.vs, b, c, u0, kStream, p.dv, sb, vec);
         }
         __syncthreads();
-        float s[4][2], g[4][2];
+        float s[U][2], g[U][2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) s[u][0] = s[u][1] = g[u][0] = g[u][1] = 0.f;
-        dots<4, 2, 16>(s, a1 + ti * 4 * ld, ld, b1 + tj * ld, ld, p.d);
-        dots<4, 2, 16>(g, a2 + ti * 4 * lv, lv, b2 + tj * lv, lv, p.dv);
+        for (int u = 0; u < U; ++u) s[u][0] = s[u][1] = g[u][0] = g[u][1] = 0.f;
+        dots<U, 2, 16>(s, a1 + ti * U * ld, ld, b1 + tj * ld, ld, p.d);
+        dots<U, 2, 16>(g, a2 + ti * U * lv, lv, b2 + tj * lv, lv, p.dv);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                const int kept = ti * 4 + u, str = tj + 16 * w;
+                const int kept = ti * U + u, str = tj + 16 * w;
                 const float bias = KEYS ? kb[kept] : sb[str], lse2 = KEYS ? sb[str] : kb[kept];
                 const float dd = KEYS ? sd[str] : kd[kept];
                 const bool off = bias == -INFINITY || lse2 == INFINITY;
@@ -402,12 +411,12 @@ __global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnPara
                 sS[kept * LS + str] = off ? 0.f : pr * (g[u][w] - dd);
             }
         __syncwarp();  // a kept row's weights are written and read by its 16 threads, of one warp
-        weigh<4, C>(g1, sS + ti * 4 * LS, LS, b1, ld, kStream, 4 * tj, p.d);
-        if constexpr (KEYS) weigh<4, C>(g2, sP + ti * 4 * LS, LS, b2, lv, kStream, 4 * tj, p.dv);
+        weigh<U, C>(g1, sS + ti * U * LS, LS, b1, ld, kStream, 4 * tj, p.d);
+        if constexpr (KEYS) weigh<U, C>(g2, sP + ti * U * LS, LS, b2, lv, kStream, 4 * tj, p.dv);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int at = t0 + ti * 4 + u;
+    for (int u = 0; u < U; ++u) {
+        const int at = t0 + ti * U + u;
         if (at >= (KEYS ? p.m : rows)) continue;  // keys past the length get zeros: they take no part
         T *d1 = KEYS ? (T *)p.dk + p.dks.batch * b + p.dks.token * at + p.dks.head * c
                      : (T *)p.dq + row_off(p.dqs, p, b, c, at);
@@ -450,36 +459,43 @@ cudaError_t fwd_width(const AttnParams &p, cudaStream_t s) {
     return p.dv <= 64 ? fwd<T, RPT, 1>(p, s) : p.dv <= 128 ? fwd<T, RPT, 2>(p, s) : fwd<T, RPT, 4>(p, s);
 }
 template <class T>
-cudaError_t fwd_rows(const AttnParams &p, cudaStream_t s) {
-    return p.n * p.group <= kXattnFewRows ? fwd_width<T, 1>(p, s) : fwd_width<T, 4>(p, s);
+cudaError_t fwd_rows(const AttnParams &p, int sms, cudaStream_t s) {
+    return xattn_simt_rows(p.n * p.group, p.batch * p.kv_heads, sms) == 16 ? fwd_width<T, 1>(p, s) : fwd_width<T, 4>(p, s);
 }
 
-template <class T, int C>
-cudaError_t grad(const AttnParams &p, cudaStream_t s) {
-    const int w = smem_stride(p.d) + smem_stride(p.dv);
-    const size_t smem = sizeof(float) * ((size_t)(kKept + kStream) * w + 2 * kKept * (kStream + 4) + 2 * kKept + 2 * kStream);
-    cudaError_t e = with_smem(xattn_grad_kernel<T, true, C>, smem);
-    if (e == cudaSuccess) e = with_smem(xattn_grad_kernel<T, false, C>, smem);
+template <class T, bool KEYS, int U, int C>
+cudaError_t grad_pass(const AttnParams &p, cudaStream_t s) {
+    constexpr int kept = 16 * U;
+    const int w = smem_stride(p.d) + smem_stride(p.dv), count = KEYS ? p.m : p.n * p.group;
+    if (count == 0) return cudaSuccess;
+    const size_t smem = sizeof(float) * ((size_t)(kept + kStream) * w + 2 * kept * (kStream + 4) + 2 * kept + 2 * kStream);
+    cudaError_t e = with_smem(xattn_grad_kernel<T, KEYS, U, C>, smem);
     if (e != cudaSuccess) return e;
     const bool vec = aligned4<T>(p.q, p.qs) && aligned4<T>(p.k, p.ks) && aligned4<T>(p.v, p.vs) &&
                      aligned4<T>(p.dout, p.dos);
-    const int heads = p.batch * p.kv_heads, rows = p.n * p.group;
-    if (p.m > 0)
-        xattn_grad_kernel<T, true, C><<<dim3((p.m + kKept - 1) / kKept, heads), kTileThreads, smem, s>>>(p, vec);
-    if (p.n > 0)
-        xattn_grad_kernel<T, false, C><<<dim3((rows + kKept - 1) / kKept, heads), kTileThreads, smem, s>>>(p, vec);
+    xattn_grad_kernel<T, KEYS, U, C>
+        <<<dim3((count + kept - 1) / kept, p.batch * p.kv_heads), kTileThreads, smem, s>>>(p, vec);
     return cudaGetLastError();
 }
-template <class T>
-cudaError_t grad_width(const AttnParams &p, cudaStream_t s) {
+template <class T, bool KEYS>
+cudaError_t grad_width(const AttnParams &p, int sms, cudaStream_t s) {
     const int w = p.d > p.dv ? p.d : p.dv;
-    return w <= 64 ? grad<T, 1>(p, s) : w <= 128 ? grad<T, 2>(p, s) : grad<T, 4>(p, s);
+    if (xattn_simt_rows(KEYS ? p.m : p.n * p.group, p.batch * p.kv_heads, sms) == 16)
+        return w <= 64 ? grad_pass<T, KEYS, 1, 1>(p, s) : w <= 128 ? grad_pass<T, KEYS, 1, 2>(p, s)
+                                                                   : grad_pass<T, KEYS, 1, 4>(p, s);
+    return w <= 64 ? grad_pass<T, KEYS, 4, 1>(p, s) : w <= 128 ? grad_pass<T, KEYS, 4, 2>(p, s)
+                                                               : grad_pass<T, KEYS, 4, 4>(p, s);
+}
+template <class T>
+cudaError_t grad(const AttnParams &p, int sms, cudaStream_t s) {
+    const cudaError_t e = grad_width<T, true>(p, sms, s);
+    return e != cudaSuccess ? e : grad_width<T, false>(p, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s) {
-    return bf16 ? fwd_rows<__nv_bfloat16>(p, s) : fwd_rows<float>(p, s);
+cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s) {
+    return bf16 ? fwd_rows<__nv_bfloat16>(p, sms, s) : fwd_rows<float>(p, sms, s);
 }
 cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s) {
     const size_t rows = (size_t)p.n * p.group * p.batch * p.kv_heads;
@@ -488,16 +504,20 @@ cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s)
                 : launch_dependent(xattn_combine_kernel<float>, grid, kThreads, 0, s, p);
 }
 cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s) {
-    const size_t rows = (size_t)p.batch * p.n * p.heads;
-    const unsigned grid = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
+    int per = 1;
+    while (per < 32 && 4 * per < p.dv) per *= 2;
+    const size_t threads = (size_t)p.batch * p.n * p.heads * per;
+    const unsigned grid = (unsigned)((threads + kThreads - 1) / kThreads);
     if (bf16)
-        xattn_dot_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
+        xattn_dot_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(
+            p, per, aligned4<__nv_bfloat16>(p.out, p.os) && aligned4<__nv_bfloat16>(p.dout, p.dos));
     else
-        xattn_dot_kernel<float><<<grid, kThreads, 0, s>>>(p);
+        xattn_dot_kernel<float><<<grid, kThreads, 0, s>>>(p, per,
+                                                          aligned4<float>(p.out, p.os) && aligned4<float>(p.dout, p.dos));
     return cudaGetLastError();
 }
-cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, cudaStream_t s) {
-    return bf16 ? grad_width<__nv_bfloat16>(p, s) : grad_width<float>(p, s);
+cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s) {
+    return bf16 ? grad<__nv_bfloat16>(p, sms, s) : grad<float>(p, sms, s);
 }
 
 }  // namespace fs

@@ -47,10 +47,9 @@ __host__ __device__ inline Layout layout(int atoms, int slots) {
 
 // KS: steps of 16 along the widths (d and dv, the larger of the two), zeros beyond each.
 template <bool KEYS, int KS>
-__global__ void __launch_bounds__(kThreads, 1)
-    xattn_grad_tc_kernel(const __grid_constant__ CUtensorMap map_s1, const __grid_constant__ CUtensorMap map_s2,
-                         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                         const AttnParams p, const AttnGradTc g) {
+__device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, const CUtensorMap &map_k,
+                          const CUtensorMap &map_v, const AttnParams &p, const AttnGradTc &g, int block) {
+    const CUtensorMap &map_s1 = KEYS ? map_q : map_k, &map_s2 = KEYS ? map_g : map_v;  // streamed
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
     constexpr int kAtoms = (KS + 3) / 4;
@@ -80,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads;
-    const int r0 = blockIdx.x * 128;  // first kept row (key, or packed query row)
+    const int r0 = block * 128;  // first kept row (key, or packed query row)
     const int keys = attn_keys(p, b), rows = p.n * p.group;
     const int head_tiles = (p.n + kTile - 1) / kTile;
     const int nt = KEYS ? (r0 < keys ? p.group * head_tiles : 0) : (keys + kTile - 1) / kTile;
@@ -144,9 +143,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t dst = saddr(ring + (size_t)s * 2 * L.half);
                 mbar_expect_tx(full + s, 2u * L.half);
                 for (int a = 0; a < kAtoms; ++a) {
-                    tma_load_4d(dst + a * 8192u, &map_s1, saddr(full + s), a * 64, y, h * g.s1_head, b * g.s1_batch);
-                    tma_load_4d(dst + L.half + a * 8192u, &map_s2, saddr(full + s), a * 64, y, h * g.s2_head,
-                                b * g.s2_batch);
+                    tma_load_4d(dst + a * 8192u, &map_s1, saddr(full + s), a * 64, y, h * (KEYS ? g.q_head : g.k_head),
+                                b * (KEYS ? g.q_batch : g.k_batch));
+                    tma_load_4d(dst + L.half + a * 8192u, &map_s2, saddr(full + s), a * 64, y, h * (KEYS ? g.g_head : g.v_head),
+                                b * (KEYS ? g.g_batch : g.v_batch));
                 }
                 rp.step(1, NS);
                 y += kTile;
@@ -458,8 +458,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool KEYS, int KS>
-cudaError_t launch(const AttnParams &p, AttnGradTc g, const CUtensorMap &s1, const CUtensorMap &s2,
+// Both passes in one launch: the CTAs of the second fill in behind the first's last wave.
+template <int KS>
+__global__ void __launch_bounds__(kThreads, 1)
+    xattn_grad_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_g,
+                         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                         const AttnParams p, const AttnGradTc g) {
+    grid_dependency_wait();
+    if ((int)blockIdx.x < g.key_blocks)
+        grad_pass<true, KS>(map_q, map_g, map_k, map_v, p, g, (int)blockIdx.x);
+    else
+        grad_pass<false, KS>(map_q, map_g, map_k, map_v, p, g, (int)blockIdx.x - g.key_blocks);
+}
+
+template <int KS>
+cudaError_t launch(const AttnParams &p, AttnGradTc g, const CUtensorMap &mq, const CUtensorMap &mg,
                    const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
     constexpr int atoms = (KS + 3) / 4;
     const uint32_t limit = 227u * 1024u;
@@ -468,32 +481,12 @@ cudaError_t launch(const AttnParams &p, AttnGradTc g, const CUtensorMap &s1, con
     const uint32_t need = layout(atoms, g.slots).total + 1024u;
     // at least half the shared memory: a CTA holds all of TMEM, so two on one SM would wait for each other
     const uint32_t smem = need > limit / 2 + 1024u ? need : limit / 2 + 1024u;
-    auto kern = xattn_grad_tc_kernel<KEYS, KS>;
+    auto kern = xattn_grad_tc_kernel<KS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
     if (e != cudaSuccess) return e;
-    const int blocks = ((KEYS ? p.m : p.n * p.group) + 127) / 128;
-    kern<<<dim3(blocks, p.batch * p.kv_heads), kThreads, smem, s>>>(s1, s2, mk, mv, p, g);
-    return cudaGetLastError();
-}
-
-template <int KS>
-cudaError_t both(const AttnParams &p, AttnGradTc g, const CUtensorMap &mq, const CUtensorMap &mg,
-                 const CUtensorMap &mk, const CUtensorMap &mv, const int *hb, cudaStream_t s) {
-    g.k_head = hb[4];
-    g.k_batch = hb[5];
-    g.v_head = hb[6];
-    g.v_batch = hb[7];
-    g.s1_head = hb[0];
-    g.s1_batch = hb[1];
-    g.s2_head = hb[2];
-    g.s2_batch = hb[3];
-    cudaError_t e = launch<true, KS>(p, g, mq, mg, mk, mv, s);
-    if (e != cudaSuccess) return e;
-    g.s1_head = hb[4];
-    g.s1_batch = hb[5];
-    g.s2_head = hb[6];
-    g.s2_batch = hb[7];
-    return launch<false, KS>(p, g, mk, mv, mk, mv, s);
+    g.key_blocks = (p.m + 127) / 128;
+    return launch_dependent(kern, dim3(g.key_blocks + (p.n * p.group + 127) / 128, p.batch * p.kv_heads), kThreads, smem,
+                            s, mq, mg, mk, mv, p, g);
 }
 
 }  // namespace
@@ -503,17 +496,16 @@ cudaError_t launch_xattn_grad_tc(const AttnParams &p, cudaStream_t s) {
     g.d_pad = (p.d + 15) / 16 * 16;
     g.dv_pad = (p.dv + 15) / 16 * 16;
     CUtensorMap mq, mg, mk, mv;
-    int hb[8];
-    if (!attn_map(&mq, p.q, p.qs, p.d, p.n, p.heads, p.batch, kTile, hb, hb + 1) ||
-        !attn_map(&mg, p.dout, p.dos, p.dv, p.n, p.heads, p.batch, kTile, hb + 2, hb + 3) ||
-        !attn_map(&mk, p.k, p.ks, p.d, p.m, p.kv_heads, p.batch, kTile, hb + 4, hb + 5) ||
-        !attn_map(&mv, p.v, p.vs, p.dv, p.m, p.kv_heads, p.batch, kTile, hb + 6, hb + 7))
+    if (!attn_map(&mq, p.q, p.qs, p.d, p.n, p.heads, p.batch, kTile, &g.q_head, &g.q_batch) ||
+        !attn_map(&mg, p.dout, p.dos, p.dv, p.n, p.heads, p.batch, kTile, &g.g_head, &g.g_batch) ||
+        !attn_map(&mk, p.k, p.ks, p.d, p.m, p.kv_heads, p.batch, kTile, &g.k_head, &g.k_batch) ||
+        !attn_map(&mv, p.v, p.vs, p.dv, p.m, p.kv_heads, p.batch, kTile, &g.v_head, &g.v_batch))
         return cudaErrorInvalidValue;
     const int w = p.d > p.dv ? p.d : p.dv;
-    if (w <= 32) return both<2>(p, g, mq, mg, mk, mv, hb, s);
-    if (w <= 64) return both<4>(p, g, mq, mg, mk, mv, hb, s);
-    if (w <= 96) return both<6>(p, g, mq, mg, mk, mv, hb, s);
-    return both<8>(p, g, mq, mg, mk, mv, hb, s);
+    if (w <= 32) return launch<2>(p, g, mq, mg, mk, mv, s);
+    if (w <= 64) return launch<4>(p, g, mq, mg, mk, mv, s);
+    if (w <= 96) return launch<6>(p, g, mq, mg, mk, mv, s);
+    return launch<8>(p, g, mq, mg, mk, mv, s);
 }
 
 }  // namespace fs
