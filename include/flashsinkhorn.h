@@ -452,7 +452,7 @@ FS_API size_t fs_cross_attn_workspace(const fs_attn_desc *desc, int grad);
  * Non-finite inputs that take part give non-finite outputs.  Asynchronous.
  * Errors: FS_ERR_INVALID_ARG (sizes, scale, strides, null pointers, output
  * strides that overlap, a workspace that is too small), FS_ERR_UNSUPPORTED (device not
- * compute capability 10.x; batch * heads over 65535; n * heads or m of 2^30 or more).
+ * compute capability 10.x; batch * heads over 65535; n * heads of 2^27 or more; m of 2^30 or more).
  */
 FS_API fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const void *k, const void *v,
                                const int *k_len, const float *bias, void *out, float *lse, void *workspace,

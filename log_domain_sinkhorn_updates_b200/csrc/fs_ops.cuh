@@ -97,7 +97,7 @@ cudaError_t launch_xattn_grad_tc(const AttnParams &p, cudaStream_t s);
 cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s);
 cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s);
-cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s);  // two launches
+cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s);
 
 // Softmax cross entropy: rows x [n][d] against classes w [v][d].
 struct XentParams {

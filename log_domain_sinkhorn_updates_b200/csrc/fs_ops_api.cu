@@ -100,8 +100,8 @@ fs_status check_attn(const fs_attn_desc *D, bool grad) {
         return reject(FS_ERR_INVALID_ARG, "strides must be >= 0");
     if ((long long)D->batch * D->heads > 65535)
         return reject(FS_ERR_UNSUPPORTED, "batch * heads exceeds 65535");
-    if ((long long)D->n * D->heads >= 1ll << 30 || D->m >= 1 << 30)
-        return reject(FS_ERR_UNSUPPORTED, "n * heads or m is 2^30 or more");
+    if ((long long)D->n * D->heads >= 1ll << 27 || D->m >= 1 << 30)
+        return reject(FS_ERR_UNSUPPORTED, "n * heads is 2^27 or more, or m 2^30 or more");
     const bool ok = grad ? distinct(D->dq, D->batch, D->n, D->heads, D->d) &&
                                distinct(D->dk, D->batch, D->m, D->kv_heads, D->d) &&
                                distinct(D->dvw, D->batch, D->m, D->kv_heads, D->dv)
@@ -402,7 +402,7 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
     if (attn_grad_tc(D, q, k, v, dout, dq, dk, dv))
         OPS_LAUNCH(fs::launch_xattn_grad_tc(p, s), 1);
     else
-        OPS_LAUNCH(fs::launch_xattn_grad_simt(p, bf16, dev.sms, s), (D.m > 0) + (D.n > 0));
+        OPS_LAUNCH(fs::launch_xattn_grad_simt(p, bf16, dev.sms, s), 1);
     return FS_OK;
 }
 

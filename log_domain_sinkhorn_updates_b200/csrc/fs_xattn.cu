@@ -305,23 +305,24 @@ __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParam
         p.lse[row_stat(p, b, c, r)] = l == 0.f ? -INFINITY : (float)(((double)mx + log2((double)l)) * kLn2d);
 }
 
-// D_i = dout_i.out_i of every (problem, query, head): `per` lanes take a row, four elements each at a time.
+// D_i = dout_i.out_i of every (query, head) of a problem: `per` lanes take a row, eight elements each at a time.
 template <class T>
 __global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p, int per, bool vec) {
-    const size_t at = ((size_t)blockIdx.x * kThreads + threadIdx.x) / per, rows = (size_t)p.batch * p.n * p.heads;
-    const int sub = threadIdx.x % per;
+    const unsigned at = (blockIdx.x * kThreads + threadIdx.x) / (unsigned)per, rows = (unsigned)(p.n * p.heads);
+    const int sub = threadIdx.x % per, b = blockIdx.y;
     const bool live = at < rows;
-    const int h = (int)(at % p.heads), i = (int)(at / p.heads % p.n), b = (int)(at / p.heads / p.n);
+    const int h = (int)(at % (unsigned)p.heads), i = (int)(at / (unsigned)p.heads);
     float s = 0.f;
     if (live) {
         const T *o = (const T *)p.out + p.os.batch * b + p.os.token * i + p.os.head * h;
         const T *g = (const T *)p.dout + p.dos.batch * b + p.dos.token * i + p.dos.head * h;
-        for (int k = 4 * sub; k < p.dv; k += 4 * per) {
-            if (vec && k + 4 <= p.dv) {
-                const float4 x = load4(o + k), y = load4(g + k);
-                s = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
+        for (int k = 8 * sub; k < p.dv; k += 8 * per) {
+            if (vec && k + 8 <= p.dv) {
+                const float4 x0 = load4(o + k), x1 = load4(o + k + 4), y0 = load4(g + k), y1 = load4(g + k + 4);
+                s = fmaf(x0.x, y0.x, fmaf(x0.y, y0.y, fmaf(x0.z, y0.z, fmaf(x0.w, y0.w, s))));
+                s = fmaf(x1.x, y1.x, fmaf(x1.y, y1.y, fmaf(x1.z, y1.z, fmaf(x1.w, y1.w, s))));
             } else {
-                for (int u = k; u < min(k + 4, p.dv); ++u) s = fmaf(to_f(o[u]), to_f(g[u]), s);
+                for (int u = k; u < min(k + 8, p.dv); ++u) s = fmaf(to_f(o[u]), to_f(g[u]), s);
             }
         }
     }
@@ -333,10 +334,9 @@ __global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p,
 // Otherwise: 16 U packed rows (Q, dO) against streamed keys (K, V): dq.  16 x 16 threads: U kept rows x 2 streamed
 // ones of the scores, U kept rows x 4 columns a piece of the sums.
 template <class T, bool KEYS, int U, int C>
-__global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnParams p, bool vec) {
-    extern __shared__ __align__(16) float sm[];
+__device__ void grad_pass(const AttnParams &p, bool vec, int block, float *sm) {
     constexpr int LS = kStream + 4, kKept = 16 * U;
-    const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads, t0 = blockIdx.x * kKept;
+    const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads, t0 = block * kKept;
     const int ld = smem_stride(p.d), lv = smem_stride(p.dv);
     float *a1 = sm, *a2 = a1 + kKept * ld, *b1 = a2 + kKept * lv, *b2 = b1 + kStream * ld, *sP = b2 + kStream * lv;
     float *sS = sP + kKept * LS, *kb = sS + kKept * LS;  // kept: bias, or base-2 LSE and D
@@ -430,6 +430,16 @@ __global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnPara
     }
 }
 
+// Both passes in one launch: key_blocks CTAs of the first, then those of the second.
+template <class T, int U, int C>
+__global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnParams p, bool vec, int key_blocks) {
+    extern __shared__ __align__(16) float sm[];
+    if ((int)blockIdx.x < key_blocks)
+        grad_pass<T, true, U, C>(p, vec, (int)blockIdx.x, sm);
+    else
+        grad_pass<T, false, U, C>(p, vec, (int)blockIdx.x - key_blocks, sm);
+}
+
 template <class K>
 cudaError_t with_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
@@ -463,33 +473,29 @@ cudaError_t fwd_rows(const AttnParams &p, int sms, cudaStream_t s) {
     return xattn_simt_rows(p.n * p.group, p.batch * p.kv_heads, sms) == 16 ? fwd_width<T, 1>(p, s) : fwd_width<T, 4>(p, s);
 }
 
-template <class T, bool KEYS, int U, int C>
-cudaError_t grad_pass(const AttnParams &p, cudaStream_t s) {
+template <class T, int U, int C>
+cudaError_t grad(const AttnParams &p, cudaStream_t s) {
     constexpr int kept = 16 * U;
-    const int w = smem_stride(p.d) + smem_stride(p.dv), count = KEYS ? p.m : p.n * p.group;
-    if (count == 0) return cudaSuccess;
+    const int w = smem_stride(p.d) + smem_stride(p.dv);
+    const int key_blocks = (p.m + kept - 1) / kept, row_blocks = (p.n * p.group + kept - 1) / kept;
     const size_t smem = sizeof(float) * ((size_t)(kept + kStream) * w + 2 * kept * (kStream + 4) + 2 * kept + 2 * kStream);
-    cudaError_t e = with_smem(xattn_grad_kernel<T, KEYS, U, C>, smem);
+    cudaError_t e = with_smem(xattn_grad_kernel<T, U, C>, smem);
     if (e != cudaSuccess) return e;
     const bool vec = aligned4<T>(p.q, p.qs) && aligned4<T>(p.k, p.ks) && aligned4<T>(p.v, p.vs) &&
                      aligned4<T>(p.dout, p.dos);
-    xattn_grad_kernel<T, KEYS, U, C>
-        <<<dim3((count + kept - 1) / kept, p.batch * p.kv_heads), kTileThreads, smem, s>>>(p, vec);
+    xattn_grad_kernel<T, U, C>
+        <<<dim3(key_blocks + row_blocks, p.batch * p.kv_heads), kTileThreads, smem, s>>>(p, vec, key_blocks);
     return cudaGetLastError();
 }
-template <class T, bool KEYS>
-cudaError_t grad_width(const AttnParams &p, int sms, cudaStream_t s) {
+template <class T, int U>
+cudaError_t grad_width(const AttnParams &p, cudaStream_t s) {
     const int w = p.d > p.dv ? p.d : p.dv;
-    if (xattn_simt_rows(KEYS ? p.m : p.n * p.group, p.batch * p.kv_heads, sms) == 16)
-        return w <= 64 ? grad_pass<T, KEYS, 1, 1>(p, s) : w <= 128 ? grad_pass<T, KEYS, 1, 2>(p, s)
-                                                                   : grad_pass<T, KEYS, 1, 4>(p, s);
-    return w <= 64 ? grad_pass<T, KEYS, 4, 1>(p, s) : w <= 128 ? grad_pass<T, KEYS, 4, 2>(p, s)
-                                                               : grad_pass<T, KEYS, 4, 4>(p, s);
+    return w <= 64 ? grad<T, U, 1>(p, s) : w <= 128 ? grad<T, U, 2>(p, s) : grad<T, U, 4>(p, s);
 }
 template <class T>
-cudaError_t grad(const AttnParams &p, int sms, cudaStream_t s) {
-    const cudaError_t e = grad_width<T, true>(p, sms, s);
-    return e != cudaSuccess ? e : grad_width<T, false>(p, sms, s);
+cudaError_t grad_rows(const AttnParams &p, int sms, cudaStream_t s) {
+    return xattn_simt_rows(p.m + p.n * p.group, p.batch * p.kv_heads, sms) == 16 ? grad_width<T, 1>(p, s)
+                                                                               : grad_width<T, 4>(p, s);
 }
 
 }  // namespace
@@ -505,9 +511,9 @@ cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s)
 }
 cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s) {
     int per = 1;
-    while (per < 32 && 4 * per < p.dv) per *= 2;
-    const size_t threads = (size_t)p.batch * p.n * p.heads * per;
-    const unsigned grid = (unsigned)((threads + kThreads - 1) / kThreads);
+    while (per < 32 && 8 * per < p.dv) per *= 2;
+    const unsigned long long threads = (unsigned long long)p.n * p.heads * per;  // below 2^32: n heads < 2^27
+    const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), p.batch);
     if (bf16)
         xattn_dot_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(
             p, per, aligned4<__nv_bfloat16>(p.out, p.os) && aligned4<__nv_bfloat16>(p.dout, p.dos));
@@ -517,7 +523,7 @@ cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s) {
     return cudaGetLastError();
 }
 cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s) {
-    return bf16 ? grad<__nv_bfloat16>(p, sms, s) : grad<float>(p, sms, s);
+    return bf16 ? grad_rows<__nv_bfloat16>(p, sms, s) : grad_rows<float>(p, sms, s);
 }
 
 }  // namespace fs
