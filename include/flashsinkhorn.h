@@ -430,7 +430,7 @@ typedef struct {
     int heads, kv_heads;      /* heads is a multiple of kv_heads                      */
     int d, dv;                /* widths of q and k, and of v and out (1 to 256)       */
     fs_dtype dtype;           /* FS_F32 (plain fp32 products) or FS_BF16              */
-    float scale;              /* score scale, finite and > 0                          */
+    float scale;              /* score scale, > 0, finite times log2(e)               */
     fs_view q, k, v, out;     /* strides                                              */
     fs_view dout, dq, dk, dvw; /* strides of the gradient's tensors (dvw: of dv);
                                  read by fs_cross_attn_grad only                      */
@@ -481,7 +481,8 @@ typedef struct {
     int n, v, d;              /* rows (0 allowed), classes, width                      */
     fs_dtype dtype;           /* FS_F32 (products of three bf16 planes each, good to
                                  about 2^-22 of their terms) or FS_BF16              */
-    float scale;              /* logit scale (inverse temperature), finite and > 0     */
+    float scale;              /* logit scale (inverse temperature), > 0, finite times
+                                 log2(e)                                              */
     long long ldx, ldw;       /* row strides of x and w                                */
     long long lddx, lddw;     /* row strides of dx and dw; read by the gradient only   */
     long long ignore_index;   /* target value of rows that are not counted             */
@@ -501,7 +502,7 @@ FS_API size_t fs_cross_entropy_workspace(const fs_xent_desc *desc, const void *x
  * any other target outside 0..v-1 gives loss NaN, without a read out of range.
  * Asynchronous.  Errors: FS_ERR_INVALID_ARG (sizes, scale, strides, null
  * pointers, a workspace that is too small), FS_ERR_UNSUPPORTED (device not
- * compute capability 10.x; v over 2^22 or d over 65536; n of 2^30 or more).
+ * compute capability 10.x; v over 2^22, d over 65536 or n over 2^24).
  */
 FS_API fs_status fs_cross_entropy(const fs_xent_desc *desc, const void *x, const void *w, const long long *target,
                                   float *loss, float *lse, void *workspace, size_t workspace_bytes, void *stream);

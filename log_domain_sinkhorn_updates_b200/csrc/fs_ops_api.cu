@@ -84,6 +84,8 @@ bool distinct(const fs_view &s, int batch, int tokens, int heads, int w) {
 }
 bool nonneg(const fs_view &s) { return s.batch >= 0 && s.token >= 0 && s.head >= 0; }
 
+bool scale_ok(float s) { return s > 0.f && std::isfinite(s * fs::kLog2e); }
+
 // ------------------------------------------------------------------ cross attention
 fs_status check_attn(const fs_attn_desc *D, bool grad) {
     if (!D) return reject(FS_ERR_INVALID_ARG, "null descriptor");
@@ -93,8 +95,7 @@ fs_status check_attn(const fs_attn_desc *D, bool grad) {
     if (D->d < 1 || D->dv < 1 || D->d > 256 || D->dv > 256)
         return reject(FS_ERR_INVALID_ARG, "d and dv must be 1 to 256");
     if (D->dtype != FS_F32 && D->dtype != FS_BF16) return reject(FS_ERR_INVALID_ARG, "unknown dtype");
-    if (!(D->scale > 0.f) || !std::isfinite(D->scale))
-        return reject(FS_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (!scale_ok(D->scale)) return reject(FS_ERR_INVALID_ARG, "scale must be > 0, and finite times log2(e)");
     if (!nonneg(D->q) || !nonneg(D->k) || !nonneg(D->v) || !nonneg(D->out) ||
         (grad && (!nonneg(D->dout) || !nonneg(D->dq) || !nonneg(D->dk) || !nonneg(D->dvw))))
         return reject(FS_ERR_INVALID_ARG, "strides must be >= 0");
@@ -226,13 +227,12 @@ fs_status check_xent(const fs_xent_desc *D, bool grad) {
     if (!D) return reject(FS_ERR_INVALID_ARG, "null descriptor");
     if (D->n < 0 || D->v < 1 || D->d < 1) return reject(FS_ERR_INVALID_ARG, "n must be >= 0, v and d >= 1");
     if (D->dtype != FS_F32 && D->dtype != FS_BF16) return reject(FS_ERR_INVALID_ARG, "unknown dtype");
-    if (!(D->scale > 0.f) || !std::isfinite(D->scale))
-        return reject(FS_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (!scale_ok(D->scale)) return reject(FS_ERR_INVALID_ARG, "scale must be > 0, and finite times log2(e)");
     if (D->ldx < 0 || D->ldw < 0) return reject(FS_ERR_INVALID_ARG, "row strides must be >= 0");
     if (grad && ((D->n > 1 && D->lddx < D->d) || (D->v > 1 && D->lddw < D->d)))
         return reject(FS_ERR_INVALID_ARG, "an output's row stride is below d");
-    if (D->v > 1 << 22 || D->d > 65536 || D->n >= 1 << 30)
-        return reject(FS_ERR_UNSUPPORTED, "v over 2^22, d over 65536 or n of 2^30 or more");
+    if (D->v > 1 << 22 || D->d > 65536 || D->n > 1 << 24)
+        return reject(FS_ERR_UNSUPPORTED, "v over 2^22, d over 65536 or n over 2^24");
     return FS_OK;
 }
 

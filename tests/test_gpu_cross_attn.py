@@ -68,6 +68,9 @@ SIZES = [
     (1, 20, 70, 2, 1, 256, 256),
     (1, 400, 20, 2, 2, 128, 96),
     (1, 513, 384, 7, 7, 72, 72),
+    (1, 30, 100, 2, 1, 64, 200),
+    (1, 140, 200, 2, 1, 128, 8),
+    (2, 100, 90, 3, 3, 8, 64),
     # enough heads that one CTA walks many tiles: one row block a CTA, and two
     (1, 128, 650, 100, 100, 32, 32),
     (2, 40, 900, 60, 60, 128, 128),
@@ -219,6 +222,92 @@ def test_same_bits_again_on_another_stream_and_in_a_graph(dtype, n):
     for other in (b, c, *outs):
         for name in a:
             assert torch.equal(a[name], other[name]), name
+
+
+@pytest.mark.parametrize("m", [100, 3000])
+def test_without_lse_and_with_a_workspace_of_its_own(m):
+    fs = _fs()
+    q, k, v, _ = make(2, 1, m, 8, 2, 64, 64, BF16, seed=31)
+    want, _ = forward(q, k, v)
+    out = torch.zeros_like(q)
+    need = fs.fs_cross_attn_workspace(q, k, v, out)
+    ws = torch.full((need + 1024,), 255, dtype=torch.uint8, device="cuda")
+    fs.fs_cross_attn(q, k, v, out, workspace=ws)
+    assert torch.equal(out, want)
+    assert (ws[need:] == 255).all()  # nothing behind it
+    if need:
+        with pytest.raises(fs.FsError):  # not on 256 bytes
+            fs.fs_cross_attn(q, k, v, out, workspace=ws[8:])
+
+
+def test_calls_at_once_on_two_streams():
+    fs = _fs()
+    sets = [make(2, 70, 900, 8, 4, 64, 64, BF16, seed=s) for s in (1, 2)]
+    want = [run(*t) for t in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (t, s) in enumerate(zip(sets, streams)):
+            with torch.cuda.stream(s):
+                out, lse = forward(*t[:3])
+                got[i].append([out, lse, *gradient(*t[:3], out, lse, t[3])])
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for r in runs:
+            assert all(torch.equal(a, b) for a, b in zip(w.values(), r))
+
+
+def test_offsets_past_32_bits():
+    """Keys and values of more than 2^31 elements each; only the last ones count, so a wrong offset shows."""
+    m, Hk, d = 1_100_000, 16, 128
+    k = torch.zeros(1, m, Hk, d, dtype=BF16, device="cuda")
+    v = torch.full_like(k, math.nan)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    tail = 300
+    k[:, -tail:] = torch.randn(1, tail, Hk, d, device="cuda", generator=g).to(BF16)
+    v[:, -tail:] = torch.randn(1, tail, Hk, d, device="cuda", generator=g).to(BF16)
+    q = torch.randn(1, 1, 2 * Hk, d, device="cuda", generator=g).to(BF16)
+    bias = torch.full((1, m), -math.inf, device="cuda")
+    bias[:, -tail:] = 0.0
+    out, lse = forward(q, k, v, bias=bias)
+    ref.check({"out": out, "lse": lse}, ref.attention(q, k[:, -tail:], v[:, -tail:]))
+    dout = torch.randn(q.shape, device="cuda", generator=g).to(BF16)
+    dq, dk, dv = gradient(q, k, v, out, lse, dout, bias=bias)
+    want = ref.attention(q, k[:, -tail:], v[:, -tail:], dout=dout)
+    ref.check({"dq": dq, "dk": dk[:, -tail:], "dv": dv[:, -tail:]}, want)
+    assert (dk[:, :-tail] == 0).all() and (dv[:, :-tail] == 0).all()
+
+
+FIRST_IN_CAPTURE = """
+import torch
+import log_domain_sinkhorn_updates_b200 as fs
+q = torch.randn(1, 3, 2, 64, device="cuda", dtype=torch.bfloat16)
+k = torch.randn(1, 500, 2, 64, device="cuda", dtype=torch.bfloat16)
+out, lse = torch.zeros_like(q), torch.zeros(1, 2, 3, device="cuda")
+x, w = torch.randn(5, 64, device="cuda"), torch.randn(70, 64, device="cuda")
+t, loss, z = torch.zeros(5, dtype=torch.long, device="cuda"), torch.zeros(5, device="cuda"), torch.zeros(5, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    fs.fs_cross_attn(q, k, k, out, lse)
+    fs.fs_cross_entropy(x, w, t, loss, z)
+g.replay()
+torch.cuda.synchronize()
+want = torch.softmax(torch.einsum("bihd,bjhd->bhij", q.float(), k.float()) / 8, -1)
+want = torch.einsum("bhij,bjhd->bihd", want, k.float())
+assert (out.float() - want).abs().max() < 0.05 and (z - torch.logsumexp(x @ w.t(), 1)).abs().max() < 1e-3
+print("captured")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout[-500:] + r.stderr[-1500:]
 
 
 def test_gradient_against_differences():

@@ -105,6 +105,9 @@ def test_strides(dtype):
     odd = torch.full((n, d + 1), math.nan, dtype=dtype, device="cuda")
     odd[:, 1:] = x
     ref.check(run(odd[:, 1:], w, target, dloss), want)
+    oddw = torch.full((v * (d + 1) + 1,), math.nan, dtype=dtype, device="cuda")[1:].view(v, d + 1)
+    oddw[:, :d] = w
+    ref.check(run(x, oddw[:, :d], target, dloss), want)
     xe = x[:1].expand(n, -1)
     ref.check(run(xe, w, target, dloss), ref.cross_entropy(xe, w, target, dloss=dloss))
     loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
@@ -166,6 +169,49 @@ def test_several_pieces_of_the_vocabulary(dtype):
     # counts (4000 + 64) U
     bound = bound * ((n + 64) / 4064 if dtype == F32 else 1.5)
     ref.check({"dw": got["dw"]}, {"dw": (val, bound)})
+
+
+@pytest.mark.parametrize("size", [(3, 1500, 40000, F32), (2, 5000, 40001, BF16)])
+def test_wide_rows_copied_in_several_pieces(size):
+    n, v, d, dtype = size
+    x, w, target, dloss = make(n, v, d, dtype, seed=14, ignored=False)
+    target[0] = v - 1
+    ref.check(run(x, w, target, dloss), ref.cross_entropy(x, w, target, dloss=dloss))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 class weights.  The classes but the last few repeat one row, so the 64-bit sums are short."""
+    fs = _fs()
+    v, d, tail, n = 1_100_000, 2048, 300, 3
+    g = torch.Generator(device="cuda").manual_seed(2)
+    row = torch.randn(1, d, device="cuda", generator=g).to(BF16) / 32
+    w = row.expand(v, d).contiguous()
+    w[-tail:] = (torch.randn(tail, d, device="cuda", generator=g) / 32).to(BF16)
+    x = torch.randn(n, d, device="cuda", generator=g).to(BF16)
+    target = torch.tensor([v - 1, v - tail, 5], device="cuda")
+    dloss = torch.ones(n, device="cuda")
+    got = run(x, w, target, dloss)
+    z0, zt = x.double() @ row[0].double(), x.double() @ w[-tail:].double().t()
+    lse = torch.logaddexp(z0 + math.log(v - tail), torch.logsumexp(zt, 1))
+    hit = torch.stack([zt[0, -1], zt[1, 0], z0[2]])
+    # the sum over 4297 tiles of 256: (256 + 4297 + 16) U; logits below 8 of 2048 terms of size below 60 together
+    tol = (256 + 4297 + 16) * ref.U + 2 * (d + 8) * ref.U * 60
+    assert (got["lse"] - lse).abs().max() <= tol and (got["loss"] - (lse - hit)).abs().max() <= 2 * tol
+    pt = torch.exp(zt - lse[:, None])
+    pt[0, -1] -= 1.0
+    pt[1, 0] -= 1.0
+    p0 = torch.exp(z0 - lse)
+    want = pt.t() @ x.double()
+    lim = (4 * ref.BF + 2 * tol) * (pt.abs().t() @ x.double().abs()) + 1e-9
+    assert ((got["dw"][-tail:].double() - want).abs() <= lim).all()
+    one = p0 @ x.double()
+    lim0 = (4 * ref.BF + 2 * tol) * (p0 @ x.double().abs())
+    assert ((got["dw"][6:-tail:1000].double() - one).abs() <= lim0).all()
+    dx = pt @ w[-tail:].double() + ((v - tail) * p0)[:, None] * row.double()
+    dx[2] -= row[0].double()
+    # every p is rounded to bf16, and the fp32 sums run over at most 1.1e6 terms of one sign a column in parts
+    size = pt.abs() @ w[-tail:].double().abs() + ((v - tail) * p0 + 1)[:, None] * row.double().abs()
+    assert ((got["dx"].double() - dx).abs() <= (4 * ref.BF + 2 * tol + v / 16 * ref.U) * size).all()
 
 
 def test_no_rows():

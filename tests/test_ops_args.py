@@ -29,7 +29,7 @@ def _attn(**kw):
 
 BAD_ATTN = [dict(batch=-1), dict(n=-1), dict(m=-1), dict(heads=0), dict(kv_heads=0), dict(heads=3), dict(d=0),
             dict(d=257), dict(dv=0), dict(dv=300), dict(dtype=2), dict(dtype=-1), dict(scale=0.0), dict(scale=-1.0),
-            dict(scale=float("nan")), dict(scale=float("inf")), dict(k=(-1, 64, 64)), dict(q=(0, -8, 64))]
+            dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(k=(-1, 64, 64)), dict(q=(0, -8, 64))]
 # of the forward's out, and of the gradient's dq, dk and dv: elements on top of one another
 BAD_VIEWS = [(0, 256, 64), (1280, 0, 64), (1280, 256, 0), (1280, 256, 63), (1279, 256, 64), (1280, 255, 64)]
 
@@ -100,13 +100,13 @@ def test_cross_entropy_descriptors(L):
 
     assert forward(None) == FS_ERR_INVALID_ARG and grad(None) == FS_ERR_INVALID_ARG
     for kw in [dict(n=-1), dict(v=0), dict(d=0), dict(dtype=5), dict(scale=0.0), dict(scale=-2.0),
-               dict(scale=float("nan")), dict(scale=float("inf")), dict(ldx=-1), dict(ldw=-64)]:
+               dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(ldx=-1), dict(ldw=-64)]:
         assert forward(_xent(**kw)) == FS_ERR_INVALID_ARG, kw
         assert grad(_xent(**kw)) == FS_ERR_INVALID_ARG, kw
         assert L.fs_cross_entropy_workspace(ctypes.byref(_xent(**kw)), None, None, 1) == 0
     for kw in [dict(lddx=63), dict(lddw=0)]:
         assert grad(_xent(**kw)) == FS_ERR_INVALID_ARG, kw
-    for kw in [dict(v=(1 << 22) + 1), dict(d=65537), dict(n=1 << 30)]:
+    for kw in [dict(v=(1 << 22) + 1), dict(d=65537), dict(n=(1 << 24) + 1)]:
         assert forward(_xent(lddx=1 << 17, lddw=1 << 17, **kw)) == FS_ERR_UNSUPPORTED, kw
     for null in range(5):
         assert forward(_xent(), null) == FS_ERR_INVALID_ARG
