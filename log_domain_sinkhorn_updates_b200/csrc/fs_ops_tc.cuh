@@ -127,19 +127,19 @@ __device__ __forceinline__ void stage_packed(uint8_t *dst, const void *src, cons
                                    (((ch & 7) ^ (row & 7)) << 4)) = v;
     }
 }
-// Zeroes the rows of a tile (`rows` x 64-element columns, `atoms` of them) whose bit of dead[row / 32] is set.
-// By one warp.
-__device__ __forceinline__ void clear_rows(uint8_t *tile, int rows, int atoms, const unsigned *dead, int lane) {
-    for (int e = lane; e < rows * 8; e += 32) {
-        const int row = e >> 3;
-        unsigned word = dead[0];
-        for (int u = 1; u < rows / 32; ++u)
-            if (row / 32 == u) word = dead[u];
-        if (word >> (row & 31) & 1u)
+// Zeroes the rows of a tile (ROWS x 64-element columns, `atoms` of them) whose bit of dead[row / 32] is set.  By one
+// warp: a lane takes its rows whole (each starting at another piece, so that they lie in different banks), and a tile
+// with few masked rows costs few stores.
+template <int ROWS>
+__device__ __forceinline__ void clear_rows(uint8_t *tile, int atoms, const unsigned (&dead)[ROWS / 32], int lane) {
+#pragma unroll
+    for (int u = 0; u < ROWS / 32; ++u)
+        if (dead[u] >> lane & 1u)
             for (int a = 0; a < atoms; ++a)
-                *reinterpret_cast<uint4 *>(tile + a * rows * 128 + row * 128 + (e & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-    }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<uint4 *>(tile + a * ROWS * 128 + (32 * u + lane) * 128 + ((k + lane) & 7) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
 }
 
 }  // namespace tc

@@ -173,36 +173,31 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                 dead[u] = __ballot_sync(~0u, attn_bias2(p, b, r0 + 32 * u + lane, keys) == -INFINITY);
             if (!mbar_wait_near(stfull, 0, p.timeout_ns)) ok = false;
             if (dead[0] | dead[1] | dead[2] | dead[3]) {
-                clear_rows(st1, 128, kAtoms, dead, lane);
-                clear_rows(st2, 128, kAtoms, dead, lane);
+                clear_rows<128>(st1, kAtoms, dead, lane);
+                clear_rows<128>(st2, kAtoms, dead, lane);
                 fence_async();
                 __syncwarp();
             }
             if (lane == 0) mbar_arrive(stready);
         }
         RingPos rp{0, 0};
-        int i0 = 0, h = c * p.group;  // KEYS: first query and head of the tile
-        for (int t = 0; ok && t < nt; ++t) {
-            const int j = t % kColSlots;
-            float *col = sCols + j * 2 * kTile;
-            float v0[2], v1[2] = {0.f, 0.f};
-            unsigned dead[2] = {0u, 0u};
-            bool any = !KEYS && p.bias != nullptr;
+        int i0 = 0, h = c * p.group;  // KEYS: first query and head of the next tile
+        // KEYS: -L (base 2) and -D of a query; one without a key, or past the end, gives P = 0.  ROWS: a key's bias.
+        float n0[2], n1[2] = {0.f, 0.f};  // read a tile ahead
+        auto fetch = [&](int t) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                if (KEYS) {  // -L (base 2) and -D; a row without a key, or past the end, gives P = 0
+                if (KEYS) {
                     const int i = i0 + 32 * u + lane;
-                    v0[u] = -INFINITY;
-                    if (i < p.n) {
+                    n0[u] = -INFINITY;
+                    n1[u] = 0.f;
+                    if (t < nt && i < p.n) {
                         const size_t at = ((size_t)b * p.heads + h) * p.n + i;
-                        const float l = __ldg(p.lse + at);
-                        v0[u] = l == -INFINITY ? -INFINITY : -l * kLog2e;
-                        v1[u] = -__ldg(p.dot + at);
+                        n0[u] = __ldg(p.lse + at);
+                        n1[u] = __ldg(p.dot + at);
                     }
                 } else {
-                    v0[u] = attn_bias2(p, b, t * kTile + 32 * u + lane, keys);
-                    dead[u] = __ballot_sync(~0u, v0[u] == -INFINITY);
-                    any = any || dead[u];
+                    n0[u] = attn_bias2(p, b, t * kTile + 32 * u + lane, keys);
                 }
             }
             i0 += kTile;
@@ -210,6 +205,24 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                 i0 = 0;
                 ++h;
             }
+        };
+        fetch(0);
+        for (int t = 0; ok && t < nt; ++t) {
+            const int j = t % kColSlots;
+            float *col = sCols + j * 2 * kTile;
+            float v0[2], v1[2];
+            unsigned dead[2] = {0u, 0u};
+            bool any = !KEYS && p.bias != nullptr;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                v0[u] = KEYS ? (n0[u] == -INFINITY ? -INFINITY : -n0[u] * kLog2e) : n0[u];
+                v1[u] = -n1[u];
+                if (!KEYS) {
+                    dead[u] = __ballot_sync(~0u, v0[u] == -INFINITY);
+                    any = any || dead[u];
+                }
+            }
+            fetch(t + 1);
             if (t >= kColSlots && !mbar_wait_near(cempty + j, ((uint32_t)(t / kColSlots) & 1u) ^ 1u, p.timeout_ns)) ok = false;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -225,8 +238,8 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                 rp.step(1, NS);
                 if (dead[0] | dead[1]) {
                     uint8_t *tile = ring + (size_t)s * 2 * L.half;
-                    clear_rows(tile, kTile, kAtoms, dead, lane);
-                    clear_rows(tile + L.half, kTile, kAtoms, dead, lane);
+                    clear_rows<kTile>(tile, kAtoms, dead, lane);
+                    clear_rows<kTile>(tile + L.half, kAtoms, dead, lane);
                     fence_async();
                     __syncwarp();
                 }

@@ -204,14 +204,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- bias slices and masked rows ----------------
         bool ok = true;
         RingPos rp{0, 0};
+        float bv[kTS / 32], next[kTS / 32];  // base-2 bias of a tile's keys, read a tile ahead
+#pragma unroll
+        for (int u = 0; u < kTS / 32; ++u) next[u] = attn_bias2(p, b, j_beg + 32 * u + lane, j_end);
         for (int t = 0; ok && t < nt; ++t) {
             const int j = t % kBiasSlots;
-            float bv[kTS / 32];
             unsigned dead[kTS / 32], cleared = 0;
             bool any = p.bias != nullptr;
 #pragma unroll
             for (int u = 0; u < kTS / 32; ++u) {
-                bv[u] = attn_bias2(p, b, j_beg + t * kTS + 32 * u + lane, j_end);
+                bv[u] = next[u];
+                next[u] = attn_bias2(p, b, j_beg + (t + 1) * kTS + 32 * u + lane, j_end);
                 dead[u] = __ballot_sync(~0u, bv[u] == -INFINITY);
                 cleared |= dead[u];
             }
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 rp.step(1, NS);
                 if (cleared) {
                     uint8_t *tile = ring + (size_t)s * L.slot;
-                    clear_rows(tile, kTS, kv ? g.vatoms : g.datoms, dead, lane);
+                    clear_rows<kTS>(tile, kv ? g.vatoms : g.datoms, dead, lane);
                     fence_async();
                     __syncwarp();
                 }
