@@ -26,10 +26,12 @@ struct AttnParams {
     void *out, *dq, *dk, *dv_out;
     float *lse;           // [batch][heads][n], natural log (out of the forward, into the gradient); may be null forward
     float *dot;           // gradient: [batch][heads][n], D_i = dout_i.out_i
-    int splits;           // parts of the key axis (forward)
-    int split_keys;       // keys of a part
-    float *part_o;        // [splits][batch][kv_heads][n group][dv], relative to part_ml's maximum
-    float2 *part_ml;      // [splits][batch][kv_heads][n group]: running max (base 2) and sum
+    // Forward: a unit is unit_rows packed rows of a key head.  Units from main_units on are split over their keys into
+    // `splits` parts of split_keys keys, a CTA each, which the joining pass adds up; 1: no unit is.
+    int unit_rows, blocks;   // and the units of a head
+    int main_units, tail_units, splits, split_keys;
+    float *part_o;           // [splits][tail_units][unit_rows][dv], relative to part_ml's maximum
+    float2 *part_ml;         // [splits][tail_units][unit_rows]: reference (base 2) and sum
     unsigned long long timeout_ns;
     int *err;
 };
@@ -55,6 +57,28 @@ cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, int threads, size_
 // Valid keys of problem b.
 __device__ __forceinline__ int attn_keys(const AttnParams &p, int b) {
     return p.k_len ? min(max(__ldg(p.k_len + b), 0), p.m) : p.m;
+}
+// The work of a CTA of the forward.
+struct AttnUnit {
+    int r0, c, b;       // first packed row, key head, problem
+    int j_beg, j_end;   // its keys
+    size_t part;        // first row of part_ml and part_o, where it is a part
+    bool whole;
+};
+__device__ __forceinline__ AttnUnit attn_unit(const AttnParams &p) {
+    AttnUnit w;
+    const int x = blockIdx.x, t = x - p.main_units;
+    w.whole = p.splits == 1 || t < 0;
+    const int tu = w.whole ? 0 : t / p.splits, sp = w.whole ? 0 : t % p.splits;
+    const int u = w.whole ? x : p.main_units + tu;
+    w.r0 = u % p.blocks * p.unit_rows;
+    w.c = u / p.blocks % p.kv_heads;
+    w.b = u / p.blocks / p.kv_heads;
+    const int keys = attn_keys(p, w.b);
+    w.j_beg = sp * p.split_keys;
+    w.j_end = w.whole ? keys : min(keys, w.j_beg + p.split_keys);
+    w.part = ((size_t)sp * p.tail_units + tu) * p.unit_rows;
+    return w;
 }
 // Base-2 bias of key j (valid or not): -inf where it is masked.
 __device__ __forceinline__ float attn_bias2(const AttnParams &p, int b, int j, int keys) {
@@ -90,11 +114,11 @@ struct AttnGradTc {
 bool attn_tc_view(const void *base, const fs_view &s, int tokens, int heads, int batch, bool map);
 bool attn_map(CUtensorMap *map, const void *base, const fs_view &s, int w, int tokens, int heads, int batch,
               int box_rows, int *hm, int *bm);
-cudaError_t launch_xattn_tc(const AttnParams &p, bool two_blocks, cudaStream_t s);
+cudaError_t launch_xattn_tc(const AttnParams &p, cudaStream_t s);
 
 cudaError_t launch_xattn_grad_tc(const AttnParams &p, cudaStream_t s);
 
-cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s);
+cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s);

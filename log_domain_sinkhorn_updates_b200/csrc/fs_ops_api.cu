@@ -112,47 +112,57 @@ fs_status check_attn(const fs_attn_desc *D, bool grad) {
 }
 
 struct AttnPlan {
-    int splits = 1, split_keys = 0;
-    bool two_blocks = false;  // tensor cores: 256 rows a CTA
+    int unit_rows = 0, blocks = 0, main_units = 0, tail_units = 0, splits = 1, split_keys = 0;  // as in AttnParams
     size_t part_ml = 0, part_o = 0, dot = 0, total = 0;  // workspace offsets, and its size
 };
 
 AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, bool ragged, const Device &dev) {
     AttnPlan L;
     const size_t rows = (size_t)D.n * (D.heads / D.kv_heads), heads = (size_t)D.batch * D.kv_heads;
-    L.split_keys = std::max(D.m, 1);
     if (grad) {
         L.total = align256((size_t)D.batch * D.heads * D.n * 4);
         return L;
     }
     if (rows == 0 || heads == 0) return L;
-    // Rows of a CTA (tensor cores: 128, or 256 in two blocks that share every tile) and parts of the keys: what costs
-    // least, in tiles of 128 keys.  A CTA takes its tiles (two blocks: 1.28 times as long each, 2.3 us against 1.8 at
-    // width 128) and 1.5 tiles' time to start and end; waves of CTAs, one an SM (CUDA cores: two); where lengths
-    // differ, CTAs fill in behind short ones, and the tail is half a CTA instead of the rest of a wave (32 requests
-    // of up to 4096 keys: 96 us in one part, 82 in two).
-    const int slots = tc ? dev.sms : 2 * dev.sms, side = tc ? 128 : fs::xattn_simt_rows(D.n * (D.heads / D.kv_heads), (int)heads, dev.sms);
+    // Rows of a unit (tensor cores: 128, or 256 in two blocks that share every tile), and which units are split over
+    // their keys: what costs least, in tiles of 128 keys.  A CTA takes its tiles (two blocks: 1.28 times as long each,
+    // 2.3 us against 1.8 at width 128) and 1.5 tiles' time to start and end; waves of CTAs, one an SM (CUDA cores:
+    // two); where lengths differ, CTAs fill in behind short ones, and the tail is half a CTA instead of the rest of a
+    // wave (32 requests of up to 4096 keys: 96 us in one part, 82 in two).  Either every unit is split, or only those
+    // behind the last full wave, so that they fill the SMs too; the joining pass costs a launch, and the parts' sums
+    // written and read back (4 TB/s, 1.8 us a tile).
+    const int slots = tc ? dev.sms : 2 * dev.sms;
+    const int side = tc ? 128 : fs::xattn_simt_rows(D.n * (D.heads / D.kv_heads), (int)heads, dev.sms);
     const int tile = 128, tiles = up(std::max(D.m, 1), tile);
     double best = 1e300;
     for (int two = 0; two < (tc && rows > 128 ? 2 : 1); ++two) {
-        const size_t side2 = (size_t)side << two, ctas = (rows + side2 - 1) / side2 * heads;
-        for (int s = 1; s <= std::min(tiles, 128) && (s == 1 || ctas < 3 * (size_t)slots); ++s) {
+        const int unit = side << two;
+        const long long units = (long long)((rows + unit - 1) / unit * heads), rest = units % slots;
+        const double per = two ? 1.28 : 1.0;
+        auto consider = [&](long long tail, int s) {
             const int t = up(tiles, s), parts = up(tiles, t);
-            // the joining pass: a launch, and the parts' sums written and read back (4 TB/s, 1.8 us a tile)
-            const double join = 2.0 + 0.02 * parts + (double)rows * heads * parts * D.dv * 8.0 / 4e6 / 1.8;
-            const double n = (double)(ctas * parts) / slots, waves = ragged && n > 1.0 ? n + 0.5 : std::ceil(n);
-            const double cost = waves * (t * (two ? 1.28 : 1.0) + 1.5) + (parts > 1 ? join : 0.0);
+            const double join = 2.0 + 0.02 * parts + (double)tail * unit * parts * D.dv * 8.0 / 4e6 / 1.8;
+            const double n = (double)(tail * parts) / slots, waves = ragged && n > 1.0 ? n + 0.5 : std::ceil(n);
+            const double cost = (double)((units - tail) / slots) * (tiles * per + 1.5) + waves * (t * per + 1.5) +
+                                (parts > 1 ? join : 0.0);
             if (cost < best - 1e-9) {
                 best = cost;
+                L.unit_rows = unit;
+                L.blocks = (int)((rows + unit - 1) / unit);
                 L.splits = parts;
                 L.split_keys = t * tile;
-                L.two_blocks = two != 0;
+                L.tail_units = parts > 1 ? (int)tail : 0;
+                L.main_units = (int)(units - L.tail_units);
             }
-        }
+        };
+        for (int s = 1; s <= std::min(tiles, 128) && (s == 1 || units < 3ll * slots); ++s) consider(units, s);
+        if (!ragged && units > slots && rest)
+            for (int s = 2; s <= std::min(tiles, 16); ++s) consider(rest, s);
     }
     if (L.splits > 1) {
-        L.part_o = align256(rows * heads * L.splits * sizeof(float2));
-        L.total = L.part_o + align256(rows * heads * L.splits * D.dv * sizeof(float));
+        const size_t parts = (size_t)L.splits * L.tail_units * L.unit_rows;
+        L.part_o = align256(parts * sizeof(float2));
+        L.total = L.part_o + align256(parts * D.dv * sizeof(float));
     }
     return L;
 }
@@ -203,6 +213,10 @@ fs::AttnParams attn_params(const fs_attn_desc &D, const AttnPlan &L, const Devic
     p.dqs = D.dq;
     p.dks = D.dk;
     p.dvs = D.dvw;
+    p.unit_rows = L.unit_rows;
+    p.blocks = L.blocks;
+    p.main_units = L.main_units;
+    p.tail_units = L.tail_units;
     p.splits = L.splits;
     p.split_keys = L.split_keys;
     char *w = static_cast<char *>(ws);
@@ -364,9 +378,9 @@ fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const void *k, 
     p.lse = lse;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (tc)
-        OPS_LAUNCH(fs::launch_xattn_tc(p, L.two_blocks, s), 1);
+        OPS_LAUNCH(fs::launch_xattn_tc(p, s), 1);
     else
-        OPS_LAUNCH(fs::launch_xattn_simt(p, bf16, dev.sms, s), 1);
+        OPS_LAUNCH(fs::launch_xattn_simt(p, bf16, s), 1);
     if (p.splits > 1) OPS_LAUNCH(fs::launch_xattn_combine(p, bf16, s), 1);
     return FS_OK;
 }

@@ -153,13 +153,10 @@ template <class T, int RPT, int C>
 __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnParams p, bool vec) {
     extern __shared__ __align__(16) float sm[];
     constexpr int R = 16 * RPT, LP = kKeys + 4;
-    const int tiles = (p.n * p.group + R - 1) / R;
-    const int r0 = (blockIdx.x % tiles) * R, sp = blockIdx.x / tiles;
-    const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads;
+    const AttnUnit unit = attn_unit(p);
+    const int r0 = unit.r0, c = unit.c, b = unit.b, j_beg = unit.j_beg, j_end = unit.j_end;
     const int ld = smem_stride(p.d), lv = smem_stride(p.dv);
     float *sQ = sm, *sK = sQ + R * ld, *sV = sK + kKeys * ld, *sP = sV + kKeys * lv, *sB = sP + R * LP;
-    const int keys = attn_keys(p, b);
-    const int j_beg = sp * p.split_keys, j_end = min(keys, j_beg + p.split_keys);
     stage_rows<T>(sQ, p.q, p.qs, p, b, c, r0, R, p.d, vec);
     const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
     float4 o[RPT][C];
@@ -221,8 +218,8 @@ __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnPara
     for (int u = 0; u < RPT; ++u) {
         const int r = r0 + ti * RPT + u;
         if (r >= p.n * p.group) continue;
-        if (p.splits > 1) {
-            const size_t at = ((size_t)(sp * p.batch + b) * p.kv_heads + c) * p.n * p.group + r;
+        if (!unit.whole) {
+            const size_t at = unit.part + ti * RPT + u;
             if (tj == 0) p.part_ml[at] = make_float2(mx[u], l[u]);
 #pragma unroll
             for (int k = 0; k < C; ++k) put4(p.part_o + at * p.dv, o[u][k], 4 * tj + 64 * k, p.dv, 1.f);
@@ -241,11 +238,14 @@ __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnPara
 // Joins the parts of a row, in the parts' order.  One warp per packed row.
 template <class T>
 __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParams p) {
-    const size_t rows = (size_t)p.n * p.group, all = rows * p.batch * p.kv_heads;
+    const size_t all = (size_t)p.tail_units * p.unit_rows;
     const size_t at = (size_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
     if (at >= all) return;
     const int lane = threadIdx.x % 32;
-    const int r = (int)(at % rows), c = (int)(at / rows % p.kv_heads), b = (int)(at / rows / p.kv_heads);
+    const int unit = p.main_units + (int)(at / p.unit_rows);
+    const int r = unit % p.blocks * p.unit_rows + (int)(at % p.unit_rows);
+    const int c = unit / p.blocks % p.kv_heads, b = unit / p.blocks / p.kv_heads;
+    if (r >= p.n * p.group) return;
     grid_dependency_wait();
     float mx = -INFINITY;
     for (int s = lane; s < p.splits; s += 32) mx = fmaxf(mx, p.part_ml[s * all + at].x);
@@ -459,9 +459,7 @@ cudaError_t fwd(const AttnParams &p, cudaStream_t s) {
     cudaError_t e = with_smem(xattn_simt_kernel<T, RPT, C>, smem);
     if (e != cudaSuccess) return e;
     const bool vec = aligned4<T>(p.q, p.qs) && aligned4<T>(p.k, p.ks) && aligned4<T>(p.v, p.vs);
-    const int tiles = (p.n * p.group + R - 1) / R;
-    xattn_simt_kernel<T, RPT, C>
-        <<<dim3(tiles * p.splits, p.batch * p.kv_heads), kTileThreads, smem, s>>>(p, vec);
+    xattn_simt_kernel<T, RPT, C><<<p.main_units + p.tail_units * p.splits, kTileThreads, smem, s>>>(p, vec);
     return cudaGetLastError();
 }
 template <class T, int RPT>
@@ -469,8 +467,8 @@ cudaError_t fwd_width(const AttnParams &p, cudaStream_t s) {
     return p.dv <= 64 ? fwd<T, RPT, 1>(p, s) : p.dv <= 128 ? fwd<T, RPT, 2>(p, s) : fwd<T, RPT, 4>(p, s);
 }
 template <class T>
-cudaError_t fwd_rows(const AttnParams &p, int sms, cudaStream_t s) {
-    return xattn_simt_rows(p.n * p.group, p.batch * p.kv_heads, sms) == 16 ? fwd_width<T, 1>(p, s) : fwd_width<T, 4>(p, s);
+cudaError_t fwd_rows(const AttnParams &p, cudaStream_t s) {
+    return p.unit_rows == 16 ? fwd_width<T, 1>(p, s) : fwd_width<T, 4>(p, s);
 }
 
 template <class T, int U, int C>
@@ -500,11 +498,11 @@ cudaError_t grad_rows(const AttnParams &p, int sms, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s) {
-    return bf16 ? fwd_rows<__nv_bfloat16>(p, sms, s) : fwd_rows<float>(p, sms, s);
+cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s) {
+    return bf16 ? fwd_rows<__nv_bfloat16>(p, s) : fwd_rows<float>(p, s);
 }
 cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s) {
-    const size_t rows = (size_t)p.n * p.group * p.batch * p.kv_heads;
+    const size_t rows = (size_t)p.tail_units * p.unit_rows;
     const unsigned grid = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
     return bf16 ? launch_dependent(xattn_combine_kernel<__nv_bfloat16>, grid, kThreads, 0, s, p)
                 : launch_dependent(xattn_combine_kernel<float>, grid, kThreads, 0, s, p);

@@ -130,11 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rows = p.n * p.group;
-    const int blocks = (rows + QT * 128 - 1) / (QT * 128);
-    const int rb = blockIdx.x % blocks, sp = blockIdx.x / blocks;
-    const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads;
-    const int keys = attn_keys(p, b);
-    const int j_beg = sp * p.split_keys, j_end = min(keys, j_beg + p.split_keys);
+    const AttnUnit unit = attn_unit(p);
+    const int c = unit.c, b = unit.b, j_beg = unit.j_beg, j_end = unit.j_end;
     const int nt = j_end > j_beg ? (j_end - j_beg + kTS - 1) / kTS : 0;
 
     if (threadIdx.x == 0) {
@@ -319,10 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3, grp = (warp - 4) >> 2;
         const int rl = q * 32 + lane;
         const int blk = QT == 2 ? grp : 0;
-        const int r = (rb * QT + blk) * 128 + rl;  // packed row
-        const bool warp_live = (rb * QT + blk) * 128 + q * 32 < rows;
+        const int r = unit.r0 + blk * 128 + rl;  // packed row
+        const bool warp_live = unit.r0 + blk * 128 + q * 32 < rows;
         // Q into shared memory, 16 bytes at a time, as the 128-byte swizzle lays it
-        stage_packed<(KS + 3) / 4>(sQ, p.q, p.qs, p, b, c, rb * QT * 128, QT * 128, p.d, (int)threadIdx.x - 128, 256);
+        stage_packed<(KS + 3) / 4>(sQ, p.q, p.qs, p, b, c, unit.r0, QT * 128, p.d, (int)threadIdx.x - 128, 256);
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(qfull);
@@ -434,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (warp_live && (QT == 2 || grp == 0)) {
             const bool live = r < rows;
-            if (p.splits > 1) {
-                const size_t at = ((size_t)(sp * p.batch + b) * p.kv_heads + c) * rows + r;
+            if (!unit.whole) {
+                const size_t at = unit.part + blk * 128 + rl;
                 if (live) p.part_ml[at] = make_float2(m, l);
                 if (nt > 0)
                     for (int k = 0; k < p.dv; k += 16) {
@@ -505,10 +502,9 @@ cudaError_t launch(const AttnParams &p, AttnTc g, const CUtensorMap &mk, const C
     const uint32_t smem = layout(QT, g.datoms, g.vatoms, g.slots).total + 1024u;
     cudaError_t e = cudaFuncSetAttribute(xattn_tc_kernel<QT, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
     if (e != cudaSuccess) return e;
-    const int blocks = (p.n * p.group + QT * 128 - 1) / (QT * 128);
     // at least half the shared memory: a CTA holds all of TMEM, so two on one SM would wait for each other
-    xattn_tc_kernel<QT, KS><<<dim3(blocks * p.splits, p.batch * p.kv_heads), kThreads,
-                          smem > limit / 2 + 1024u ? smem : limit / 2 + 1024u, s>>>(mk, mv, p, g);
+    xattn_tc_kernel<QT, KS><<<p.main_units + p.tail_units * p.splits, kThreads,
+                              smem > limit / 2 + 1024u ? smem : limit / 2 + 1024u, s>>>(mk, mv, p, g);
     return cudaGetLastError();
 }
 
@@ -536,8 +532,8 @@ bool attn_tc_view(const void *base, const fs_view &s, int tokens, int heads, int
     return !(batch > 1 && (s.batch % 8 || s.batch >= big));
 }
 
-// two_blocks: 256 rows a CTA (p.splits = 1)
-cudaError_t launch_xattn_tc(const AttnParams &p, bool two_blocks, cudaStream_t s) {
+cudaError_t launch_xattn_tc(const AttnParams &p, cudaStream_t s) {
+    const bool two_blocks = p.unit_rows == 256;
     AttnTc g{};
     g.datoms = (p.d + 63) / 64;
     g.vatoms = (p.dv + 63) / 64;
