@@ -155,9 +155,12 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, bool ragged, const
                 L.main_units = (int)(units - L.tail_units);
             }
         };
-        for (int s = 1; s <= std::min(tiles, 128) && (s == 1 || units < 3ll * slots); ++s) consider(units, s);
+        // (numbers of parts that give the same tiles a part are one choice)
+        for (int s = 1; s <= std::min(tiles, 128) && (s == 1 || units < 3ll * slots); ++s)
+            if (s == 1 || up(tiles, s) != up(tiles, s - 1)) consider(units, s);
         if (!ragged && units > slots && rest)
-            for (int s = 2; s <= std::min(tiles, 16); ++s) consider(rest, s);
+            for (int s = 2; s <= std::min(tiles, 16); ++s)
+                if (up(tiles, s) != up(tiles, s - 1)) consider(rest, s);
     }
     if (L.splits > 1) {
         const size_t parts = (size_t)L.splits * L.tail_units * L.unit_rows;

@@ -95,7 +95,7 @@ __host__ __device__ inline Layout layout(int qt, int datoms, int vatoms, int slo
     L.bias = L.ring + (uint32_t)slots * L.slot;
     L.ml = L.bias + (uint32_t)(kBiasSlots * tile_keys(qt) * 4);
     L.bars = L.ml + 128 * 8;
-    L.total = L.bars + (3 * slots + 2 * kBiasSlots + 1 + 4 + 4 + 4 + 2) * 8 + 32;
+    L.total = L.bars + (3 * slots + 2 * kBiasSlots + 1 + 4 + 4 + 4 + 2) * 8 + 8;
     return L;
 }
 
@@ -126,13 +126,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *drain = pvdone + 4;   // [2] every MMA of issuer g is complete
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    volatile int *tile_masked = reinterpret_cast<volatile int *>(tmem_holder + 2);  // [kBiasSlots]
 
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rows = p.n * p.group;
     const AttnUnit unit = attn_unit(p);
     const int c = unit.c, b = unit.b, j_beg = unit.j_beg, j_end = unit.j_end;
     const int nt = j_end > j_beg ? (j_end - j_beg + kTS - 1) / kTS : 0;
+    // tiles whose scores take a bias from shared memory: all, or only the one that the keys end in
+    auto masked_tile = [&](int t) { return p.bias != nullptr || j_beg + (t + 1) * kTS > j_end; };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -201,13 +202,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- bias slices and masked rows ----------------
         bool ok = true;
         RingPos rp{0, 0};
+        RingPos bs{0, 0};
+        int used = 0;
         float bv[kTS / 32], next[kTS / 32];  // base-2 bias of a tile's keys, read a tile ahead
 #pragma unroll
         for (int u = 0; u < kTS / 32; ++u) next[u] = attn_bias2(p, b, j_beg + 32 * u + lane, j_end);
         for (int t = 0; ok && t < nt; ++t) {
-            const int j = t % kBiasSlots;
             unsigned dead[kTS / 32], cleared = 0;
-            bool any = p.bias != nullptr;
 #pragma unroll
             for (int u = 0; u < kTS / 32; ++u) {
                 bv[u] = next[u];
@@ -215,14 +216,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 dead[u] = __ballot_sync(~0u, bv[u] == -INFINITY);
                 cleared |= dead[u];
             }
-            any = any || cleared;
-            if (t >= kBiasSlots && !mbar_wait_near(bempty + j, ((uint32_t)(t / kBiasSlots) & 1u) ^ 1u, p.timeout_ns))
-                ok = false;
+            if (masked_tile(t)) {
+                if (used >= kBiasSlots && !mbar_wait_near(bempty + bs.slot, bs.phase ^ 1u, p.timeout_ns)) ok = false;
 #pragma unroll
-            for (int u = 0; u < kTS / 32; ++u) sBias[j * kTS + 32 * u + lane] = bv[u];
-            if (lane == 0) tile_masked[j] = any;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bfull + j);
+                for (int u = 0; u < kTS / 32; ++u) sBias[bs.slot * kTS + 32 * u + lane] = bv[u];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bfull + bs.slot);
+                bs.step(1, kBiasSlots);
+                ++used;
+            }
             for (int kv = 0; kv < 2; ++kv) {
                 const int s = rp.slot;
                 if (!mbar_wait_near(full + s, rp.phase, p.timeout_ns)) ok = false;
@@ -331,12 +333,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         int i = 0;  // steps of this group done
         for (int t = QT == 2 ? 0 : grp; ok && t < nt; t += QT == 2 ? 1 : 2) {
-            const int j = t % kBiasSlots;
-            if (!mbar_wait_near(bfull + j, (uint32_t)(t / kBiasSlots) & 1u, p.timeout_ns)) {
+            const bool masked = masked_tile(t);
+            const int j = masked && p.bias ? t % kBiasSlots : 0;
+            if (masked && !mbar_wait_near(bfull + j, p.bias ? (uint32_t)(t / kBiasSlots) & 1u : 0u, p.timeout_ns)) {
                 ok = false;
                 break;
             }
-            const bool masked = tile_masked[j];
 #pragma unroll 1
             for (int h = 0; h < kSteps; ++h, ++i) {
                 const int u = i & 1;
@@ -391,8 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             __syncwarp();
-            if (lane == 0) mbar_arrive(bempty + j);
-            if (*abort_flag) break;
+            if (masked && lane == 0) mbar_arrive(bempty + j);
         }
         if (ok && i > 0 && !mbar_wait_near(pvdone + 2 * grp + ((i - 1) & 1), (uint32_t)((i - 1) >> 1) & 1u, p.timeout_ns))
             ok = false;
