@@ -44,6 +44,8 @@ using namespace tc;
 constexpr int kStep = 64;       // keys of a score buffer
 constexpr int kThreads = 384;
 constexpr int kBiasSlots = 4;
+// Registers a thread of the 128 that load and issue, and of the 256 of the softmax: together the 384 x 168 of the launch.
+constexpr int kFewRegs = 88, kManyRegs = 208;
 
 // s = s c + bias over 64 scores (base 2)
 __device__ __forceinline__ void add_bias(uint32_t (&s)[64], const float *bias, float c) {
@@ -166,155 +168,154 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
-    // 128 threads give up what the 256 of the softmax take: 128 x 88 + 256 x 208 of the launch's 384 x 168 registers
     if (warp < 4) {
-    regs_dec<88>();
-    if (warp == 0) {
-        // ---------------- K and V tiles: slot 2 t holds K(t), slot 2 t + 1 V(t) ----------------
-        if (lane == 0) {
+        regs_dec<kFewRegs>();
+        if (warp == 0) {
+            // ---------------- K and V tiles: slot 2 t holds K(t), slot 2 t + 1 V(t) ----------------
+            if (lane == 0) {
+                bool ok = true;
+                RingPos rp{0, 0};
+                int i = 0;
+                for (; ok && i < 2 * nt; ++i) {
+                    const int s = rp.slot;
+                    if (*abort_flag) break;
+                    if (i >= NS && !mbar_wait_near(empty + s, rp.phase ^ 1u, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const int atoms = i & 1 ? g.vatoms : g.datoms;
+                    const CUtensorMap *map = i & 1 ? &map_v : &map_k;
+                    const int hm = i & 1 ? g.v_head : g.k_head, bm = i & 1 ? g.v_batch : g.k_batch;
+                    const uint32_t dst = saddr(ring + (size_t)s * L.slot);
+                    mbar_expect_tx(full + s, (uint32_t)atoms * kAtom);
+                    for (int a = 0; a < atoms; ++a)
+                        tma_load_4d(dst + a * kAtom, map, saddr(full + s), a * 64, j_beg + (i >> 1) * kTS, c * hm, b * bm);
+                    rp.step(1, NS);
+                }
+                if (!ok) {
+                    atomicOr(p.err, kDevErrTimeout);
+                    *abort_flag = 1;
+                }
+                for (int k = max(0, i - NS); k < i; ++k) mbar_wait_near(full + (k % NS), (uint32_t)(k / NS) & 1u, p.timeout_ns);
+            }
+            __syncwarp();
+        } else if (warp == 3) {
+            // ---------------- bias slices and masked rows ----------------
             bool ok = true;
             RingPos rp{0, 0};
-            int i = 0;
-            for (; ok && i < 2 * nt; ++i) {
-                const int s = rp.slot;
+            RingPos bs{0, 0};
+            int used = 0;
+            float bv[kTS / 32], next[kTS / 32];  // base-2 bias of a tile's keys, read a tile ahead
+#pragma unroll
+            for (int u = 0; u < kTS / 32; ++u) next[u] = attn_bias2(p, b, j_beg + 32 * u + lane, j_end);
+            for (int t = 0; ok && t < nt; ++t) {
+                unsigned dead[kTS / 32], cleared = 0;
+#pragma unroll
+                for (int u = 0; u < kTS / 32; ++u) {
+                    bv[u] = next[u];
+                    next[u] = attn_bias2(p, b, j_beg + (t + 1) * kTS + 32 * u + lane, j_end);
+                    dead[u] = __ballot_sync(~0u, bv[u] == -INFINITY);
+                    cleared |= dead[u];
+                }
+                if (masked_tile(t)) {
+                    if (used >= kBiasSlots && !mbar_wait_near(bempty + bs.slot, bs.phase ^ 1u, p.timeout_ns)) ok = false;
+#pragma unroll
+                    for (int u = 0; u < kTS / 32; ++u) sBias[bs.slot * kTS + 32 * u + lane] = bv[u];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bfull + bs.slot);
+                    bs.step(1, kBiasSlots);
+                    ++used;
+                }
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int s = rp.slot;
+                    if (!mbar_wait_near(full + s, rp.phase, p.timeout_ns)) ok = false;
+                    rp.step(1, NS);
+                    if (cleared) {
+                        uint8_t *tile = ring + (size_t)s * L.slot;
+                        clear_rows<kTS>(tile, kv ? g.vatoms : g.datoms, dead, lane);
+                        fence_async();
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(ready + s);
+                }
                 if (*abort_flag) break;
-                if (i >= NS && !mbar_wait_near(empty + s, rp.phase ^ 1u, p.timeout_ns)) {
+            }
+            if (!ok && lane == 0) {
+                atomicOr(p.err, kDevErrTimeout);
+                *abort_flag = 1;
+            }
+            __syncwarp();
+        } else {
+            // ---------------- MMA issuers (warps 1 and 2, one a group) ----------------
+            const bool lead = elect_lane();
+            const int grp = warp - 1;
+            const uint32_t idesc_s = make_idesc<0, 128, kStep>();
+            const uint32_t idesc_o = idesc_mn(g.dv_pad);
+            const uint64_t qd = make_sdesc(saddr(sQ) + (QT == 2 ? grp : 0) * g.datoms * 16384u, 128u);
+            const uint64_t k0 = make_sdesc(saddr(ring), 128u), v0 = sdesc_mn(saddr(ring), kAtom);
+            const uint32_t slot16 = L.slot >> 4;
+            const uint32_t ts = tmem_base + (uint32_t)(grp * 128), to = ts + 256u;
+            // this group's tiles: all of them, or those of its parity
+            const int mine = QT == 2 ? nt : (nt - grp + 1) / 2, steps = kSteps * mine;
+            constexpr int kNext = QT == 2 ? 2 : 4;  // slots from a tile of the group to its next
+            RingPos kp{QT == 2 ? 0 : 2 * grp, 0}, vp{QT == 2 ? 1 : 2 * grp + 1, 0};
+            // S of step i (part h of its tile) into buffer i & 1
+            auto s_product = [&](int i) {
+                const int h = i % kSteps, u = i & 1;
+                if (h == 0 && !mbar_wait_near(ready + kp.slot, kp.phase, p.timeout_ns)) return false;
+                tc_fence_after();
+                if (lead) {
+                    const uint64_t kd = k0 + (uint64_t)(kp.slot * slot16 + h * 512);
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+                        tc_mma<0>(ts + 64u * u, qd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
+                                  kd + (uint64_t)((k / 4) * (kAtom / 16) + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
+                    tc_commit(saddr(sfull + 2 * grp + u));
+                    if (h == kSteps - 1) tc_commit(saddr(empty + kp.slot));
+                }
+                __syncwarp();
+                if (h == kSteps - 1) kp.step(kNext, NS);
+                return true;
+            };
+            bool ok = steps == 0 || mbar_wait_near(qfull, 0, p.timeout_ns);
+            for (int i = 0; ok && i < min(steps, 2); ++i) ok = s_product(i);
+            for (int i = 0; ok && i < steps; ++i) {
+                const int h = i % kSteps, u = i & 1;
+                const uint32_t ph = (uint32_t)(i >> 1) & 1u;
+                if ((h == 0 && !mbar_wait_near(ready + vp.slot, vp.phase, p.timeout_ns)) ||
+                    !mbar_wait_near(pready + 2 * grp + u, ph, p.timeout_ns) || *abort_flag) {
                     ok = false;
                     break;
                 }
-                const int atoms = i & 1 ? g.vatoms : g.datoms;
-                const CUtensorMap *map = i & 1 ? &map_v : &map_k;
-                const int hm = i & 1 ? g.v_head : g.k_head, bm = i & 1 ? g.v_batch : g.k_batch;
-                const uint32_t dst = saddr(ring + (size_t)s * L.slot);
-                mbar_expect_tx(full + s, (uint32_t)atoms * kAtom);
-                for (int a = 0; a < atoms; ++a)
-                    tma_load_4d(dst + a * kAtom, map, saddr(full + s), a * 64, j_beg + (i >> 1) * kTS, c * hm, b * bm);
-                rp.step(1, NS);
-            }
-            if (!ok) {
-                atomicOr(p.err, kDevErrTimeout);
-                *abort_flag = 1;
-            }
-            for (int k = max(0, i - NS); k < i; ++k) mbar_wait_near(full + (k % NS), (uint32_t)(k / NS) & 1u, p.timeout_ns);
-        }
-        __syncwarp();
-    } else if (warp == 3) {
-        // ---------------- bias slices and masked rows ----------------
-        bool ok = true;
-        RingPos rp{0, 0};
-        RingPos bs{0, 0};
-        int used = 0;
-        float bv[kTS / 32], next[kTS / 32];  // base-2 bias of a tile's keys, read a tile ahead
+                tc_fence_after();
+                if (lead) {
+                    const uint64_t vd = v0 + (uint64_t)(vp.slot * slot16 + h * 512);
 #pragma unroll
-        for (int u = 0; u < kTS / 32; ++u) next[u] = attn_bias2(p, b, j_beg + 32 * u + lane, j_end);
-        for (int t = 0; ok && t < nt; ++t) {
-            unsigned dead[kTS / 32], cleared = 0;
-#pragma unroll
-            for (int u = 0; u < kTS / 32; ++u) {
-                bv[u] = next[u];
-                next[u] = attn_bias2(p, b, j_beg + (t + 1) * kTS + 32 * u + lane, j_end);
-                dead[u] = __ballot_sync(~0u, bv[u] == -INFINITY);
-                cleared |= dead[u];
-            }
-            if (masked_tile(t)) {
-                if (used >= kBiasSlots && !mbar_wait_near(bempty + bs.slot, bs.phase ^ 1u, p.timeout_ns)) ok = false;
-#pragma unroll
-                for (int u = 0; u < kTS / 32; ++u) sBias[bs.slot * kTS + 32 * u + lane] = bv[u];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bfull + bs.slot);
-                bs.step(1, kBiasSlots);
-                ++used;
-            }
-            for (int kv = 0; kv < 2; ++kv) {
-                const int s = rp.slot;
-                if (!mbar_wait_near(full + s, rp.phase, p.timeout_ns)) ok = false;
-                rp.step(1, NS);
-                if (cleared) {
-                    uint8_t *tile = ring + (size_t)s * L.slot;
-                    clear_rows<kTS>(tile, kv ? g.vatoms : g.datoms, dead, lane);
-                    fence_async();
-                    __syncwarp();
+                    for (int k = 0; k < kStep / 16; ++k)  // 16 keys: 8 TMEM columns of P, 2048 bytes of V
+                        tc_mma_ts(to, ts + 64u * u + 8u * k, vd + (uint64_t)(k * 128), idesc_o, i > 0 || k > 0 ? 1u : 0u);
+                    tc_commit(saddr(pvdone + 2 * grp + u));
+                    if (h == kSteps - 1) tc_commit(saddr(empty + vp.slot));
                 }
-                if (lane == 0) mbar_arrive(ready + s);
+                __syncwarp();
+                if (h == kSteps - 1) vp.step(kNext, NS);
+                // the S after next takes the columns of this P: not before the products that read it are complete (the
+                // softmax has the other buffer's S meanwhile)
+                if (i + 2 < steps) ok = mbar_wait_near(pvdone + 2 * grp + u, ph, p.timeout_ns) && s_product(i + 2);
             }
-            if (*abort_flag) break;
-        }
-        if (!ok && lane == 0) {
-            atomicOr(p.err, kDevErrTimeout);
-            *abort_flag = 1;
-        }
-        __syncwarp();
-    } else {
-        // ---------------- MMA issuers (warps 1 and 2, one a group) ----------------
-        const bool lead = elect_lane();
-        const int grp = warp - 1;
-        const uint32_t idesc_s = make_idesc<0, 128, kStep>();
-        const uint32_t idesc_o = idesc_mn(g.dv_pad);
-        const uint64_t qd = make_sdesc(saddr(sQ) + (QT == 2 ? grp : 0) * g.datoms * 16384u, 128u);
-        const uint64_t k0 = make_sdesc(saddr(ring), 128u), v0 = sdesc_mn(saddr(ring), kAtom);
-        const uint32_t slot16 = L.slot >> 4;
-        const uint32_t ts = tmem_base + (uint32_t)(grp * 128), to = ts + 256u;
-        // this group's tiles: all of them, or those of its parity
-        const int mine = QT == 2 ? nt : (nt - grp + 1) / 2, steps = kSteps * mine;
-        constexpr int kNext = QT == 2 ? 2 : 4;  // slots from a tile of the group to its next
-        RingPos kp{QT == 2 ? 0 : 2 * grp, 0}, vp{QT == 2 ? 1 : 2 * grp + 1, 0};
-        // S of step i (part h of its tile) into buffer i & 1
-        auto s_product = [&](int i) {
-            const int h = i % kSteps, u = i & 1;
-            if (h == 0 && !mbar_wait_near(ready + kp.slot, kp.phase, p.timeout_ns)) return false;
-            tc_fence_after();
             if (lead) {
-                const uint64_t kd = k0 + (uint64_t)(kp.slot * slot16 + h * 512);
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    tc_mma<0>(ts + 64u * u, qd + (uint64_t)((k / 4) * 1024 + (k % 4) * 2),
-                              kd + (uint64_t)((k / 4) * (kAtom / 16) + (k % 4) * 2), idesc_s, k > 0 ? 1u : 0u);
-                tc_commit(saddr(sfull + 2 * grp + u));
-                if (h == kSteps - 1) tc_commit(saddr(empty + kp.slot));
+                if (!ok) {
+                    atomicOr(p.err, kDevErrTimeout);
+                    *abort_flag = 1;
+                }
+                tc_commit(saddr(drain + grp));
             }
             __syncwarp();
-            if (h == kSteps - 1) kp.step(kNext, NS);
-            return true;
-        };
-        bool ok = steps == 0 || mbar_wait_near(qfull, 0, p.timeout_ns);
-        for (int i = 0; ok && i < min(steps, 2); ++i) ok = s_product(i);
-        for (int i = 0; ok && i < steps; ++i) {
-            const int h = i % kSteps, u = i & 1;
-            const uint32_t ph = (uint32_t)(i >> 1) & 1u;
-            if ((h == 0 && !mbar_wait_near(ready + vp.slot, vp.phase, p.timeout_ns)) ||
-                !mbar_wait_near(pready + 2 * grp + u, ph, p.timeout_ns) || *abort_flag) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            if (lead) {
-                const uint64_t vd = v0 + (uint64_t)(vp.slot * slot16 + h * 512);
-#pragma unroll
-                for (int k = 0; k < kStep / 16; ++k)  // 16 keys: 8 TMEM columns of P, 2048 bytes of V
-                    tc_mma_ts(to, ts + 64u * u + 8u * k, vd + (uint64_t)(k * 128), idesc_o, i > 0 || k > 0 ? 1u : 0u);
-                tc_commit(saddr(pvdone + 2 * grp + u));
-                if (h == kSteps - 1) tc_commit(saddr(empty + vp.slot));
-            }
+            mbar_wait_near(drain + grp, 0, p.timeout_ns);
             __syncwarp();
-            if (h == kSteps - 1) vp.step(kNext, NS);
-            // the S after next takes the columns of this P: not before the products that read it are complete (the
-            // softmax has the other buffer's S meanwhile)
-            if (i + 2 < steps) ok = mbar_wait_near(pvdone + 2 * grp + u, ph, p.timeout_ns) && s_product(i + 2);
         }
-        if (lead) {
-            if (!ok) {
-                atomicOr(p.err, kDevErrTimeout);
-                *abort_flag = 1;
-            }
-            tc_commit(saddr(drain + grp));
-        }
-        __syncwarp();
-        mbar_wait_near(drain + grp, 0, p.timeout_ns);
-        __syncwarp();
-    }
     } else {
         // ---------------- softmax groups ----------------
-        regs_inc<208>();
+        regs_inc<kManyRegs>();
         const int q = warp & 3, grp = (warp - 4) >> 2;
         const int rl = q * 32 + lane;
         const int blk = QT == 2 ? grp : 0;
@@ -503,6 +504,12 @@ cudaError_t launch(const AttnParams &p, AttnTc g, const CUtensorMap &mk, const C
     const uint32_t smem = layout(QT, g.datoms, g.vatoms, g.slots).total + 1024u;
     cudaError_t e = cudaFuncSetAttribute(xattn_tc_kernel<QT, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
     if (e != cudaSuccess) return e;
+    // The softmax takes registers that the launch must have brought: a build with fewer would wait for them.
+    static const int regs = [] {
+        cudaFuncAttributes a{};
+        return cudaFuncGetAttributes(&a, xattn_tc_kernel<QT, KS>) == cudaSuccess ? a.numRegs : 0;
+    }();
+    if (regs * kThreads < 128 * kFewRegs + 256 * kManyRegs) return cudaErrorInvalidConfiguration;
     // at least half the shared memory: a CTA holds all of TMEM, so two on one SM would wait for each other
     xattn_tc_kernel<QT, KS><<<p.main_units + p.tail_units * p.splits, kThreads,
                               smem > limit / 2 + 1024u ? smem : limit / 2 + 1024u, s>>>(mk, mv, p, g);

@@ -76,6 +76,8 @@ SIZES = [
     (2, 40, 900, 60, 60, 128, 128),
     (2, 150, 1300, 80, 80, 128, 64),
     (3, 260, 700, 64, 32, 96, 96),
+    # more units than SMs: those behind the last full wave are split over their keys
+    (2, 300, 1100, 64, 64, 64, 64),
 ]
 
 
