@@ -490,8 +490,9 @@ typedef struct {
 
 /* Bytes of workspace of fs_cross_entropy (grad = 0) or fs_cross_entropy_grad
  * (grad = 1) on the current device; 0 if the descriptor is not valid.  Of x and
- * w only the address's alignment counts: bf16 rows that do not start on 16 bytes
- * are copied to rows that do, fp32 rows to three bf16 planes.  The gradient's
+ * w only the address's alignment counts (to 128 bytes): bf16 rows that do not
+ * start on 16 bytes, or of a long x on 128, are copied to rows that do, fp32
+ * rows to three bf16 planes.  The gradient's
  * holds the logit gradients of one piece of the classes (up to 256 MiB, or 256
  * classes if those take more), and partial sums of dx. */
 FS_API size_t fs_cross_entropy_workspace(const fs_xent_desc *desc, const void *x, const void *w, int grad);

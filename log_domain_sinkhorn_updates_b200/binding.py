@@ -361,7 +361,7 @@ def fs_selftest_wait(h: Handle, timeout_ms=50) -> int:
 
 # ---- row-softmax operators without a handle ----
 # A call's descriptor and workspace size follow from the tensors' shapes, strides, types and
-# device (and whether they start on 16 bytes) alone, so they are checked and built once for each such combination and kept (at most
+# device (and the alignment they start on) alone, so they are checked and built once for each such combination and kept (at most
 # _PLAN_LIMIT of them; no data, address or tensor is kept).
 _plans = {}
 _PLAN_LIMIT = 4096
@@ -563,7 +563,7 @@ def fs_cross_entropy(x, w, target, loss, lse, scale=1.0, ignore_index=-100, stre
     import torch
     L = lib()
     xp, wp = x.data_ptr(), w.data_ptr()
-    desc, ref, need = _plan(("xent", scale, ignore_index, xp & 15, wp & 15, *_geometry(x, w)),
+    desc, ref, need = _plan(("xent", scale, ignore_index, xp & 127, wp & 15, *_geometry(x, w)),
                             lambda: (_xent_desc(x, w, scale, ignore_index), x.device),
                             lambda d: L.fs_cross_entropy_workspace(d, xp, wp, 0))
     dev, shape = x.get_device(), (desc.n,)
@@ -580,7 +580,7 @@ def fs_cross_entropy_grad(x, w, target, lse, dloss, dx, dw, dlse=None, scale=1.0
     import torch
     L = lib()
     xp, wp = x.data_ptr(), w.data_ptr()
-    desc, ref, need = _plan(("xent_grad", scale, ignore_index, xp & 15, wp & 15, *_geometry(x, w, dx, dw)),
+    desc, ref, need = _plan(("xent_grad", scale, ignore_index, xp & 127, wp & 15, *_geometry(x, w, dx, dw)),
                             lambda: (_xent_grad_desc(x, w, dx, dw, scale, ignore_index), x.device),
                             lambda d: L.fs_cross_entropy_workspace(d, xp, wp, 1))
     dev, shape = x.get_device(), (desc.n,)

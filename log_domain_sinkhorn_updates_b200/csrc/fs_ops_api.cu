@@ -269,7 +269,11 @@ XentPlan plan_xent(const fs_xent_desc &D, const void *x, const void *w, bool gra
     const bool f32 = D.dtype == FS_F32;
     const size_t n = (size_t)std::max(D.n, 1), budget = (size_t)256 << 20;
     L.planes = f32 ? 3 : 1;
-    L.pack_x = f32 || !fs::xent_tc_rows(x, D.ldx, D.n);
+    // x is read again by every column tile: rows that do not start on 128 bytes take two lines of L2 a box row, and
+    // are copied where there are enough tiles to repay it (1021 x 50021 x 1000: forward 89 us as they lie, 79 copied,
+    // copy included; 512 x 16384 x 520: 19 against 21; w is read once a band of row tiles, and its copy does not pay).
+    const bool lines = D.ldx % 64 == 0 && reinterpret_cast<uintptr_t>(x) % 128 == 0;
+    L.pack_x = f32 || !fs::xent_tc_rows(x, D.ldx, D.n) || (!lines && (long long)D.n * D.v >= 1ll << 25);
     L.pack_w = f32 || !fs::xent_tc_rows(w, D.ldw, D.v);
     L.dp = up(D.d, 64) * 64;
     // Pieces of the classes whose logit gradients, and whose copies of w, stay within 256 MiB each.

@@ -301,6 +301,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 128; ++k)
                             if (c0 + k >= g.N) r[k] = 0xff800000u;  // -inf
                     }
+                    if (half == 0) {
+                        // a first reference from 16 columns: where they are typical, the tile needs no pass for its
+                        // maximum (a sum past 2^12 against it brings one)
+                        float a = max3(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[2]));
+                        float b = max3(__uint_as_float(r[3]), __uint_as_float(r[4]), __uint_as_float(r[5]));
+#pragma unroll
+                        for (int k = 6; k < 16; k += 4) {
+                            a = max3(a, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+                            if (k + 3 < 16) b = max3(b, __uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
+                        }
+                        mx = fmaxf(a, b) * p.scale2;
+                        if (!(fabsf(mx) < INFINITY)) mx = -INFINITY;
+                    }
                     consume128_folded(r, p.scale2, mx, l);
                 } else if constexpr (EPI == kDl) {
                     const long long at = target - p.c0 - c0;
