@@ -408,7 +408,9 @@ FS_API fs_status fs_update_f_noalloc(int n, int m, int d, float eps, const float
  * graphs) that can overlap need one each.  Outputs must not overlap inputs,
  * the workspace or one another.  Argument errors are returned before any
  * work is enqueued, with a message in fs_last_error(NULL).
- * Results do not depend on timing: every sum has a fixed order.
+ * Results do not depend on timing: every sum has a fixed order.  What a call
+ * looks up once per device is stale after cudaDeviceReset: do not use these
+ * calls on a device that has been reset.
  * ------------------------------------------------------------------------ */
 
 /* Element strides of a [batch][token][head][width] tensor; width is contiguous. */

@@ -79,6 +79,7 @@ class FsError(RuntimeError):
 
 
 _lib = None
+_torch = None  # the torch module, bound when an operator without a handle is first called
 
 
 def lib():
@@ -373,11 +374,6 @@ def _same(what, cond):
         raise ValueError(what)
 
 
-def _geometry(*tensors):
-    """What a plan depends on, as a dictionary key."""
-    return tuple([x for t in tensors for x in (t.shape, t.stride(), t.dtype, t.get_device())])
-
-
 def _op_dtype(first, *others):
     """The operators' dtype code; every tensor must share it and the device."""
     dt = _OP_DTYPES.get(str(first.dtype))
@@ -394,9 +390,9 @@ def _op_dtype(first, *others):
 
 
 def _side(t, dtype, shape, device, what):
-    """Address of a contiguous side array (lengths, bias, statistics, targets), or None."""
+    """Address of a contiguous side array (lengths, bias, statistics, targets)."""
     if t is None:
-        return None
+        raise ValueError(f"{what} is needed")
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on the tensors' device")
     return t.data_ptr()
@@ -415,7 +411,7 @@ def _plan(key, build, query):
     """(descriptor, reference to it, workspace bytes) of `key`, built on its first use."""
     plan = _plans.get(key)
     if plan is None:
-        import torch
+        torch = _torch
         desc, device = build()
         with torch.cuda.device(device):
             plan = (desc, ctypes.byref(desc), int(query(ctypes.byref(desc))))
@@ -425,35 +421,37 @@ def _plan(key, build, query):
     return plan
 
 
-def _op_call(device, need, stream, workspace, call):
-    """Run `call(workspace address, bytes, stream)` on device number `device`: on the given stream
-    or that device's current one, with the given workspace or one from torch's allocator (in that
-    stream's order; under graph capture, of the capture's own pool)."""
-    import torch
-    if torch.cuda.current_device() != device:
-        with torch.cuda.device(device):
-            return _op_call(device, need, stream, workspace, call)
+def _ready():
+    """(library, torch), both loaded."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return lib(), _torch
+
+
+def _raw_stream(torch, device, stream):
+    """The given stream's address, or that of the device's current one."""
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device)
-    else:
-        if stream.device.index != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
-        raw = stream.cuda_stream
-    size, address = 0, None
-    if workspace is not None:
-        if workspace.get_device() != device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the tensors' device")
-        size, address = workspace.numel() * workspace.element_size(), workspace.data_ptr()
-    elif need:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
+    return stream.cuda_stream
+
+
+def _scratch(torch, device, need, stream, workspace):
+    """(workspace, its bytes): the given one, or one from torch's allocator in the stream's order (under
+    graph capture, of the capture's own pool).  The caller holds it until its work is enqueued."""
+    if workspace is None:
+        if not need:
+            return None, 0
         if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        else:
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        size, address = need, workspace.data_ptr()
-    status = call(address, size, raw)
-    if status != FS_OK:
-        _check(status)
+            return torch.empty(need, dtype=torch.uint8, device=device), need
+        with torch.cuda.stream(stream):
+            return torch.empty(need, dtype=torch.uint8, device=device), need
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the tensors' device")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _attn_desc(q, k, v, out, scale):
@@ -477,13 +475,6 @@ def _attn_grad_desc(q, k, v, out, dout, dq, dk, dv, scale):
     return desc
 
 
-def _attn_sides(desc, device, k_len, bias, lse):
-    import torch
-    return (_side(k_len, torch.int32, (desc.batch,), device, "k_len"),
-            _side(bias, torch.float32, (desc.batch, desc.m), device, "bias"),
-            _side(lse, torch.float32, (desc.batch, desc.heads, desc.n), device, "lse"))
-
-
 def fs_cross_attn(q, k, v, out, lse=None, k_len=None, bias=None, scale=None, stream=None, workspace=None):
     """Cross attention: out[b, i, h] = sum_j softmax_j(scale q_i.k_j + bias_j) v_j.
 
@@ -495,32 +486,55 @@ def fs_cross_attn(q, k, v, out, lse=None, k_len=None, bias=None, scale=None, str
     anything; a row without a key gives 0 and lse -inf.  scale: 1/sqrt(d) if None.  stream: the
     device's current one if None (tensors used on another stream must be kept alive by the
     caller).  workspace: uint8 tensor of fs_cross_attn_workspace bytes; allocated if None."""
-    L = lib()
-    desc, ref, need = _plan(("attn", scale, *_geometry(q, k, v, out)),
-                            lambda: (_attn_desc(q, k, v, out, scale), q.device),
-                            lambda d: L.fs_cross_attn_workspace(d, 0))
+    L, torch = _ready()
     dev = q.get_device()
-    kl, bp, lp = _attn_sides(desc, dev, k_len, bias, lse)
-    _op_call(dev, need, stream, workspace,
-             lambda ws, size, s: L.fs_cross_attn(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), kl, bp, out.data_ptr(),
-                                                 lp, ws, size, s))
+    desc, ref, need = _plan(
+        (scale, dev, q.dtype, k.dtype, v.dtype, out.dtype, k.get_device(), v.get_device(), out.get_device(), q.shape,
+         k.shape, v.shape, out.shape, q.stride(), k.stride(), v.stride(), out.stride()),
+        lambda: (_attn_desc(q, k, v, out, scale), q.device), lambda d: L.fs_cross_attn_workspace(d, 0))
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return fs_cross_attn(q, k, v, out, lse, k_len, bias, scale, stream, workspace)
+    if k_len is not None:
+        k_len = _side(k_len, torch.int32, (desc.batch,), dev, "k_len")
+    if bias is not None:
+        bias = _side(bias, torch.float32, (desc.batch, desc.m), dev, "bias")
+    if lse is not None:
+        lse = _side(lse, torch.float32, (desc.batch, desc.heads, desc.n), dev, "lse")
+    raw = _raw_stream(torch, dev, stream)
+    ws, size = _scratch(torch, dev, need, stream, workspace)
+    status = L.fs_cross_attn(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), k_len, bias, out.data_ptr(), lse,
+                             ws.data_ptr() if size else None, size, raw)
+    if status:
+        _check(status)
 
 
 def fs_cross_attn_grad(q, k, v, out, lse, dout, dq, dk, dv, k_len=None, bias=None, scale=None, stream=None,
                        workspace=None):
     """Gradients dq, dk, dv of fs_cross_attn from its out and lse and the gradient dout of out
     (shapes of q, k, v and out; the other arguments as in the forward)."""
-    L = lib()
-    desc, ref, need = _plan(("attn_grad", scale, *_geometry(q, k, v, out, dout, dq, dk, dv)),
-                            lambda: (_attn_grad_desc(q, k, v, out, dout, dq, dk, dv, scale), q.device),
-                            lambda d: L.fs_cross_attn_workspace(d, 1))
+    L, torch = _ready()
     dev = q.get_device()
-    _same("lse is needed", lse is not None)
-    kl, bp, lp = _attn_sides(desc, dev, k_len, bias, lse)
-    _op_call(dev, need, stream, workspace,
-             lambda ws, size, s: L.fs_cross_attn_grad(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), kl, bp,
-                                                      out.data_ptr(), lp, dout.data_ptr(), dq.data_ptr(),
-                                                      dk.data_ptr(), dv.data_ptr(), ws, size, s))
+    tensors = (q, k, v, out, dout, dq, dk, dv)
+    desc, ref, need = _plan(
+        (scale, dev, *[x for t in tensors for x in (t.shape, t.stride(), t.dtype, t.get_device())]),
+        lambda: (_attn_grad_desc(q, k, v, out, dout, dq, dk, dv, scale), q.device),
+        lambda d: L.fs_cross_attn_workspace(d, 1))
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return fs_cross_attn_grad(q, k, v, out, lse, dout, dq, dk, dv, k_len, bias, scale, stream, workspace)
+    lse = _side(lse, torch.float32, (desc.batch, desc.heads, desc.n), dev, "lse")
+    if k_len is not None:
+        k_len = _side(k_len, torch.int32, (desc.batch,), dev, "k_len")
+    if bias is not None:
+        bias = _side(bias, torch.float32, (desc.batch, desc.m), dev, "bias")
+    raw = _raw_stream(torch, dev, stream)
+    ws, size = _scratch(torch, dev, need, stream, workspace)
+    status = L.fs_cross_attn_grad(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), k_len, bias, out.data_ptr(), lse,
+                                  dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                  ws.data_ptr() if size else None, size, raw)
+    if status:
+        _check(status)
 
 
 def fs_cross_attn_workspace(q, k, v, out, dout=None, dq=None, dk=None, dv=None) -> int:
@@ -560,36 +574,51 @@ def fs_cross_entropy(x, w, target, loss, lse, scale=1.0, ignore_index=-100, stre
     float32 or bfloat16, rows contiguous, any row stride), target int64 [n]; writes loss and lse,
     float32 [n].  loss_i = lse_i - z_{i, target_i}, 0 where the target is ignore_index, NaN where it
     is anything else outside the classes.  stream, workspace: as in fs_cross_attn."""
-    import torch
-    L = lib()
-    xp, wp = x.data_ptr(), w.data_ptr()
-    desc, ref, need = _plan(("xent", scale, ignore_index, xp & 127, wp & 15, *_geometry(x, w)),
-                            lambda: (_xent_desc(x, w, scale, ignore_index), x.device),
-                            lambda d: L.fs_cross_entropy_workspace(d, xp, wp, 0))
-    dev, shape = x.get_device(), (desc.n,)
-    tp = _side(target, torch.int64, shape, dev, "target")
-    lo, le = _side(loss, torch.float32, shape, dev, "loss"), _side(lse, torch.float32, shape, dev, "lse")
-    _op_call(dev, need, stream, workspace,
-             lambda ws, size, s: L.fs_cross_entropy(ref, xp, wp, tp, lo, le, ws, size, s))
+    L, torch = _ready()
+    dev, xp, wp = x.get_device(), x.data_ptr(), w.data_ptr()
+    desc, ref, need = _plan(
+        (scale, ignore_index, xp & 127, wp & 15, dev, w.get_device(), x.dtype, w.dtype, x.shape, w.shape, x.stride(),
+         w.stride()),
+        lambda: (_xent_desc(x, w, scale, ignore_index), x.device),
+        lambda d: L.fs_cross_entropy_workspace(d, xp, wp, 0))
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return fs_cross_entropy(x, w, target, loss, lse, scale, ignore_index, stream, workspace)
+    shape = (desc.n,)
+    target = _side(target, torch.int64, shape, dev, "target")
+    loss, lse = _side(loss, torch.float32, shape, dev, "loss"), _side(lse, torch.float32, shape, dev, "lse")
+    raw = _raw_stream(torch, dev, stream)
+    ws, size = _scratch(torch, dev, need, stream, workspace)
+    status = L.fs_cross_entropy(ref, xp, wp, target, loss, lse, ws.data_ptr() if size else None, size, raw)
+    if status:
+        _check(status)
 
 
 def fs_cross_entropy_grad(x, w, target, lse, dloss, dx, dw, dlse=None, scale=1.0, ignore_index=-100, stream=None,
                           workspace=None):
     """Gradients dx and dw (shapes of x and w) from the forward's lse and the gradients dloss and
     dlse (float32 [n]; dlse None for 0) of its outputs.  Other arguments as in the forward."""
-    import torch
-    L = lib()
-    xp, wp = x.data_ptr(), w.data_ptr()
-    desc, ref, need = _plan(("xent_grad", scale, ignore_index, xp & 127, wp & 15, *_geometry(x, w, dx, dw)),
-                            lambda: (_xent_grad_desc(x, w, dx, dw, scale, ignore_index), x.device),
-                            lambda d: L.fs_cross_entropy_workspace(d, xp, wp, 1))
-    dev, shape = x.get_device(), (desc.n,)
-    tp = _side(target, torch.int64, shape, dev, "target")
-    le, dl, dz = (_side(t, torch.float32, shape, dev, what)
-                  for t, what in ((lse, "lse"), (dloss, "dloss"), (dlse, "dlse")))
-    _op_call(dev, need, stream, workspace,
-             lambda ws, size, s: L.fs_cross_entropy_grad(ref, xp, wp, tp, le, dl, dz, dx.data_ptr(), dw.data_ptr(),
-                                                         ws, size, s))
+    L, torch = _ready()
+    dev, xp, wp = x.get_device(), x.data_ptr(), w.data_ptr()
+    desc, ref, need = _plan(
+        (scale, ignore_index, xp & 127, wp & 15, dev,
+         *[y for t in (x, w, dx, dw) for y in (t.shape, t.stride(), t.dtype, t.get_device())]),
+        lambda: (_xent_grad_desc(x, w, dx, dw, scale, ignore_index), x.device),
+        lambda d: L.fs_cross_entropy_workspace(d, xp, wp, 1))
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return fs_cross_entropy_grad(x, w, target, lse, dloss, dx, dw, dlse, scale, ignore_index, stream, workspace)
+    shape = (desc.n,)
+    target = _side(target, torch.int64, shape, dev, "target")
+    lse, dloss = _side(lse, torch.float32, shape, dev, "lse"), _side(dloss, torch.float32, shape, dev, "dloss")
+    if dlse is not None:
+        dlse = _side(dlse, torch.float32, shape, dev, "dlse")
+    raw = _raw_stream(torch, dev, stream)
+    ws, size = _scratch(torch, dev, need, stream, workspace)
+    status = L.fs_cross_entropy_grad(ref, xp, wp, target, lse, dloss, dlse, dx.data_ptr(), dw.data_ptr(),
+                                     ws.data_ptr() if size else None, size, raw)
+    if status:
+        _check(status)
 
 
 def fs_cross_entropy_workspace(x, w, dx=None, dw=None) -> int:

@@ -2,6 +2,8 @@
 // passes: cross attention and softmax cross entropy, with their gradients.
 #pragma once
 
+#include <atomic>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -36,6 +38,19 @@ struct AttnParams {
     int *err;
 };
 
+// Allows a kernel `bytes` of dynamic shared memory, once a device (Kernel: one function, so that each has its own list).
+template <auto Kernel>
+cudaError_t allow_smem(size_t bytes) {
+    static std::atomic<size_t> allowed[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && allowed[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) allowed[dev].store(bytes, std::memory_order_relaxed);
+    return e;
+}
+
 // A kernel launched by launch_dependent may start before the stream's last one has ended (its launch then costs no
 // gap); nothing that one wrote may be read before this wait.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -58,6 +73,19 @@ cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, int threads, size_
 __device__ __forceinline__ int attn_keys(const AttnParams &p, int b) {
     return p.k_len ? min(max(__ldg(p.k_len + b), 0), p.m) : p.m;
 }
+// The problem of place `place` in the forward's order: with lengths, the longest first (ties: the lowest index), so
+// that short ones fill in behind; as they come where there are more than 32.  By whole warps.
+__device__ __forceinline__ int attn_problem(const AttnParams &p, int place) {
+    if (!p.k_len || p.batch > 32 || p.batch == 1) return place;
+    const int lane = threadIdx.x & 31, len = lane < p.batch ? attn_keys(p, lane) : -1;
+    int before = 0;
+    for (int j = 0; j < p.batch; ++j) {
+        const int other = __shfl_sync(~0u, len, j);
+        before += other > len || (other == len && j < lane);
+    }
+    return __ffs(__ballot_sync(~0u, lane < p.batch && before == place)) - 1;
+}
+
 // The work of a CTA of the forward.
 struct AttnUnit {
     int r0, c, b;       // first packed row, key head, problem
@@ -73,7 +101,7 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnParams &p) {
     const int u = w.whole ? x : p.main_units + tu;
     w.r0 = u % p.blocks * p.unit_rows;
     w.c = u / p.blocks % p.kv_heads;
-    w.b = u / p.blocks / p.kv_heads;
+    w.b = attn_problem(p, u / p.blocks / p.kv_heads);
     const int keys = attn_keys(p, w.b);
     w.j_beg = sp * p.split_keys;
     w.j_end = w.whole ? keys : min(keys, w.j_beg + p.split_keys);

@@ -127,10 +127,11 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, bool ragged, const
     // Rows of a unit (tensor cores: 128, or 256 in two blocks that share every tile), and which units are split over
     // their keys: what costs least, in tiles of 128 keys.  A CTA takes its tiles (two blocks: 1.28 times as long each,
     // 2.3 us against 1.8 at width 128) and 1.5 tiles' time to start and end; waves of CTAs, one an SM (CUDA cores:
-    // two); where lengths differ, CTAs fill in behind short ones, and the tail is half a CTA instead of the rest of a
-    // wave (32 requests of up to 4096 keys: 96 us in one part, 82 in two).  Either every unit is split, or only those
-    // behind the last full wave, so that they fill the SMs too; the joining pass costs a launch, and the parts' sums
-    // written and read back (4 TB/s, 1.8 us a tile).
+    // two).  With lengths, the longest problems come first and short ones fill in, so that the waves need not be whole,
+    // and parts of unequal problems cost more (32 requests of up to 4096 keys: 66 us in one part, 89 in two; 8: 52 in
+    // one, 33 in two, 30 in three, 37 in four).  Either every unit is split, or only those behind the last full wave,
+    // so that they fill the SMs too; the joining pass costs a launch, and the parts' sums written and read back
+    // (4 TB/s, 1.8 us a tile).
     const int slots = tc ? dev.sms : 2 * dev.sms;
     const int side = tc ? 128 : fs::xattn_simt_rows(D.n * (D.heads / D.kv_heads), (int)heads, dev.sms);
     const int tile = 128, tiles = up(std::max(D.m, 1), tile);
@@ -141,9 +142,11 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, bool ragged, const
         const double per = two ? 1.28 : 1.0;
         auto consider = [&](long long tail, int s) {
             const int t = up(tiles, s), parts = up(tiles, t);
-            const double join = 2.0 + 0.02 * parts + (double)tail * unit * parts * D.dv * 8.0 / 4e6 / 1.8;
-            const double n = (double)(tail * parts) / slots, waves = ragged && n > 1.0 ? n + 0.5 : std::ceil(n);
-            const double cost = (double)((units - tail) / slots) * (tiles * per + 1.5) + waves * (t * per + 1.5) +
+            const double live = (double)rows * heads / units;  // rows of a unit
+            const double join = 2.0 + 0.02 * parts + tail * live * parts * D.dv * 8.0 / 4e6 / 1.8;
+            const double n = (double)(tail * parts) / slots, ends = ragged && parts > 1 ? 3.0 : 1.5;
+            const double waves = ragged && n > 1.0 ? n + 0.1 : std::ceil(n);
+            const double cost = (double)((units - tail) / slots) * (tiles * per + 1.5) + waves * (t * per + ends) +
                                 (parts > 1 ? join : 0.0);
             if (cost < best - 1e-9) {
                 best = cost;

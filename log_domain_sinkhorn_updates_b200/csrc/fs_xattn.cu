@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParam
     const int lane = threadIdx.x % 32;
     const int unit = p.main_units + (int)(at / p.unit_rows);
     const int r = unit % p.blocks * p.unit_rows + (int)(at % p.unit_rows);
-    const int c = unit / p.blocks % p.kv_heads, b = unit / p.blocks / p.kv_heads;
+    const int c = unit / p.blocks % p.kv_heads, b = attn_problem(p, unit / p.blocks / p.kv_heads);
     if (r >= p.n * p.group) return;
     grid_dependency_wait();
     float mx = -INFINITY;
@@ -440,10 +440,6 @@ __global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnPara
         grad_pass<T, false, U, C>(p, vec, (int)blockIdx.x - key_blocks, sm);
 }
 
-template <class K>
-cudaError_t with_smem(K kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
 // Whether four elements of every row can be loaded at once.
 template <class T>
 bool aligned4(const void *base, const fs_view &s) {
@@ -456,7 +452,7 @@ cudaError_t fwd(const AttnParams &p, cudaStream_t s) {
     constexpr int R = 16 * RPT;
     const size_t smem = sizeof(float) * ((size_t)(R + kKeys) * smem_stride(p.d) + kKeys * smem_stride(p.dv) +
                                          R * (kKeys + 4) + kKeys);
-    cudaError_t e = with_smem(xattn_simt_kernel<T, RPT, C>, smem);
+    cudaError_t e = allow_smem<&xattn_simt_kernel<T, RPT, C>>(smem);
     if (e != cudaSuccess) return e;
     const bool vec = aligned4<T>(p.q, p.qs) && aligned4<T>(p.k, p.ks) && aligned4<T>(p.v, p.vs);
     xattn_simt_kernel<T, RPT, C><<<p.main_units + p.tail_units * p.splits, kTileThreads, smem, s>>>(p, vec);
@@ -477,7 +473,7 @@ cudaError_t grad(const AttnParams &p, cudaStream_t s) {
     const int w = smem_stride(p.d) + smem_stride(p.dv);
     const int key_blocks = (p.m + kept - 1) / kept, row_blocks = (p.n * p.group + kept - 1) / kept;
     const size_t smem = sizeof(float) * ((size_t)(kept + kStream) * w + 2 * kept * (kStream + 4) + 2 * kept + 2 * kStream);
-    cudaError_t e = with_smem(xattn_grad_kernel<T, U, C>, smem);
+    cudaError_t e = allow_smem<&xattn_grad_kernel<T, U, C>>(smem);
     if (e != cudaSuccess) return e;
     const bool vec = aligned4<T>(p.q, p.qs) && aligned4<T>(p.k, p.ks) && aligned4<T>(p.v, p.vs) &&
                      aligned4<T>(p.dout, p.dos);

@@ -494,8 +494,8 @@ cudaError_t launch(const AttnParams &p, AttnGradTc g, const CUtensorMap &mq, con
     const uint32_t need = layout(atoms, g.slots).total + 1024u;
     // at least half the shared memory: a CTA holds all of TMEM, so two on one SM would wait for each other
     const uint32_t smem = need > limit / 2 + 1024u ? need : limit / 2 + 1024u;
-    auto kern = xattn_grad_tc_kernel<KS>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
+    constexpr auto kern = &xattn_grad_tc_kernel<KS>;
+    cudaError_t e = allow_smem<kern>(limit);
     if (e != cudaSuccess) return e;
     g.key_blocks = (p.m + 127) / 128;
     return launch_dependent(kern, dim3(g.key_blocks + (p.n * p.group + 127) / 128, p.batch * p.kv_heads), kThreads, smem,

@@ -502,7 +502,7 @@ cudaError_t launch(const AttnParams &p, AttnTc g, const CUtensorMap &mk, const C
     g.slots = QT == 2 ? 8 : 12;
     while (layout(QT, g.datoms, g.vatoms, g.slots).total + 1024u > limit) --g.slots;
     const uint32_t smem = layout(QT, g.datoms, g.vatoms, g.slots).total + 1024u;
-    cudaError_t e = cudaFuncSetAttribute(xattn_tc_kernel<QT, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
+    cudaError_t e = allow_smem<&xattn_tc_kernel<QT, KS>>(limit);
     if (e != cudaSuccess) return e;
     // The softmax takes registers that the launch must have brought: a build with fewer would wait for them.
     static const int regs = [] {

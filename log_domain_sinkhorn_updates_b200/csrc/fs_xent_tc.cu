@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int EPI, bool A_MN, bool B_MN, bool F32>
 cudaError_t launch(const XentParams &p, const XentGemm &g, const CUtensorMap &a, const CUtensorMap &b,
                    cudaStream_t s) {
-    auto kern = xent_tc_kernel<EPI, A_MN, B_MN, F32>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    constexpr auto kern = &xent_tc_kernel<EPI, A_MN, B_MN, F32>;
+    cudaError_t e = allow_smem<kern>(kSmem);
     if (e != cudaSuccess) return e;
     const int tiles = g.mt * g.nt * g.parts;
     cudaLaunchConfig_t cfg = {};
