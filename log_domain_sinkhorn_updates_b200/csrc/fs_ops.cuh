@@ -74,9 +74,12 @@ __device__ __forceinline__ int attn_keys(const AttnParams &p, int b) {
     return p.k_len ? min(max(__ldg(p.k_len + b), 0), p.m) : p.m;
 }
 // The problem of place `place` in the forward's order: with lengths, the longest first (ties: the lowest index), so
-// that short ones fill in behind; as they come where there are more than 32.  By whole warps.
+// that short ones fill in behind; as they come where there are more than 32.  By whole warps.  LENGTHS (p.k_len is
+// given) is a template parameter where it matters: a problem that is not a function of the block index alone costs the
+// tensor-core forward 4 %.
+template <bool LENGTHS>
 __device__ __forceinline__ int attn_problem(const AttnParams &p, int place) {
-    if (!p.k_len || p.batch > 32 || p.batch == 1) return place;
+    if (!LENGTHS || p.batch > 32 || p.batch == 1) return place;
     const int lane = threadIdx.x & 31, len = lane < p.batch ? attn_keys(p, lane) : -1;
     int before = 0;
     for (int j = 0; j < p.batch; ++j) {
@@ -93,6 +96,7 @@ struct AttnUnit {
     size_t part;        // first row of part_ml and part_o, where it is a part
     bool whole;
 };
+template <bool LENGTHS>
 __device__ __forceinline__ AttnUnit attn_unit(const AttnParams &p) {
     AttnUnit w;
     const int x = blockIdx.x, t = x - p.main_units;
@@ -101,7 +105,7 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnParams &p) {
     const int u = w.whole ? x : p.main_units + tu;
     w.r0 = u % p.blocks * p.unit_rows;
     w.c = u / p.blocks % p.kv_heads;
-    w.b = attn_problem(p, u / p.blocks / p.kv_heads);
+    w.b = attn_problem<LENGTHS>(p, u / p.blocks / p.kv_heads);
     const int keys = attn_keys(p, w.b);
     w.j_beg = sp * p.split_keys;
     w.j_end = w.whole ? keys : min(keys, w.j_beg + p.split_keys);

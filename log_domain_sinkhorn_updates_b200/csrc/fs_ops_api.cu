@@ -129,7 +129,7 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, bool ragged, const
     // 2.3 us against 1.8 at width 128) and 1.5 tiles' time to start and end; waves of CTAs, one an SM (CUDA cores:
     // two).  With lengths, the longest problems come first and short ones fill in, so that the waves need not be whole,
     // and parts of unequal problems cost more (32 requests of up to 4096 keys: 66 us in one part, 89 in two; 8: 52 in
-    // one, 33 in two, 30 in three, 37 in four).  Either every unit is split, or only those behind the last full wave,
+    // one, 33 in two, 30 in three, 37 in four; 32 of 4096 each: 100 whole, 104 with the last wave in four parts).  Either every unit is split, or only those behind the last full wave,
     // so that they fill the SMs too; the joining pass costs a launch, and the parts' sums written and read back
     // (4 TB/s, 1.8 us a tile).
     const int slots = tc ? dev.sms : 2 * dev.sms;
@@ -144,7 +144,7 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, bool ragged, const
             const int t = up(tiles, s), parts = up(tiles, t);
             const double live = (double)rows * heads / units;  // rows of a unit
             const double join = 2.0 + 0.02 * parts + tail * live * parts * D.dv * 8.0 / 4e6 / 1.8;
-            const double n = (double)(tail * parts) / slots, ends = ragged && parts > 1 ? 3.0 : 1.5;
+            const double n = (double)(tail * parts) / slots, ends = parts == 1 ? 1.5 : ragged ? 3.0 : 2.5;
             const double waves = ragged && n > 1.0 ? n + 0.1 : std::ceil(n);
             const double cost = (double)((units - tail) / slots) * (tiles * per + 1.5) + waves * (t * per + ends) +
                                 (parts > 1 ? join : 0.0);

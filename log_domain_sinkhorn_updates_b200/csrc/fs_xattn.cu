@@ -153,7 +153,7 @@ template <class T, int RPT, int C>
 __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnParams p, bool vec) {
     extern __shared__ __align__(16) float sm[];
     constexpr int R = 16 * RPT, LP = kKeys + 4;
-    const AttnUnit unit = attn_unit(p);
+    const AttnUnit unit = p.k_len ? attn_unit<true>(p) : attn_unit<false>(p);
     const int r0 = unit.r0, c = unit.c, b = unit.b, j_beg = unit.j_beg, j_end = unit.j_end;
     const int ld = smem_stride(p.d), lv = smem_stride(p.dv);
     float *sQ = sm, *sK = sQ + R * ld, *sV = sK + kKeys * ld, *sP = sV + kKeys * lv, *sB = sP + R * LP;
@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParam
     const int lane = threadIdx.x % 32;
     const int unit = p.main_units + (int)(at / p.unit_rows);
     const int r = unit % p.blocks * p.unit_rows + (int)(at % p.unit_rows);
-    const int c = unit / p.blocks % p.kv_heads, b = attn_problem(p, unit / p.blocks / p.kv_heads);
+    const int c = unit / p.blocks % p.kv_heads, place = unit / p.blocks / p.kv_heads;
+    const int b = p.k_len ? attn_problem<true>(p, place) : place;
     if (r >= p.n * p.group) return;
     grid_dependency_wait();
     float mx = -INFINITY;

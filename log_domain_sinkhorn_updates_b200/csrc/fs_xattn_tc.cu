@@ -103,7 +103,7 @@ __host__ __device__ inline Layout layout(int qt, int datoms, int vatoms, int slo
 
 // KS: steps of 16 along d, fixed at compile time (descriptor offsets are then
 // immediates); what lies beyond d is zero in shared memory.
-template <int QT, int KS>
+template <int QT, int KS, bool LENGTHS>
 __global__ void __launch_bounds__(kThreads, 1)
     xattn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                     const AttnParams p, const AttnTc g) {
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rows = p.n * p.group;
-    const AttnUnit unit = attn_unit(p);
+    const AttnUnit unit = attn_unit<LENGTHS>(p);
     const int c = unit.c, b = unit.b, j_beg = unit.j_beg, j_end = unit.j_end;
     const int nt = j_end > j_beg ? (j_end - j_beg + kTS - 1) / kTS : 0;
     // tiles whose scores take a bias from shared memory: all, or only the one that the keys end in
@@ -496,24 +496,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int QT, int KS>
+template <int QT, int KS, bool LENGTHS>
 cudaError_t launch(const AttnParams &p, AttnTc g, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t s) {
     const uint32_t limit = 227u * 1024u;
     g.slots = QT == 2 ? 8 : 12;
     while (layout(QT, g.datoms, g.vatoms, g.slots).total + 1024u > limit) --g.slots;
     const uint32_t smem = layout(QT, g.datoms, g.vatoms, g.slots).total + 1024u;
-    cudaError_t e = allow_smem<&xattn_tc_kernel<QT, KS>>(limit);
+    cudaError_t e = allow_smem<&xattn_tc_kernel<QT, KS, LENGTHS>>(limit);
     if (e != cudaSuccess) return e;
     // The softmax takes registers that the launch must have brought: a build with fewer would wait for them.
     static const int regs = [] {
         cudaFuncAttributes a{};
-        return cudaFuncGetAttributes(&a, xattn_tc_kernel<QT, KS>) == cudaSuccess ? a.numRegs : 0;
+        return cudaFuncGetAttributes(&a, xattn_tc_kernel<QT, KS, LENGTHS>) == cudaSuccess ? a.numRegs : 0;
     }();
     if (regs * kThreads < 128 * kFewRegs + 256 * kManyRegs) return cudaErrorInvalidConfiguration;
     // at least half the shared memory: a CTA holds all of TMEM, so two on one SM would wait for each other
-    xattn_tc_kernel<QT, KS><<<p.main_units + p.tail_units * p.splits, kThreads,
+    xattn_tc_kernel<QT, KS, LENGTHS><<<p.main_units + p.tail_units * p.splits, kThreads,
                               smem > limit / 2 + 1024u ? smem : limit / 2 + 1024u, s>>>(mk, mv, p, g);
     return cudaGetLastError();
+}
+
+template <bool LENGTHS>
+cudaError_t launch_width(const AttnParams &p, const AttnTc &g, const CUtensorMap &mk, const CUtensorMap &mv,
+                         cudaStream_t s) {
+    const int ks = (p.d + 31) / 32 * 2;
+    if (p.unit_rows == 256)
+        return ks == 2   ? launch<2, 2, LENGTHS>(p, g, mk, mv, s)
+               : ks == 4 ? launch<2, 4, LENGTHS>(p, g, mk, mv, s)
+               : ks == 6 ? launch<2, 6, LENGTHS>(p, g, mk, mv, s)
+                         : launch<2, 8, LENGTHS>(p, g, mk, mv, s);
+    return ks == 2   ? launch<1, 2, LENGTHS>(p, g, mk, mv, s)
+           : ks == 4 ? launch<1, 4, LENGTHS>(p, g, mk, mv, s)
+           : ks == 6 ? launch<1, 6, LENGTHS>(p, g, mk, mv, s)
+                     : launch<1, 8, LENGTHS>(p, g, mk, mv, s);
 }
 
 }  // namespace
@@ -550,12 +565,7 @@ cudaError_t launch_xattn_tc(const AttnParams &p, cudaStream_t s) {
     if (!attn_map(&mk, p.k, p.ks, p.d, p.m, p.kv_heads, p.batch, tile_keys(two_blocks ? 2 : 1), &g.k_head, &g.k_batch) ||
         !attn_map(&mv, p.v, p.vs, p.dv, p.m, p.kv_heads, p.batch, tile_keys(two_blocks ? 2 : 1), &g.v_head, &g.v_batch))
         return cudaErrorInvalidValue;
-    const int ks = (p.d + 31) / 32 * 2;
-    if (two_blocks)
-        return ks == 2 ? launch<2, 2>(p, g, mk, mv, s) : ks == 4 ? launch<2, 4>(p, g, mk, mv, s)
-               : ks == 6 ? launch<2, 6>(p, g, mk, mv, s) : launch<2, 8>(p, g, mk, mv, s);
-    return ks == 2 ? launch<1, 2>(p, g, mk, mv, s) : ks == 4 ? launch<1, 4>(p, g, mk, mv, s)
-           : ks == 6 ? launch<1, 6>(p, g, mk, mv, s) : launch<1, 8>(p, g, mk, mv, s);
+    return p.k_len ? launch_width<true>(p, g, mk, mv, s) : launch_width<false>(p, g, mk, mv, s);
 }
 
 }  // namespace fs
