@@ -199,7 +199,7 @@ struct XentGemm {
     int a_plane, b_plane;    // elements from plane to plane of the operands
     int pairs;               // CTA pairs of the grid
     int a_rows;              // rows of a box of A (K contiguous)
-    int vec;                 // out's rows can be written 16 bytes at a time
+    int vec;                 // out's rows can be written 16 bytes (1) or 32 (2) at a time
     int add;                 // fp32 out: 1: onto what it holds
     void *out;
     long long ldo;

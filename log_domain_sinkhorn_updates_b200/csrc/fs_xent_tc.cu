@@ -60,8 +60,14 @@ struct Tile {
     int m0, n0, k0, kb, part;  // first row and column, first K element, K blocks of a plane pair, part
 };
 __device__ __forceinline__ Tile tile_of(const XentGemm &g, int t) {
-    const int per_part = g.mt * g.nt;
     Tile o;
+    if (g.mt == 1 && g.parts == 1) {  // one row tile: no divisions between the loads of two tiles
+        o.part = o.m0 = o.k0 = 0;
+        o.n0 = t * kTile;
+        o.kb = (g.K + kBK - 1) / kBK;
+        return o;
+    }
+    const int per_part = g.mt * g.nt;
     o.part = t / per_part;
     const int r = t % per_part;
     const int band = r / (kGroupRows * g.nt), rows = min(kGroupRows, g.mt - band * kGroupRows);
@@ -396,18 +402,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __nv_bfloat16 *dst = (__nv_bfloat16 *)g.out + g.ldo * row + c0;
                     if (live) {
 #pragma unroll
-                        for (int k = 0; k < 128; k += 8) {
-                            uint4 w;
-                            w.x = bf16x2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
-                            w.y = bf16x2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
-                            w.z = bf16x2(__uint_as_float(r[k + 4]), __uint_as_float(r[k + 5]));
-                            w.w = bf16x2(__uint_as_float(r[k + 6]), __uint_as_float(r[k + 7]));
-                            if (g.vec && c0 + k + 8 <= g.N) {
-                                *reinterpret_cast<uint4 *>(dst + k) = w;
-                            } else {
+                        for (int k = 0; k < 128; k += 16) {
+                            uint32_t w[8];
 #pragma unroll
-                                for (int u = 0; u < 8; ++u)
-                                    if (c0 + k + u < g.N) dst[k + u] = __float2bfloat16_rn(__uint_as_float(r[k + u]));
+                            for (int u = 0; u < 8; ++u)
+                                w[u] = bf16x2(__uint_as_float(r[k + 2 * u]), __uint_as_float(r[k + 2 * u + 1]));
+                            if (g.vec == 2 && c0 + k + 16 <= g.N) {
+                                st_v8(dst + k, w);  // whole 32-byte sectors
+                                continue;
+                            }
+#pragma unroll
+                            for (int v = 0; v < 16; v += 8) {
+                                if (g.vec && c0 + k + v + 8 <= g.N) {
+                                    *reinterpret_cast<uint4 *>(dst + k + v) =
+                                        make_uint4(w[v / 2], w[v / 2 + 1], w[v / 2 + 2], w[v / 2 + 3]);
+                                } else {
+#pragma unroll
+                                    for (int u = 0; u < 8; ++u)
+                                        if (c0 + k + v + u < g.N)
+                                            dst[k + v + u] = __float2bfloat16_rn(__uint_as_float(r[k + v + u]));
+                                }
                             }
                         }
                     }
@@ -496,7 +510,9 @@ cudaError_t launch_out(const XentParams &p, XentGemm &g, void *out, long long ld
                        const CUtensorMap &b, cudaStream_t s) {
     g.out = out;
     g.ldo = ldo;
-    g.vec = ldo % (p.planes == 3 ? 4 : 8) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    const long long bytes = ldo * (p.planes == 3 ? 4 : 2);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(out);
+    g.vec = bytes % 32 == 0 && at % 32 == 0 ? 2 : bytes % 16 == 0 && at % 16 == 0 ? 1 : 0;
     return p.planes == 3 ? launch<kOut, A_MN, B_MN, true>(p, g, a, b, s) : launch<kOut, A_MN, B_MN, false>(p, g, a, b, s);
 }
 
