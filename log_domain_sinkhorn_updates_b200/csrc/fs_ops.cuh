@@ -34,6 +34,10 @@ struct AttnParams {
     int main_units, tail_units, splits, split_keys;
     float *part_o;           // [splits][tail_units][unit_rows][dv], relative to part_ml's maximum
     float2 *part_ml;         // [splits][tail_units][unit_rows]: reference (base 2) and sum
+    // Gradient on the tensor cores: the streamed tiles of a CTA in parts, a CTA each (1: not split), whose raw sums
+    // [part][batch kv_heads][padded rows][width] a joining pass adds up.
+    int key_parts, row_parts;
+    float *part_dk, *part_dv, *part_dq;
     unsigned long long timeout_ns;
     int *err;
 };
@@ -140,7 +144,7 @@ struct AttnTc {
 struct AttnGradTc {
     int d_pad, dv_pad;  // rounded up to 16
     int slots;          // ring of streamed tiles
-    int key_blocks;     // CTAs of the pass that keeps keys; those that keep rows follow
+    int key_blocks, row_blocks;  // units of the pass that keeps keys, and of the one that keeps rows (CTAs behind it)
     int q_head, q_batch, g_head, g_batch, k_head, k_batch, v_head, v_batch;  // as above (g: dout)
 };
 bool attn_tc_view(const void *base, const fs_view &s, int tokens, int heads, int batch, bool map);
@@ -149,6 +153,7 @@ bool attn_map(CUtensorMap *map, const void *base, const fs_view &s, int w, int t
 cudaError_t launch_xattn_tc(const AttnParams &p, cudaStream_t s);
 
 cudaError_t launch_xattn_grad_tc(const AttnParams &p, cudaStream_t s);
+cudaError_t launch_xattn_grad_join(const AttnParams &p, cudaStream_t s);  // where key_parts or row_parts > 1
 
 cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s);

@@ -113,6 +113,8 @@ fs_status check_attn(const fs_attn_desc *D, bool grad) {
 
 struct AttnPlan {
     int unit_rows = 0, blocks = 0, main_units = 0, tail_units = 0, splits = 1, split_keys = 0;  // as in AttnParams
+    int key_parts = 1, row_parts = 1;
+    size_t part_dk = 0, part_dv = 0, part_dq = 0;
     size_t part_ml = 0, part_o = 0, dot = 0, total = 0;  // workspace offsets, and its size
 };
 
@@ -121,6 +123,29 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, bool ragged, const
     const size_t rows = (size_t)D.n * (D.heads / D.kv_heads), heads = (size_t)D.batch * D.kv_heads;
     if (grad) {
         L.total = align256((size_t)D.batch * D.heads * D.n * 4);
+        const size_t key_blocks = up(D.m, 128), row_blocks = (rows + 127) / 128;
+        if (!tc || rows == 0 || heads == 0 || D.m == 0 || (key_blocks + row_blocks) * heads >= (size_t)dev.sms) return L;
+        // Fewer CTAs than SMs: the streamed tiles of a CTA are split so that all SMs have about as many (a tile of the
+        // pass that keeps keys takes 1.25 of the other's, 0.85 us at width 128), four a part at least, where that saves
+        // more than the joining pass costs (10 tiles' time, and the sums written and read back at 4 TB/s): 2000 queries of 8
+        // heads on one key head, 64 keys of 128: 232 us whole, 43 split; 1000 x 1000, 4 heads: 21 whole, 24 split.
+        const int key_tiles = D.heads / D.kv_heads * up(D.n, 64), row_tiles = up(D.m, 64);
+        const double each = (key_blocks * 1.25 * key_tiles + row_blocks * (double)row_tiles) * heads / dev.sms;
+        const int kp = (int)std::min({std::max(1.0, key_tiles * 1.25 / each), std::max(1.0, key_tiles / 4.0), 64.0});
+        const int rp = (int)std::min({std::max(1.0, row_tiles / each), std::max(1.0, row_tiles / 4.0), 64.0});
+        const size_t dk = kp > 1 ? kp * heads * key_blocks * 128 * D.d * sizeof(float) : 0;
+        const size_t dv = kp > 1 ? kp * heads * key_blocks * 128 * D.dv * sizeof(float) : 0;
+        const size_t dq = rp > 1 ? rp * heads * row_blocks * 128 * D.d * sizeof(float) : 0;
+        const double before = std::max(key_tiles * 1.25, (double)row_tiles);
+        const double after = std::max(key_tiles * 1.25 / kp, (double)row_tiles / rp) + 10.0 + 2.0 * (dk + dv + dq) / 4e6 / 0.85;
+        if ((kp > 1 || rp > 1) && after < before) {
+            L.key_parts = kp;
+            L.row_parts = rp;
+            L.part_dk = L.total;
+            L.part_dv = L.part_dk + align256(dk);
+            L.part_dq = L.part_dv + align256(dv);
+            L.total = L.part_dq + align256(dq);
+        }
         return L;
     }
     if (rows == 0 || heads == 0) return L;
@@ -226,6 +251,11 @@ fs::AttnParams attn_params(const fs_attn_desc &D, const AttnPlan &L, const Devic
     p.splits = L.splits;
     p.split_keys = L.split_keys;
     char *w = static_cast<char *>(ws);
+    p.key_parts = L.key_parts;
+    p.row_parts = L.row_parts;
+    p.part_dk = reinterpret_cast<float *>(w + L.part_dk);
+    p.part_dv = reinterpret_cast<float *>(w + L.part_dv);
+    p.part_dq = reinterpret_cast<float *>(w + L.part_dq);
     p.part_ml = reinterpret_cast<float2 *>(w + L.part_ml);
     p.part_o = reinterpret_cast<float *>(w + L.part_o);
     p.dot = reinterpret_cast<float *>(w + L.dot);
@@ -406,7 +436,8 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
         return reject(FS_ERR_INVALID_ARG, "null argument");
     Device dev;
     if ((st = current_device(&dev)) != FS_OK) return st;
-    const AttnPlan L = plan_attn(D, true, false, false, dev);
+    const bool tc = attn_grad_tc(D, q, k, v, dout, dq, dk, dv);
+    const AttnPlan L = plan_attn(D, true, tc, false, dev);
     if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
     fs::AttnParams p = attn_params(D, L, dev, workspace);
     p.q = q;
@@ -423,9 +454,10 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = D.dtype == FS_BF16;
     if (D.n > 0) OPS_LAUNCH(fs::launch_xattn_dot(p, bf16, s), 1);
-    if (attn_grad_tc(D, q, k, v, dout, dq, dk, dv))
+    if (tc) {
         OPS_LAUNCH(fs::launch_xattn_grad_tc(p, s), 1);
-    else
+        if (L.key_parts > 1 || L.row_parts > 1) OPS_LAUNCH(fs::launch_xattn_grad_join(p, s), 1);
+    } else
         OPS_LAUNCH(fs::launch_xattn_grad_simt(p, bf16, dev.sms, s), 1);
     return FS_OK;
 }

@@ -48,7 +48,7 @@ __host__ __device__ inline Layout layout(int atoms, int slots) {
 // KS: steps of 16 along the widths (d and dv, the larger of the two), zeros beyond each.
 template <bool KEYS, int KS>
 __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, const CUtensorMap &map_k,
-                          const CUtensorMap &map_v, const AttnParams &p, const AttnGradTc &g, int block) {
+                          const CUtensorMap &map_v, const AttnParams &p, const AttnGradTc &g, int block, int part) {
     const CUtensorMap &map_s1 = KEYS ? map_q : map_k, &map_s2 = KEYS ? map_g : map_v;  // streamed
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
@@ -82,7 +82,9 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
     const int r0 = block * 128;  // first kept row (key, or packed query row)
     const int keys = attn_keys(p, b), rows = p.n * p.group;
     const int head_tiles = (p.n + kTile - 1) / kTile;
-    const int nt = KEYS ? (r0 < keys ? p.group * head_tiles : 0) : (keys + kTile - 1) / kTile;
+    const int all = KEYS ? (r0 < keys ? p.group * head_tiles : 0) : (keys + kTile - 1) / kTile;
+    const int parts = KEYS ? p.key_parts : p.row_parts;
+    const int t_beg = (int)((long long)all * part / parts), nt = (int)((long long)all * (part + 1) / parts) - t_beg;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -131,7 +133,8 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                                     c * g.v_head, b * g.v_batch);
                     }
             }
-            int t = 0, y = 0, h = KEYS ? c * p.group : c;
+            int t = 0, y = (KEYS ? t_beg % head_tiles : t_beg) * kTile;
+            int h = KEYS ? c * p.group + t_beg / head_tiles : c;
             RingPos rp{0, 0};
             for (; ok && t < nt; ++t) {
                 const int s = rp.slot;
@@ -181,7 +184,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
             if (lane == 0) mbar_arrive(stready);
         }
         RingPos rp{0, 0};
-        int i0 = 0, h = c * p.group;  // KEYS: first query and head of the next tile
+        int i0 = t_beg % head_tiles * kTile, h = c * p.group + t_beg / head_tiles;  // KEYS: of the next tile
         // KEYS: -L (base 2) and -D of a query; one without a key, or past the end, gives P = 0.  ROWS: a key's bias.
         float n0[2], n1[2] = {0.f, 0.f};  // read a tile ahead
         auto fetch = [&](int t) {
@@ -197,7 +200,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                         n1[u] = __ldg(p.dot + at);
                     }
                 } else {
-                    n0[u] = attn_bias2(p, b, t * kTile + 32 * u + lane, keys);
+                    n0[u] = attn_bias2(p, b, (t_beg + t) * kTile + 32 * u + lane, keys);
                 }
             }
             i0 += kTile;
@@ -443,6 +446,23 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                   p.dqs.head * (c * p.group + row % p.group);
         }
         const uint32_t to = tmem_base + lanes + (second ? kSum2 : kSum1);
+        if (parts > 1) {  // a part: its raw sums
+            float *base = KEYS ? (second ? p.part_dk : p.part_dv) : p.part_dq;
+            const size_t padded = (size_t)(KEYS ? g.key_blocks : g.row_blocks) * 128;
+            float *raw = base + (((size_t)part * gridDim.y + blockIdx.y) * padded + row) * width;
+            for (int k = KEYS ? 0 : 32 * grp; k < width; k += KEYS ? 32 : 64) {
+                uint32_t o[32];
+                if (nt > 0) {
+                    tmem_ld32(to + k, o);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int u = 0; u < 32; u += 4)
+                    if (live && k + u < width)
+                        *reinterpret_cast<uint4 *>(raw + k + u) =
+                            nt > 0 ? make_uint4(o[u], o[u + 1], o[u + 2], o[u + 3]) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        } else {
         for (int k = KEYS ? 0 : 32 * grp; k < width; k += KEYS ? 32 : 64) {
             uint32_t o[32];
             if (nt > 0) {
@@ -461,6 +481,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                 if (live && k + u < width) *reinterpret_cast<uint4 *>(dst + k + u) = w;  // widths: multiples of 8
             }
         }
+        }
     }
 
     tc_fence_before();
@@ -478,10 +499,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                          const AttnParams p, const AttnGradTc g) {
     grid_dependency_wait();
-    if ((int)blockIdx.x < g.key_blocks)
-        grad_pass<true, KS>(map_q, map_g, map_k, map_v, p, g, (int)blockIdx.x);
+    const int x = blockIdx.x, keys = g.key_blocks * p.key_parts;
+    if (x < keys)
+        grad_pass<true, KS>(map_q, map_g, map_k, map_v, p, g, x / p.key_parts, x % p.key_parts);
     else
-        grad_pass<false, KS>(map_q, map_g, map_k, map_v, p, g, (int)blockIdx.x - g.key_blocks);
+        grad_pass<false, KS>(map_q, map_g, map_k, map_v, p, g, (x - keys) / p.row_parts, (x - keys) % p.row_parts);
+}
+
+// Adds the parts' sums in their order, eight elements a thread: dk and dv of every key, then dq of every row.
+__global__ void __launch_bounds__(256) xattn_grad_join_kernel(const AttnParams p, int key_padded, int row_padded) {
+    const int d8 = p.d / 8, v8 = p.dv / 8, rows = p.n * p.group, hb = blockIdx.y, heads = gridDim.y;
+    const int c = hb % p.kv_heads, b = hb / p.kv_heads;
+    const unsigned e = blockIdx.x * 256u + threadIdx.x;
+    const unsigned keys = p.key_parts > 1 ? (unsigned)p.m * (d8 + v8) : 0u;
+    grid_dependency_wait();
+    const float *part;
+    __nv_bfloat16 *dst;
+    int row, k, parts, padded, width;
+    float mul = p.scale;
+    if (e < keys) {
+        row = (int)(e / (unsigned)(d8 + v8));
+        k = (int)(e % (unsigned)(d8 + v8));
+        const bool value = k >= d8;
+        k = (value ? k - d8 : k) * 8;
+        const fs_view &s = value ? p.dvs : p.dks;
+        part = value ? p.part_dv : p.part_dk;
+        dst = (__nv_bfloat16 *)(value ? p.dv_out : p.dk) + s.batch * b + s.token * row + s.head * c + k;
+        width = value ? p.dv : p.d;
+        if (value) mul = 1.f;
+        parts = p.key_parts;
+        padded = key_padded;
+    } else {
+        row = (int)((e - keys) / (unsigned)d8);
+        k = (int)((e - keys) % (unsigned)d8) * 8;
+        if (p.row_parts == 1 || row >= rows) return;
+        part = p.part_dq;
+        dst = (__nv_bfloat16 *)p.dq + p.dqs.batch * b + p.dqs.token * (row / p.group) +
+              p.dqs.head * (c * p.group + row % p.group) + k;
+        width = p.d;
+        parts = p.row_parts;
+        padded = row_padded;
+    }
+    const float4 *src = reinterpret_cast<const float4 *>(part + ((size_t)hb * padded + row) * width + k);
+    const size_t step = (size_t)heads * padded * width / 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const float4 u = src[i * step], v = src[i * step + 1];
+        x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
+        y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+    }
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(bf16x2(x.x * mul, x.y * mul), bf16x2(x.z * mul, x.w * mul),
+                                                 bf16x2(y.x * mul, y.y * mul), bf16x2(y.z * mul, y.w * mul));
 }
 
 template <int KS>
@@ -498,8 +567,9 @@ cudaError_t launch(const AttnParams &p, AttnGradTc g, const CUtensorMap &mq, con
     cudaError_t e = allow_smem<kern>(limit);
     if (e != cudaSuccess) return e;
     g.key_blocks = (p.m + 127) / 128;
-    return launch_dependent(kern, dim3(g.key_blocks + (p.n * p.group + 127) / 128, p.batch * p.kv_heads), kThreads, smem,
-                            s, mq, mg, mk, mv, p, g);
+    g.row_blocks = (p.n * p.group + 127) / 128;
+    return launch_dependent(kern, dim3(g.key_blocks * p.key_parts + g.row_blocks * p.row_parts, p.batch * p.kv_heads),
+                            kThreads, smem, s, mq, mg, mk, mv, p, g);
 }
 
 }  // namespace
@@ -519,6 +589,14 @@ cudaError_t launch_xattn_grad_tc(const AttnParams &p, cudaStream_t s) {
     if (w <= 64) return launch<4>(p, g, mq, mg, mk, mv, s);
     if (w <= 96) return launch<6>(p, g, mq, mg, mk, mv, s);
     return launch<8>(p, g, mq, mg, mk, mv, s);
+}
+
+cudaError_t launch_xattn_grad_join(const AttnParams &p, cudaStream_t s) {
+    const int rows = p.n * p.group, d8 = p.d / 8;
+    const unsigned long long work = (p.key_parts > 1 ? (unsigned long long)p.m * (d8 + p.dv / 8) : 0ull) +
+                                    (p.row_parts > 1 ? (unsigned long long)rows * d8 : 0ull);
+    return launch_dependent(xattn_grad_join_kernel, dim3((unsigned)((work + 255) / 256), p.batch * p.kv_heads), 256, 0, s, p,
+                            (p.m + 127) / 128 * 128, (rows + 127) / 128 * 128);
 }
 
 }  // namespace fs
