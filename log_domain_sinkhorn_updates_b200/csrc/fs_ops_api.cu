@@ -118,7 +118,10 @@ struct AttnPlan {
     size_t part_ml = 0, part_o = 0, dot = 0, total = 0;  // workspace offsets, and its size
 };
 
-AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, bool ragged, const Device &dev) {
+// kind: the kernels that take the call.
+enum AttnKind { kSimt = 0, kTensor = 1, kToken = 2 };
+AttnPlan plan_attn(const fs_attn_desc &D, bool grad, AttnKind kind, bool ragged, const Device &dev) {
+    const bool tc = kind == kTensor;
     AttnPlan L;
     const size_t rows = (size_t)D.n * (D.heads / D.kv_heads), heads = (size_t)D.batch * D.kv_heads;
     if (grad) {
@@ -158,7 +161,9 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, bool ragged, const
     // so that they fill the SMs too; the joining pass costs a launch, and the parts' sums written and read back
     // (4 TB/s, 1.8 us a tile).
     const int slots = tc ? dev.sms : 2 * dev.sms;
-    const int side = tc ? 128 : fs::xattn_simt_rows(D.n * (D.heads / D.kv_heads), (int)heads, dev.sms);
+    const int side = tc               ? 128
+                     : kind == kToken ? (rows <= 2 ? (int)rows : 4)
+                                      : fs::xattn_simt_rows(D.n * (D.heads / D.kv_heads), (int)heads, dev.sms);
     const int tile = 128, tiles = up(std::max(D.m, 1), tile);
     double best = 1e300;
     for (int two = 0; two < (tc && rows > 128 ? 2 : 1); ++two) {
@@ -199,8 +204,9 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, bool tc, bool ragged, const
 }
 size_t attn_workspace(const fs_attn_desc &D, bool grad, const Device &dev) {
     size_t most = 0;  // over the kernels and the lengths that a call may bring
-    for (int k = 0; k < 4; ++k)
-        if (!(k & 1) || D.dtype == FS_BF16) most = std::max(most, plan_attn(D, grad, k & 1, k & 2, dev).total);
+    for (int k = 0; k < 6; ++k)
+        if (k / 2 != kTensor || D.dtype == FS_BF16)
+            most = std::max(most, plan_attn(D, grad, (AttnKind)(k / 2), k & 1, dev).total);
     return most;
 }
 
@@ -406,7 +412,10 @@ fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const void *k, 
     Device dev;
     if ((st = current_device(&dev)) != FS_OK) return st;
     const bool bf16 = D.dtype == FS_BF16, tc = attn_tc(D, q, k, v, out);
-    const AttnPlan L = plan_attn(D, false, tc, k_len != nullptr, dev);
+    const AttnKind kind = tc ? kTensor
+                          : fs::xattn_token_ok(q, D.q, k, D.k, v, D.v, D.d, D.dv, D.n * (D.heads / D.kv_heads), bf16) ? kToken
+                                                                                                                    : kSimt;
+    const AttnPlan L = plan_attn(D, false, kind, k_len != nullptr, dev);
     if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
     fs::AttnParams p = attn_params(D, L, dev, workspace);
     p.q = q;
@@ -437,7 +446,7 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
     Device dev;
     if ((st = current_device(&dev)) != FS_OK) return st;
     const bool tc = attn_grad_tc(D, q, k, v, dout, dq, dk, dv);
-    const AttnPlan L = plan_attn(D, true, tc, false, dev);
+    const AttnPlan L = plan_attn(D, true, tc ? kTensor : kSimt, false, dev);
     if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
     fs::AttnParams p = attn_params(D, L, dev, workspace);
     p.q = q;

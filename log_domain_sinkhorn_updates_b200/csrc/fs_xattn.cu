@@ -235,6 +235,129 @@ __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnPara
     }
 }
 
+// Few rows (a unit of RT <= 4): what counts is to stream K and V.  Eight lanes take a key (four keys a warp at once),
+// each lane a 16-byte piece in every 32 of the width, so that a row is read in whole lines and a score takes three
+// shuffles; every group of lanes keeps its own running maximum, sum and output, joined at the end (lanes by shuffles,
+// warps through shared memory, in a fixed order).  The next keys' rows are loaded before this one's arithmetic.  C:
+// 32-element pieces of the widths.
+template <class T, int RT, int C>
+__global__ void __launch_bounds__(kTileThreads, 1) xattn_token_kernel(const AttnParams p) {
+    __shared__ float so[8][RT][32 * C + 4];
+    __shared__ float2 sml[8][RT];
+    const AttnUnit unit = p.k_len ? attn_unit<true>(p) : attn_unit<false>(p);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, grp = lane / 8, sub = lane % 8;
+    const int b = unit.b, c = unit.c, rows = p.n * p.group;
+    float4 q[RT][C], o[RT][C];
+    float mx[RT], l[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        mx[r] = -INFINITY;
+        l[r] = 0.f;
+        const bool live = unit.r0 + r < rows;
+        const T *src = (const T *)p.q + (live ? row_off(p.qs, p, b, c, unit.r0 + r) : 0);
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            const int e = 32 * k + 4 * sub;
+            q[r][k] = live && e < p.d ? load4(src + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+            q[r][k].x *= p.scale2, q[r][k].y *= p.scale2, q[r][k].z *= p.scale2, q[r][k].w *= p.scale2;
+            o[r][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    const T *kb = (const T *)p.k + p.ks.batch * b + p.ks.head * c, *vb = (const T *)p.v + p.vs.batch * b + p.vs.head * c;
+    float4 kn[C], vn[C];
+    float bn;
+    auto fetch = [&](int j) {  // key j's bias, and its rows unless it is masked (or past the part)
+        bn = attn_bias2(p, b, j, unit.j_end);
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            const int e = 32 * k + 4 * sub;
+            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+            kn[k] = bn != -INFINITY && e < p.d ? load4(kb + p.ks.token * j + e) : zero;
+            vn[k] = bn != -INFINITY && e < p.dv ? load4(vb + p.vs.token * j + e) : zero;
+        }
+    };
+    const int first = unit.j_beg + 4 * warp + grp;
+    fetch(first);
+    for (int j = first; j - grp < unit.j_end; j += 32) {  // whole warps: the shuffles take every lane
+        float4 kc[C], vc[C];
+        const float bias = bn;
+#pragma unroll
+        for (int k = 0; k < C; ++k) kc[k] = kn[k], vc[k] = vn[k];
+        fetch(j + 32);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            float z = 0.f;
+#pragma unroll
+            for (int k = 0; k < C; ++k)
+                z = fmaf(q[r][k].x, kc[k].x, fmaf(q[r][k].y, kc[k].y, fmaf(q[r][k].z, kc[k].z, fmaf(q[r][k].w, kc[k].w, z))));
+            z += __shfl_xor_sync(~0u, z, 1);
+            z += __shfl_xor_sync(~0u, z, 2);
+            z += __shfl_xor_sync(~0u, z, 4);
+            z += bias;
+            if (z > mx[r]) {  // the same on the eight lanes of the key
+                const float f = exp2f(mx[r] - z);
+                mx[r] = z;
+                l[r] *= f;
+#pragma unroll
+                for (int k = 0; k < C; ++k) o[r][k].x *= f, o[r][k].y *= f, o[r][k].z *= f, o[r][k].w *= f;
+            }
+            const float e = z == -INFINITY ? 0.f : exp2f(z - mx[r]);  // a NaN stays one
+            l[r] += e;
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                o[r][k].x = fmaf(e, vc[k].x, o[r][k].x);
+                o[r][k].y = fmaf(e, vc[k].y, o[r][k].y);
+                o[r][k].z = fmaf(e, vc[k].z, o[r][k].z);
+                o[r][k].w = fmaf(e, vc[k].w, o[r][k].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        float top = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 8));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+        const float f = exp2f(mx[r] - (top == -INFINITY ? 0.f : top));
+        float lw = l[r] * f;
+        lw += __shfl_xor_sync(~0u, lw, 8);
+        lw += __shfl_xor_sync(~0u, lw, 16);
+        if (lane == 0) sml[warp][r] = make_float2(top, lw);
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            float4 x = o[r][k];
+            x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+#pragma unroll
+            for (int s = 8; s <= 16; s *= 2) {
+                x.x += __shfl_xor_sync(~0u, x.x, s);
+                x.y += __shfl_xor_sync(~0u, x.y, s);
+                x.z += __shfl_xor_sync(~0u, x.z, s);
+                x.w += __shfl_xor_sync(~0u, x.w, s);
+            }
+            if (grp == 0) *reinterpret_cast<float4 *>(&so[warp][r][32 * k + 4 * sub]) = x;
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < RT * p.dv; e += kTileThreads) {
+        const int r = e / p.dv, k = e % p.dv, row = unit.r0 + r;
+        if (row >= rows) break;  // rows come in order
+        float top = -INFINITY, sum = 0.f, x = 0.f;
+        for (int w = 0; w < 8; ++w) top = fmaxf(top, sml[w][r].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        for (int w = 0; w < 8; ++w) {
+            const float f = exp2f(sml[w][r].x - ref);
+            sum += sml[w][r].y * f;
+            x = fmaf(so[w][r][k], f, x);
+        }
+        if (!unit.whole) {
+            if (k == 0) p.part_ml[unit.part + r] = make_float2(top, sum);
+            p.part_o[(unit.part + r) * p.dv + k] = x;
+        } else {
+            from_f(sum == 0.f ? 0.f : x / sum, (T *)p.out + row_off(p.os, p, b, c, row) + k);
+            if (p.lse && k == 0)
+                p.lse[row_stat(p, b, c, row)] = sum == 0.f ? -INFINITY : (float)(((double)top + log2((double)sum)) * kLn2d);
+        }
+    }
+}
+
 // Joins the parts of a row, in the parts' order.  One warp per packed row.
 template <class T>
 __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParams p) {
@@ -463,8 +586,20 @@ template <class T, int RPT>
 cudaError_t fwd_width(const AttnParams &p, cudaStream_t s) {
     return p.dv <= 64 ? fwd<T, RPT, 1>(p, s) : p.dv <= 128 ? fwd<T, RPT, 2>(p, s) : fwd<T, RPT, 4>(p, s);
 }
+template <class T, int RT>
+cudaError_t token(const AttnParams &p, cudaStream_t s) {
+    const int ctas = p.main_units + p.tail_units * p.splits, w = p.d > p.dv ? p.d : p.dv;
+    if (w <= 32)
+        xattn_token_kernel<T, RT, 1><<<ctas, kTileThreads, 0, s>>>(p);
+    else if (w <= 64)
+        xattn_token_kernel<T, RT, 2><<<ctas, kTileThreads, 0, s>>>(p);
+    else
+        xattn_token_kernel<T, RT, 4><<<ctas, kTileThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
 template <class T>
 cudaError_t fwd_rows(const AttnParams &p, cudaStream_t s) {
+    if (p.unit_rows <= 4) return p.unit_rows == 1 ? token<T, 1>(p, s) : p.unit_rows == 2 ? token<T, 2>(p, s) : token<T, 4>(p, s);
     return p.unit_rows == 16 ? fwd_width<T, 1>(p, s) : fwd_width<T, 4>(p, s);
 }
 
@@ -494,6 +629,13 @@ cudaError_t grad_rows(const AttnParams &p, int sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool xattn_token_ok(const void *q, const fs_view &qs, const void *k, const fs_view &ks, const void *v, const fs_view &vs,
+                    int d, int dv, int rows, bool bf16) {
+    if (rows > 8 || d > 128 || dv > 128 || d % 4 || dv % 4) return false;
+    return bf16 ? aligned4<__nv_bfloat16>(q, qs) && aligned4<__nv_bfloat16>(k, ks) && aligned4<__nv_bfloat16>(v, vs)
+                : aligned4<float>(q, qs) && aligned4<float>(k, ks) && aligned4<float>(v, vs);
+}
 
 cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s) {
     return bf16 ? fwd_rows<__nv_bfloat16>(p, s) : fwd_rows<float>(p, s);
