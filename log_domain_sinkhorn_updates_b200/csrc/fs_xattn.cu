@@ -21,6 +21,7 @@ constexpr int kTileThreads = 256;
 constexpr int kKeys = 64;      // keys of a forward tile
 constexpr int kStream = 32;    // streamed rows of a gradient tile
 constexpr int kMaxD = 256;
+constexpr size_t kMaxSmem = 227 * 1024;
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -76,21 +77,46 @@ __device__ void stage(float *sm, int cnt, int w, bool vec, Row row) {
             if (r0 + u * step < cnt && k < w) *reinterpret_cast<float4 *>(sm + (r0 + u * step) * ld + k) = v[u];
     }
 }
-// packed query rows [r0, ...), and keys [j0, ...) (zeros where bias2 says the key is masked)
+// The same by asynchronous copies where that can be (fp32, aligned rows); the caller commits and waits.
+template <class T, class Row>
+__device__ void stage_tile(float *sm, int cnt, int w, bool vec, const T *any, Row row) {
+    if (sizeof(T) != 4 || !vec) {
+        stage<T>(sm, cnt, w, vec, row);
+        return;
+    }
+    const int ld = smem_stride(w), pieces = (w + 3) / 4;
+    int per = 1;
+    while (per < pieces) per *= 2;
+    const int k = (int)threadIdx.x % per * 4, step = kTileThreads / per;
+    if (k >= w) return;
+    for (int r = (int)threadIdx.x / per; r < cnt; r += step) {
+        const T *src = row(r);
+        const int bytes = src ? min(16, (w - k) * 4) : 0;  // the rest of the piece becomes zeros
+        const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(sm + r * ld + k));
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src ? src + k : any), "r"(bytes)
+                     : "memory");
+    }
+}
+__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// packed query rows [r0, ...), and keys [j0, ...) of a problem (zeros where a key is masked, or not below j_end)
 template <class T>
 __device__ void stage_rows(float *sm, const void *src, const fs_view &s, const AttnParams &p, int b, int c, int r0,
                            int cnt, int w, bool vec) {
     const int rows = p.n * p.group;
-    stage<T>(sm, cnt, w, vec, [&](int r) -> const T * {
+    stage_tile<T>(sm, cnt, w, vec, (const T *)src, [&](int r) -> const T * {
         return r0 + r < rows ? (const T *)src + row_off(s, p, b, c, r0 + r) : nullptr;
     });
 }
 template <class T>
-__device__ void stage_keys(float *sm, const void *src, const fs_view &s, int b, int c, int j0, int cnt, int w,
-                           const float *bias2, bool vec) {
+__device__ void stage_keys(float *sm, const void *src, const fs_view &s, const AttnParams &p, int b, int c, int j0,
+                           int cnt, int w, int j_end, bool vec) {
     const T *base = (const T *)src + s.batch * b + s.head * c;
-    stage<T>(sm, cnt, w, vec,
-             [&](int j) -> const T * { return bias2[j] == -INFINITY ? nullptr : base + s.token * (j0 + j); });
+    stage_tile<T>(sm, cnt, w, vec, (const T *)src, [&](int j) -> const T * {
+        return attn_bias2(p, b, j0 + j, j_end) == -INFINITY ? nullptr : base + s.token * (j0 + j);
+    });
 }
 
 // acc[u][w] += sum_k a[ia + u][k] b[ib + 16 w][k] over rows of the tiles (strides la and lb)
@@ -150,14 +176,26 @@ __device__ __forceinline__ void put4(T *dst, float4 v, int k, int width, float m
 // One CTA: 16 RPT packed rows of a key head over one part of the keys, 16 x 16 threads of RPT rows x 4 keys.  C:
 // 64-column pieces of dv.
 template <class T, int RPT, int C>
-__global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnParams p, bool vec) {
+__global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnParams p, bool vec, int bufs) {
     extern __shared__ __align__(16) float sm[];
     constexpr int R = 16 * RPT, LP = kKeys + 4;
     const AttnUnit unit = p.k_len ? attn_unit<true>(p) : attn_unit<false>(p);
     const int r0 = unit.r0, c = unit.c, b = unit.b, j_beg = unit.j_beg, j_end = unit.j_end;
     const int ld = smem_stride(p.d), lv = smem_stride(p.dv);
-    float *sQ = sm, *sK = sQ + R * ld, *sV = sK + kKeys * ld, *sP = sV + kKeys * lv, *sB = sP + R * LP;
+    const int tile = kKeys * (ld + lv) + kKeys;  // K, V and the bias of one buffer
+    float *sQ = sm, *sP = sQ + R * ld, *ring = sP + R * LP;
+    // tile t into buffer t % bufs: with two, it arrives under the arithmetic of the tile before
+    auto fetch = [&](int t) {
+        float *sK = ring + t % bufs * tile, *sV = sK + kKeys * ld, *sB = sV + kKeys * lv;
+        const int j0 = j_beg + t * kKeys;
+        if (threadIdx.x < kKeys) sB[threadIdx.x] = attn_bias2(p, b, j0 + threadIdx.x, j_end);
+        stage_keys<T>(sK, p.k, p.ks, p, b, c, j0, kKeys, p.d, j_end, vec);
+        stage_keys<T>(sV, p.v, p.vs, p, b, c, j0, kKeys, p.dv, j_end, vec);
+    };
+    const int nt = j_end > j_beg ? (j_end - j_beg + kKeys - 1) / kKeys : 0;
     stage_rows<T>(sQ, p.q, p.qs, p, b, c, r0, R, p.d, vec);
+    if (bufs == 2 && nt > 0) fetch(0);
+    stage_commit();
     const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
     float4 o[RPT][C];
     float mx[RPT], l[RPT];
@@ -168,13 +206,19 @@ __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnPara
 #pragma unroll
         for (int k = 0; k < C; ++k) o[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int j0 = j_beg; j0 < j_end; j0 += kKeys) {
+    for (int t = 0; t < nt; ++t) {
+        if (bufs == 1) {
+            __syncthreads();
+            fetch(t);
+            stage_commit();
+            stage_wait<0>();
+        } else {
+            if (t + 1 < nt) fetch(t + 1);
+            stage_commit();
+            stage_wait<1>();
+        }
         __syncthreads();
-        if (threadIdx.x < kKeys) sB[threadIdx.x] = attn_bias2(p, b, j0 + threadIdx.x, j_end);
-        __syncthreads();
-        stage_keys<T>(sK, p.k, p.ks, b, c, j0, kKeys, p.d, sB, vec);
-        stage_keys<T>(sV, p.v, p.vs, b, c, j0, kKeys, p.dv, sB, vec);
-        __syncthreads();
+        const float *sK = ring + t % bufs * tile, *sV = sK + kKeys * ld, *sB = sV + kKeys * lv;
         float z[RPT][4];
 #pragma unroll
         for (int u = 0; u < RPT; ++u)
@@ -213,7 +257,9 @@ __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnPara
         }
         __syncwarp();  // a row's weights are written and read by its 16 threads, of one warp
         weigh<RPT, C>(o, sP + ti * RPT * LP, LP, sV, lv, kKeys, 4 * tj, p.dv);
+        if (bufs == 2) __syncthreads();  // the buffer is filled again
     }
+    stage_wait<0>();
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
         const int r = r0 + ti * RPT + u;
@@ -458,13 +504,14 @@ __global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p,
 // Otherwise: 16 U packed rows (Q, dO) against streamed keys (K, V): dq.  16 x 16 threads: U kept rows x 2 streamed
 // ones of the scores, U kept rows x 4 columns a piece of the sums.
 template <class T, bool KEYS, int U, int C>
-__device__ void grad_pass(const AttnParams &p, bool vec, int block, float *sm) {
+__device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, float *sm) {
     constexpr int LS = kStream + 4, kKept = 16 * U;
     const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads, t0 = block * kKept;
     const int ld = smem_stride(p.d), lv = smem_stride(p.dv);
-    float *a1 = sm, *a2 = a1 + kKept * ld, *b1 = a2 + kKept * lv, *b2 = b1 + kStream * ld, *sP = b2 + kStream * lv;
-    float *sS = sP + kKept * LS, *kb = sS + kKept * LS;  // kept: bias, or base-2 LSE and D
-    float *kd = kb + kKept, *sb = kd + kKept, *sd = sb + kStream;
+    float *a1 = sm, *a2 = a1 + kKept * ld, *sP = a2 + kKept * lv, *sS = sP + kKept * LS;
+    float *kb = sS + kKept * LS, *kd = kb + kKept;  // kept: bias, or base-2 LSE and D
+    float *ring = kd + kKept;
+    const int tile = kStream * (ld + lv) + 2 * kStream;  // the streamed pair, and bias, or base-2 LSE and D
     const int keys = attn_keys(p, b), rows = p.n * p.group;
     const int end = KEYS ? (t0 < keys ? rows : 0) : keys;
     // base-2 LSE (+inf: an empty row, or one past the end) and D of packed row r
@@ -483,14 +530,33 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int block, float *sm) {
         else
             stat(t0 + threadIdx.x, kb + threadIdx.x, kd + threadIdx.x);
     }
-    __syncthreads();
+    auto fetch = [&](int t) {  // as in the forward
+        float *b1 = ring + t % bufs * tile, *b2 = b1 + kStream * ld, *sb = b2 + kStream * lv, *sd = sb + kStream;
+        const int u0 = t * kStream;
+        if (threadIdx.x < kStream) {
+            if (KEYS)
+                stat(u0 + threadIdx.x, sb + threadIdx.x, sd + threadIdx.x);
+            else
+                sb[threadIdx.x] = attn_bias2(p, b, u0 + threadIdx.x, keys);
+        }
+        if (KEYS) {
+            stage_rows<T>(b1, p.q, p.qs, p, b, c, u0, kStream, p.d, vec);
+            stage_rows<T>(b2, p.dout, p.dos, p, b, c, u0, kStream, p.dv, vec);
+        } else {
+            stage_keys<T>(b1, p.k, p.ks, p, b, c, u0, kStream, p.d, keys, vec);
+            stage_keys<T>(b2, p.v, p.vs, p, b, c, u0, kStream, p.dv, keys, vec);
+        }
+    };
+    const int nt = (end + kStream - 1) / kStream;
     if (KEYS) {
-        stage_keys<T>(a1, p.k, p.ks, b, c, t0, kKept, p.d, kb, vec);
-        stage_keys<T>(a2, p.v, p.vs, b, c, t0, kKept, p.dv, kb, vec);
+        stage_keys<T>(a1, p.k, p.ks, p, b, c, t0, kKept, p.d, keys, vec);
+        stage_keys<T>(a2, p.v, p.vs, p, b, c, t0, kKept, p.dv, keys, vec);
     } else {
         stage_rows<T>(a1, p.q, p.qs, p, b, c, t0, kKept, p.d, vec);
         stage_rows<T>(a2, p.dout, p.dos, p, b, c, t0, kKept, p.dv, vec);
     }
+    if (bufs == 2 && nt > 0) fetch(0);
+    stage_commit();
     const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
     float4 g1[U][C], g2[U][KEYS ? C : 1];
 #pragma unroll
@@ -500,23 +566,19 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int block, float *sm) {
             g1[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (KEYS) g2[u][KEYS ? k : 0] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-    for (int u0 = 0; u0 < end; u0 += kStream) {
-        __syncthreads();
-        if (threadIdx.x < kStream) {
-            if (KEYS)
-                stat(u0 + threadIdx.x, sb + threadIdx.x, sd + threadIdx.x);
-            else
-                sb[threadIdx.x] = attn_bias2(p, b, u0 + threadIdx.x, keys);
-        }
-        __syncthreads();
-        if (KEYS) {
-            stage_rows<T>(b1, p.q, p.qs, p, b, c, u0, kStream, p.d, vec);
-            stage_rows<T>(b2, p.dout, p.dos, p, b, c, u0, kStream, p.dv, vec);
+    for (int t = 0; t < nt; ++t) {
+        if (bufs == 1) {
+            __syncthreads();
+            fetch(t);
+            stage_commit();
+            stage_wait<0>();
         } else {
-            stage_keys<T>(b1, p.k, p.ks, b, c, u0, kStream, p.d, sb, vec);
-            stage_keys<T>(b2, p.v, p.vs, b, c, u0, kStream, p.dv, sb, vec);
+            if (t + 1 < nt) fetch(t + 1);
+            stage_commit();
+            stage_wait<1>();
         }
         __syncthreads();
+        const float *b1 = ring + t % bufs * tile, *b2 = b1 + kStream * ld, *sb = b2 + kStream * lv, *sd = sb + kStream;
         float s[U][2], g[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) s[u][0] = s[u][1] = g[u][0] = g[u][1] = 0.f;
@@ -537,7 +599,9 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int block, float *sm) {
         __syncwarp();  // a kept row's weights are written and read by its 16 threads, of one warp
         weigh<U, C>(g1, sS + ti * U * LS, LS, b1, ld, kStream, 4 * tj, p.d);
         if constexpr (KEYS) weigh<U, C>(g2, sP + ti * U * LS, LS, b2, lv, kStream, 4 * tj, p.dv);
+        if (bufs == 2) __syncthreads();  // the buffer is filled again
     }
+    stage_wait<0>();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int at = t0 + ti * U + u;
@@ -556,12 +620,12 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int block, float *sm) {
 
 // Both passes in one launch: key_blocks CTAs of the first, then those of the second.
 template <class T, int U, int C>
-__global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnParams p, bool vec, int key_blocks) {
+__global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnParams p, bool vec, int bufs, int key_blocks) {
     extern __shared__ __align__(16) float sm[];
     if ((int)blockIdx.x < key_blocks)
-        grad_pass<T, true, U, C>(p, vec, (int)blockIdx.x, sm);
+        grad_pass<T, true, U, C>(p, vec, bufs, (int)blockIdx.x, sm);
     else
-        grad_pass<T, false, U, C>(p, vec, (int)blockIdx.x - key_blocks, sm);
+        grad_pass<T, false, U, C>(p, vec, bufs, (int)blockIdx.x - key_blocks, sm);
 }
 
 // Whether four elements of every row can be loaded at once.
@@ -574,12 +638,14 @@ bool aligned4(const void *base, const fs_view &s) {
 template <class T, int RPT, int C>
 cudaError_t fwd(const AttnParams &p, cudaStream_t s) {
     constexpr int R = 16 * RPT;
-    const size_t smem = sizeof(float) * ((size_t)(R + kKeys) * smem_stride(p.d) + kKeys * smem_stride(p.dv) +
-                                         R * (kKeys + 4) + kKeys);
+    const size_t fixed = (size_t)R * smem_stride(p.d) + R * (kKeys + 4);
+    const size_t tile = (size_t)kKeys * (smem_stride(p.d) + smem_stride(p.dv)) + kKeys;
+    const int bufs = (fixed + 2 * tile) * sizeof(float) <= kMaxSmem ? 2 : 1;
+    const size_t smem = (fixed + bufs * tile) * sizeof(float);
     cudaError_t e = allow_smem<&xattn_simt_kernel<T, RPT, C>>(smem);
     if (e != cudaSuccess) return e;
     const bool vec = aligned4<T>(p.q, p.qs) && aligned4<T>(p.k, p.ks) && aligned4<T>(p.v, p.vs);
-    xattn_simt_kernel<T, RPT, C><<<p.main_units + p.tail_units * p.splits, kTileThreads, smem, s>>>(p, vec);
+    xattn_simt_kernel<T, RPT, C><<<p.main_units + p.tail_units * p.splits, kTileThreads, smem, s>>>(p, vec, bufs);
     return cudaGetLastError();
 }
 template <class T, int RPT>
@@ -608,13 +674,15 @@ cudaError_t grad(const AttnParams &p, cudaStream_t s) {
     constexpr int kept = 16 * U;
     const int w = smem_stride(p.d) + smem_stride(p.dv);
     const int key_blocks = (p.m + kept - 1) / kept, row_blocks = (p.n * p.group + kept - 1) / kept;
-    const size_t smem = sizeof(float) * ((size_t)(kept + kStream) * w + 2 * kept * (kStream + 4) + 2 * kept + 2 * kStream);
+    const size_t fixed = (size_t)kept * w + 2 * kept * (kStream + 4) + 2 * kept, tile = (size_t)kStream * w + 2 * kStream;
+    const int bufs = (fixed + 2 * tile) * sizeof(float) <= kMaxSmem ? 2 : 1;
+    const size_t smem = (fixed + bufs * tile) * sizeof(float);
     cudaError_t e = allow_smem<&xattn_grad_kernel<T, U, C>>(smem);
     if (e != cudaSuccess) return e;
     const bool vec = aligned4<T>(p.q, p.qs) && aligned4<T>(p.k, p.ks) && aligned4<T>(p.v, p.vs) &&
                      aligned4<T>(p.dout, p.dos);
     xattn_grad_kernel<T, U, C>
-        <<<dim3(key_blocks + row_blocks, p.batch * p.kv_heads), kTileThreads, smem, s>>>(p, vec, key_blocks);
+        <<<dim3(key_blocks + row_blocks, p.batch * p.kv_heads), kTileThreads, smem, s>>>(p, vec, bufs, key_blocks);
     return cudaGetLastError();
 }
 template <class T, int U>
