@@ -447,14 +447,16 @@ FS_API size_t fs_cross_attn_workspace(const fs_attn_desc *desc, int grad);
  * to 0..m), or NULL for m.  bias: device fp32 [batch][m], or NULL; a value of
  * -1e30 or less masks its key.  Keys past the length or masked take no part:
  * their k and v may hold anything, NaN included.  A row without a key gives
- * out = 0 and lse = -inf.  lse: device fp32 [batch][heads][n], natural log; may
+ * out = 0 and lse = -inf (q too may hold anything where the length is 0; where
+ * the bias masks every key it has to be finite).  lse: device fp32 [batch][heads][n], natural log; may
  * be NULL.  bf16 on the tensor cores: scores and sums in fp32, the weights
  * e^{S - max} rounded to bf16 for their product with v.  Where few rows face
  * many keys (single tokens) the keys are split over the SMs and joined in order.
  * Non-finite inputs that take part give non-finite outputs.  Asynchronous.
  * Errors: FS_ERR_INVALID_ARG (sizes, scale, strides, null pointers, output
- * strides that overlap, a workspace that is too small), FS_ERR_UNSUPPORTED (device not
- * compute capability 10.x; batch * heads over 65535; n * heads of 2^27 or more; m of 2^30 or more).
+ * strides that overlap, a workspace that is too small), FS_ERR_UNSUPPORTED
+ * (device not compute capability 10.x; batch * heads over 65535; n * heads of
+ * 2^27 or more; m of 2^30 or more).
  */
 FS_API fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const void *k, const void *v,
                                const int *k_len, const float *bias, void *out, float *lse, void *workspace,
@@ -517,7 +519,8 @@ FS_API fs_status fs_cross_entropy(const fs_xent_desc *desc, const void *x, const
  *   dx_i = scale sum_j dz_ij w_j,   dw_j = scale sum_i dz_ij x_i
  * dx [n][d] and dw [v][d] of `dtype`.  dloss of ignored rows is not used.
  * Taken in pieces of the classes: the logits of a piece again, dz of the piece
- * (rounded to bf16 for bf16 inputs, in three planes for fp32), its share of dx (summed in fp32) and its rows of dw.
+ * (rounded to bf16 for bf16 inputs, in three planes for fp32), its share of dx
+ * (summed in fp32) and its rows of dw.
  * A target outside 0..v-1 that is not ignore_index makes the gradients NaN.
  * Asynchronous.  Errors as fs_cross_entropy.
  */

@@ -362,8 +362,8 @@ def fs_selftest_wait(h: Handle, timeout_ms=50) -> int:
 
 # ---- row-softmax operators without a handle ----
 # A call's descriptor and workspace size follow from the tensors' shapes, strides, types and
-# device (and the alignment they start on) alone, so they are checked and built once for each such combination and kept (at most
-# _PLAN_LIMIT of them; no data, address or tensor is kept).
+# device (and the alignment they start on) alone, so they are checked and built once for each
+# such combination and kept (at most _PLAN_LIMIT of them; no data, address or tensor is kept).
 _plans = {}
 _PLAN_LIMIT = 4096
 _OP_DTYPES = {"torch.float32": FS_F32, "torch.bfloat16": FS_BF16}
@@ -488,6 +488,7 @@ def fs_cross_attn(q, k, v, out, lse=None, k_len=None, bias=None, scale=None, str
     caller).  workspace: uint8 tensor of fs_cross_attn_workspace bytes; allocated if None."""
     L, torch = _ready()
     dev = q.get_device()
+    scale = None if scale is None else float(scale)  # plans are kept by its value
     desc, ref, need = _plan(
         (scale, dev, q.dtype, k.dtype, v.dtype, out.dtype, k.get_device(), v.get_device(), out.get_device(), q.shape,
          k.shape, v.shape, out.shape, q.stride(), k.stride(), v.stride(), out.stride()),
@@ -515,6 +516,7 @@ def fs_cross_attn_grad(q, k, v, out, lse, dout, dq, dk, dv, k_len=None, bias=Non
     (shapes of q, k, v and out; the other arguments as in the forward)."""
     L, torch = _ready()
     dev = q.get_device()
+    scale = None if scale is None else float(scale)  # plans are kept by its value
     tensors = (q, k, v, out, dout, dq, dk, dv)
     desc, ref, need = _plan(
         (scale, dev, *[x for t in tensors for x in (t.shape, t.stride(), t.dtype, t.get_device())]),
@@ -576,6 +578,7 @@ def fs_cross_entropy(x, w, target, loss, lse, scale=1.0, ignore_index=-100, stre
     is anything else outside the classes.  stream, workspace: as in fs_cross_attn."""
     L, torch = _ready()
     dev, xp, wp = x.get_device(), x.data_ptr(), w.data_ptr()
+    scale, ignore_index = float(scale), int(ignore_index)  # plans are kept by their values
     desc, ref, need = _plan(
         (scale, ignore_index, xp & 127, wp & 15, dev, w.get_device(), x.dtype, w.dtype, x.shape, w.shape, x.stride(),
          w.stride()),
@@ -600,6 +603,7 @@ def fs_cross_entropy_grad(x, w, target, lse, dloss, dx, dw, dlse=None, scale=1.0
     dlse (float32 [n]; dlse None for 0) of its outputs.  Other arguments as in the forward."""
     L, torch = _ready()
     dev, xp, wp = x.get_device(), x.data_ptr(), w.data_ptr()
+    scale, ignore_index = float(scale), int(ignore_index)  # plans are kept by their values
     desc, ref, need = _plan(
         (scale, ignore_index, xp & 127, wp & 15, dev,
          *[y for t in (x, w, dx, dw) for y in (t.shape, t.stride(), t.dtype, t.get_device())]),

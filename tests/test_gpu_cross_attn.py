@@ -357,6 +357,64 @@ def test_equals_the_barycentric_map():
     fs.fs_destroy(h)
 
 
+@pytest.mark.parametrize("dtype,d,dv", [(F32, 64, 64), (F32, 128, 36), (F32, 20, 128), (BF16, 36, 20), (BF16, 64, 64)])
+@pytest.mark.parametrize("n,H,Hk", [(1, 3, 1), (4, 1, 1), (1, 5, 1), (2, 8, 2), (3, 6, 2), (3, 3, 1)])
+def test_few_rows(n, H, Hk, dtype, d, dv):
+    """1 to 9 rows a key head, lengths that leave parts and problems without a key."""
+    for m in (0, 1, 31, 33, 2500):
+        q, k, v, dout = make(3, n, m, H, Hk, d, dv, dtype, seed=m + n)
+        k_len = torch.tensor([m, 0, m // 3 + 1], dtype=torch.int32, device="cuda")
+        for kw in ({}, {"k_len": k_len}):
+            out, lse = forward(q, k, v, **kw)
+            ref.check({"out": out, "lse": lse}, ref.attention(q, k, v, **kw))
+    _fs().fs_check()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("size", [(2, 600, 64, 8, 1, 64, 128), (3, 5, 1300, 4, 2, 128, 64), (2, 1, 900, 2, 2, 32, 32)])
+def test_gradient_of_few_heads_and_ragged_lengths(size, dtype):
+    """Few enough CTAs that the gradient's streamed tiles are split; lengths that leave parts without a key."""
+    q, k, v, dout = make(*size, dtype, seed=11)
+    m = size[2]
+    for lens in ([m, 0, 1], [m // 2 + 3, m, m - 1]):
+        kw = {"k_len": torch.tensor(lens[:size[0]], dtype=torch.int32, device="cuda")}
+        ref.check(run(q, k, v, dout, **kw), ref.attention(q, k, v, dout=dout, **kw))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_problems_than_are_ordered_by_length(dtype):
+    B, n, m = 41, 3, 700
+    q, k, v, dout = make(B, n, m, 4, 2, 64, 64, dtype, seed=13)
+    g = torch.Generator().manual_seed(3)
+    kw = {"k_len": torch.randint(-5, m + 20, (B,), dtype=torch.int32, generator=g).cuda()}
+    ref.check(run(q, k, v, dout, **kw), ref.attention(q, k, v, dout=dout, **kw))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [1, 6, 200])
+def test_anything_in_the_queries_of_a_problem_without_keys(dtype, n):
+    """Padding of a batch: length 0, NaN in q, k, v and the gradient; the other problems keep their bits."""
+    q, k, v, dout = make(3, n, 400, 4, 2, 64, 64, dtype, seed=17)
+    kw = {"k_len": torch.tensor([400, 0, 77], dtype=torch.int32, device="cuda")}
+    clean = run(q, k, v, dout, **kw)
+    for t in (q, k, v, dout):
+        t[1] = math.nan
+    got = run(q, k, v, dout, **kw)
+    for name in got:
+        assert torch.equal(got[name], clean[name]), name
+    assert (got["out"][1] == 0).all() and (got["dk"][1] == 0).all() and (got["dv"][1] == 0).all()
+
+
+def test_a_scale_given_as_a_tensor_is_read_at_every_call():
+    q, k, v, _ = make(1, 4, 50, 2, 2, 64, 64, F32, seed=19)
+    scale = torch.tensor(0.1)
+    forward(q, k, v, scale=scale)
+    scale.fill_(0.4)
+    out, lse = forward(q, k, v, scale=scale)
+    want_out, want_lse = forward(q, k, v, scale=0.4000000059604645)
+    assert torch.equal(out, want_out) and torch.equal(lse, want_lse)
+
+
 def test_refusals():
     fs = _fs()
     q, k, v, dout = make(2, 5, 9, 4, 2, 64, 64, BF16)

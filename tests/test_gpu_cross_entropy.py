@@ -242,6 +242,19 @@ def test_gradient_against_differences():
         assert (slope - (got[name].double() * u).sum()).abs() <= (want[name][1] * u.abs()).sum() + 1e-6
 
 
+def test_a_scale_given_as_a_tensor_is_read_at_every_call():
+    x, w = (torch.randn(s, 64, device="cuda", generator=torch.Generator(device="cuda").manual_seed(s)) for s in (9, 300))
+    target = torch.arange(9, device="cuda")
+    scale, got = torch.tensor(0.1), []
+    for value in (0.1, 0.5):
+        scale.fill_(value)
+        for sc in (scale, float(scale)):
+            got.append((torch.empty(9, device="cuda"), torch.empty(9, device="cuda")))
+            _fs().fs_cross_entropy(x, w, target, *got[-1], scale=sc)
+    assert torch.equal(got[2][0], got[3][0]) and torch.equal(got[2][1], got[3][1])
+    assert not torch.equal(got[1][1], got[3][1])
+
+
 def test_refusals():
     fs = _fs()
     x, w, target, dloss = make(20, 30, 64, BF16)
