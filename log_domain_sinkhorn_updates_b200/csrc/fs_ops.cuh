@@ -42,7 +42,7 @@ struct AttnParams {
     int *err;
 };
 
-// Allows a kernel `bytes` of dynamic shared memory, once a device (Kernel: one function, so that each has its own list).
+// Allows a kernel `bytes` of dynamic shared memory, once a device (Kernel: one function, each with a list of its own).
 template <auto Kernel>
 cudaError_t allow_smem(size_t bytes) {
     static std::atomic<size_t> allowed[64];
@@ -157,8 +157,8 @@ cudaError_t launch_xattn_grad_join(const AttnParams &p, cudaStream_t s);  // whe
 
 cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s);
 // Whether the CUDA-core forward takes the few rows of a key head by the token kernel (units of 1, 2 or 4 rows).
-bool xattn_token_ok(const void *q, const fs_view &qs, const void *k, const fs_view &ks, const void *v, const fs_view &vs,
-                    int d, int dv, int rows, bool bf16);
+bool xattn_token_ok(const void *q, const fs_view &qs, const void *k, const fs_view &ks, const void *v,
+                    const fs_view &vs, int d, int dv, int rows, bool bf16);
 cudaError_t launch_xattn_combine(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s);

@@ -130,8 +130,9 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, AttnKind kind, bool ragged,
         if (!tc || rows == 0 || heads == 0 || D.m == 0 || (key_blocks + row_blocks) * heads >= (size_t)dev.sms) return L;
         // Fewer CTAs than SMs: the streamed tiles of a CTA are split so that all SMs have about as many (a tile of the
         // pass that keeps keys takes 1.25 of the other's, 0.85 us at width 128), four a part at least, where that saves
-        // more than the joining pass costs (10 tiles' time, and the sums written and read back at 4 TB/s): 2000 queries of 8
-        // heads on one key head, 64 keys of 128: 232 us whole, 43 split; 1000 x 1000, 4 heads: 21 whole, 24 split.
+        // more than the joining pass costs (10 tiles' time, and the sums written and read back at 4 TB/s): 2000
+        // queries of 8 heads on one key head, 64 keys of 128: 232 us whole, 43 split; 1000 x 1000, 4 heads: 21 whole,
+        // 24 split.
         const int key_tiles = D.heads / D.kv_heads * up(D.n, 64), row_tiles = up(D.m, 64);
         const double each = (key_blocks * 1.25 * key_tiles + row_blocks * (double)row_tiles) * heads / dev.sms;
         const int kp = (int)std::min({std::max(1.0, key_tiles * 1.25 / each), std::max(1.0, key_tiles / 4.0), 64.0});
@@ -140,7 +141,8 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, AttnKind kind, bool ragged,
         const size_t dv = kp > 1 ? kp * heads * key_blocks * 128 * D.dv * sizeof(float) : 0;
         const size_t dq = rp > 1 ? rp * heads * row_blocks * 128 * D.d * sizeof(float) : 0;
         const double before = std::max(key_tiles * 1.25, (double)row_tiles);
-        const double after = std::max(key_tiles * 1.25 / kp, (double)row_tiles / rp) + 10.0 + 2.0 * (dk + dv + dq) / 4e6 / 0.85;
+        const double after =
+            std::max(key_tiles * 1.25 / kp, (double)row_tiles / rp) + 10.0 + 2.0 * (dk + dv + dq) / 4e6 / 0.85;
         if ((kp > 1 || rp > 1) && after < before) {
             L.key_parts = kp;
             L.row_parts = rp;
@@ -157,9 +159,9 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, AttnKind kind, bool ragged,
     // 2.3 us against 1.8 at width 128) and 1.5 tiles' time to start and end; waves of CTAs, one an SM (CUDA cores:
     // two).  With lengths, the longest problems come first and short ones fill in, so that the waves need not be whole,
     // and parts of unequal problems cost more (32 requests of up to 4096 keys: 66 us in one part, 89 in two; 8: 52 in
-    // one, 33 in two, 30 in three, 37 in four; 32 of 4096 each: 100 whole, 104 with the last wave in four parts).  Either every unit is split, or only those behind the last full wave,
-    // so that they fill the SMs too; the joining pass costs a launch, and the parts' sums written and read back
-    // (4 TB/s, 1.8 us a tile).
+    // one, 33 in two, 30 in three, 37 in four; 32 of 4096 each: 100 whole, 104 with the last wave in four parts).
+    // Either every unit is split, or only those behind the last full wave, so that they fill the SMs too; the joining
+    // pass costs a launch, and the parts' sums written and read back (4 TB/s, 1.8 us a tile).
     const int slots = tc ? dev.sms : 2 * dev.sms;
     const int side = tc               ? 128
                      : kind == kToken ? (rows <= 2 ? (int)rows : 4)
@@ -412,9 +414,9 @@ fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const void *k, 
     Device dev;
     if ((st = current_device(&dev)) != FS_OK) return st;
     const bool bf16 = D.dtype == FS_BF16, tc = attn_tc(D, q, k, v, out);
-    const AttnKind kind = tc ? kTensor
-                          : fs::xattn_token_ok(q, D.q, k, D.k, v, D.v, D.d, D.dv, D.n * (D.heads / D.kv_heads), bf16) ? kToken
-                                                                                                                    : kSimt;
+    const int rows = D.n * (D.heads / D.kv_heads);
+    const bool few = !tc && fs::xattn_token_ok(q, D.q, k, D.k, v, D.v, D.d, D.dv, rows, bf16);
+    const AttnKind kind = tc ? kTensor : few ? kToken : kSimt;
     const AttnPlan L = plan_attn(D, false, kind, k_len != nullptr, dev);
     if ((st = check_workspace(workspace, workspace_bytes, L.total)) != FS_OK) return st;
     fs::AttnParams p = attn_params(D, L, dev, workspace);

@@ -8,6 +8,13 @@
 //   D_i = dout_i.out_i,  P = e^{S - L},  dS_ij = P_ij (dout_i.v_j - D_i)
 //   dv_j = sum_i P_ij dout_i,  dk_j = scale sum_i dS_ij q_i,  dq_i = scale sum_j dS_ij k_j
 //
+// Tiles of rows and keys as fp32 in shared memory, 16 x 16 threads with a block
+// of each product in registers; where shared memory allows it the next tile
+// arrives under this one's arithmetic (fp32: asynchronous copies).  What bounds
+// it is shared memory: a 16-byte read for every 8 FMAs of a thread.  Up to 8 rows
+// a key head (single tokens) have a kernel that streams K and V through
+// registers alone: what bounds it is memory.
+//
 // The heads that share a key head are rows of one problem: row r = i group + h.
 // Keys past the length or masked by the bias are staged as zeros, so nothing
 // that stands in their memory reaches a sum.
@@ -309,7 +316,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) xattn_token_kernel(const Attn
             o[r][k] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
-    const T *kb = (const T *)p.k + p.ks.batch * b + p.ks.head * c, *vb = (const T *)p.v + p.vs.batch * b + p.vs.head * c;
+    const T *kb = (const T *)p.k + p.ks.batch * b + p.ks.head * c;
+    const T *vb = (const T *)p.v + p.vs.batch * b + p.vs.head * c;
     float4 kn[C], vn[C];
     float bn;
     auto fetch = [&](int j) {  // key j's bias, and its rows unless it is masked (or past the part)
@@ -335,7 +343,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) xattn_token_kernel(const Attn
             float z = 0.f;
 #pragma unroll
             for (int k = 0; k < C; ++k)
-                z = fmaf(q[r][k].x, kc[k].x, fmaf(q[r][k].y, kc[k].y, fmaf(q[r][k].z, kc[k].z, fmaf(q[r][k].w, kc[k].w, z))));
+                z = fmaf(q[r][k].x, kc[k].x,
+                         fmaf(q[r][k].y, kc[k].y, fmaf(q[r][k].z, kc[k].z, fmaf(q[r][k].w, kc[k].w, z))));
             z += __shfl_xor_sync(~0u, z, 1);
             z += __shfl_xor_sync(~0u, z, 2);
             z += __shfl_xor_sync(~0u, z, 4);
@@ -399,7 +408,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) xattn_token_kernel(const Attn
         } else {
             from_f(sum == 0.f ? 0.f : x / sum, (T *)p.out + row_off(p.os, p, b, c, row) + k);
             if (p.lse && k == 0)
-                p.lse[row_stat(p, b, c, row)] = sum == 0.f ? -INFINITY : (float)(((double)top + log2((double)sum)) * kLn2d);
+                p.lse[row_stat(p, b, c, row)] =
+                    sum == 0.f ? -INFINITY : (float)(((double)top + log2((double)sum)) * kLn2d);
         }
     }
 }
@@ -620,7 +630,8 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, fl
 
 // Both passes in one launch: key_blocks CTAs of the first, then those of the second.
 template <class T, int U, int C>
-__global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnParams p, bool vec, int bufs, int key_blocks) {
+__global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnParams p, bool vec, int bufs,
+                                                                  int key_blocks) {
     extern __shared__ __align__(16) float sm[];
     if ((int)blockIdx.x < key_blocks)
         grad_pass<T, true, U, C>(p, vec, bufs, (int)blockIdx.x, sm);
@@ -665,7 +676,9 @@ cudaError_t token(const AttnParams &p, cudaStream_t s) {
 }
 template <class T>
 cudaError_t fwd_rows(const AttnParams &p, cudaStream_t s) {
-    if (p.unit_rows <= 4) return p.unit_rows == 1 ? token<T, 1>(p, s) : p.unit_rows == 2 ? token<T, 2>(p, s) : token<T, 4>(p, s);
+    if (p.unit_rows == 1) return token<T, 1>(p, s);
+    if (p.unit_rows == 2) return token<T, 2>(p, s);
+    if (p.unit_rows == 4) return token<T, 4>(p, s);
     return p.unit_rows == 16 ? fwd_width<T, 1>(p, s) : fwd_width<T, 4>(p, s);
 }
 
@@ -674,7 +687,8 @@ cudaError_t grad(const AttnParams &p, cudaStream_t s) {
     constexpr int kept = 16 * U;
     const int w = smem_stride(p.d) + smem_stride(p.dv);
     const int key_blocks = (p.m + kept - 1) / kept, row_blocks = (p.n * p.group + kept - 1) / kept;
-    const size_t fixed = (size_t)kept * w + 2 * kept * (kStream + 4) + 2 * kept, tile = (size_t)kStream * w + 2 * kStream;
+    const size_t fixed = (size_t)kept * w + 2 * kept * (kStream + 4) + 2 * kept;
+    const size_t tile = (size_t)kStream * w + 2 * kStream;
     const int bufs = (fixed + 2 * tile) * sizeof(float) <= kMaxSmem ? 2 : 1;
     const size_t smem = (fixed + bufs * tile) * sizeof(float);
     cudaError_t e = allow_smem<&xattn_grad_kernel<T, U, C>>(smem);
@@ -698,8 +712,8 @@ cudaError_t grad_rows(const AttnParams &p, int sms, cudaStream_t s) {
 
 }  // namespace
 
-bool xattn_token_ok(const void *q, const fs_view &qs, const void *k, const fs_view &ks, const void *v, const fs_view &vs,
-                    int d, int dv, int rows, bool bf16) {
+bool xattn_token_ok(const void *q, const fs_view &qs, const void *k, const fs_view &ks, const void *v,
+                    const fs_view &vs, int d, int dv, int rows, bool bf16) {
     if (rows > 8 || d > 128 || dv > 128 || d % 4 || dv % 4) return false;
     return bf16 ? aligned4<__nv_bfloat16>(q, qs) && aligned4<__nv_bfloat16>(k, ks) && aligned4<__nv_bfloat16>(v, vs)
                 : aligned4<float>(q, qs) && aligned4<float>(k, ks) && aligned4<float>(v, vs);
@@ -723,8 +737,8 @@ cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s) {
         xattn_dot_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(
             p, per, aligned4<__nv_bfloat16>(p.out, p.os) && aligned4<__nv_bfloat16>(p.dout, p.dos));
     else
-        xattn_dot_kernel<float><<<grid, kThreads, 0, s>>>(p, per,
-                                                          aligned4<float>(p.out, p.os) && aligned4<float>(p.dout, p.dos));
+        xattn_dot_kernel<float><<<grid, kThreads, 0, s>>>(
+            p, per, aligned4<float>(p.out, p.os) && aligned4<float>(p.dout, p.dos));
     return cudaGetLastError();
 }
 cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s) {

@@ -16,8 +16,13 @@
 // tile under two descriptors.  Seven products instead of the five of one
 // combined pass, in exchange for sums that never leave the SM.
 //
-// TMEM (512 columns): two or three buffers of S / P and dP / dS (64 columns each), the sums behind them.  Warps: 0 loads by TMA, 1 allocates TMEM, 1 and 3 issue the
-// MMAs of the scores and of the sums, 2 statistics, bias and masks, 4..7 and 8..11 turn scores into P and dS for even and odd tiles.
+// Where there are fewer CTAs than SMs the streamed tiles are split into parts,
+// whose raw sums a second kernel adds in their order.
+//
+// TMEM (512 columns): two or three buffers of S / P and dP / dS (64 columns
+// each), the sums behind them.  Warps: 0 loads by TMA, 1 allocates TMEM, 1 and 3
+// issue the MMAs of the scores and of the sums, 2 statistics, bias and masks,
+// 4..7 and 8..11 turn scores into P and dS for even and odd tiles.
 #include <cuda.h>
 
 #include "fs_ops_tc.cuh"
@@ -148,8 +153,8 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                 for (int a = 0; a < kAtoms; ++a) {
                     tma_load_4d(dst + a * 8192u, &map_s1, saddr(full + s), a * 64, y, h * (KEYS ? g.q_head : g.k_head),
                                 b * (KEYS ? g.q_batch : g.k_batch));
-                    tma_load_4d(dst + L.half + a * 8192u, &map_s2, saddr(full + s), a * 64, y, h * (KEYS ? g.g_head : g.v_head),
-                                b * (KEYS ? g.g_batch : g.v_batch));
+                    tma_load_4d(dst + L.half + a * 8192u, &map_s2, saddr(full + s), a * 64, y,
+                                h * (KEYS ? g.g_head : g.v_head), b * (KEYS ? g.g_batch : g.v_batch));
                 }
                 rp.step(1, NS);
                 y += kTile;
@@ -163,7 +168,8 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                 *abort_flag = 1;
             }
             if (KEYS && nt > 0) mbar_wait_near(stfull, 0, p.timeout_ns);
-            for (int k = max(0, t - NS); k < t; ++k) mbar_wait_near(full + (k % NS), (uint32_t)(k / NS) & 1u, p.timeout_ns);
+            for (int k = max(0, t - NS); k < t; ++k)
+                mbar_wait_near(full + (k % NS), (uint32_t)(k / NS) & 1u, p.timeout_ns);
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -226,7 +232,8 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                 }
             }
             fetch(t + 1);
-            if (t >= kColSlots && !mbar_wait_near(cempty + j, ((uint32_t)(t / kColSlots) & 1u) ^ 1u, p.timeout_ns)) ok = false;
+            if (t >= kColSlots && !mbar_wait_near(cempty + j, ((uint32_t)(t / kColSlots) & 1u) ^ 1u, p.timeout_ns))
+                ok = false;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 col[32 * u + lane] = v0[u];
@@ -463,24 +470,24 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                             nt > 0 ? make_uint4(o[u], o[u + 1], o[u + 2], o[u + 3]) : make_uint4(0u, 0u, 0u, 0u);
             }
         } else {
-        for (int k = KEYS ? 0 : 32 * grp; k < width; k += KEYS ? 32 : 64) {
-            uint32_t o[32];
-            if (nt > 0) {
-                tmem_ld32(to + k, o);
-                tmem_ld_wait();
-            }
-#pragma unroll
-            for (int u = 0; u < 32; u += 8) {
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            for (int k = KEYS ? 0 : 32 * grp; k < width; k += KEYS ? 32 : 64) {
+                uint32_t o[32];
                 if (nt > 0) {
-                    w.x = bf16x2(__uint_as_float(o[u]) * mul, __uint_as_float(o[u + 1]) * mul);
-                    w.y = bf16x2(__uint_as_float(o[u + 2]) * mul, __uint_as_float(o[u + 3]) * mul);
-                    w.z = bf16x2(__uint_as_float(o[u + 4]) * mul, __uint_as_float(o[u + 5]) * mul);
-                    w.w = bf16x2(__uint_as_float(o[u + 6]) * mul, __uint_as_float(o[u + 7]) * mul);
+                    tmem_ld32(to + k, o);
+                    tmem_ld_wait();
                 }
-                if (live && k + u < width) *reinterpret_cast<uint4 *>(dst + k + u) = w;  // widths: multiples of 8
+    #pragma unroll
+                for (int u = 0; u < 32; u += 8) {
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (nt > 0) {
+                        w.x = bf16x2(__uint_as_float(o[u]) * mul, __uint_as_float(o[u + 1]) * mul);
+                        w.y = bf16x2(__uint_as_float(o[u + 2]) * mul, __uint_as_float(o[u + 3]) * mul);
+                        w.z = bf16x2(__uint_as_float(o[u + 4]) * mul, __uint_as_float(o[u + 5]) * mul);
+                        w.w = bf16x2(__uint_as_float(o[u + 6]) * mul, __uint_as_float(o[u + 7]) * mul);
+                    }
+                    if (live && k + u < width) *reinterpret_cast<uint4 *>(dst + k + u) = w;  // widths: multiples of 8
+                }
             }
-        }
         }
     }
 
@@ -595,8 +602,8 @@ cudaError_t launch_xattn_grad_join(const AttnParams &p, cudaStream_t s) {
     const int rows = p.n * p.group, d8 = p.d / 8;
     const unsigned long long work = (p.key_parts > 1 ? (unsigned long long)p.m * (d8 + p.dv / 8) : 0ull) +
                                     (p.row_parts > 1 ? (unsigned long long)rows * d8 : 0ull);
-    return launch_dependent(xattn_grad_join_kernel, dim3((unsigned)((work + 255) / 256), p.batch * p.kv_heads), 256, 0, s, p,
-                            (p.m + 127) / 128 * 128, (rows + 127) / 128 * 128);
+    return launch_dependent(xattn_grad_join_kernel, dim3((unsigned)((work + 255) / 256), p.batch * p.kv_heads), 256, 0,
+                            s, p, (p.m + 127) / 128 * 128, (rows + 127) / 128 * 128);
 }
 
 }  // namespace fs

@@ -1,6 +1,6 @@
 // Cross attention forward on the sm_100a tensor cores: S = Q K^T and O += P V
-// per 128-key tile with S, P and O in TMEM, one pass over the keys with a
-// running maximum and sum a row.
+// per 64 keys with S, P and O in TMEM, one pass over the keys with a running
+// maximum and sum a row.  Tiles of K and V: 128 keys (QT = 2) or 64 (QT = 1).
 //
 // A CTA has 128-row blocks of Q (rows r = query x heads that share the key
 // head) and two softmax groups of 128 threads, a thread a row:
@@ -14,8 +14,8 @@
 // turns one buffer into weights, the products of the other and its next scores
 // run: with one 128-key buffer, softmax, P V and the next S were a chain.
 // P (bf16) is written over the S it came from and is the A operand of the P V
-// product there; V is its right factor as it lies in
-// memory (width contiguous), by the descriptor.
+// product there; V is its right factor as it lies in memory (width contiguous),
+// by the descriptor.
 //
 // The maximum is lazy: the weights of 64 keys are taken against the running
 // reference as it stands, and only where their sum passes 2^12 (which any score
@@ -44,7 +44,7 @@ using namespace tc;
 constexpr int kStep = 64;       // keys of a score buffer
 constexpr int kThreads = 384;
 constexpr int kBiasSlots = 4;
-// Registers a thread of the 128 that load and issue, and of the 256 of the softmax: together the 384 x 168 of the launch.
+// Registers a thread of the 128 that load and issue, and of the 256 of the softmax: together the launch's 384 x 168.
 constexpr int kFewRegs = 88, kManyRegs = 208;
 
 // s = s c + bias over 64 scores (base 2)
@@ -189,14 +189,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t dst = saddr(ring + (size_t)s * L.slot);
                     mbar_expect_tx(full + s, (uint32_t)atoms * kAtom);
                     for (int a = 0; a < atoms; ++a)
-                        tma_load_4d(dst + a * kAtom, map, saddr(full + s), a * 64, j_beg + (i >> 1) * kTS, c * hm, b * bm);
+                        tma_load_4d(dst + a * kAtom, map, saddr(full + s), a * 64, j_beg + (i >> 1) * kTS, c * hm,
+                                    b * bm);
                     rp.step(1, NS);
                 }
                 if (!ok) {
                     atomicOr(p.err, kDevErrTimeout);
                     *abort_flag = 1;
                 }
-                for (int k = max(0, i - NS); k < i; ++k) mbar_wait_near(full + (k % NS), (uint32_t)(k / NS) & 1u, p.timeout_ns);
+                for (int k = max(0, i - NS); k < i; ++k)
+                    mbar_wait_near(full + (k % NS), (uint32_t)(k / NS) & 1u, p.timeout_ns);
             }
             __syncwarp();
         } else if (warp == 3) {
@@ -218,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     cleared |= dead[u];
                 }
                 if (masked_tile(t)) {
-                    if (used >= kBiasSlots && !mbar_wait_near(bempty + bs.slot, bs.phase ^ 1u, p.timeout_ns)) ok = false;
+                    if (used >= kBiasSlots && !mbar_wait_near(bempty + bs.slot, bs.phase ^ 1u, p.timeout_ns))
+                        ok = false;
 #pragma unroll
                     for (int u = 0; u < kTS / 32; ++u) sBias[bs.slot * kTS + 32 * u + lane] = bv[u];
                     __syncwarp();
@@ -562,8 +565,9 @@ cudaError_t launch_xattn_tc(const AttnParams &p, cudaStream_t s) {
     g.vatoms = (p.dv + 63) / 64;
     g.dv_pad = (p.dv + 15) / 16 * 16;
     CUtensorMap mk, mv;
-    if (!attn_map(&mk, p.k, p.ks, p.d, p.m, p.kv_heads, p.batch, tile_keys(two_blocks ? 2 : 1), &g.k_head, &g.k_batch) ||
-        !attn_map(&mv, p.v, p.vs, p.dv, p.m, p.kv_heads, p.batch, tile_keys(two_blocks ? 2 : 1), &g.v_head, &g.v_batch))
+    const int box = tile_keys(two_blocks ? 2 : 1);
+    if (!attn_map(&mk, p.k, p.ks, p.d, p.m, p.kv_heads, p.batch, box, &g.k_head, &g.k_batch) ||
+        !attn_map(&mv, p.v, p.vs, p.dv, p.m, p.kv_heads, p.batch, box, &g.v_head, &g.v_batch))
         return cudaErrorInvalidValue;
     return p.k_len ? launch_width<true>(p, g, mk, mv, s) : launch_width<false>(p, g, mk, mv, s);
 }
