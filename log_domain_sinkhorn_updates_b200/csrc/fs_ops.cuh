@@ -20,6 +20,7 @@ constexpr float kBiasMask = -1e30f;
 
 struct AttnParams {
     int batch, n, m, heads, kv_heads, group, d, dv;
+    unsigned group_mul, group_shift;  // r / group without a division (row_query in fs_xattn.cu)
     float scale, scale2;  // score scale, and times log2(e)
     fs_view qs, ks, vs, os, dos, dqs, dks, dvs;  // element strides (batch, token, head)
     const void *q, *k, *v, *dout;

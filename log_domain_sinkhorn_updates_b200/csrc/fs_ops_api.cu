@@ -240,6 +240,10 @@ fs::AttnParams attn_params(const fs_attn_desc &D, const AttnPlan &L, const Devic
     p.heads = D.heads;
     p.kv_heads = D.kv_heads;
     p.group = D.heads / D.kv_heads;
+    int log = 0;
+    while (1 << log < p.group) ++log;
+    p.group_mul = (unsigned)(((1ull << (31 + log)) + p.group - 1) / p.group);
+    p.group_shift = (unsigned)std::max(0, log - 1);
     p.d = D.d;
     p.dv = D.dv;
     p.scale = D.scale;

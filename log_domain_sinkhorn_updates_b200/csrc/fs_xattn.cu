@@ -35,17 +35,30 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void from_f(float v, float *o) { *o = v; }
 __device__ __forceinline__ void from_f(float v, __nv_bfloat16 *o) { *o = __float2bfloat16_rn(v); }
 
+// The query of packed row r: r / group without a division (r < 2^31: m = ceil(2^(31 + s) / group), s = ceil(log2
+// group), is too large by less than group / group of 2^(31 + s) / r, so the product's integer part is the quotient).
+__device__ __forceinline__ int row_query(const AttnParams &p, int r) {
+    return p.group == 1 ? r : (int)(__umulhi((unsigned)r, p.group_mul) >> p.group_shift);
+}
 // Element offset of packed row r (of key head c, problem b) in a query-side tensor.
 __device__ __forceinline__ long long row_off(const fs_view &s, const AttnParams &p, int b, int c, int r) {
-    return s.batch * b + s.token * (r / p.group) + s.head * (c * p.group + r % p.group);
+    const int i = row_query(p, r);
+    return s.batch * b + s.token * i + s.head * (c * p.group + r - i * p.group);
 }
 __device__ __forceinline__ size_t row_stat(const AttnParams &p, int b, int c, int r) {
-    return ((size_t)b * p.heads + c * p.group + r % p.group) * p.n + r / p.group;
+    const int i = row_query(p, r);
+    return ((size_t)b * p.heads + c * p.group + r - i * p.group) * p.n + i;
 }
 
 // Row stride in shared memory of a tile of width w: an odd number of 16-byte pieces, so that eight rows' pieces at
 // one column lie in different banks.
 __host__ __device__ inline int smem_stride(int w) { return ((w + 3) / 4 | 1) * 4; }
+// The tiles' stride in a kernel of C 64-column pieces: known to the compiler, so that rows are offsets of one address,
+// but for the widest, whose shared memory it would cost.
+template <int C>
+__host__ __device__ __forceinline__ int tile_stride(int w) {
+    return C <= 2 ? 64 * C + 4 : smem_stride(w);
+}
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
@@ -53,11 +66,11 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
     return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
                        __uint_as_float(v.y & 0xffff0000u));
 }
-// `cnt` rows of width w into sm (stride smem_stride(w), zeros up to a multiple of 4); row(r) is a row's address, or
+// `cnt` rows of width w into sm (stride ld, zeros up to a multiple of 4); row(r) is a row's address, or
 // null for a row of zeros.  vec: every row is aligned to four elements.
 template <class T, class Row>
-__device__ void stage(float *sm, int cnt, int w, bool vec, Row row) {
-    const int ld = smem_stride(w), pieces = (w + 3) / 4;
+__device__ void stage(float *sm, int ld, int cnt, int w, bool vec, Row row) {
+    const int pieces = (w + 3) / 4;
     int per = 1;
     while (per < pieces) per *= 2;
     const int k = (int)threadIdx.x % per * 4, step = kTileThreads / per;
@@ -86,12 +99,12 @@ __device__ void stage(float *sm, int cnt, int w, bool vec, Row row) {
 }
 // The same by asynchronous copies where that can be (fp32, aligned rows); the caller commits and waits.
 template <class T, class Row>
-__device__ void stage_tile(float *sm, int cnt, int w, bool vec, const T *any, Row row) {
+__device__ void stage_tile(float *sm, int ld, int cnt, int w, bool vec, const T *any, Row row) {
     if (sizeof(T) != 4 || !vec) {
-        stage<T>(sm, cnt, w, vec, row);
+        stage<T>(sm, ld, cnt, w, vec, row);
         return;
     }
-    const int ld = smem_stride(w), pieces = (w + 3) / 4;
+    const int pieces = (w + 3) / 4;
     int per = 1;
     while (per < pieces) per *= 2;
     const int k = (int)threadIdx.x % per * 4, step = kTileThreads / per;
@@ -110,18 +123,18 @@ __device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group
 
 // packed query rows [r0, ...), and keys [j0, ...) of a problem (zeros where a key is masked, or not below j_end)
 template <class T>
-__device__ void stage_rows(float *sm, const void *src, const fs_view &s, const AttnParams &p, int b, int c, int r0,
+__device__ void stage_rows(float *sm, int ld, const void *src, const fs_view &s, const AttnParams &p, int b, int c, int r0,
                            int cnt, int w, bool vec) {
     const int rows = p.n * p.group;
-    stage_tile<T>(sm, cnt, w, vec, (const T *)src, [&](int r) -> const T * {
+    stage_tile<T>(sm, ld, cnt, w, vec, (const T *)src, [&](int r) -> const T * {
         return r0 + r < rows ? (const T *)src + row_off(s, p, b, c, r0 + r) : nullptr;
     });
 }
 template <class T>
-__device__ void stage_keys(float *sm, const void *src, const fs_view &s, const AttnParams &p, int b, int c, int j0,
+__device__ void stage_keys(float *sm, int ld, const void *src, const fs_view &s, const AttnParams &p, int b, int c, int j0,
                            int cnt, int w, int j_end, bool vec) {
     const T *base = (const T *)src + s.batch * b + s.head * c;
-    stage_tile<T>(sm, cnt, w, vec, (const T *)src, [&](int j) -> const T * {
+    stage_tile<T>(sm, ld, cnt, w, vec, (const T *)src, [&](int j) -> const T * {
         return attn_bias2(p, b, j0 + j, j_end) == -INFINITY ? nullptr : base + s.token * (j0 + j);
     });
 }
@@ -181,26 +194,26 @@ __device__ __forceinline__ void put4(T *dst, float4 v, int k, int width, float m
 }
 
 // One CTA: 16 RPT packed rows of a key head over one part of the keys, 16 x 16 threads of RPT rows x 4 keys.  C:
-// 64-column pieces of dv.
+// 64-column pieces of the widths.
 template <class T, int RPT, int C>
 __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnParams p, bool vec, int bufs) {
     extern __shared__ __align__(16) float sm[];
     constexpr int R = 16 * RPT, LP = kKeys + 4;
     const AttnUnit unit = p.k_len ? attn_unit<true>(p) : attn_unit<false>(p);
     const int r0 = unit.r0, c = unit.c, b = unit.b, j_beg = unit.j_beg, j_end = unit.j_end;
-    const int ld = smem_stride(p.d), lv = smem_stride(p.dv);
+    const int ld = tile_stride<C>(p.d), lv = tile_stride<C>(p.dv);
     const int tile = kKeys * (ld + lv) + kKeys;  // K, V and the bias of one buffer
     float *sQ = sm, *sP = sQ + R * ld, *ring = sP + R * LP;
     // tile t into buffer t % bufs: with two, it arrives under the arithmetic of the tile before
     auto fetch = [&](int t) {
-        float *sK = ring + t % bufs * tile, *sV = sK + kKeys * ld, *sB = sV + kKeys * lv;
+        float *sK = ring + (bufs == 2 ? t & 1 : 0) * tile, *sV = sK + kKeys * ld, *sB = sV + kKeys * lv;
         const int j0 = j_beg + t * kKeys;
         if (threadIdx.x < kKeys) sB[threadIdx.x] = attn_bias2(p, b, j0 + threadIdx.x, j_end);
-        stage_keys<T>(sK, p.k, p.ks, p, b, c, j0, kKeys, p.d, j_end, vec);
-        stage_keys<T>(sV, p.v, p.vs, p, b, c, j0, kKeys, p.dv, j_end, vec);
+        stage_keys<T>(sK, ld, p.k, p.ks, p, b, c, j0, kKeys, p.d, j_end, vec);
+        stage_keys<T>(sV, lv, p.v, p.vs, p, b, c, j0, kKeys, p.dv, j_end, vec);
     };
     const int nt = j_end > j_beg ? (j_end - j_beg + kKeys - 1) / kKeys : 0;
-    stage_rows<T>(sQ, p.q, p.qs, p, b, c, r0, R, p.d, vec);
+    stage_rows<T>(sQ, ld, p.q, p.qs, p, b, c, r0, R, p.d, vec);
     if (bufs == 2 && nt > 0) fetch(0);
     stage_commit();
     const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
@@ -225,7 +238,7 @@ __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnPara
             stage_wait<1>();
         }
         __syncthreads();
-        const float *sK = ring + t % bufs * tile, *sV = sK + kKeys * ld, *sB = sV + kKeys * lv;
+        const float *sK = ring + (bufs == 2 ? t & 1 : 0) * tile, *sV = sK + kKeys * ld, *sB = sV + kKeys * lv;
         float z[RPT][4];
 #pragma unroll
         for (int u = 0; u < RPT; ++u)
@@ -517,7 +530,7 @@ template <class T, bool KEYS, int U, int C>
 __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, float *sm) {
     constexpr int LS = kStream + 4, kKept = 16 * U;
     const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads, t0 = block * kKept;
-    const int ld = smem_stride(p.d), lv = smem_stride(p.dv);
+    const int ld = tile_stride<C>(p.d), lv = tile_stride<C>(p.dv);
     float *a1 = sm, *a2 = a1 + kKept * ld, *sP = a2 + kKept * lv, *sS = sP + kKept * LS;
     float *kb = sS + kKept * LS, *kd = kb + kKept;  // kept: bias, or base-2 LSE and D
     float *ring = kd + kKept;
@@ -541,7 +554,7 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, fl
             stat(t0 + threadIdx.x, kb + threadIdx.x, kd + threadIdx.x);
     }
     auto fetch = [&](int t) {  // as in the forward
-        float *b1 = ring + t % bufs * tile, *b2 = b1 + kStream * ld, *sb = b2 + kStream * lv, *sd = sb + kStream;
+        float *b1 = ring + (bufs == 2 ? t & 1 : 0) * tile, *b2 = b1 + kStream * ld, *sb = b2 + kStream * lv, *sd = sb + kStream;
         const int u0 = t * kStream;
         if (threadIdx.x < kStream) {
             if (KEYS)
@@ -550,20 +563,20 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, fl
                 sb[threadIdx.x] = attn_bias2(p, b, u0 + threadIdx.x, keys);
         }
         if (KEYS) {
-            stage_rows<T>(b1, p.q, p.qs, p, b, c, u0, kStream, p.d, vec);
-            stage_rows<T>(b2, p.dout, p.dos, p, b, c, u0, kStream, p.dv, vec);
+            stage_rows<T>(b1, ld, p.q, p.qs, p, b, c, u0, kStream, p.d, vec);
+            stage_rows<T>(b2, lv, p.dout, p.dos, p, b, c, u0, kStream, p.dv, vec);
         } else {
-            stage_keys<T>(b1, p.k, p.ks, p, b, c, u0, kStream, p.d, keys, vec);
-            stage_keys<T>(b2, p.v, p.vs, p, b, c, u0, kStream, p.dv, keys, vec);
+            stage_keys<T>(b1, ld, p.k, p.ks, p, b, c, u0, kStream, p.d, keys, vec);
+            stage_keys<T>(b2, lv, p.v, p.vs, p, b, c, u0, kStream, p.dv, keys, vec);
         }
     };
     const int nt = (end + kStream - 1) / kStream;
     if (KEYS) {
-        stage_keys<T>(a1, p.k, p.ks, p, b, c, t0, kKept, p.d, keys, vec);
-        stage_keys<T>(a2, p.v, p.vs, p, b, c, t0, kKept, p.dv, keys, vec);
+        stage_keys<T>(a1, ld, p.k, p.ks, p, b, c, t0, kKept, p.d, keys, vec);
+        stage_keys<T>(a2, lv, p.v, p.vs, p, b, c, t0, kKept, p.dv, keys, vec);
     } else {
-        stage_rows<T>(a1, p.q, p.qs, p, b, c, t0, kKept, p.d, vec);
-        stage_rows<T>(a2, p.dout, p.dos, p, b, c, t0, kKept, p.dv, vec);
+        stage_rows<T>(a1, ld, p.q, p.qs, p, b, c, t0, kKept, p.d, vec);
+        stage_rows<T>(a2, lv, p.dout, p.dos, p, b, c, t0, kKept, p.dv, vec);
     }
     if (bufs == 2 && nt > 0) fetch(0);
     stage_commit();
@@ -588,7 +601,7 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, fl
             stage_wait<1>();
         }
         __syncthreads();
-        const float *b1 = ring + t % bufs * tile, *b2 = b1 + kStream * ld, *sb = b2 + kStream * lv, *sd = sb + kStream;
+        const float *b1 = ring + (bufs == 2 ? t & 1 : 0) * tile, *b2 = b1 + kStream * ld, *sb = b2 + kStream * lv, *sd = sb + kStream;
         float s[U][2], g[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) s[u][0] = s[u][1] = g[u][0] = g[u][1] = 0.f;
@@ -649,8 +662,9 @@ bool aligned4(const void *base, const fs_view &s) {
 template <class T, int RPT, int C>
 cudaError_t fwd(const AttnParams &p, cudaStream_t s) {
     constexpr int R = 16 * RPT;
-    const size_t fixed = (size_t)R * smem_stride(p.d) + R * (kKeys + 4);
-    const size_t tile = (size_t)kKeys * (smem_stride(p.d) + smem_stride(p.dv)) + kKeys;
+    const int ld = tile_stride<C>(p.d), lv = tile_stride<C>(p.dv);
+    const size_t fixed = (size_t)R * ld + R * (kKeys + 4);
+    const size_t tile = (size_t)kKeys * (ld + lv) + kKeys;
     const int bufs = (fixed + 2 * tile) * sizeof(float) <= kMaxSmem ? 2 : 1;
     const size_t smem = (fixed + bufs * tile) * sizeof(float);
     cudaError_t e = allow_smem<&xattn_simt_kernel<T, RPT, C>>(smem);
@@ -661,7 +675,8 @@ cudaError_t fwd(const AttnParams &p, cudaStream_t s) {
 }
 template <class T, int RPT>
 cudaError_t fwd_width(const AttnParams &p, cudaStream_t s) {
-    return p.dv <= 64 ? fwd<T, RPT, 1>(p, s) : p.dv <= 128 ? fwd<T, RPT, 2>(p, s) : fwd<T, RPT, 4>(p, s);
+    const int w = p.d > p.dv ? p.d : p.dv;
+    return w <= 64 ? fwd<T, RPT, 1>(p, s) : w <= 128 ? fwd<T, RPT, 2>(p, s) : fwd<T, RPT, 4>(p, s);
 }
 template <class T, int RT>
 cudaError_t token(const AttnParams &p, cudaStream_t s) {
@@ -685,7 +700,7 @@ cudaError_t fwd_rows(const AttnParams &p, cudaStream_t s) {
 template <class T, int U, int C>
 cudaError_t grad(const AttnParams &p, cudaStream_t s) {
     constexpr int kept = 16 * U;
-    const int w = smem_stride(p.d) + smem_stride(p.dv);
+    const int w = tile_stride<C>(p.d) + tile_stride<C>(p.dv);
     const int key_blocks = (p.m + kept - 1) / kept, row_blocks = (p.n * p.group + kept - 1) / kept;
     const size_t fixed = (size_t)kept * w + 2 * kept * (kStream + 4) + 2 * kept;
     const size_t tile = (size_t)kStream * w + 2 * kStream;
