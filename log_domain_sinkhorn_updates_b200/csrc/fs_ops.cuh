@@ -35,7 +35,7 @@ struct AttnParams {
     int main_units, tail_units, splits, split_keys;
     float *part_o;           // [splits][tail_units][unit_rows][dv], relative to part_ml's maximum
     float2 *part_ml;         // [splits][tail_units][unit_rows]: reference (base 2) and sum
-    // Gradient on the tensor cores: the streamed tiles of a CTA in parts, a CTA each (1: not split), whose raw sums
+    // Gradient: the streamed tiles of a CTA in parts, a CTA each (1: not split), whose raw sums
     // [part][batch kv_heads][padded rows][width] a joining pass adds up.
     int key_parts, row_parts;
     float *part_dk, *part_dv, *part_dq;
@@ -157,6 +157,7 @@ cudaError_t launch_xattn_grad_tc(const AttnParams &p, cudaStream_t s);
 cudaError_t launch_xattn_grad_join(const AttnParams &p, cudaStream_t s);  // where key_parts or row_parts > 1
 
 cudaError_t launch_xattn_simt(const AttnParams &p, bool bf16, cudaStream_t s);
+cudaError_t launch_xattn_grad_join_simt(const AttnParams &p, bool bf16, cudaStream_t s);  // as launch_xattn_grad_join
 // Whether the CUDA-core forward takes the few rows of a key head by the token kernel (units of 1, 2 or 4 rows).
 bool xattn_token_ok(const void *q, const fs_view &qs, const void *k, const fs_view &ks, const void *v,
                     const fs_view &vs, int d, int dv, int rows, bool bf16);

@@ -126,23 +126,32 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, AttnKind kind, bool ragged,
     const size_t rows = (size_t)D.n * (D.heads / D.kv_heads), heads = (size_t)D.batch * D.kv_heads;
     if (grad) {
         L.total = align256((size_t)D.batch * D.heads * D.n * 4);
-        const size_t key_blocks = up(D.m, 128), row_blocks = (rows + 127) / 128;
-        if (!tc || rows == 0 || heads == 0 || D.m == 0 || (key_blocks + row_blocks) * heads >= (size_t)dev.sms) return L;
-        // Fewer CTAs than SMs: the streamed tiles of a CTA are split so that all SMs have about as many (a tile of the
-        // pass that keeps keys takes 1.25 of the other's, 0.85 us at width 128), four a part at least, where that saves
-        // more than the joining pass costs (10 tiles' time, and the sums written and read back at 4 TB/s): 2000
-        // queries of 8 heads on one key head, 64 keys of 128: 232 us whole, 43 split; 1000 x 1000, 4 heads: 21 whole,
-        // 24 split.
-        const int key_tiles = D.heads / D.kv_heads * up(D.n, 64), row_tiles = up(D.m, 64);
-        const double each = (key_blocks * 1.25 * key_tiles + row_blocks * (double)row_tiles) * heads / dev.sms;
-        const int kp = (int)std::min({std::max(1.0, key_tiles * 1.25 / each), std::max(1.0, key_tiles / 4.0), 64.0});
-        const int rp = (int)std::min({std::max(1.0, row_tiles / each), std::max(1.0, row_tiles / 4.0), 64.0});
-        const size_t dk = kp > 1 ? kp * heads * key_blocks * 128 * D.d * sizeof(float) : 0;
-        const size_t dv = kp > 1 ? kp * heads * key_blocks * 128 * D.dv * sizeof(float) : 0;
-        const size_t dq = rp > 1 ? rp * heads * row_blocks * 128 * D.d * sizeof(float) : 0;
-        const double before = std::max(key_tiles * 1.25, (double)row_tiles);
-        const double after =
-            std::max(key_tiles * 1.25 / kp, (double)row_tiles / rp) + 10.0 + 2.0 * (dk + dv + dq) / 4e6 / 0.85;
+        const int group = D.heads / D.kv_heads, wide = std::max(D.d, D.dv);
+        if (rows == 0 || heads == 0 || D.m == 0) return L;
+        if (!tc && fs::xattn_simt_rows(D.m + D.n * group, (int)heads, dev.sms) != 16) return L;
+        // Where some CTAs would stream for longer than an even share of all tiles takes the CTAs that run at once (tensor
+        // cores: one an SM; CUDA cores, blocks of 16: two, or four up to width 64, where more of them hide each other's
+        // waits), their tiles are split to about that share, four a part at least (CUDA cores: three).  A tile of the
+        // pass that keeps keys takes 1.25 of the other's: tensor cores 0.85 us at width 128, CUDA cores 3 us at width 64.
+        // It has to save more than the joining pass costs, and the sums written and read back at 4 TB/s.  Tensor
+        // cores, 2000 queries of 8 heads on one key head, 64 keys of 128: 232 us whole, 43 split; 1000 x 1000, 4 heads:
+        // 21 whole, 24 split.  CUDA cores, fp32, 2 x 200 x 300, 4 on 2 heads of 40: 75 whole, 45 split; 4 heads: 44
+        // whole, 47 split.
+        const size_t side = tc ? 128 : 16;
+        const double slots = dev.sms * (tc ? 1.0 : wide <= 64 ? 4.0 : 2.0);
+        const size_t key_blocks = (D.m + side - 1) / side, row_blocks = (rows + side - 1) / side;
+        const int key_tiles = tc ? group * up(D.n, 64) : up((int)rows, 32), row_tiles = up(D.m, tc ? 64 : 32);
+        const double least = tc ? 4.0 : 3.0, join_us = tc ? 8.5 : 15.0;
+        const double tile_us = tc ? 0.85 : 3.0 * std::max(64, wide) / 64;
+        const double each = (key_blocks * 1.25 * key_tiles + row_blocks * (double)row_tiles) * heads / slots;
+        const int kp = (int)std::min({std::max(1.0, key_tiles * 1.25 / each), std::max(1.0, key_tiles / least), 64.0});
+        const int rp = (int)std::min({std::max(1.0, row_tiles / each), std::max(1.0, row_tiles / least), 64.0});
+        const size_t dk = kp > 1 ? kp * heads * key_blocks * side * D.d * sizeof(float) : 0;
+        const size_t dv = kp > 1 ? kp * heads * key_blocks * side * D.dv * sizeof(float) : 0;
+        const size_t dq = rp > 1 ? rp * heads * row_blocks * side * D.d * sizeof(float) : 0;
+        const double before = std::max({key_tiles * 1.25, (double)row_tiles, each});
+        const double after = std::max({key_tiles * 1.25 / kp, (double)row_tiles / rp, each}) +
+                             (join_us + 2.0 * (dk + dv + dq) / 4e6) / tile_us;
         if ((kp > 1 || rp > 1) && after < before) {
             L.key_parts = kp;
             L.row_parts = rp;
@@ -472,8 +481,10 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
     if (tc) {
         OPS_LAUNCH(fs::launch_xattn_grad_tc(p, s), 1);
         if (L.key_parts > 1 || L.row_parts > 1) OPS_LAUNCH(fs::launch_xattn_grad_join(p, s), 1);
-    } else
+    } else {
         OPS_LAUNCH(fs::launch_xattn_grad_simt(p, bf16, dev.sms, s), 1);
+        if (L.key_parts > 1 || L.row_parts > 1) OPS_LAUNCH(fs::launch_xattn_grad_join_simt(p, bf16, s), 1);
+    }
     return FS_OK;
 }
 

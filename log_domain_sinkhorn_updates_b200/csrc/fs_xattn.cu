@@ -10,10 +10,16 @@
 //
 // Tiles of rows and keys as fp32 in shared memory, 16 x 16 threads with a block
 // of each product in registers; where shared memory allows it the next tile
-// arrives under this one's arithmetic (fp32: asynchronous copies).  What bounds
-// it is shared memory: a 16-byte read for every 8 FMAs of a thread.  Up to 8 rows
-// a key head (single tokens) have a kernel that streams K and V through
-// registers alone: what bounds it is memory.
+// arrives under this one's arithmetic (fp32: asynchronous copies).  Products go
+// two to an instruction (forward, 4 x 1024 x 1024, 8 heads of 64: 348 -> 338 us).
+// What bounds it is shared memory's latency: 2 of 6 cycles between a warp's
+// instructions wait for it, the FMA pipe is 35 to 40 % active (2 x 1024 x 1024, 8
+// heads of 64: forward 24 TFLOP/s, gradient 25).  Where few CTAs stream for long
+// (4 queries of 8 heads against 5000 keys: 892 -> 49 us) the gradient's streamed
+// tiles are split into parts, whose sums a second kernel adds.  Up to 8 rows a
+// key head (single tokens) have a kernel that streams K and V through
+// registers alone: what bounds it is memory (fp32, 65536 keys of 8 heads of 128:
+// 124 us).
 //
 // The heads that share a key head are rows of one problem: row r = i group + h.
 // Keys past the length or masked by the bias are staged as zeros, so nothing
@@ -139,25 +145,35 @@ __device__ void stage_keys(float *sm, int ld, const void *src, const fs_view &s,
     });
 }
 
-// acc[u][w] += sum_k a[ia + u][k] b[ib + 16 w][k] over rows of the tiles (strides la and lb)
+// acc[u][w] = sum_k a[u][k] b[BSTEP w][k] over rows of the tiles (strides la and lb); even and odd k are summed apart
+// and added at the end.
 template <int U, int W, int BSTEP>
 __device__ __forceinline__ void dots(float (&acc)[U][W], const float *a, int la, const float *b, int lb, int width) {
+    uint64_t two[U][W];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int w = 0; w < W; ++w) two[u][w] = 0ull;
     for (int k = 0; k < width; k += 4) {
-        float4 x[U], y[W];
+        ulonglong2 x[U], y[W];
 #pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = *reinterpret_cast<const float4 *>(a + u * la + k);
+        for (int u = 0; u < U; ++u) x[u] = *reinterpret_cast<const ulonglong2 *>(a + u * la + k);
 #pragma unroll
-        for (int w = 0; w < W; ++w) y[w] = *reinterpret_cast<const float4 *>(b + w * BSTEP * lb + k);
+        for (int w = 0; w < W; ++w) y[w] = *reinterpret_cast<const ulonglong2 *>(b + w * BSTEP * lb + k);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                acc[u][w] = fmaf(x[u].x, y[w].x, acc[u][w]);
-                acc[u][w] = fmaf(x[u].y, y[w].y, acc[u][w]);
-                acc[u][w] = fmaf(x[u].z, y[w].z, acc[u][w]);
-                acc[u][w] = fmaf(x[u].w, y[w].w, acc[u][w]);
-            }
+            for (int w = 0; w < W; ++w)
+                two[u][w] = fma2(x[u].y, y[w].y, fma2(x[u].x, y[w].x, two[u][w]));
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            float even, odd;
+            unpack2(two[u][w], even, odd);
+            acc[u][w] = even + odd;
+        }
 }
 // o[u][k] += sum_j wt[u][j] val[j][col + 64 k .. + 3] over `cnt` rows of val
 template <int U, int C>
@@ -240,10 +256,6 @@ __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnPara
         __syncthreads();
         const float *sK = ring + (bufs == 2 ? t & 1 : 0) * tile, *sV = sK + kKeys * ld, *sB = sV + kKeys * lv;
         float z[RPT][4];
-#pragma unroll
-        for (int u = 0; u < RPT; ++u)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) z[u][w] = 0.f;
         dots<RPT, 4, 16>(z, sQ + ti * RPT * ld, ld, sK + tj * ld, ld, p.d);
 #pragma unroll
         for (int u = 0; u < RPT; ++u) {
@@ -527,7 +539,7 @@ __global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p,
 // Otherwise: 16 U packed rows (Q, dO) against streamed keys (K, V): dq.  16 x 16 threads: U kept rows x 2 streamed
 // ones of the scores, U kept rows x 4 columns a piece of the sums.
 template <class T, bool KEYS, int U, int C>
-__device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, float *sm) {
+__device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, int part, float *sm) {
     constexpr int LS = kStream + 4, kKept = 16 * U;
     const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads, t0 = block * kKept;
     const int ld = tile_stride<C>(p.d), lv = tile_stride<C>(p.dv);
@@ -536,7 +548,9 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, fl
     float *ring = kd + kKept;
     const int tile = kStream * (ld + lv) + 2 * kStream;  // the streamed pair, and bias, or base-2 LSE and D
     const int keys = attn_keys(p, b), rows = p.n * p.group;
-    const int end = KEYS ? (t0 < keys ? rows : 0) : keys;
+    const int all = ((KEYS ? (t0 < keys ? rows : 0) : keys) + kStream - 1) / kStream;
+    const int parts = KEYS ? p.key_parts : p.row_parts;
+    const int t_beg = (int)((long long)all * part / parts), nt = (int)((long long)all * (part + 1) / parts) - t_beg;
     // base-2 LSE (+inf: an empty row, or one past the end) and D of packed row r
     auto stat = [&](int r, float *lse2, float *d) {
         *lse2 = INFINITY;
@@ -555,7 +569,7 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, fl
     }
     auto fetch = [&](int t) {  // as in the forward
         float *b1 = ring + (bufs == 2 ? t & 1 : 0) * tile, *b2 = b1 + kStream * ld, *sb = b2 + kStream * lv, *sd = sb + kStream;
-        const int u0 = t * kStream;
+        const int u0 = (t_beg + t) * kStream;
         if (threadIdx.x < kStream) {
             if (KEYS)
                 stat(u0 + threadIdx.x, sb + threadIdx.x, sd + threadIdx.x);
@@ -570,7 +584,6 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, fl
             stage_keys<T>(b2, lv, p.v, p.vs, p, b, c, u0, kStream, p.dv, keys, vec);
         }
     };
-    const int nt = (end + kStream - 1) / kStream;
     if (KEYS) {
         stage_keys<T>(a1, ld, p.k, p.ks, p, b, c, t0, kKept, p.d, keys, vec);
         stage_keys<T>(a2, lv, p.v, p.vs, p, b, c, t0, kKept, p.dv, keys, vec);
@@ -601,10 +614,9 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, fl
             stage_wait<1>();
         }
         __syncthreads();
-        const float *b1 = ring + (bufs == 2 ? t & 1 : 0) * tile, *b2 = b1 + kStream * ld, *sb = b2 + kStream * lv, *sd = sb + kStream;
+        const float *b1 = ring + (bufs == 2 ? t & 1 : 0) * tile, *b2 = b1 + kStream * ld;
+        const float *sb = b2 + kStream * lv, *sd = sb + kStream;
         float s[U][2], g[U][2];
-#pragma unroll
-        for (int u = 0; u < U; ++u) s[u][0] = s[u][1] = g[u][0] = g[u][1] = 0.f;
         dots<U, 2, 16>(s, a1 + ti * U * ld, ld, b1 + tj * ld, ld, p.d);
         dots<U, 2, 16>(g, a2 + ti * U * lv, lv, b2 + tj * lv, lv, p.dv);
 #pragma unroll
@@ -629,6 +641,19 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, fl
     for (int u = 0; u < U; ++u) {
         const int at = t0 + ti * U + u;
         if (at >= (KEYS ? p.m : rows)) continue;  // keys past the length get zeros: they take no part
+        if (parts > 1) {  // a part: its raw sums
+            const int blocks = ((KEYS ? p.m : rows) + kKept - 1) / kKept;
+            const size_t to = ((size_t)part * gridDim.y + blockIdx.y) * blocks * kKept + at;
+            float *d1 = (KEYS ? p.part_dk : p.part_dq) + to * p.d;
+#pragma unroll
+            for (int k = 0; k < C; ++k) put4(d1, g1[u][k], 4 * tj + 64 * k, p.d, 1.f);
+            if (KEYS) {
+                float *d2 = p.part_dv + to * p.dv;
+#pragma unroll
+                for (int k = 0; k < C; ++k) put4(d2, g2[u][KEYS ? k : 0], 4 * tj + 64 * k, p.dv, 1.f);
+            }
+            continue;
+        }
         T *d1 = KEYS ? (T *)p.dk + p.dks.batch * b + p.dks.token * at + p.dks.head * c
                      : (T *)p.dq + row_off(p.dqs, p, b, c, at);
 #pragma unroll
@@ -643,13 +668,47 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, fl
 
 // Both passes in one launch: key_blocks CTAs of the first, then those of the second.
 template <class T, int U, int C>
-__global__ void __launch_bounds__(kTileThreads) xattn_grad_kernel(const AttnParams p, bool vec, int bufs,
-                                                                  int key_blocks) {
+__global__ void __launch_bounds__(kTileThreads)
+    xattn_grad_kernel(const AttnParams p, bool vec, int bufs, int key_blocks) {
     extern __shared__ __align__(16) float sm[];
-    if ((int)blockIdx.x < key_blocks)
-        grad_pass<T, true, U, C>(p, vec, bufs, (int)blockIdx.x, sm);
+    const int x = blockIdx.x, keys = key_blocks * p.key_parts;
+    if (x < keys)
+        grad_pass<T, true, U, C>(p, vec, bufs, x / p.key_parts, x % p.key_parts, sm);
     else
-        grad_pass<T, false, U, C>(p, vec, bufs, (int)blockIdx.x - key_blocks, sm);
+        grad_pass<T, false, U, C>(p, vec, bufs, (x - keys) / p.row_parts, (x - keys) % p.row_parts, sm);
+}
+
+// Adds the parts' sums in their order, an element a thread: dk and dv of every key, then dq of every row.
+template <class T>
+__global__ void __launch_bounds__(256) xattn_grad_join_simt_kernel(const AttnParams p, int key_padded, int row_padded) {
+    const int hb = blockIdx.y, c = hb % p.kv_heads, b = hb / p.kv_heads, rows = p.n * p.group, wide = p.d + p.dv;
+    const size_t keys = p.key_parts > 1 ? (size_t)p.m * wide : 0, e = (size_t)blockIdx.x * 256 + threadIdx.x;
+    grid_dependency_wait();
+    const float *src;
+    T *dst;
+    size_t step;
+    int parts;
+    float mul = p.scale;
+    if (e < keys) {
+        const int row = (int)(e / wide), k = (int)(e % wide), width = k < p.d ? p.d : p.dv, col = k < p.d ? k : k - p.d;
+        const fs_view &s = k < p.d ? p.dks : p.dvs;
+        if (k >= p.d) mul = 1.f;
+        src = (k < p.d ? p.part_dk : p.part_dv) + ((size_t)hb * key_padded + row) * width + col;
+        dst = (T *)(k < p.d ? p.dk : p.dv_out) + s.batch * b + s.token * row + s.head * c + col;
+        step = (size_t)gridDim.y * key_padded * width;
+        parts = p.key_parts;
+    } else {
+        if (p.row_parts == 1 || e - keys >= (size_t)rows * p.d) return;
+        const int row = (int)((e - keys) / p.d), col = (int)((e - keys) % p.d);
+        src = p.part_dq + ((size_t)hb * row_padded + row) * p.d + col;
+        dst = (T *)p.dq + row_off(p.dqs, p, b, c, row) + col;
+        step = (size_t)gridDim.y * row_padded * p.d;
+        parts = p.row_parts;
+    }
+    float x = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) x += src[i * step];
+    from_f(x * mul, dst);
 }
 
 // Whether four elements of every row can be loaded at once.
@@ -711,7 +770,8 @@ cudaError_t grad(const AttnParams &p, cudaStream_t s) {
     const bool vec = aligned4<T>(p.q, p.qs) && aligned4<T>(p.k, p.ks) && aligned4<T>(p.v, p.vs) &&
                      aligned4<T>(p.dout, p.dos);
     xattn_grad_kernel<T, U, C>
-        <<<dim3(key_blocks + row_blocks, p.batch * p.kv_heads), kTileThreads, smem, s>>>(p, vec, bufs, key_blocks);
+        <<<dim3(key_blocks * p.key_parts + row_blocks * p.row_parts, p.batch * p.kv_heads), kTileThreads, smem, s>>>(
+            p, vec, bufs, key_blocks);
     return cudaGetLastError();
 }
 template <class T, int U>
@@ -758,6 +818,13 @@ cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s) {
 }
 cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s) {
     return bf16 ? grad_rows<__nv_bfloat16>(p, sms, s) : grad_rows<float>(p, sms, s);
+}
+cudaError_t launch_xattn_grad_join_simt(const AttnParams &p, bool bf16, cudaStream_t s) {
+    const int rows = p.n * p.group, key_padded = (p.m + 15) / 16 * 16, row_padded = (rows + 15) / 16 * 16;
+    const size_t work = (p.key_parts > 1 ? (size_t)p.m * (p.d + p.dv) : 0) + (p.row_parts > 1 ? (size_t)rows * p.d : 0);
+    const dim3 grid((unsigned)((work + 255) / 256), p.batch * p.kv_heads);
+    return bf16 ? launch_dependent(xattn_grad_join_simt_kernel<__nv_bfloat16>, grid, 256, 0, s, p, key_padded, row_padded)
+                : launch_dependent(xattn_grad_join_simt_kernel<float>, grid, 256, 0, s, p, key_padded, row_padded);
 }
 
 }  // namespace fs

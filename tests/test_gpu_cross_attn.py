@@ -382,6 +382,26 @@ def test_gradient_of_few_heads_and_ragged_lengths(size, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("size", [(1, 4, 5000, 8, 1, 128, 128), (1, 1, 9000, 4, 2, 64, 32), (1, 300, 260, 4, 4, 200, 130),
+                                  (2, 200, 300, 4, 2, 40, 40), (1, 2000, 10, 1, 1, 64, 63)])
+def test_gradient_split_over_its_streamed_rows(size, dtype):
+    """Few rows against many keys, many rows against few, with a mask; outputs into parts of larger buffers."""
+    q, k, v, dout = make(*size, dtype, seed=23)
+    B, n, m, H, Hk, d, dv = size
+    bias = torch.randn(B, m, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    bias[:, 3::7] = -math.inf
+    want = ref.attention(q, k, v, dout=dout, bias=bias)
+    got = run(q, k, v, dout, bias=bias)
+    ref.check(got, want)
+    bigk = torch.full((B, Hk, m + 1, d + 8), 3.0, dtype=dtype, device="cuda")
+    bigq = torch.full((B, n + 1, H, d), 3.0, dtype=dtype, device="cuda")
+    dk, dq, gv = bigk[:, :, :m, :d].transpose(1, 2), bigq[:, :n], torch.empty_like(v)
+    _fs().fs_cross_attn_grad(q, k, v, got["out"], got["lse"], dout, dq, dk, gv, bias=bias)
+    assert torch.equal(dq, got["dq"]) and torch.equal(dk, got["dk"]) and torch.equal(gv, got["dv"])
+    assert (bigk[:, :, m] == 3).all() and (bigk[..., d:] == 3).all() and (bigq[:, n] == 3).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_more_problems_than_are_ordered_by_length(dtype):
     B, n, m = 41, 3, 700
     q, k, v, dout = make(B, n, m, 4, 2, 64, 64, dtype, seed=13)
