@@ -321,7 +321,7 @@ struct XentPlan {
 XentPlan plan_xent(const fs_xent_desc &D, const void *x, const void *w, bool grad, const Device &dev) {
     XentPlan L;
     const bool f32 = D.dtype == FS_F32;
-    const size_t n = (size_t)std::max(D.n, 1), budget = (size_t)256 << 20;
+    const size_t n = (size_t)std::max(D.n, 1), room = (size_t)256 << 20;
     L.planes = f32 ? 3 : 1;
     // x is read again by every column tile: rows that do not start on 128 bytes take two lines of L2 a box row, and
     // are copied where there are enough tiles to repay it (1021 x 50021 x 1000: forward 89 us as they lie, 79 copied,
@@ -332,8 +332,8 @@ XentPlan plan_xent(const fs_xent_desc &D, const void *x, const void *w, bool gra
     L.dp = up(D.d, 64) * 64;
     // Pieces of the classes whose logit gradients, and whose copies of w, stay within 256 MiB each.
     size_t fit = (size_t)up(D.v, 256) * 256;
-    if (grad) fit = std::min(fit, budget / (n * L.planes * 2) / 256 * 256);
-    if (L.pack_w) fit = std::min(fit, budget / ((size_t)L.dp * L.planes * 2) / 256 * 256);
+    if (grad) fit = std::min(fit, room / (n * L.planes * 2) / 256 * 256);
+    if (L.pack_w) fit = std::min(fit, room / ((size_t)L.dp * L.planes * 2) / 256 * 256);
     if (grad && f32) fit = std::min(fit, (size_t)8 * fs::kXentF32Terms);  // at most 8 parts of it in the dx product
     L.piece = (int)std::max<size_t>(256, fit);
     size_t at = 0;
