@@ -505,6 +505,8 @@ FS_API size_t fs_cross_entropy_workspace(const fs_xent_desc *desc, const void *x
  * Forward: loss and lse, device fp32 [n] (natural log).  target: device int64
  * [n].  A row whose target is ignore_index has loss 0 (its lse is computed);
  * any other target outside 0..v-1 gives loss NaN, without a read out of range.
+ * A logit of NaN or +inf makes its row's lse and loss NaN; one of -inf weighs
+ * nothing (a row of them alone has lse -inf).
  * Asynchronous.  Errors: FS_ERR_INVALID_ARG (sizes, scale, strides, null
  * pointers, a workspace that is too small), FS_ERR_UNSUPPORTED (device not
  * compute capability 10.x; v over 2^22, d over 65536 or n over 2^24).

@@ -330,9 +330,10 @@ __device__ __forceinline__ void rescale_block(const float (&z)[CNT], float &m, f
         mx[(k / 8) & 3] = max3(mx[(k / 8) & 3], z[k + 6], z[k + 7]);
     }
     const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-    if (tmax == -INFINITY) return;  // nothing but padding so far
-    const float mnew = fmaxf(m, tmax);
-    l = (m == -INFINITY ? 0.f : l * ex2_approx(m - mnew)) + sum_exp2<CNT>(z, mnew);
+    // Nothing but padding (or NaN, which the maximum passes over) so far: added against 0, padding gives 0 and a NaN
+    // stays in the sum.
+    const float mnew = fmaxf(m, tmax), ref = mnew == -INFINITY ? 0.f : mnew;
+    l = (m == -INFINITY ? l : l * ex2_approx(m - ref)) + sum_exp2<CNT>(z, ref);
     m = mnew;
 }
 

@@ -89,8 +89,7 @@ __global__ void __launch_bounds__(256) xent_finish_kernel(const XentParams p, in
             for (int w = 1; w < 8; ++w) join(mx, l, warps[w].x, warps[w].y);
     }
     if (!live || sub) return;
-    // no sum at all: every logit was NaN
-    const double lse = l == 0.f ? (double)NAN : ((double)mx + log2((double)l)) * kLn2d;
+    const double lse = ((double)mx + log2((double)l)) * kLn2d;  // no sum at all: every logit was -inf, and so is lse
     p.lse[i] = (float)lse;
     const long long t = p.target[i];
     p.loss[i] = t == p.ignore ? 0.f : (t < 0 || t >= p.v ? NAN : (float)(lse - (double)p.hit[i]));
