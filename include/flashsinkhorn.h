@@ -445,7 +445,10 @@ FS_API size_t fs_cross_attn_workspace(const fs_attn_desc *desc, int grad);
 /*
  * Forward.  k_len: device int [batch], the valid keys of each problem (clamped
  * to 0..m), or NULL for m.  bias: device fp32 [batch][m], or NULL; a value of
- * -1e30 or less masks its key.  Keys past the length or masked take no part:
+ * -1e30 or less masks its key.  Where the largest kept bias of a problem is over
+ * 64 in size, biases are measured from it, so a constant of any size on every key
+ * (a sample masked with -1e9) costs the scores nothing.  Keys past the length or
+ * masked take no part:
  * their k and v may hold anything, NaN included.  A row without a key gives
  * out = 0 and lse = -inf (q too may hold anything where the length is 0; where
  * the bias masks every key it has to be finite).  lse: device fp32 [batch][heads][n], natural log; may
@@ -468,7 +471,10 @@ FS_API fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const vo
  *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
  * (dk and dv summed over the heads that share a key head).  Keys that take no
  * part get zeros.  k_len and bias as in the forward; no gradient of bias.  On
- * the tensor cores P and dS are rounded to bf16 for their products.
+ * the tensor cores P and dS are rounded to bf16 for their products.  P comes from
+ * the scores and the fp32 lse: its relative error is at least 2^-24 of |lse| (from
+ * scores alone: where the largest bias is over 64 in size, the row's sum is taken
+ * again beside it).
  * Asynchronous.  Errors as fs_cross_attn.
  */
 FS_API fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void *k, const void *v,

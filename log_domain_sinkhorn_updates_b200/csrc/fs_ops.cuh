@@ -17,6 +17,16 @@ namespace fs {
 // the type's lowest value then leave an empty row empty instead of making all
 // of its keys equally likely, and times log2(e) no kept bias leaves fp32.
 constexpr float kBiasMask = -1e30f;
+// Biases are measured from the largest kept one where that is more than this in size (attn_top): against a bias of -1e9
+// on every key of a problem (a sample masked with a finite constant), fp32 would lose the scores, and an LSE of that
+// size the logarithm of the sum.  Up to it the largest costs the scores 2^-18 at most, and nothing is taken off.
+constexpr float kBiasNear = 64.f;
+
+// A row's statistics over one part of the keys: what the part's biases are measured from, the reference (base 2) of its
+// scores beside them, and the sum.
+struct AttnPart {
+    float top, m, l;
+};
 
 struct AttnParams {
     int batch, n, m, heads, kv_heads, group, d, dv;
@@ -29,12 +39,17 @@ struct AttnParams {
     void *out, *dq, *dk, *dv_out;
     float *lse;           // [batch][heads][n], natural log (out of the forward, into the gradient); may be null forward
     float *dot;           // gradient: [batch][heads][n], D_i = dout_i.out_i
+    float *lse2;          // gradient: [batch][heads][n], base-2 LSE measured from `top`
+    float *top;           // gradient: [batch], what the problem's biases are measured from; null without a bias
+    // 1: the forward's kernels, at a gradient's start, write top, and lse2 of the problems where top is not 0: there one
+    // fp32 number does not hold the LSE, and the gradient cannot do with the forward's.  Their CTAs leave at once elsewhere.
+    int stats;
     // Forward: a unit is unit_rows packed rows of a key head.  Units from main_units on are split over their keys into
     // `splits` parts of split_keys keys, a CTA each, which the joining pass adds up; 1: no unit is.
     int unit_rows, blocks;   // and the units of a head
     int main_units, tail_units, splits, split_keys;
-    float *part_o;           // [splits][tail_units][unit_rows][dv], relative to part_ml's maximum
-    float2 *part_ml;         // [splits][tail_units][unit_rows]: reference (base 2) and sum
+    float *part_o;           // [splits][tail_units][unit_rows][dv], relative to part_ml's reference
+    AttnPart *part_ml;       // [splits][tail_units][unit_rows]
     // Gradient: the streamed tiles of a CTA in parts, a CTA each (1: not split), whose raw sums
     // [part][batch kv_heads][padded rows][width] a joining pass adds up.
     int key_parts, row_parts;
@@ -117,12 +132,40 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnParams &p) {
     w.part = ((size_t)sp * p.tail_units + tu) * p.unit_rows;
     return w;
 }
-// Base-2 bias of key j (valid or not): -inf where it is masked.
-__device__ __forceinline__ float attn_bias2(const AttnParams &p, int b, int j, int keys) {
+// What the biases of keys [j_beg, j_end) of problem b are measured from: the largest kept one, or 0 where it is near 0.
+// By a whole block of THREADS threads; scratch: a float a warp.
+template <int THREADS>
+__device__ __forceinline__ float attn_top(const AttnParams &p, int b, int j_beg, int j_end, float *scratch) {
+    if (!p.bias) return 0.f;
+    const float *bias = p.bias + (size_t)b * p.m;
+    float top = -INFINITY;
+#pragma unroll 8
+    for (int j = j_beg + (int)threadIdx.x; j < j_end; j += THREADS) {
+        const float v = __ldg(bias + j);
+        if (v > kBiasMask) top = fmaxf(top, v);
+    }
+    for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+    if (threadIdx.x % 32 == 0) scratch[threadIdx.x / 32] = top;
+    __syncthreads();
+    for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, scratch[w]);
+    __syncthreads();
+    return top != -INFINITY && fabsf(top) > kBiasNear ? top : 0.f;
+}
+// Statistics for a gradient (AttnParams::stats): whether the problem needs none.
+__device__ __forceinline__ bool attn_stats_done(const AttnParams &p, const AttnUnit &unit, float top) {
+    if (!p.stats) return false;
+    if (threadIdx.x == 0 && unit.r0 == 0 && unit.c == 0) p.top[unit.b] = top;
+    return top == 0.f;
+}
+// Base-2 bias of key j (valid or not), measured from top: -inf where it is masked.
+__device__ __forceinline__ float attn_bias2(const AttnParams &p, int b, int j, int keys, float top) {
     if (j >= keys) return -INFINITY;
     if (!p.bias) return 0.f;
     const float v = __ldg(p.bias + (size_t)b * p.m + j);
-    return v <= kBiasMask ? -INFINITY : v * kLog2e;
+    return v <= kBiasMask ? -INFINITY : (v - top) * kLog2e;
+}
+__device__ __forceinline__ bool attn_masked(const AttnParams &p, int b, int j, int keys) {
+    return j >= keys || (p.bias && __ldg(p.bias + (size_t)b * p.m + j) <= kBiasMask);
 }
 
 // TMA map of a bf16 tensor of `dims` axes (innermost first, contiguous), 128-byte swizzle; strides in elements

@@ -115,7 +115,7 @@ struct AttnPlan {
     int unit_rows = 0, blocks = 0, main_units = 0, tail_units = 0, splits = 1, split_keys = 0;  // as in AttnParams
     int key_parts = 1, row_parts = 1;
     size_t part_dk = 0, part_dv = 0, part_dq = 0;
-    size_t part_ml = 0, part_o = 0, dot = 0, total = 0;  // workspace offsets, and its size
+    size_t part_ml = 0, part_o = 0, dot = 0, lse2 = 0, top = 0, total = 0;  // workspace offsets, and its size
 };
 
 // kind: the kernels that take the call.
@@ -125,7 +125,9 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, AttnKind kind, bool ragged,
     AttnPlan L;
     const size_t rows = (size_t)D.n * (D.heads / D.kv_heads), heads = (size_t)D.batch * D.kv_heads;
     if (grad) {
-        L.total = align256((size_t)D.batch * D.heads * D.n * 4);
+        L.lse2 = align256((size_t)D.batch * D.heads * D.n * sizeof(float));
+        L.top = 2 * L.lse2;
+        L.total = L.top + align256(D.batch * sizeof(float));
         const int group = D.heads / D.kv_heads, wide = std::max(D.d, D.dv);
         if (rows == 0 || heads == 0 || D.m == 0) return L;
         if (!tc && fs::xattn_simt_rows(D.m + D.n * group, (int)heads, dev.sms) != 16) return L;
@@ -208,7 +210,7 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, AttnKind kind, bool ragged,
     }
     if (L.splits > 1) {
         const size_t parts = (size_t)L.splits * L.tail_units * L.unit_rows;
-        L.part_o = align256(parts * sizeof(float2));
+        L.part_o = align256(parts * sizeof(fs::AttnPart));
         L.total = L.part_o + align256(parts * D.dv * sizeof(float));
     }
     return L;
@@ -277,9 +279,11 @@ fs::AttnParams attn_params(const fs_attn_desc &D, const AttnPlan &L, const Devic
     p.part_dk = reinterpret_cast<float *>(w + L.part_dk);
     p.part_dv = reinterpret_cast<float *>(w + L.part_dv);
     p.part_dq = reinterpret_cast<float *>(w + L.part_dq);
-    p.part_ml = reinterpret_cast<float2 *>(w + L.part_ml);
+    p.part_ml = reinterpret_cast<fs::AttnPart *>(w + L.part_ml);
     p.part_o = reinterpret_cast<float *>(w + L.part_o);
     p.dot = reinterpret_cast<float *>(w + L.dot);
+    p.lse2 = reinterpret_cast<float *>(w + L.lse2);
+    p.top = reinterpret_cast<float *>(w + L.top);
     p.timeout_ns = kTimeoutNs;
     p.err = dev.err;
     return p;
@@ -477,6 +481,17 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
     p.dv_out = dv;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = D.dtype == FS_BF16;
+    if (!bias || D.n == 0) p.top = nullptr;
+    if (p.top) {
+        const AttnPlan F = plan_attn(D, false, tc ? kTensor : kSimt, false, dev);
+        fs::AttnParams f = p;
+        f.stats = 1;
+        f.unit_rows = F.unit_rows;
+        f.blocks = F.blocks;
+        f.main_units = F.blocks * D.kv_heads * D.batch;  // none is split
+        f.splits = 1;
+        OPS_LAUNCH(tc ? fs::launch_xattn_tc(f, s) : fs::launch_xattn_simt(f, bf16, s), 1);
+    }
     if (D.n > 0) OPS_LAUNCH(fs::launch_xattn_dot(p, bf16, s), 1);
     if (tc) {
         OPS_LAUNCH(fs::launch_xattn_grad_tc(p, s), 1);

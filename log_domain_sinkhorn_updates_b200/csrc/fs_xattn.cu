@@ -141,7 +141,7 @@ __device__ void stage_keys(float *sm, int ld, const void *src, const fs_view &s,
                            int cnt, int w, int j_end, bool vec) {
     const T *base = (const T *)src + s.batch * b + s.head * c;
     stage_tile<T>(sm, ld, cnt, w, vec, (const T *)src, [&](int j) -> const T * {
-        return attn_bias2(p, b, j0 + j, j_end) == -INFINITY ? nullptr : base + s.token * (j0 + j);
+        return attn_masked(p, b, j0 + j, j_end) ? nullptr : base + s.token * (j0 + j);
     });
 }
 
@@ -219,12 +219,16 @@ __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnPara
     const int r0 = unit.r0, c = unit.c, b = unit.b, j_beg = unit.j_beg, j_end = unit.j_end;
     const int ld = tile_stride<C>(p.d), lv = tile_stride<C>(p.dv);
     const int tile = kKeys * (ld + lv) + kKeys;  // K, V and the bias of one buffer
-    float *sQ = sm, *sP = sQ + R * ld, *ring = sP + R * LP;
+    float *sTop = sm, *sQ = sm + 4, *sP = sQ + R * ld, *ring = sP + R * LP;
+    const float top = attn_top<kTileThreads>(p, b, j_beg, j_end, sP);
+    if (attn_stats_done(p, unit, top)) return;
+    if (threadIdx.x == 0) *sTop = top;  // read again at the end
+    __syncthreads();
     // tile t into buffer t % bufs: with two, it arrives under the arithmetic of the tile before
     auto fetch = [&](int t) {
         float *sK = ring + (bufs == 2 ? t & 1 : 0) * tile, *sV = sK + kKeys * ld, *sB = sV + kKeys * lv;
         const int j0 = j_beg + t * kKeys;
-        if (threadIdx.x < kKeys) sB[threadIdx.x] = attn_bias2(p, b, j0 + threadIdx.x, j_end);
+        if (threadIdx.x < kKeys) sB[threadIdx.x] = attn_bias2(p, b, j0 + threadIdx.x, j_end, top);
         stage_keys<T>(sK, ld, p.k, p.ks, p, b, c, j0, kKeys, p.d, j_end, vec);
         stage_keys<T>(sV, lv, p.v, p.vs, p, b, c, j0, kKeys, p.dv, j_end, vec);
     };
@@ -298,18 +302,22 @@ __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnPara
         if (r >= p.n * p.group) continue;
         if (!unit.whole) {
             const size_t at = unit.part + ti * RPT + u;
-            if (tj == 0) p.part_ml[at] = make_float2(mx[u], l[u]);
+            if (tj == 0) p.part_ml[at] = {*sTop, mx[u], l[u]};
 #pragma unroll
             for (int k = 0; k < C; ++k) put4(p.part_o + at * p.dv, o[u][k], 4 * tj + 64 * k, p.dv, 1.f);
             continue;
         }
         const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];  // 0: no key is left (a NaN row stays NaN)
+        if (p.stats) {
+            if (tj == 0) p.lse2[row_stat(p, b, c, r)] = (float)((double)mx[u] + log2((double)l[u]));
+            continue;
+        }
         T *dst = (T *)p.out + row_off(p.os, p, b, c, r);
 #pragma unroll
         for (int k = 0; k < C; ++k) put4(dst, o[u][k], 4 * tj + 64 * k, p.dv, inv);
         if (p.lse && tj == 0)
             p.lse[row_stat(p, b, c, r)] =
-                l[u] == 0.f ? -INFINITY : (float)(((double)mx[u] + log2((double)l[u])) * kLn2d);
+                l[u] == 0.f ? -INFINITY : (float)(((double)mx[u] + log2((double)l[u])) * kLn2d + *sTop);
     }
 }
 
@@ -325,6 +333,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) xattn_token_kernel(const Attn
     const AttnUnit unit = p.k_len ? attn_unit<true>(p) : attn_unit<false>(p);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, grp = lane / 8, sub = lane % 8;
     const int b = unit.b, c = unit.c, rows = p.n * p.group;
+    const float bias_top = attn_top<kTileThreads>(p, b, unit.j_beg, unit.j_end, &sml[0][0].x);
     float4 q[RT][C], o[RT][C];
     float mx[RT], l[RT];
 #pragma unroll
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) xattn_token_kernel(const Attn
     float4 kn[C], vn[C];
     float bn;
     auto fetch = [&](int j) {  // key j's bias, and its rows unless it is masked (or past the part)
-        bn = attn_bias2(p, b, j, unit.j_end);
+        bn = attn_bias2(p, b, j, unit.j_end, bias_top);
 #pragma unroll
         for (int k = 0; k < C; ++k) {
             const int e = 32 * k + 4 * sub;
@@ -428,13 +437,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) xattn_token_kernel(const Attn
             x = fmaf(so[w][r][k], f, x);
         }
         if (!unit.whole) {
-            if (k == 0) p.part_ml[unit.part + r] = make_float2(top, sum);
+            if (k == 0) p.part_ml[unit.part + r] = {bias_top, top, sum};
             p.part_o[(unit.part + r) * p.dv + k] = x;
         } else {
             from_f(sum == 0.f ? 0.f : x / sum, (T *)p.out + row_off(p.os, p, b, c, row) + k);
             if (p.lse && k == 0)
                 p.lse[row_stat(p, b, c, row)] =
-                    sum == 0.f ? -INFINITY : (float)(((double)top + log2((double)sum)) * kLn2d);
+                    sum == 0.f ? -INFINITY : (float)(((double)top + log2((double)sum)) * kLn2d + bias_top);
         }
     }
 }
@@ -452,8 +461,16 @@ __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParam
     const int b = p.k_len ? attn_problem<true>(p, place) : place;
     if (r >= p.n * p.group) return;
     grid_dependency_wait();
+    // the largest bias reference, and the largest score reference measured from it
+    float from = -INFINITY;
+    for (int s = lane; s < p.splits; s += 32) {
+        const AttnPart ml = p.part_ml[s * all + at];
+        if (ml.l != 0.f) from = fmaxf(from, ml.top);
+    }
+    for (int w = 16; w; w >>= 1) from = fmaxf(from, __shfl_xor_sync(~0u, from, w));
+    auto reference = [&](const AttnPart &ml) { return ml.l == 0.f ? -INFINITY : (ml.top - from) * kLog2e + ml.m; };
     float mx = -INFINITY;
-    for (int s = lane; s < p.splits; s += 32) mx = fmaxf(mx, p.part_ml[s * all + at].x);
+    for (int s = lane; s < p.splits; s += 32) mx = fmaxf(mx, reference(p.part_ml[s * all + at]));
     for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, w));
     const float ref = mx == -INFINITY ? 0.f : mx;
     float l = 0.f, o[kMaxD / 32];
@@ -461,10 +478,10 @@ __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParam
     for (int k = 0; k < kMaxD / 32; ++k) o[k] = 0.f;
     for (int s0 = 0; s0 < p.splits; s0 += 32) {
         // a lane's part: its weight; 0 where it has no key (its sums were not written)
-        const float2 ml = s0 + lane < p.splits ? p.part_ml[(s0 + lane) * all + at] : make_float2(-INFINITY, 0.f);
-        const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - ref);
-        const unsigned has = __ballot_sync(~0u, ml.y != 0.f);
-        float lw = ml.y * f;
+        const AttnPart ml = s0 + lane < p.splits ? p.part_ml[(s0 + lane) * all + at] : AttnPart{0.f, -INFINITY, 0.f};
+        const float f = ml.l == 0.f ? 0.f : exp2f(reference(ml) - ref);
+        const unsigned has = __ballot_sync(~0u, ml.l != 0.f);
+        float lw = ml.l * f;
         for (int w = 16; w; w >>= 1) lw += __shfl_xor_sync(~0u, lw, w);
         l += lw;
         const int cnt = min(32, p.splits - s0);
@@ -507,10 +524,11 @@ __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParam
         if (e < p.dv) from_f(o[k] * inv, dst + e);
     }
     if (p.lse && lane == 0)
-        p.lse[row_stat(p, b, c, r)] = l == 0.f ? -INFINITY : (float)(((double)mx + log2((double)l)) * kLn2d);
+        p.lse[row_stat(p, b, c, r)] = l == 0.f ? -INFINITY : (float)(((double)mx + log2((double)l)) * kLn2d + from);
 }
 
-// D_i = dout_i.out_i of every (query, head) of a problem: `per` lanes take a row, eight elements each at a time.
+// D_i = dout_i.out_i of every (query, head) of a problem: `per` lanes take a row, eight elements each at a time.  And
+// its base-2 LSE, unless the forward kernels have taken that (AttnParams::stats).
 template <class T>
 __global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p, int per, bool vec) {
     const unsigned at = (blockIdx.x * kThreads + threadIdx.x) / (unsigned)per, rows = (unsigned)(p.n * p.heads);
@@ -532,7 +550,11 @@ __global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p,
         }
     }
     for (int w = per / 2; w; w >>= 1) s += __shfl_xor_sync(~0u, s, w);
-    if (live && sub == 0) p.dot[((size_t)b * p.heads + h) * p.n + i] = s;
+    grid_dependency_wait();
+    if (!live || sub) return;
+    const size_t to = ((size_t)b * p.heads + h) * p.n + i;
+    p.dot[to] = s;
+    if (!p.top || p.top[b] == 0.f) p.lse2[to] = p.lse[to] * kLog2e;
 }
 
 // KEYS: one CTA keeps 16 U keys of a key head (K, V) and streams its packed rows (Q, dO) in tiles of 32: dk and dv.
@@ -548,6 +570,7 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, in
     float *ring = kd + kKept;
     const int tile = kStream * (ld + lv) + 2 * kStream;  // the streamed pair, and bias, or base-2 LSE and D
     const int keys = attn_keys(p, b), rows = p.n * p.group;
+    const float top = p.top ? p.top[b] : 0.f;
     const int all = ((KEYS ? (t0 < keys ? rows : 0) : keys) + kStream - 1) / kStream;
     const int parts = KEYS ? p.key_parts : p.row_parts;
     const int t_beg = (int)((long long)all * part / parts), nt = (int)((long long)all * (part + 1) / parts) - t_beg;
@@ -556,14 +579,14 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, in
         *lse2 = INFINITY;
         *d = 0.f;
         if (r < rows) {
-            const float v = p.lse[row_stat(p, b, c, r)];
-            if (v != -INFINITY) *lse2 = v * kLog2e;
+            const float v = p.lse2[row_stat(p, b, c, r)];
+            if (v != -INFINITY) *lse2 = v;
             *d = p.dot[row_stat(p, b, c, r)];
         }
     };
     if (threadIdx.x < kKept) {
         if (KEYS)
-            kb[threadIdx.x] = attn_bias2(p, b, t0 + threadIdx.x, keys);
+            kb[threadIdx.x] = attn_bias2(p, b, t0 + threadIdx.x, keys, top);
         else
             stat(t0 + threadIdx.x, kb + threadIdx.x, kd + threadIdx.x);
     }
@@ -574,7 +597,7 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, in
             if (KEYS)
                 stat(u0 + threadIdx.x, sb + threadIdx.x, sd + threadIdx.x);
             else
-                sb[threadIdx.x] = attn_bias2(p, b, u0 + threadIdx.x, keys);
+                sb[threadIdx.x] = attn_bias2(p, b, u0 + threadIdx.x, keys, top);
         }
         if (KEYS) {
             stage_rows<T>(b1, ld, p.q, p.qs, p, b, c, u0, kStream, p.d, vec);
@@ -722,7 +745,7 @@ template <class T, int RPT, int C>
 cudaError_t fwd(const AttnParams &p, cudaStream_t s) {
     constexpr int R = 16 * RPT;
     const int ld = tile_stride<C>(p.d), lv = tile_stride<C>(p.dv);
-    const size_t fixed = (size_t)R * ld + R * (kKeys + 4);
+    const size_t fixed = 4 + (size_t)R * ld + R * (kKeys + 4);
     const size_t tile = (size_t)kKeys * (ld + lv) + kKeys;
     const int bufs = (fixed + 2 * tile) * sizeof(float) <= kMaxSmem ? 2 : 1;
     const size_t smem = (fixed + bufs * tile) * sizeof(float);
@@ -808,12 +831,12 @@ cudaError_t launch_xattn_dot(const AttnParams &p, bool bf16, cudaStream_t s) {
     while (per < 32 && 8 * per < p.dv) per *= 2;
     const unsigned long long threads = (unsigned long long)p.n * p.heads * per;  // below 2^32: n heads < 2^27
     const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), p.batch);
-    if (bf16)
-        xattn_dot_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(
-            p, per, aligned4<__nv_bfloat16>(p.out, p.os) && aligned4<__nv_bfloat16>(p.dout, p.dos));
-    else
-        xattn_dot_kernel<float><<<grid, kThreads, 0, s>>>(
-            p, per, aligned4<float>(p.out, p.os) && aligned4<float>(p.dout, p.dos));
+    const bool vec = bf16 ? aligned4<__nv_bfloat16>(p.out, p.os) && aligned4<__nv_bfloat16>(p.dout, p.dos)
+                          : aligned4<float>(p.out, p.os) && aligned4<float>(p.dout, p.dos);
+    const auto kernel = bf16 ? xattn_dot_kernel<__nv_bfloat16> : xattn_dot_kernel<float>;
+    // behind the statistics, which the row products do not need
+    if (p.top) return launch_dependent(kernel, grid, kThreads, 0, s, p, per, vec);
+    kernel<<<grid, kThreads, 0, s>>>(p, per, vec);
     return cudaGetLastError();
 }
 cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, int sms, cudaStream_t s) {

@@ -86,6 +86,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
     const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads;
     const int r0 = block * 128;  // first kept row (key, or packed query row)
     const int keys = attn_keys(p, b), rows = p.n * p.group;
+    const float top = p.top ? p.top[b] : 0.f;
     const int head_tiles = (p.n + kTile - 1) / kTile;
     const int all = KEYS ? (r0 < keys ? p.group * head_tiles : 0) : (keys + kTile - 1) / kTile;
     const int parts = KEYS ? p.key_parts : p.row_parts;
@@ -179,7 +180,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
             unsigned dead[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                dead[u] = __ballot_sync(~0u, attn_bias2(p, b, r0 + 32 * u + lane, keys) == -INFINITY);
+                dead[u] = __ballot_sync(~0u, attn_masked(p, b, r0 + 32 * u + lane, keys));
             if (!mbar_wait_near(stfull, 0, p.timeout_ns)) ok = false;
             if (dead[0] | dead[1] | dead[2] | dead[3]) {
                 clear_rows<128>(st1, kAtoms, dead, lane);
@@ -202,11 +203,11 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                     n1[u] = 0.f;
                     if (t < nt && i < p.n) {
                         const size_t at = ((size_t)b * p.heads + h) * p.n + i;
-                        n0[u] = __ldg(p.lse + at);
-                        n1[u] = __ldg(p.dot + at);
+                        n0[u] = p.lse2[at];
+                        n1[u] = p.dot[at];
                     }
                 } else {
-                    n0[u] = attn_bias2(p, b, (t_beg + t) * kTile + 32 * u + lane, keys);
+                    n0[u] = attn_bias2(p, b, (t_beg + t) * kTile + 32 * u + lane, keys, top);
                 }
             }
             i0 += kTile;
@@ -224,7 +225,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
             bool any = !KEYS && p.bias != nullptr;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                v0[u] = KEYS ? (n0[u] == -INFINITY ? -INFINITY : -n0[u] * kLog2e) : n0[u];
+                v0[u] = KEYS ? (n0[u] == -INFINITY ? -INFINITY : -n0[u]) : n0[u];
                 v1[u] = -n1[u];
                 if (!KEYS) {
                     dead[u] = __ballot_sync(~0u, v0[u] == -INFINITY);
@@ -349,7 +350,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
         const int row = r0 + q * 32 + lane;
         float nl = 0.f, nd = 0.f;  // KEYS: the key's bias; ROWS: -L (base 2) and -D of the row
         if (KEYS) {
-            nl = attn_bias2(p, b, row, keys);
+            nl = attn_bias2(p, b, row, keys, top);
         } else {
             const int tid = (int)threadIdx.x - 128;
             stage_packed<kAtoms>(st1, p.q, p.qs, p, b, c, r0, 128, p.d, tid, 256);
@@ -360,8 +361,8 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
             nl = -INFINITY;
             if (row < rows) {
                 const size_t at = ((size_t)b * p.heads + c * p.group + row % p.group) * p.n + row / p.group;
-                const float l = p.lse[at];
-                nl = l == -INFINITY ? -INFINITY : -l * kLog2e;
+                const float l = p.lse2[at];
+                nl = l == -INFINITY ? -INFINITY : -l;
                 nd = -p.dot[at];
             }
         }

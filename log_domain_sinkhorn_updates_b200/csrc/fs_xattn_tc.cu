@@ -97,7 +97,7 @@ __host__ __device__ inline Layout layout(int qt, int datoms, int vatoms, int slo
     L.bias = L.ring + (uint32_t)slots * L.slot;
     L.ml = L.bias + (uint32_t)(kBiasSlots * tile_keys(qt) * 4);
     L.bars = L.ml + 128 * 8;
-    L.total = L.bars + (3 * slots + 2 * kBiasSlots + 1 + 4 + 4 + 4 + 2) * 8 + 8;
+    L.total = L.bars + (3 * slots + 2 * kBiasSlots + 1 + 4 + 4 + 4 + 2) * 8 + 16;
     return L;
 }
 
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *drain = pvdone + 4;   // [2] every MMA of issuer g is complete
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    float *top_holder = reinterpret_cast<float *>(tmem_holder + 2);
 
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rows = p.n * p.group;
@@ -137,7 +138,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tiles whose scores take a bias from shared memory: all, or only the one that the keys end in
     auto masked_tile = [&](int t) { return p.bias != nullptr || j_beg + (t + 1) * kTS > j_end; };
 
+    const float top = attn_top<kThreads>(p, b, j_beg, j_end, reinterpret_cast<float *>(sML));
+    if (attn_stats_done(p, unit, top)) return;
     if (threadIdx.x == 0) {
+        *top_holder = top;  // read again by the warps that need it
         for (int s = 0; s < NS; ++s) {
             mbar_init(full + s, 1);
             mbar_init(ready + s, 1);
@@ -207,15 +211,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             RingPos rp{0, 0};
             RingPos bs{0, 0};
             int used = 0;
+            const float from = *top_holder;
             float bv[kTS / 32], next[kTS / 32];  // base-2 bias of a tile's keys, read a tile ahead
 #pragma unroll
-            for (int u = 0; u < kTS / 32; ++u) next[u] = attn_bias2(p, b, j_beg + 32 * u + lane, j_end);
+            for (int u = 0; u < kTS / 32; ++u) next[u] = attn_bias2(p, b, j_beg + 32 * u + lane, j_end, from);
             for (int t = 0; ok && t < nt; ++t) {
                 unsigned dead[kTS / 32], cleared = 0;
 #pragma unroll
                 for (int u = 0; u < kTS / 32; ++u) {
                     bv[u] = next[u];
-                    next[u] = attn_bias2(p, b, j_beg + (t + 1) * kTS + 32 * u + lane, j_end);
+                    next[u] = attn_bias2(p, b, j_beg + (t + 1) * kTS + 32 * u + lane, j_end, from);
                     dead[u] = __ballot_sync(~0u, bv[u] == -INFINITY);
                     cleared |= dead[u];
                 }
@@ -438,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool live = r < rows;
             if (!unit.whole) {
                 const size_t at = unit.part + blk * 128 + rl;
-                if (live) p.part_ml[at] = make_float2(m, l);
+                if (live) p.part_ml[at] = {*top_holder, m, l};
                 if (nt > 0)
                     for (int k = 0; k < p.dv; k += 16) {
                         uint32_t o[16];
@@ -456,6 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 *reinterpret_cast<float4 *>(p.part_o + at * p.dv + k + u) =
                                     make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
                     }
+            } else if (p.stats) {
+                if (live)
+                    p.lse2[((size_t)b * p.heads + c * p.group + r % p.group) * p.n + r / p.group] =
+                        (float)((double)m + log2((double)l));
             } else {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const int h = c * p.group + r % p.group, i = r / p.group;
@@ -486,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (p.lse && live)
                     p.lse[((size_t)b * p.heads + h) * p.n + i] =
-                        l == 0.f ? -INFINITY : (float)(((double)m + log2((double)l)) * kLn2d);
+                        l == 0.f ? -INFINITY : (float)(((double)m + log2((double)l)) * kLn2d + *top_holder);
             }
         }
     }

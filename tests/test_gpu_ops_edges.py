@@ -47,3 +47,64 @@ def test_infinite_logits(first):
     w[:] = -math.inf
     _fs().fs_cross_entropy(x, w, target, loss, lse)
     assert torch.isnan(loss).all() and torch.isneginf(lse).all()
+
+
+def _shifted(q, k, v, dout, bias, k_len=None):
+    """The 64-bit form with every problem's largest kept bias taken off: softmax and gradients are the same, and the
+    bounds are those of biases of the remaining size.  Returns the form and those largest biases."""
+    live = ~(bias <= ref.MASK)
+    if k_len is not None:
+        live &= torch.arange(bias.shape[1], device="cuda")[None] < k_len.clamp(0, bias.shape[1])[:, None]
+    top = torch.where(live, bias.double(), -math.inf).amax(dim=1)
+    top = torch.where(torch.isinf(top), torch.zeros_like(top), top)
+    rest = torch.where(live, bias.double() - top[:, None], -math.inf)
+    return ref.attention(q, k, v, dout=dout, bias=rest, k_len=k_len), top
+
+
+def _check_shifted(got, want, top):
+    ref.check(got, want, [name for name in got if name != "lse"])
+    lse, bound = want["lse"]
+    full = lse + top[:, None, None]
+    some = ~torch.isinf(full)
+    assert torch.equal(torch.isneginf(got["lse"]), ~some)
+    off = (got["lse"].double() - full).abs()
+    assert (off[some] <= (bound + ref.U * full.abs())[some]).all()
+
+
+BIG = [-1e9, -1e8, -65504.0, -1e4, -65.0, 1e6, 1e9, -9e29]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,d", [(1, 64), (9, 128), (150, 64), (40, 200)])
+@pytest.mark.parametrize("size", BIG)
+def test_biases_of_any_size_on_every_key(dtype, n, d, size):
+    """A sample masked with a finite constant: its scores still decide, forward and gradient.  Beside it one with
+    ordinary biases, one with the constant on all keys but a few, and one that is masked altogether."""
+    m = 700
+    q, k, v, dout = attn.make(5, n, m, 4, 2, d, d, dtype, seed=n)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    step = max(0.25, 2.0 ** (math.floor(math.log2(abs(size))) - 23))
+    bias = torch.full((5, m), size, device="cuda")
+    bias[0, torch.rand(m, device="cuda", generator=g) < 0.3] += step
+    bias[1] = 0.5 * torch.randn(m, device="cuda", generator=g)
+    bias[2, 100:130] = 0.0
+    bias[3] = -math.inf
+    bias[4, ::3] = -math.inf
+    k_len = torch.tensor([m, 333, m, m, 70], dtype=torch.int32, device="cuda")
+    for lens in (None, k_len):
+        got = attn.run(q, k, v, dout, bias=bias, k_len=lens)
+        _check_shifted(got, *_shifted(q, k, v, dout, bias, lens))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("size", [(2, 1, 9000, 4, 2, 64, 64), (2, 5, 6000, 8, 1, 128, 128), (2, 3, 4000, 1, 1, 40, 200)])
+def test_parts_with_biases_of_different_sizes(dtype, size):
+    """Keys split over CTAs whose largest biases are far apart, or nearly the same at 1e9."""
+    q, k, v, dout = attn.make(*size, dtype, seed=5)
+    m = size[2]
+    for first, rest in [(-1e9, 0.0), (0.0, -1e9), (-1e9, -1e9 + 64), (1e9, 1e9), (-1e5, -1e5 - 3.0)]:
+        bias = torch.full((2, m), rest, device="cuda")
+        bias[:, :m // 2] = first
+        bias[1, m - 3:] = max(first, rest)
+        got = attn.run(q, k, v, dout, bias=bias)
+        _check_shifted(got, *_shifted(q, k, v, dout, bias))
