@@ -470,7 +470,7 @@ FS_API fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const vo
  *   P_ij = e^{S_ij - lse_i},  D_i = dout_i.out_i,  dS_ij = P_ij (dout_i.v_j - D_i)
  *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
  * (dk and dv summed over the heads that share a key head).  Keys that take no
- * part get zeros.  k_len and bias as in the forward; no gradient of bias.  On
+ * part get zeros, also beside a query or a dout that is not finite.  k_len and bias as in the forward; no gradient of bias.  On
  * the tensor cores P and dS are rounded to bf16 for their products.  P comes from
  * the scores and the fp32 lse: its relative error is at least 2^-24 of |lse| (from
  * scores alone: where the largest bias is over 64 in size, the row's sum is taken

@@ -663,7 +663,11 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, in
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int at = t0 + ti * U + u;
-        if (at >= (KEYS ? p.m : rows)) continue;  // keys past the length get zeros: they take no part
+        if (at >= (KEYS ? p.m : rows)) continue;
+        if (KEYS && kb[ti * U + u] == -INFINITY) {  // takes no part: zeros, whatever stands in a query or its gradient
+#pragma unroll
+            for (int k = 0; k < C; ++k) g1[u][k] = g2[u][KEYS ? k : 0] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         if (parts > 1) {  // a part: its raw sums
             const int blocks = ((KEYS ? p.m : rows) + kKept - 1) / kKept;
             const size_t to = ((size_t)part * gridDim.y + blockIdx.y) * blocks * kKept + at;

@@ -454,6 +454,8 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                   p.dqs.head * (c * p.group + row % p.group);
         }
         const uint32_t to = tmem_base + lanes + (second ? kSum2 : kSum1);
+        // a key that takes no part gets zeros, whatever stands in a query or its gradient
+        const bool zero = nt == 0 || (KEYS && nl == -INFINITY);
         if (parts > 1) {  // a part: its raw sums
             float *base = KEYS ? (second ? p.part_dk : p.part_dv) : p.part_dq;
             const size_t padded = (size_t)(KEYS ? g.key_blocks : g.row_blocks) * 128;
@@ -468,7 +470,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                 for (int u = 0; u < 32; u += 4)
                     if (live && k + u < width)
                         *reinterpret_cast<uint4 *>(raw + k + u) =
-                            nt > 0 ? make_uint4(o[u], o[u + 1], o[u + 2], o[u + 3]) : make_uint4(0u, 0u, 0u, 0u);
+                            zero ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(o[u], o[u + 1], o[u + 2], o[u + 3]);
             }
         } else {
             for (int k = KEYS ? 0 : 32 * grp; k < width; k += KEYS ? 32 : 64) {
@@ -477,10 +479,10 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                     tmem_ld32(to + k, o);
                     tmem_ld_wait();
                 }
-    #pragma unroll
+#pragma unroll
                 for (int u = 0; u < 32; u += 8) {
                     uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                    if (nt > 0) {
+                    if (!zero) {
                         w.x = bf16x2(__uint_as_float(o[u]) * mul, __uint_as_float(o[u + 1]) * mul);
                         w.y = bf16x2(__uint_as_float(o[u + 2]) * mul, __uint_as_float(o[u + 3]) * mul);
                         w.z = bf16x2(__uint_as_float(o[u + 4]) * mul, __uint_as_float(o[u + 5]) * mul);

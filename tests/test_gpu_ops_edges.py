@@ -108,3 +108,28 @@ def test_parts_with_biases_of_different_sizes(dtype, size):
         bias[1, m - 3:] = max(first, rest)
         got = attn.run(q, k, v, dout, bias=bias)
         _check_shifted(got, *_shifted(q, k, v, dout, bias))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("size", [(2, 50, 300, 4, 2, 64, 64), (2, 900, 300, 4, 2, 128, 96), (1, 3, 4000, 2, 1, 64, 64),
+                                  (1, 70, 200, 2, 2, 200, 72)])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_masked_keys_get_zeros_beside_rows_that_are_not_finite(dtype, size, value):
+    """A NaN or infinity in one query, or in its gradient, reaches every key that takes part and no other."""
+    q, k, v, dout = attn.make(*size, dtype, seed=29)
+    B, n, m = size[:3]
+    bias = torch.zeros(B, m, device="cuda")
+    bias[:, 20:25] = -math.inf
+    bias[:, 30] = torch.finfo(F32).min
+    k_len = torch.full((B,), m - 130, dtype=torch.int32, device="cuda")
+    dead = (bias <= -1e30) | (torch.arange(m, device="cuda")[None] >= k_len[:, None])
+    clean = attn.run(q, k, v, dout, bias=bias, k_len=k_len)
+    for t in (q, dout):
+        kept = t[:, n // 2].clone()
+        t[:, n // 2] = value
+        got = attn.run(q, k, v, dout, bias=bias, k_len=k_len)
+        t[:, n // 2] = kept
+        assert (got["dk"][dead] == 0).all() and (got["dv"][dead] == 0).all()
+        assert not torch.isfinite(got["dk"][~dead]).all()
+        others = torch.arange(n, device="cuda") != n // 2
+        assert torch.equal(got["dq"][:, others], clean["dq"][:, others])
