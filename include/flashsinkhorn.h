@@ -448,11 +448,10 @@ FS_API size_t fs_cross_attn_workspace(const fs_attn_desc *desc, int grad);
  * -1e30 or less masks its key.  Where the largest kept bias of a problem is over
  * 64 in size, biases are measured from it, so a constant of any size on every key
  * (a sample masked with -1e9) costs the scores nothing.  Keys past the length or
- * masked take no part:
- * their k and v may hold anything, NaN included.  A row without a key gives
- * out = 0 and lse = -inf (q too may hold anything where the length is 0; where
- * the bias masks every key it has to be finite).  lse: device fp32 [batch][heads][n], natural log; may
- * be NULL.  bf16 on the tensor cores: scores and sums in fp32, the weights
+ * masked take no part: their k and v may hold anything, NaN included.  A row
+ * without a key gives out = 0 and lse = -inf, and its q too may hold anything.
+ * lse: device fp32 [batch][heads][n], natural log; may be NULL.  bf16 on the
+ * tensor cores: scores and sums in fp32, the weights
  * e^{S - max} rounded to bf16 for their product with v.  Where few rows face
  * many keys (single tokens) the keys are split over the SMs and joined in order.
  * Non-finite inputs that take part give non-finite outputs.  Asynchronous.

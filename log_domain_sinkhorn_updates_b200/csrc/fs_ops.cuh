@@ -41,7 +41,7 @@ struct AttnParams {
     float *dot;           // gradient: [batch][heads][n], D_i = dout_i.out_i
     float *lse2;          // gradient: [batch][heads][n], base-2 LSE measured from `top`
     float *top;           // gradient: [batch], what the problem's biases are measured from; null without a bias
-    // 1: the forward's kernels, at a gradient's start, write top, and lse2 of the problems where top is not 0: there one
+    // 1: the forward's kernels, at a gradient's start, write top, and lse2 of the problems where it is large: there one
     // fp32 number does not hold the LSE, and the gradient cannot do with the forward's.  Their CTAs leave at once elsewhere.
     int stats;
     // Forward: a unit is unit_rows packed rows of a key head.  Units from main_units on are split over their keys into
@@ -132,7 +132,8 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnParams &p) {
     w.part = ((size_t)sp * p.tail_units + tu) * p.unit_rows;
     return w;
 }
-// What the biases of keys [j_beg, j_end) of problem b are measured from: the largest kept one, or 0 where it is near 0.
+// What the biases of keys [j_beg, j_end) of problem b are measured from: the largest kept one, or 0 where it is near 0;
+// -inf where none is kept: the caller then takes no key at all, and a query of such a problem may hold anything.
 // By a whole block of THREADS threads; scratch: a float a warp.
 template <int THREADS>
 __device__ __forceinline__ float attn_top(const AttnParams &p, int b, int j_beg, int j_end, float *scratch) {
@@ -149,13 +150,17 @@ __device__ __forceinline__ float attn_top(const AttnParams &p, int b, int j_beg,
     __syncthreads();
     for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, scratch[w]);
     __syncthreads();
-    return top != -INFINITY && fabsf(top) > kBiasNear ? top : 0.f;
+    return fabsf(top) > kBiasNear ? top : 0.f;
 }
 // Statistics for a gradient (AttnParams::stats): whether the problem needs none.
 __device__ __forceinline__ bool attn_stats_done(const AttnParams &p, const AttnUnit &unit, float top) {
     if (!p.stats) return false;
     if (threadIdx.x == 0 && unit.r0 == 0 && unit.c == 0) p.top[unit.b] = top;
-    return top == 0.f;
+    return top == 0.f || top == -INFINITY;
+}
+// Gradient: the keys of problem b that take part, as attn_top found them.
+__device__ __forceinline__ int attn_grad_keys(const AttnParams &p, int b) {
+    return p.top && p.top[b] == -INFINITY ? 0 : attn_keys(p, b);
 }
 // Base-2 bias of key j (valid or not), measured from top: -inf where it is masked.
 __device__ __forceinline__ float attn_bias2(const AttnParams &p, int b, int j, int keys, float top) {

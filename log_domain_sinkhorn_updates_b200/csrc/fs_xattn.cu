@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kTileThreads) xattn_simt_kernel(const AttnPara
         stage_keys<T>(sK, ld, p.k, p.ks, p, b, c, j0, kKeys, p.d, j_end, vec);
         stage_keys<T>(sV, lv, p.v, p.vs, p, b, c, j0, kKeys, p.dv, j_end, vec);
     };
-    const int nt = j_end > j_beg ? (j_end - j_beg + kKeys - 1) / kKeys : 0;
+    const int nt = j_end > j_beg && top != -INFINITY ? (j_end - j_beg + kKeys - 1) / kKeys : 0;
     stage_rows<T>(sQ, ld, p.q, p.qs, p, b, c, r0, R, p.d, vec);
     if (bufs == 2 && nt > 0) fetch(0);
     stage_commit();
@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) xattn_token_kernel(const Attn
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, grp = lane / 8, sub = lane % 8;
     const int b = unit.b, c = unit.c, rows = p.n * p.group;
     const float bias_top = attn_top<kTileThreads>(p, b, unit.j_beg, unit.j_end, &sml[0][0].x);
+    const int j_end = bias_top == -INFINITY ? unit.j_beg : unit.j_end;
     float4 q[RT][C], o[RT][C];
     float mx[RT], l[RT];
 #pragma unroll
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) xattn_token_kernel(const Attn
     float4 kn[C], vn[C];
     float bn;
     auto fetch = [&](int j) {  // key j's bias, and its rows unless it is masked (or past the part)
-        bn = attn_bias2(p, b, j, unit.j_end, bias_top);
+        bn = attn_bias2(p, b, j, j_end, bias_top);
 #pragma unroll
         for (int k = 0; k < C; ++k) {
             const int e = 32 * k + 4 * sub;
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) xattn_token_kernel(const Attn
     };
     const int first = unit.j_beg + 4 * warp + grp;
     fetch(first);
-    for (int j = first; j - grp < unit.j_end; j += 32) {  // whole warps: the shuffles take every lane
+    for (int j = first; j - grp < j_end; j += 32) {  // whole warps: the shuffles take every lane
         float4 kc[C], vc[C];
         const float bias = bn;
 #pragma unroll
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p,
     if (!live || sub) return;
     const size_t to = ((size_t)b * p.heads + h) * p.n + i;
     p.dot[to] = s;
-    if (!p.top || p.top[b] == 0.f) p.lse2[to] = p.lse[to] * kLog2e;
+    if (!p.top || p.top[b] == 0.f || p.top[b] == -INFINITY) p.lse2[to] = p.lse[to] * kLog2e;
 }
 
 // KEYS: one CTA keeps 16 U keys of a key head (K, V) and streams its packed rows (Q, dO) in tiles of 32: dk and dv.
@@ -569,7 +570,7 @@ __device__ void grad_pass(const AttnParams &p, bool vec, int bufs, int block, in
     float *kb = sS + kKept * LS, *kd = kb + kKept;  // kept: bias, or base-2 LSE and D
     float *ring = kd + kKept;
     const int tile = kStream * (ld + lv) + 2 * kStream;  // the streamed pair, and bias, or base-2 LSE and D
-    const int keys = attn_keys(p, b), rows = p.n * p.group;
+    const int keys = attn_grad_keys(p, b), rows = p.n * p.group;
     const float top = p.top ? p.top[b] : 0.f;
     const int all = ((KEYS ? (t0 < keys ? rows : 0) : keys) + kStream - 1) / kStream;
     const int parts = KEYS ? p.key_parts : p.row_parts;

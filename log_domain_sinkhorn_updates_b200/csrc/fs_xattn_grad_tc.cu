@@ -85,7 +85,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
     const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int c = blockIdx.y % p.kv_heads, b = blockIdx.y / p.kv_heads;
     const int r0 = block * 128;  // first kept row (key, or packed query row)
-    const int keys = attn_keys(p, b), rows = p.n * p.group;
+    const int keys = attn_grad_keys(p, b), rows = p.n * p.group;
     const float top = p.top ? p.top[b] : 0.f;
     const int head_tiles = (p.n + kTile - 1) / kTile;
     const int all = KEYS ? (r0 < keys ? p.group * head_tiles : 0) : (keys + kTile - 1) / kTile;

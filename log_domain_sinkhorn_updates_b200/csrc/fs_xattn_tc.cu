@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rows = p.n * p.group;
     const AttnUnit unit = attn_unit<LENGTHS>(p);
     const int c = unit.c, b = unit.b, j_beg = unit.j_beg, j_end = unit.j_end;
-    const int nt = j_end > j_beg ? (j_end - j_beg + kTS - 1) / kTS : 0;
+    const int most = j_end > j_beg ? (j_end - j_beg + kTS - 1) / kTS : 0;
     // tiles whose scores take a bias from shared memory: all, or only the one that the keys end in
     auto masked_tile = [&](int t) { return p.bias != nullptr || j_beg + (t + 1) * kTS > j_end; };
 
@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    const int nt = *top_holder == -INFINITY ? 0 : most;
     if (warp < 4) {
         regs_dec<kFewRegs>();
         if (warp == 0) {

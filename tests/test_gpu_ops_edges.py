@@ -133,3 +133,25 @@ def test_masked_keys_get_zeros_beside_rows_that_are_not_finite(dtype, size, valu
         assert not torch.isfinite(got["dk"][~dead]).all()
         others = torch.arange(n, device="cuda") != n // 2
         assert torch.equal(got["dq"][:, others], clean["dq"][:, others])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,m", [(1, 400), (6, 3000), (200, 400)])
+def test_anything_in_the_queries_of_a_problem_whose_keys_are_all_masked(dtype, n, m):
+    """Padding of a batch by masks: NaN in q, k, v and the gradient; the other problems keep their bits."""
+    q, k, v, dout = attn.make(4, n, m, 4, 2, 64, 64, dtype, seed=17)
+    bias = torch.zeros(4, m, device="cuda")
+    bias[1] = -math.inf
+    bias[2] = torch.finfo(F32).min
+    bias[3, 5:] = -1e30
+    for k_len in (None, torch.tensor([m, m, m, 77], dtype=torch.int32, device="cuda")):
+        kw = {"bias": bias, "k_len": k_len}
+        clean = attn.run(q, k, v, dout, **kw)
+        bad = [t.clone() for t in (q, k, v, dout)]
+        for t in bad:
+            t[1:3] = math.nan
+        got = attn.run(*bad, **kw)
+        for name in got:
+            assert torch.equal(got[name], clean[name]), name
+        assert all((got[name][1:3] == 0).all() for name in ("out", "dq", "dk", "dv"))
+        assert torch.isneginf(got["lse"][1:3]).all()
