@@ -3,6 +3,7 @@
 #pragma once
 
 #include <atomic>
+#include <mutex>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -59,12 +60,17 @@ struct AttnParams {
 };
 
 // Allows a kernel `bytes` of dynamic shared memory, once a device (Kernel: one function, each with a list of its own).
+// Sizes differ from call to call, so the limit only rises, under a lock: of two threads on first use the one that asks
+// for less could otherwise set its limit last and the other record its own.
 template <auto Kernel>
 cudaError_t allow_smem(size_t bytes) {
     static std::atomic<size_t> allowed[64];
+    static std::mutex mu;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev < 64 && allowed[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    std::lock_guard<std::mutex> lock(mu);
     if (dev < 64 && allowed[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
     e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e == cudaSuccess && dev < 64) allowed[dev].store(bytes, std::memory_order_relaxed);

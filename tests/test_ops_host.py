@@ -1,0 +1,83 @@
+"""Host code of the handle-less operators on the CPU: what two threads, or a failing CUDA call, can do to what is kept
+between calls (the CUDA runtime's part is played by the tests)."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "log_domain_sinkhorn_updates_b200", "csrc")
+
+# Two threads ask for different shared-memory limits of one kernel at once.  The runtime's part: the limit is the last one
+# set, and the call for the larger one is still under way when the other thread has its answer.
+RUNTIME = r"""
+#include <chrono>
+#include <condition_variable>
+#include <mutex>
+static std::mutex mu;
+static std::condition_variable cv;
+int limit = 0, large_set = 0, small_done = 0;
+void wait_for(int &flag) {
+    std::unique_lock<std::mutex> l(mu);
+    cv.wait_for(l, std::chrono::milliseconds(500), [&] { return flag != 0; });
+}
+void raise_flag(int &flag) {
+    std::lock_guard<std::mutex> l(mu);
+    flag = 1;
+    cv.notify_all();
+}
+extern "C" {
+int cudaGetDevice(int *d) { *d = 0; return 0; }
+int cudaFuncSetAttribute(const void *, int, int bytes) {
+    {
+        std::lock_guard<std::mutex> l(mu);
+        limit = bytes;
+    }
+    if (bytes == 200000) {
+        raise_flag(large_set);
+        wait_for(small_done);
+    }
+    return 0;
+}
+void **__cudaRegisterFatBinary(void *) { return nullptr; }
+void __cudaRegisterFatBinaryEnd(void **) {}
+void __cudaUnregisterFatBinary(void **) {}
+char __cudaInitModule(void **) { return 0; }
+}
+"""
+THREADS = r"""
+#include <cstdio>
+#include <thread>
+#include "fs_ops.cuh"
+extern int limit, large_set, small_done;
+void wait_for(int &);
+void raise_flag(int &);
+void kernel() {}
+int main() {
+    std::thread large([] { fs::allow_smem<&kernel>(200000); });
+    std::thread small([] {
+        wait_for(large_set);
+        fs::allow_smem<&kernel>(100000);
+        raise_flag(small_done);
+    });
+    large.join();
+    small.join();
+    fs::allow_smem<&kernel>(200000);
+    std::printf("limit %d\n", limit);
+    return limit >= 200000 ? 0 : 1;
+}
+"""
+
+
+def test_two_threads_on_first_use_leave_the_larger_shared_memory_limit(tmp_path):
+    from log_domain_sinkhorn_updates_b200 import build
+    if not shutil.which(build.NVCC):
+        pytest.skip("no nvcc")
+    (tmp_path / "runtime.cpp").write_text(RUNTIME)
+    (tmp_path / "threads.cu").write_text(THREADS)
+    subprocess.run([build.NVCC, "-std=c++17", "-cudart", "none", "-gencode", "arch=compute_100a,code=sm_100a", "-I", CSRC,
+                    "-I", os.path.join(ROOT, "include"), "threads.cu", "runtime.cpp", "-o", "limits", "-lpthread"],
+                   check=True, cwd=tmp_path)
+    r = subprocess.run([str(tmp_path / "limits")], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout + r.stderr
