@@ -543,6 +543,14 @@ FS_API fs_status fs_cross_entropy_grad(const fs_xent_desc *desc, const void *x, 
  */
 FS_API fs_status fs_check(void *stream);
 
+/*
+ * Failure-path self test of these calls: enqueues a kernel whose one bounded wait
+ * (the same wait, and the same error) can never complete and ends after about
+ * timeout_ms.  Asynchronous; the next fs_check reports FS_ERR_TIMEOUT, once.
+ * FS_ERR_INVALID_ARG for timeout_ms < 1.
+ */
+FS_API fs_status fs_selftest_check(int timeout_ms, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

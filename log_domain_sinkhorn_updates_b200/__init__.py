@@ -13,7 +13,7 @@ __all__ = ["fs_create", "fs_update_f", "fs_update_g", "fs_solve", "fs_marginal_e
            "fs_get_info", "fs_destroy", "fs_last_error", "fs_solve_host", "fs_kernel_launches", "fs_update_f_noalloc",
            "fs_transport_apply", "fs_barycentric_map", "fs_grad_x", "fs_transport_apply_t", "fs_grad_y", "fs_hvp_x",
            "fs_selftest_wait", "fs_cross_attn", "fs_cross_attn_grad", "fs_cross_attn_workspace", "fs_cross_entropy",
-           "fs_cross_entropy_grad", "fs_cross_entropy_workspace", "fs_check",
+           "fs_cross_entropy_grad", "fs_cross_entropy_workspace", "fs_check", "fs_selftest_check",
            "FsError", "Handle"]
 
 

@@ -29,7 +29,7 @@ EXPORTS = ["fs_create", "fs_update_f", "fs_update_g", "fs_solve", "fs_marginal_e
            "fs_update_f_noalloc", "fs_transport_apply", "fs_barycentric_map", "fs_grad_x",
            "fs_transport_apply_t", "fs_grad_y", "fs_hvp_x", "fs_selftest_wait", "fs_cross_attn", "fs_cross_attn_grad",
            "fs_cross_attn_workspace", "fs_cross_entropy", "fs_cross_entropy_grad", "fs_cross_entropy_workspace",
-           "fs_check"]
+           "fs_check", "fs_selftest_check"]
 
 
 class FsDesc(ctypes.Structure):
@@ -122,6 +122,7 @@ def lib():
         L.fs_cross_entropy.argtypes = [xd] + [vp] * 6 + [szt, vp]
         L.fs_cross_entropy_grad.argtypes = [xd] + [vp] * 9 + [szt, vp]
         L.fs_check.argtypes = [vp]
+        L.fs_selftest_check.argtypes = [ctypes.c_int, vp]
         L.fs_cross_attn_workspace.restype = L.fs_cross_entropy_workspace.restype = szt
         for name in EXPORTS:
             if name not in ("fs_last_error", "fs_kernel_launches", "fs_cross_attn_workspace",
@@ -641,3 +642,11 @@ def fs_check(stream=None):
     s = torch.cuda.current_stream() if stream is None else stream
     with torch.cuda.device(s.device):
         _check(lib().fs_check(ctypes.c_void_p(s.cuda_stream)))
+
+
+def fs_selftest_check(timeout_ms=50, stream=None):
+    """Enqueue a bounded wait that runs out after timeout_ms: the next fs_check raises FsError (FS_ERR_TIMEOUT)."""
+    import torch
+    s = torch.cuda.current_stream() if stream is None else stream
+    with torch.cuda.device(s.device):
+        _check(lib().fs_selftest_check(int(timeout_ms), ctypes.c_void_p(s.cuda_stream)))

@@ -1,7 +1,7 @@
 // C entry points of the row-softmax operators: cross attention and softmax
-// cross entropy.  Host code only: argument checks, the choice between the
-// tensor-core and the CUDA-core kernels, the plan of splits and pieces, the
-// layout of the caller's workspace, and the launches.
+// cross entropy.  Host code (but for the error word): argument checks, the choice
+// between the tensor-core and the CUDA-core kernels, the plan of splits and
+// pieces, the layout of the caller's workspace, and the launches.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
@@ -12,7 +12,11 @@
 
 namespace {
 
-__device__ int g_ops_err;  // error bits of the handle-less calls on this device
+__device__ int g_ops_err;    // error bits of the handle-less calls on this device
+__device__ int g_ops_taken;  // those that the fs_check under way has taken
+
+// In one step, so that a bit that another stream's kernel raises meanwhile is taken now or stays for the next check.
+__global__ void take_errors_kernel() { g_ops_taken = atomicExch(&g_ops_err, 0); }
 
 constexpr int kMaxDevices = 64;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
@@ -576,15 +580,32 @@ fs_status fs_cross_entropy_grad(const fs_xent_desc *desc, const void *x, const v
     return FS_OK;
 }
 
+fs_status fs_selftest_check(int timeout_ms, void *stream) {
+    if (timeout_ms < 1) return reject(FS_ERR_INVALID_ARG, "timeout_ms must be >= 1");
+    Device dev;
+    fs_status st = current_device(&dev);
+    if (st != FS_OK) return st;
+    OPS_LAUNCH(fs::launch_wait_probe((unsigned long long)timeout_ms * 1000000ull, dev.err,
+                                     static_cast<cudaStream_t>(stream)), 1);
+    return FS_OK;
+}
+
 fs_status fs_check(void *stream) {
     Device dev;
     fs_status st = current_device(&dev);
     if (st != FS_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    static std::mutex mu;  // one check at a time has the word of taken bits
     int bits = 0;
-    cudaError_t e = cudaMemcpyAsync(&bits, dev.err, sizeof(int), cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(dev.err, 0, sizeof(int), s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    cudaError_t e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess) {
+        std::lock_guard<std::mutex> lock(mu);
+        take_errors_kernel<<<1, 1, 0, s>>>();
+        e = cudaGetLastError();
+        if (e == cudaSuccess) fs::count_launches(1);
+        if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(&bits, g_ops_taken, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
     if (e != cudaSuccess) return reject(FS_ERR_CUDA, "fs_check: %s", cudaGetErrorString(e));
     if (bits & fs::kDevErrTimeout) return reject(FS_ERR_TIMEOUT, "a bounded device wait timed out");
     return FS_OK;

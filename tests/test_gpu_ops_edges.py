@@ -155,3 +155,52 @@ def test_anything_in_the_queries_of_a_problem_whose_keys_are_all_masked(dtype, n
             assert torch.equal(got[name], clean[name]), name
         assert all((got[name][1:3] == 0).all() for name in ("out", "dq", "dk", "dv"))
         assert torch.isneginf(got["lse"][1:3]).all()
+
+
+def test_a_wait_that_runs_out_is_reported_once_and_the_calls_stay_usable():
+    fs = _fs()
+    fs.fs_check()
+    fs.fs_selftest_check(20)
+    with pytest.raises(fs.FsError, match="FS_ERR_TIMEOUT"):
+        fs.fs_check()
+    fs.fs_check()
+    with pytest.raises(fs.FsError, match="FS_ERR_INVALID_ARG"):
+        fs.fs_selftest_check(0)
+    q, k, v, dout = attn.make(1, 9, 50, 2, 1, 64, 64, BF16)
+    ref.check(attn.run(q, k, v, dout), ref.attention(q, k, v, dout=dout))
+
+
+def test_checks_on_one_stream_miss_nothing_that_another_raises():
+    """A thread checks one stream without a pause, another raises errors on a second stream: each is reported once."""
+    import threading
+    import time
+    fs = _fs()
+    fs.fs_check()
+    mine, other = torch.cuda.Stream(), torch.cuda.Stream()
+    rounds, seen, stop, failures = 400, [0], threading.Event(), []
+
+    def checks():
+        while not stop.is_set():
+            try:
+                fs.fs_check(mine)
+            except fs.FsError as e:
+                if "FS_ERR_TIMEOUT" not in str(e):
+                    failures.append(e)
+                    return
+                seen[0] += 1
+
+    t = threading.Thread(target=checks)
+    t.start()
+    try:
+        for i in range(rounds):
+            fs.fs_selftest_check(1, other)
+            other.synchronize()
+            until = time.monotonic() + 1.0
+            while seen[0] <= i and time.monotonic() < until and not failures:
+                time.sleep(0)
+            if seen[0] != i + 1:
+                break
+    finally:
+        stop.set()
+        t.join()
+    assert not failures and seen[0] == rounds, (failures, seen[0])
