@@ -44,6 +44,10 @@ __device__ __forceinline__ bool mbar_wait_near(uint64_t *b, uint32_t parity, uns
         if (t - t0 > limit_ns) return false;
     }
 }
+// What decides for a whole warp: every lane's answer.  A wait's time, or an abort flag, may run out for some lanes and not
+// for others, and the barriers, votes, TMEM and MMA instructions that follow take all 32: without the vote a wait that
+// ran out could leave part of a warp at one of them for good.
+__device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(~0u, ok); }
 // A ring position that moves without divisions: slot and the parity of its use.
 struct RingPos {
     int slot;

@@ -181,7 +181,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 dead[u] = __ballot_sync(~0u, attn_masked(p, b, r0 + 32 * u + lane, keys));
-            if (!mbar_wait_near(stfull, 0, p.timeout_ns)) ok = false;
+            if (!warp_all(mbar_wait_near(stfull, 0, p.timeout_ns))) ok = false;
             if (dead[0] | dead[1] | dead[2] | dead[3]) {
                 clear_rows<128>(st1, kAtoms, dead, lane);
                 clear_rows<128>(st2, kAtoms, dead, lane);
@@ -233,7 +233,8 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                 }
             }
             fetch(t + 1);
-            if (t >= kColSlots && !mbar_wait_near(cempty + j, ((uint32_t)(t / kColSlots) & 1u) ^ 1u, p.timeout_ns))
+            if (t >= kColSlots &&
+                !warp_all(mbar_wait_near(cempty + j, ((uint32_t)(t / kColSlots) & 1u) ^ 1u, p.timeout_ns)))
                 ok = false;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -245,7 +246,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
             if (lane == 0) mbar_arrive(cfull + j);
             if (!KEYS) {
                 const int s = rp.slot;
-                if (!mbar_wait_near(full + s, rp.phase, p.timeout_ns)) ok = false;
+                if (!warp_all(mbar_wait_near(full + s, rp.phase, p.timeout_ns))) ok = false;
                 rp.step(1, NS);
                 if (dead[0] | dead[1]) {
                     uint8_t *tile = ring + (size_t)s * 2 * L.half;
@@ -256,7 +257,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                 }
                 if (lane == 0) mbar_arrive(ready + s);
             }
-            if (*abort_flag) break;
+            if (!warp_all(!*abort_flag)) break;
         }
         if (!ok && lane == 0) {
             atomicOr(p.err, kDevErrTimeout);
@@ -273,13 +274,14 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
         const uint64_t r1 = make_sdesc(saddr(ring), 128u), r2 = make_sdesc(saddr(ring) + L.half, 128u);
         const uint64_t c1 = sdesc_mn(saddr(ring), 8192u), c2 = sdesc_mn(saddr(ring) + L.half, 8192u);
         const uint32_t slot16 = 2 * L.half >> 4;
-        bool ok = nt == 0 || mbar_wait_near(stready, 0, p.timeout_ns);
+        bool ok = nt == 0 || warp_all(mbar_wait_near(stready, 0, p.timeout_ns));
         RingPos sp{0, 0}, bp{0, 0};  // the next tile's slot and buffer (each warp counts its own)
         // S and dP of tile t into its buffers, once the products that read them last are complete
         auto scores = [&](int t) {
             const int u = bp.slot;
-            if (t >= NB && !mbar_wait_near(pfree + u, bp.phase ^ 1u, p.timeout_ns)) return false;
-            if (!mbar_wait_near((KEYS ? full : ready) + sp.slot, sp.phase, p.timeout_ns)) return false;
+            if (!warp_all((t < NB || mbar_wait_near(pfree + u, bp.phase ^ 1u, p.timeout_ns)) &&
+                          mbar_wait_near((KEYS ? full : ready) + sp.slot, sp.phase, p.timeout_ns)))
+                return false;
             tc_fence_after();
             if (lead) {
                 const uint64_t b1 = r1 + (uint64_t)(sp.slot * slot16), b2 = r2 + (uint64_t)(sp.slot * slot16);
@@ -302,7 +304,7 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
         // the sums over tile t's streamed rows, once its P and dS are written
         auto sums = [&](int t) {
             const int u = bp.slot, xs = sp.slot;
-            if (!mbar_wait_near(pready + u, bp.phase, p.timeout_ns) || *abort_flag) return false;
+            if (!warp_all(mbar_wait_near(pready + u, bp.phase, p.timeout_ns) && !*abort_flag)) return false;
             tc_fence_after();
             if (lead) {
                 const uint64_t m1 = c1 + (uint64_t)(xs * slot16), m2 = c2 + (uint64_t)(xs * slot16);
@@ -373,8 +375,8 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
         for (int t = grp; t < nt; t += 2) {
             const int j = t % kColSlots, u = bp.slot;
             const uint32_t ts = tmem_base + lanes + 128u * u, td = ts + 64u;
-            if (!mbar_wait_near(sfull + u, bp.phase, p.timeout_ns) ||
-                !mbar_wait_near(cfull + j, (uint32_t)(t / kColSlots) & 1u, p.timeout_ns)) {
+            if (!warp_all(mbar_wait_near(sfull + u, bp.phase, p.timeout_ns) &&
+                          mbar_wait_near(cfull + j, (uint32_t)(t / kColSlots) & 1u, p.timeout_ns) && !*abort_flag)) {
                 ok = false;
                 break;
             }
@@ -430,9 +432,8 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
                 mbar_arrive(cempty + j);
             }
             bp.step(2, NB);
-            if (*abort_flag) break;
         }
-        if (ok && nt > 0 && !mbar_wait_near(done, 0, p.timeout_ns)) ok = false;
+        if (ok && nt > 0 && !warp_all(mbar_wait_near(done, 0, p.timeout_ns))) ok = false;
         if (!ok) {
             atomicOr(p.err, kDevErrTimeout);
             *abort_flag = 1;

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     cleared |= dead[u];
                 }
                 if (masked_tile(t)) {
-                    if (used >= kBiasSlots && !mbar_wait_near(bempty + bs.slot, bs.phase ^ 1u, p.timeout_ns))
+                    if (used >= kBiasSlots && !warp_all(mbar_wait_near(bempty + bs.slot, bs.phase ^ 1u, p.timeout_ns)))
                         ok = false;
 #pragma unroll
                     for (int u = 0; u < kTS / 32; ++u) sBias[bs.slot * kTS + 32 * u + lane] = bv[u];
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 for (int kv = 0; kv < 2; ++kv) {
                     const int s = rp.slot;
-                    if (!mbar_wait_near(full + s, rp.phase, p.timeout_ns)) ok = false;
+                    if (!warp_all(mbar_wait_near(full + s, rp.phase, p.timeout_ns))) ok = false;
                     rp.step(1, NS);
                     if (cleared) {
                         uint8_t *tile = ring + (size_t)s * L.slot;
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (lane == 0) mbar_arrive(ready + s);
                 }
-                if (*abort_flag) break;
+                if (!warp_all(!*abort_flag)) break;
             }
             if (!ok && lane == 0) {
                 atomicOr(p.err, kDevErrTimeout);
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // S of step i (part h of its tile) into buffer i & 1
             auto s_product = [&](int i) {
                 const int h = i % kSteps, u = i & 1;
-                if (h == 0 && !mbar_wait_near(ready + kp.slot, kp.phase, p.timeout_ns)) return false;
+                if (h == 0 && !warp_all(mbar_wait_near(ready + kp.slot, kp.phase, p.timeout_ns))) return false;
                 tc_fence_after();
                 if (lead) {
                     const uint64_t kd = k0 + (uint64_t)(kp.slot * slot16 + h * 512);
@@ -286,13 +286,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (h == kSteps - 1) kp.step(kNext, NS);
                 return true;
             };
-            bool ok = steps == 0 || mbar_wait_near(qfull, 0, p.timeout_ns);
+            bool ok = steps == 0 || warp_all(mbar_wait_near(qfull, 0, p.timeout_ns));
             for (int i = 0; ok && i < min(steps, 2); ++i) ok = s_product(i);
             for (int i = 0; ok && i < steps; ++i) {
                 const int h = i % kSteps, u = i & 1;
                 const uint32_t ph = (uint32_t)(i >> 1) & 1u;
-                if ((h == 0 && !mbar_wait_near(ready + vp.slot, vp.phase, p.timeout_ns)) ||
-                    !mbar_wait_near(pready + 2 * grp + u, ph, p.timeout_ns) || *abort_flag) {
+                if (!warp_all((h != 0 || mbar_wait_near(ready + vp.slot, vp.phase, p.timeout_ns)) &&
+                              mbar_wait_near(pready + 2 * grp + u, ph, p.timeout_ns) && !*abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (h == kSteps - 1) vp.step(kNext, NS);
                 // the S after next takes the columns of this P: not before the products that read it are complete (the
                 // softmax has the other buffer's S meanwhile)
-                if (i + 2 < steps) ok = mbar_wait_near(pvdone + 2 * grp + u, ph, p.timeout_ns) && s_product(i + 2);
+                if (i + 2 < steps) ok = warp_all(mbar_wait_near(pvdone + 2 * grp + u, ph, p.timeout_ns)) && s_product(i + 2);
             }
             if (lead) {
                 if (!ok) {
@@ -345,14 +345,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = QT == 2 ? 0 : grp; ok && t < nt; t += QT == 2 ? 1 : 2) {
             const bool masked = masked_tile(t);
             const int j = masked && p.bias ? t % kBiasSlots : 0;
-            if (masked && !mbar_wait_near(bfull + j, p.bias ? (uint32_t)(t / kBiasSlots) & 1u : 0u, p.timeout_ns)) {
+            if (masked &&
+                !warp_all(mbar_wait_near(bfull + j, p.bias ? (uint32_t)(t / kBiasSlots) & 1u : 0u, p.timeout_ns))) {
                 ok = false;
                 break;
             }
 #pragma unroll 1
             for (int h = 0; h < kSteps; ++h, ++i) {
                 const int u = i & 1;
-                if (!mbar_wait_near(sfull + 2 * grp + u, (uint32_t)(i >> 1) & 1u, p.timeout_ns)) {
+                if (!warp_all(mbar_wait_near(sfull + 2 * grp + u, (uint32_t)(i >> 1) & 1u, p.timeout_ns))) {
                     ok = false;
                     break;
                 }
@@ -374,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // sum with them, once the products so far are complete
                         const float mn = over ? fmaxf(m, max_of64(s) * mul) : m;
                         if (i > 0) {
-                            if (!mbar_wait_near(pvdone + 2 * grp + (u ^ 1), (uint32_t)((i - 1) >> 1) & 1u, p.timeout_ns)) {
+                            if (!warp_all(mbar_wait_near(pvdone + 2 * grp + (u ^ 1), (uint32_t)((i - 1) >> 1) & 1u,
+                                                         p.timeout_ns))) {
                                 ok = false;
                                 break;
                             }
@@ -405,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (masked && lane == 0) mbar_arrive(bempty + j);
         }
-        if (ok && i > 0 && !mbar_wait_near(pvdone + 2 * grp + ((i - 1) & 1), (uint32_t)((i - 1) >> 1) & 1u, p.timeout_ns))
+        if (ok && i > 0 &&
+            !warp_all(mbar_wait_near(pvdone + 2 * grp + ((i - 1) & 1), (uint32_t)((i - 1) >> 1) & 1u, p.timeout_ns)))
             ok = false;
         if (!ok) {
             atomicOr(p.err, kDevErrTimeout);

@@ -206,10 +206,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = pair; ok && t < tiles; t += pairs, ++n) {
                 const int blocks = tile_of(g, t).kb * g.segments;
                 const int b = n & 1;
-                if (n >= 2 && !mbar_wait_cluster(sempty + b, ((uint32_t)(n >> 1) & 1u) ^ 1u, p.timeout_ns)) ok = false;
+                if (n >= 2 && !warp_all(mbar_wait_cluster(sempty + b, ((uint32_t)(n >> 1) & 1u) ^ 1u, p.timeout_ns)))
+                    ok = false;
                 const uint32_t dt = tmem_base + (uint32_t)(b * 256);
                 for (int kb = 0; ok && kb < blocks; ++kb) {
-                    if (!mbar_wait_near(full + rp.slot, rp.phase, p.timeout_ns) || *abort_flag) {
+                    if (!warp_all(mbar_wait_near(full + rp.slot, rp.phase, p.timeout_ns) && !*abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (ign) target = -1;
                 }
             }
-            if (!mbar_wait_near(sfull + grp, (uint32_t)(n >> 1) & 1u, p.timeout_ns)) {
+            if (!warp_all(mbar_wait_near(sfull + grp, (uint32_t)(n >> 1) & 1u, p.timeout_ns) && !*abort_flag)) {
                 ok = false;
                 break;
             }
@@ -428,7 +429,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (EPI == kLse && live) p.part[((size_t)p.c0 + T.n0) / kTile * g.M + row] = make_float2(mx, l);
-            if (*abort_flag) break;
         }
         if (!ok) {
             atomicOr(p.err, kDevErrTimeout);
