@@ -439,7 +439,8 @@ typedef struct {
 } fs_attn_desc;
 
 /* Bytes of workspace of fs_cross_attn (grad = 0) or fs_cross_attn_grad (grad = 1)
- * for this problem on the current device; 0 if the descriptor is not valid. */
+ * for this problem on the current device; 0 if none is needed or the descriptor is
+ * not valid, SIZE_MAX if the device could not be asked (fs_last_error says why). */
 FS_API size_t fs_cross_attn_workspace(const fs_attn_desc *desc, int grad);
 
 /*
@@ -498,12 +499,12 @@ typedef struct {
 } fs_xent_desc;
 
 /* Bytes of workspace of fs_cross_entropy (grad = 0) or fs_cross_entropy_grad
- * (grad = 1) on the current device; 0 if the descriptor is not valid.  Of x and
- * w only the address's alignment counts (to 128 bytes): bf16 rows that do not
- * start on 16 bytes, or of a long x on 128, are copied to rows that do, fp32
- * rows to three bf16 planes.  The gradient's
- * holds the logit gradients of one piece of the classes (up to 256 MiB, or 256
- * classes if those take more), and partial sums of dx. */
+ * (grad = 1) on the current device; 0 and SIZE_MAX as fs_cross_attn_workspace.
+ * Of x and w only the address's alignment counts (to 128 bytes): bf16 rows that do
+ * not start on 16 bytes, or of a long x on 128, are copied to rows that do, fp32
+ * rows to three bf16 planes.  The gradient's holds the logit gradients of one
+ * piece of the classes (up to 256 MiB, or 256 classes if those take more), and
+ * partial sums of dx. */
 FS_API size_t fs_cross_entropy_workspace(const fs_xent_desc *desc, const void *x, const void *w, int grad);
 
 /*

@@ -408,6 +408,13 @@ def _view(t, what):
     return FsView(s[0], s[1], s[2])
 
 
+def _size(answer):
+    """A workspace query's answer; an error where the device could not be asked."""
+    if answer == ctypes.c_size_t(-1).value:
+        raise FsError(FS_ERR_CUDA, lib().fs_last_error(None).decode())
+    return int(answer)
+
+
 def _plan(key, build, query):
     """(descriptor, reference to it, workspace bytes) of `key`, built on its first use."""
     plan = _plans.get(key)
@@ -415,7 +422,7 @@ def _plan(key, build, query):
         torch = _torch
         desc, device = build()
         with torch.cuda.device(device):
-            plan = (desc, ctypes.byref(desc), int(query(ctypes.byref(desc))))
+            plan = (desc, ctypes.byref(desc), _size(query(ctypes.byref(desc))))
         if len(_plans) >= _PLAN_LIMIT:
             _plans.clear()
         _plans[key] = plan
@@ -546,7 +553,7 @@ def fs_cross_attn_workspace(q, k, v, out, dout=None, dq=None, dk=None, dv=None) 
     grad = dout is not None
     desc = _attn_grad_desc(q, k, v, out, dout, dq, dk, dv, None) if grad else _attn_desc(q, k, v, out, None)
     with torch.cuda.device(q.device):
-        return int(lib().fs_cross_attn_workspace(ctypes.byref(desc), int(grad)))
+        return _size(lib().fs_cross_attn_workspace(ctypes.byref(desc), int(grad)))
 
 
 def _rows(t, what):
@@ -632,7 +639,7 @@ def fs_cross_entropy_workspace(x, w, dx=None, dw=None) -> int:
     grad = dx is not None
     desc = _xent_grad_desc(x, w, dx, dw, 1.0, -100) if grad else _xent_desc(x, w, 1.0, -100)
     with torch.cuda.device(x.device):
-        return int(lib().fs_cross_entropy_workspace(ctypes.byref(desc), x.data_ptr(), w.data_ptr(), int(grad)))
+        return _size(lib().fs_cross_entropy_workspace(ctypes.byref(desc), x.data_ptr(), w.data_ptr(), int(grad)))
 
 
 def fs_check(stream=None):

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
+#include <cstdint>
 #include <cstdio>
 #include <mutex>
 
@@ -420,7 +421,8 @@ extern "C" {
 
 size_t fs_cross_attn_workspace(const fs_attn_desc *desc, int grad) {
     Device dev;
-    if (check_attn(desc, grad != 0) != FS_OK || current_device(&dev) != FS_OK) return 0;
+    if (check_attn(desc, grad != 0) != FS_OK) return 0;
+    if (current_device(&dev) != FS_OK) return SIZE_MAX;
     return attn_workspace(*desc, grad != 0, dev);
 }
 
@@ -509,7 +511,8 @@ fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void
 
 size_t fs_cross_entropy_workspace(const fs_xent_desc *desc, const void *x, const void *w, int grad) {
     Device dev;
-    if (check_xent(desc, grad != 0) != FS_OK || current_device(&dev) != FS_OK) return 0;
+    if (check_xent(desc, grad != 0) != FS_OK) return 0;
+    if (current_device(&dev) != FS_OK) return SIZE_MAX;
     return plan_xent(*desc, x, w, grad != 0, dev).total;
 }
 

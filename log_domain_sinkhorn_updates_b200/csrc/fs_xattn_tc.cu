@@ -521,10 +521,13 @@ cudaError_t launch(const AttnParams &p, AttnTc g, const CUtensorMap &mk, const C
     cudaError_t e = allow_smem<&xattn_tc_kernel<QT, KS, LENGTHS>>(limit);
     if (e != cudaSuccess) return e;
     // The softmax takes registers that the launch must have brought: a build with fewer would wait for them.
-    static const int regs = [] {
+    static std::atomic<int> regs{0};
+    if (regs == 0) {
         cudaFuncAttributes a{};
-        return cudaFuncGetAttributes(&a, xattn_tc_kernel<QT, KS, LENGTHS>) == cudaSuccess ? a.numRegs : 0;
-    }();
+        e = cudaFuncGetAttributes(&a, xattn_tc_kernel<QT, KS, LENGTHS>);
+        if (e != cudaSuccess) return e;
+        regs = a.numRegs;
+    }
     if (regs * kThreads < 128 * kFewRegs + 256 * kManyRegs) return cudaErrorInvalidConfiguration;
     // at least half the shared memory: a CTA holds all of TMEM, so two on one SM would wait for each other
     xattn_tc_kernel<QT, KS, LENGTHS><<<p.main_units + p.tail_units * p.splits, kThreads,

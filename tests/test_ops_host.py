@@ -1,5 +1,6 @@
 """Host code of the handle-less operators on the CPU: what two threads, or a failing CUDA call, can do to what is kept
 between calls (the CUDA runtime's part is played by the tests)."""
+import ctypes
 import os
 import shutil
 import subprocess
@@ -81,3 +82,39 @@ def test_two_threads_on_first_use_leave_the_larger_shared_memory_limit(tmp_path)
                    check=True, cwd=tmp_path)
     r = subprocess.run([str(tmp_path / "limits")], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_a_workspace_query_that_failed_is_not_kept(monkeypatch):
+    """A geometry's first use while the device cannot be asked raises; its next one asks again."""
+    import contextlib
+    import types
+    from log_domain_sinkhorn_updates_b200 import binding
+    monkeypatch.setattr(binding, "_torch", types.SimpleNamespace(cuda=types.SimpleNamespace(
+        device=lambda d: contextlib.nullcontext())))
+    monkeypatch.setattr(binding, "_plans", {})
+    answers = [ctypes.c_size_t(-1).value, 512, 1024]
+
+    def plan():
+        return binding._plan("geometry", lambda: (binding.FsAttnDesc(), "cuda:0"), lambda d: answers.pop(0))
+
+    with pytest.raises(binding.FsError):
+        plan()
+    assert plan()[2] == 512 and plan()[2] == 512 and answers == [1024]
+
+
+def test_workspace_queries_tell_a_failure_from_no_need():
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a device is present")
+    from log_domain_sinkhorn_updates_b200 import binding, build
+    build.build()
+    L = binding.lib()
+    view = binding.FsView(640, 64, 64)
+    good = binding.FsAttnDesc(1, 10, 10, 1, 1, 64, 64, 1, 0.125, *[view] * 8)
+    for grad in (0, 1):
+        assert L.fs_cross_attn_workspace(ctypes.byref(good), grad) == ctypes.c_size_t(-1).value
+        assert b"device" in L.fs_last_error(None).lower()
+        xent = binding.FsXentDesc(5, 9, 64, 1, 1.0, 64, 64, 64, 64, -100)
+        assert L.fs_cross_entropy_workspace(ctypes.byref(xent), None, None, grad) == ctypes.c_size_t(-1).value
+        xent.v = 0
+        assert L.fs_cross_entropy_workspace(ctypes.byref(xent), None, None, grad) == 0
