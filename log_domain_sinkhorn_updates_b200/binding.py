@@ -391,7 +391,8 @@ def _op_dtype(first, *others):
 
 
 def _side(t, dtype, shape, device, what):
-    """Address of a contiguous side array (lengths, bias, statistics, targets)."""
+    """Address of a contiguous side array (lengths, bias, statistics, targets).  The caller holds t itself until its work
+    is enqueued: a temporary's last reference is the call's, and the workspace could take the memory of one let go."""
     if t is None:
         raise ValueError(f"{what} is needed")
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
@@ -504,15 +505,12 @@ def fs_cross_attn(q, k, v, out, lse=None, k_len=None, bias=None, scale=None, str
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return fs_cross_attn(q, k, v, out, lse, k_len, bias, scale, stream, workspace)
-    if k_len is not None:
-        k_len = _side(k_len, torch.int32, (desc.batch,), dev, "k_len")
-    if bias is not None:
-        bias = _side(bias, torch.float32, (desc.batch, desc.m), dev, "bias")
-    if lse is not None:
-        lse = _side(lse, torch.float32, (desc.batch, desc.heads, desc.n), dev, "lse")
+    lenp = _side(k_len, torch.int32, (desc.batch,), dev, "k_len") if k_len is not None else None
+    biasp = _side(bias, torch.float32, (desc.batch, desc.m), dev, "bias") if bias is not None else None
+    lsep = _side(lse, torch.float32, (desc.batch, desc.heads, desc.n), dev, "lse") if lse is not None else None
     raw = _raw_stream(torch, dev, stream)
     ws, size = _scratch(torch, dev, need, stream, workspace)
-    status = L.fs_cross_attn(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), k_len, bias, out.data_ptr(), lse,
+    status = L.fs_cross_attn(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), lenp, biasp, out.data_ptr(), lsep,
                              ws.data_ptr() if size else None, size, raw)
     if status:
         _check(status)
@@ -533,14 +531,12 @@ def fs_cross_attn_grad(q, k, v, out, lse, dout, dq, dk, dv, k_len=None, bias=Non
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return fs_cross_attn_grad(q, k, v, out, lse, dout, dq, dk, dv, k_len, bias, scale, stream, workspace)
-    lse = _side(lse, torch.float32, (desc.batch, desc.heads, desc.n), dev, "lse")
-    if k_len is not None:
-        k_len = _side(k_len, torch.int32, (desc.batch,), dev, "k_len")
-    if bias is not None:
-        bias = _side(bias, torch.float32, (desc.batch, desc.m), dev, "bias")
+    lsep = _side(lse, torch.float32, (desc.batch, desc.heads, desc.n), dev, "lse")
+    lenp = _side(k_len, torch.int32, (desc.batch,), dev, "k_len") if k_len is not None else None
+    biasp = _side(bias, torch.float32, (desc.batch, desc.m), dev, "bias") if bias is not None else None
     raw = _raw_stream(torch, dev, stream)
     ws, size = _scratch(torch, dev, need, stream, workspace)
-    status = L.fs_cross_attn_grad(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), k_len, bias, out.data_ptr(), lse,
+    status = L.fs_cross_attn_grad(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), lenp, biasp, out.data_ptr(), lsep,
                                   dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                   ws.data_ptr() if size else None, size, raw)
     if status:
@@ -596,11 +592,11 @@ def fs_cross_entropy(x, w, target, loss, lse, scale=1.0, ignore_index=-100, stre
         with torch.cuda.device(dev):
             return fs_cross_entropy(x, w, target, loss, lse, scale, ignore_index, stream, workspace)
     shape = (desc.n,)
-    target = _side(target, torch.int64, shape, dev, "target")
-    loss, lse = _side(loss, torch.float32, shape, dev, "loss"), _side(lse, torch.float32, shape, dev, "lse")
+    tp = _side(target, torch.int64, shape, dev, "target")
+    lossp, lsep = _side(loss, torch.float32, shape, dev, "loss"), _side(lse, torch.float32, shape, dev, "lse")
     raw = _raw_stream(torch, dev, stream)
     ws, size = _scratch(torch, dev, need, stream, workspace)
-    status = L.fs_cross_entropy(ref, xp, wp, target, loss, lse, ws.data_ptr() if size else None, size, raw)
+    status = L.fs_cross_entropy(ref, xp, wp, tp, lossp, lsep, ws.data_ptr() if size else None, size, raw)
     if status:
         _check(status)
 
@@ -621,13 +617,12 @@ def fs_cross_entropy_grad(x, w, target, lse, dloss, dx, dw, dlse=None, scale=1.0
         with torch.cuda.device(dev):
             return fs_cross_entropy_grad(x, w, target, lse, dloss, dx, dw, dlse, scale, ignore_index, stream, workspace)
     shape = (desc.n,)
-    target = _side(target, torch.int64, shape, dev, "target")
-    lse, dloss = _side(lse, torch.float32, shape, dev, "lse"), _side(dloss, torch.float32, shape, dev, "dloss")
-    if dlse is not None:
-        dlse = _side(dlse, torch.float32, shape, dev, "dlse")
+    tp = _side(target, torch.int64, shape, dev, "target")
+    lsep, dlossp = _side(lse, torch.float32, shape, dev, "lse"), _side(dloss, torch.float32, shape, dev, "dloss")
+    dlsep = _side(dlse, torch.float32, shape, dev, "dlse") if dlse is not None else None
     raw = _raw_stream(torch, dev, stream)
     ws, size = _scratch(torch, dev, need, stream, workspace)
-    status = L.fs_cross_entropy_grad(ref, xp, wp, target, lse, dloss, dlse, dx.data_ptr(), dw.data_ptr(),
+    status = L.fs_cross_entropy_grad(ref, xp, wp, tp, lsep, dlossp, dlsep, dx.data_ptr(), dw.data_ptr(),
                                      ws.data_ptr() if size else None, size, raw)
     if status:
         _check(status)

@@ -204,3 +204,46 @@ def test_checks_on_one_stream_miss_nothing_that_another_raises():
         stop.set()
         t.join()
     assert not failures and seen[0] == rounds, (failures, seen[0])
+
+
+def test_arguments_that_only_the_call_holds():
+    """Lengths, masks, targets and statistics made in the call's own argument list live until its work is enqueued: the
+    workspace that the call takes from the allocator is not theirs."""
+    fs = _fs()
+    # cross entropy: a temporary of the size class of the workspace
+    for n, v in [(1, 1), (3, 200), (70, 5000), (900, 300)]:
+        x, w, target, dloss = xent.make(n, v, 64, BF16, seed=n)
+        want = xent.run(x, w, target, dloss)
+        need = fs.fs_cross_entropy_workspace(x, w)
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        pad = torch.empty(max(0, need // 8 - n), dtype=torch.long, device="cuda")  # so that blocks of that size exist
+        del pad
+        fs.fs_cross_entropy(x, w, target.clone(), loss, lse)
+        assert torch.equal(loss, want["loss"]) and torch.equal(lse, want["lse"])
+        fs.fs_cross_entropy(x, w, torch.cat([target, target.new_zeros(max(0, need // 8 - n))])[:n], loss, lse)
+        assert torch.equal(loss, want["loss"]) and torch.equal(lse, want["lse"])
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        fs.fs_cross_entropy_grad(x, w, target.clone(), lse.clone(), dloss.clone(), dx, dw)
+        assert torch.equal(dx, want["dx"]) and torch.equal(dw, want["dw"])
+    # attention: few rows, so the keys are split and the call has a workspace
+    for dtype, m in [(BF16, 3000), (F32, 3000), (F32, 200)]:
+        q, k, v, dout = attn.make(2, 1, m, 4, 2, 64, 64, dtype, seed=m)
+        k_len = torch.tensor([m, m // 2], dtype=torch.int32, device="cuda")
+        bias = torch.randn(2, m, device="cuda")
+        want = attn.run(q, k, v, dout, k_len=k_len, bias=bias)
+        need = fs.fs_cross_attn_workspace(q, k, v, q)
+        out, lse = torch.empty_like(q), torch.empty(2, 4, 1, device="cuda")
+        for size in (0, need // 4):
+            big = torch.zeros(size + 2 * m, device="cuda")
+            big[:2 * m] = bias.flatten()
+            lens = torch.zeros(size + 2, dtype=torch.int32, device="cuda")
+            lens[:2] = k_len
+            torch.cuda.synchronize()
+            fs.fs_cross_attn(q, k, v, out, lse, k_len=lens.clone()[:2], bias=big.clone()[:2 * m].view(2, m))
+            assert torch.equal(out, want["out"]) and torch.equal(lse, want["lse"])
+            grads = [torch.empty_like(t) for t in (q, k, v)]
+            fs.fs_cross_attn_grad(q, k, v, out, lse.clone(), dout, *grads, k_len=lens.clone()[:2],
+                                  bias=big.clone()[:2 * m].view(2, m))
+            assert all(torch.equal(g, want[name]) for g, name in zip(grads, ("dq", "dk", "dv")))

@@ -118,3 +118,16 @@ def test_workspace_queries_tell_a_failure_from_no_need():
         assert L.fs_cross_entropy_workspace(ctypes.byref(xent), None, None, grad) == ctypes.c_size_t(-1).value
         xent.v = 0
         assert L.fs_cross_entropy_workspace(ctypes.byref(xent), None, None, grad) == 0
+
+
+@pytest.mark.parametrize("name", ["fs_cross_attn", "fs_cross_attn_grad", "fs_cross_entropy", "fs_cross_entropy_grad"])
+def test_a_call_keeps_its_tensors(name):
+    """No parameter is bound to anything else (an address, say) before the work is enqueued: Python hands the last reference
+    of a temporary to the call, and the workspace could take the memory of one that the call let go."""
+    import ast
+    import inspect
+    from log_domain_sinkhorn_updates_b200 import binding
+    function = ast.parse(inspect.getsource(getattr(binding, name))).body[0]
+    tensors = {a.arg for a in function.args.args} - {"scale", "ignore_index"}
+    bound = {n.id for n in ast.walk(function) if isinstance(n, ast.Name) and isinstance(n.ctx, (ast.Store, ast.Del))}
+    assert not tensors & bound
