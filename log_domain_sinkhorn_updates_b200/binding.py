@@ -463,6 +463,20 @@ def _scratch(torch, device, need, stream, workspace):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _fits(**sizes):
+    """Sizes as the descriptors' C ints hold them (ctypes would cut them off without a word)."""
+    for name, value in sizes.items():
+        if not 0 <= value < 1 << 31:
+            raise ValueError(f"{name} is {value}, over what the call takes")
+
+
+def _ignore_index(value):
+    value = int(value)
+    if not -(1 << 63) <= value < 1 << 63:
+        raise ValueError("ignore_index is not a 64-bit integer")
+    return value
+
+
 def _attn_desc(q, k, v, out, scale):
     dt = _op_dtype(q, k, v, out)
     views = [_view(t, w) for t, w in ((q, "q"), (k, "k"), (v, "v"), (out, "out"))]
@@ -471,6 +485,7 @@ def _attn_desc(q, k, v, out, scale):
     _same("k must be [batch, m, kv_heads, d]", k.shape[0] == B and k.shape[3] == d)
     _same("v must be [batch, m, kv_heads, dv]", tuple(v.shape[:3]) == (B, m, Hk))
     _same("out must be [batch, n, heads, dv]", tuple(out.shape) == (B, n, H, dv))
+    _fits(batch=B, n=n, m=m, heads=H, kv_heads=Hk, d=d, dv=dv)
     return FsAttnDesc(B, n, m, H, Hk, d, dv, dt, float(d ** -0.5 if scale is None else scale), *views)
 
 
@@ -564,7 +579,8 @@ def _xent_desc(x, w, scale, ignore_index):
     dt = _op_dtype(x, w)
     ldx, ldw = _rows(x, "x"), _rows(w, "w")
     _same("x [n, d] and w [v, d] must share d", x.shape[1] == w.shape[1])
-    return FsXentDesc(x.shape[0], w.shape[0], x.shape[1], dt, float(scale), ldx, ldw, 0, 0, int(ignore_index))
+    _fits(rows=x.shape[0], classes=w.shape[0], width=x.shape[1])
+    return FsXentDesc(x.shape[0], w.shape[0], x.shape[1], dt, float(scale), ldx, ldw, 0, 0, ignore_index)
 
 
 def _xent_grad_desc(x, w, dx, dw, scale, ignore_index):
@@ -582,7 +598,7 @@ def fs_cross_entropy(x, w, target, loss, lse, scale=1.0, ignore_index=-100, stre
     is anything else outside the classes.  stream, workspace: as in fs_cross_attn."""
     L, torch = _ready()
     dev, xp, wp = x.get_device(), x.data_ptr(), w.data_ptr()
-    scale, ignore_index = float(scale), int(ignore_index)  # plans are kept by their values
+    scale, ignore_index = float(scale), _ignore_index(ignore_index)  # plans are kept by their values
     desc, ref, need = _plan(
         (scale, ignore_index, xp & 127, wp & 15, dev, w.get_device(), x.dtype, w.dtype, x.shape, w.shape, x.stride(),
          w.stride()),
@@ -607,7 +623,7 @@ def fs_cross_entropy_grad(x, w, target, lse, dloss, dx, dw, dlse=None, scale=1.0
     dlse (float32 [n]; dlse None for 0) of its outputs.  Other arguments as in the forward."""
     L, torch = _ready()
     dev, xp, wp = x.get_device(), x.data_ptr(), w.data_ptr()
-    scale, ignore_index = float(scale), int(ignore_index)  # plans are kept by their values
+    scale, ignore_index = float(scale), _ignore_index(ignore_index)  # plans are kept by their values
     desc, ref, need = _plan(
         (scale, ignore_index, xp & 127, wp & 15, dev,
          *[y for t in (x, w, dx, dw) for y in (t.shape, t.stride(), t.dtype, t.get_device())]),

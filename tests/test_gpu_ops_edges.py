@@ -247,3 +247,45 @@ def test_arguments_that_only_the_call_holds():
             fs.fs_cross_attn_grad(q, k, v, out, lse.clone(), dout, *grads, k_len=lens.clone()[:2],
                                   bias=big.clone()[:2 * m].view(2, m))
             assert all(torch.equal(g, want[name]) for g, name in zip(grads, ("dq", "dk", "dv")))
+
+
+def test_sizes_past_the_descriptors_are_refused():
+    """Tensors expanded to more tokens, rows or classes than a C int holds, and an ignore_index past 64 bits."""
+    fs = _fs()
+    big = 2 ** 32 + 1
+    q, one = torch.randn(1, 1, 1, 8, device="cuda"), torch.randn(1, 1, 1, 8, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((1, 1, 1), 7.0, device="cuda")
+    many = one.expand(1, big, 1, 8)
+    with pytest.raises(ValueError):
+        fs.fs_cross_attn(q, many, many, out, lse)
+    with pytest.raises(ValueError):
+        fs.fs_cross_attn(many, one, one, many)
+    with pytest.raises(ValueError):
+        fs.fs_cross_attn_grad(q, many, many, out, lse, q, out, many, many)
+    with pytest.raises(ValueError):
+        fs.fs_cross_attn_workspace(q, many, many, out)
+    x, loss, target = one.view(1, 8), torch.full((1,), 7.0, device="cuda"), torch.zeros(1, dtype=torch.long, device="cuda")
+    with pytest.raises(ValueError):
+        fs.fs_cross_entropy(x, x.expand(big, 8), target, loss, loss.clone())
+    with pytest.raises(ValueError):
+        fs.fs_cross_entropy(x.expand(big, 8), x, target, loss, loss.clone())
+    for ignore in (2 ** 64 - 100, 2 ** 63, -2 ** 63 - 1):
+        with pytest.raises(ValueError):
+            fs.fs_cross_entropy(x, x, target, loss, loss.clone(), ignore_index=ignore)
+        with pytest.raises(ValueError):
+            fs.fs_cross_entropy_grad(x, x, target, loss, loss, x.clone(), x.clone(), ignore_index=ignore)
+    assert (out == 7).all() and (lse == 7).all() and (loss == 7).all()
+    # the ends of the range are taken
+    for ignore in (2 ** 63 - 1, -2 ** 63):
+        fs.fs_cross_entropy(x, x, torch.full_like(target, ignore), loss, loss.clone(), ignore_index=ignore)
+        assert (loss == 0).all()
+    m = 2 ** 30 - 1  # the most keys that the header allows, one row of memory behind them
+    with pytest.raises(fs.FsError, match="FS_ERR_UNSUPPORTED"):
+        fs.fs_cross_attn(q, one.expand(1, m + 1, 1, 8), one.expand(1, m + 1, 1, 8), out, lse)
+    fs.fs_cross_attn(q, one.expand(1, m, 1, 8), one.expand(1, m, 1, 8), out, lse)
+    want = math.log(m) + (q.double() * one.double()).sum().item() * 8 ** -0.5
+    # equal scores: every weight is 1, their sums are exact; a group of lanes adds at most 2^30 / (64 parts x 32) = 2^19
+    # equal values, each addition off by half a unit of the sum
+    assert (out - one).abs().max() <= 2.0 ** 19 * 2.0 ** -24 * one.abs().max()
+    assert abs(lse.item() - want) <= 16 * ref.U * 30
+    fs.fs_check()
