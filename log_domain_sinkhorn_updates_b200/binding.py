@@ -486,7 +486,7 @@ def _attn_desc(q, k, v, out, scale):
     _same("v must be [batch, m, kv_heads, dv]", tuple(v.shape[:3]) == (B, m, Hk))
     _same("out must be [batch, n, heads, dv]", tuple(out.shape) == (B, n, H, dv))
     _fits(batch=B, n=n, m=m, heads=H, kv_heads=Hk, d=d, dv=dv)
-    return FsAttnDesc(B, n, m, H, Hk, d, dv, dt, float(d ** -0.5 if scale is None else scale), *views)
+    return FsAttnDesc(B, n, m, H, Hk, d, dv, dt, float(max(d, 1) ** -0.5 if scale is None else scale), *views)
 
 
 def _attn_grad_desc(q, k, v, out, dout, dq, dk, dv, scale):

@@ -289,3 +289,17 @@ def test_sizes_past_the_descriptors_are_refused():
     assert (out - one).abs().max() <= 2.0 ** 19 * 2.0 ** -24 * one.abs().max()
     assert abs(lse.item() - want) <= 16 * ref.U * 30
     fs.fs_check()
+
+
+def test_width_zero_is_refused_like_other_sizes():
+    fs = _fs()
+    for d, dv in [(0, 8), (8, 0), (0, 0)]:
+        q, v = torch.zeros(1, 2, 1, d, device="cuda"), torch.zeros(1, 2, 1, dv, device="cuda")
+        with pytest.raises(fs.FsError, match="FS_ERR_INVALID_ARG"):
+            fs.fs_cross_attn(q, q, v, v)
+        with pytest.raises(fs.FsError, match="FS_ERR_INVALID_ARG"):
+            fs.fs_cross_attn_grad(q, q, v, v, torch.zeros(1, 1, 2, device="cuda"), v, q, q, v)
+        assert fs.fs_cross_attn_workspace(q, q, v, v) == 0
+    x = torch.zeros(3, 0, device="cuda")
+    with pytest.raises(fs.FsError, match="FS_ERR_INVALID_ARG"):
+        fs.fs_cross_entropy(x, x, torch.zeros(3, dtype=torch.long, device="cuda"), *torch.zeros(2, 3, device="cuda"))
