@@ -452,9 +452,11 @@ FS_API size_t fs_cross_attn_workspace(const fs_attn_desc *desc, int grad);
  * masked take no part: their k and v may hold anything, NaN included.  A row
  * without a key gives out = 0 and lse = -inf, and its q too may hold anything.
  * lse: device fp32 [batch][heads][n], natural log; may be NULL.  bf16 on the
- * tensor cores: scores and sums in fp32, the weights
- * e^{S - max} rounded to bf16 for their product with v.  Where few rows face
- * many keys (single tokens) the keys are split over the SMs and joined in order.
+ * tensor cores: scores and sums in fp32, the weights e^{S - max} rounded to bf16
+ * for their product with v.  Where few rows face many keys (single tokens) the
+ * keys are split over the SMs and joined in order.
+ * A tensor-core sum truncates every 16 terms: m / 16 times 2^-23 of its terms'
+ * sizes where they have one sign (a bf16 step, 2^-8, at half a million keys).
  * Non-finite inputs that take part give non-finite outputs.  Asynchronous.
  * Errors: FS_ERR_INVALID_ARG (sizes, scale, strides, null pointers, output
  * strides that overlap, a workspace that is too small), FS_ERR_UNSUPPORTED
@@ -486,11 +488,17 @@ FS_API fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, con
  * Softmax cross entropy of n rows over v classes, without keeping the logits:
  *   z_ij = scale x_i.w_j,   lse_i = log sum_j e^{z_ij},   loss_i = lse_i - z_{i, target_i}
  * x [n][d] and w [v][d] of `dtype` with row strides ldx and ldw (elements).
+ * Sums run on the tensor cores, whose fp32 accumulators truncate every 16 terms: a
+ * sum of K terms is good to K / 16 times 2^-23 of the sum of their sizes if they
+ * have one sign, much better if they do not.  K is d in a logit (2^-15 at 4096,
+ * 2^-11 at 65536); in fp32 gradients at most 2048, in bf16 ones the classes of a
+ * piece (dx) and n (dw).  fp32 factors are three bf16 planes each, whose products
+ * leave out 2^-22 of a term.
  */
 typedef struct {
     int n, v, d;              /* rows (0 allowed), classes, width                      */
-    fs_dtype dtype;           /* FS_F32 (products of three bf16 planes each, good to
-                                 about 2^-22 of their terms) or FS_BF16              */
+    fs_dtype dtype;           /* FS_F32 (three bf16 planes a factor, see above) or
+                                 FS_BF16                                              */
     float scale;              /* logit scale (inverse temperature), > 0, finite times
                                  log2(e)                                              */
     long long ldx, ldw;       /* row strides of x and w                                */

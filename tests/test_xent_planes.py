@@ -151,6 +151,30 @@ def test_long_sums_of_one_sign_are_cut(n, v, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("signs", [False, True])
+@pytest.mark.parametrize("n,v,d", [(100, 300, 2048), (20, 70, 16384), (8, 5, 65536)])
+def test_wide_rows_keep_the_stated_bound(n, v, d, signs, dtype):
+    """The logits' sum is not cut: d / 16 truncations of terms of one sign, as the header states for wide rows."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x, w = (torch.rand(k, d, device="cuda", generator=g) + 0.5 for k in (n, v))
+    if signs:
+        x, w = (t * (torch.randint(0, 2, t.shape, device="cuda", generator=g) * 2 - 1) for t in (x, w))
+    x, w = x.to(dtype), w.to(dtype)
+    scale = 2.0 / d
+    target = torch.arange(n, device="cuda") % v
+    loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    _fs().fs_cross_entropy(x, w, target, loss, lse, scale=scale)
+    z = scale * (x.double() @ w.double().t())
+    want = torch.logsumexp(z, dim=1)
+    most = (scale * (d / 16 + 8) * U * (x.double().abs() @ w.double().abs().t())).amax(dim=1)
+    # beside the logits: exponentials 4 U, their sum (v / 8 additions in each of its parts) and the statistic's roundings
+    rest = (4 + min(v, 128) / 8 + 16 + 3 * want.abs()) * U
+    assert ((lse.double() - want).abs() <= most + rest).all()
+    assert ((loss.double() - (want - z.gather(1, target[:, None])[:, 0])).abs() <= 2 * most + rest + 4 * U).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n,v,d", [(300, 4099, 256), (3000, 5000, 128), (1000, 16384, 64)])
 def test_normal_inputs_in_the_norm(n, v, d):
     """Relative 2-norms against 64 bits.  Terms of mixed signs: an accumulator of K terms of size s is of size s sqrt(k)
