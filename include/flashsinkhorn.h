@@ -457,7 +457,8 @@ FS_API size_t fs_cross_attn_workspace(const fs_attn_desc *desc, int grad);
  * keys are split over the SMs and joined in order.
  * A tensor-core sum truncates every 16 terms: m / 16 times 2^-23 of its terms'
  * sizes where they have one sign (a bf16 step, 2^-8, at half a million keys).
- * Non-finite inputs that take part give non-finite outputs.  Asynchronous.
+ * A score of NaN or +inf makes its row NaN; one of -inf weighs nothing.
+ * Asynchronous.
  * Errors: FS_ERR_INVALID_ARG (sizes, scale, strides, null pointers, output
  * strides that overlap, a workspace that is too small), FS_ERR_UNSUPPORTED
  * (device not compute capability 10.x; batch * heads over 65535; n * heads of

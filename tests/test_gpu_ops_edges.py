@@ -303,3 +303,24 @@ def test_width_zero_is_refused_like_other_sizes():
     x = torch.zeros(3, 0, device="cuda")
     with pytest.raises(fs.FsError, match="FS_ERR_INVALID_ARG"):
         fs.fs_cross_entropy(x, x, torch.zeros(3, dtype=torch.long, device="cuda"), *torch.zeros(2, 3, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [1, 9, 150])
+def test_scores_that_are_not_finite_and_take_part(dtype, n):
+    """A key of infinite or NaN width makes the rows whose score with it is +inf or NaN NaN; where it is -inf, it weighs
+    nothing, and rows of such scores alone have no key."""
+    m = 300
+    q, k, v, _ = attn.make(1, n, m, 2, 1, 64, 64, dtype, seed=n)
+    q = q.abs() + 0.25
+    want = ref.attention(q, torch.cat([k[:, :140], k[:, 141:]], 1), torch.cat([v[:, :140], v[:, 141:]], 1))
+    k[0, 140, 0, 5] = -math.inf
+    out, lse = attn.forward(q, k, v)
+    ref.check({"out": out, "lse": lse}, want)
+    for value in (math.inf, math.nan):
+        k[0, 140, 0, 5] = value
+        out, lse = attn.forward(q, k, v)
+        assert torch.isnan(out).all() and torch.isnan(lse).all()
+    k[..., 5] = -math.inf
+    out, lse = attn.forward(q, k, v)
+    assert (out == 0).all() and torch.isneginf(lse).all()
