@@ -324,3 +324,32 @@ def test_scores_that_are_not_finite_and_take_part(dtype, n):
     k[..., 5] = -math.inf
     out, lse = attn.forward(q, k, v)
     assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [1, 90])
+def test_a_captured_masked_step_replayed_on_other_masks(dtype, n):
+    """What the biases are measured from is found by the kernels, so a graph captured on ordinary masks holds for a sample
+    masked with -1e9, for one without a key, and back."""
+    fs = _fs()
+    m = 700
+    q, k, v, dout = attn.make(2, n, m, 4, 2, 64, 64, dtype, seed=n)
+    k_len = torch.tensor([m, 333], dtype=torch.int32, device="cuda")
+    ordinary = torch.randn(2, m, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+    bias, lens = ordinary.clone(), k_len.clone()
+    names = ("out", "lse", "dq", "dk", "dv")
+    bufs = dict(zip(names, (torch.zeros_like(q), torch.zeros(2, 4, n, device="cuda"), *(torch.zeros_like(t) for t in (q, k, v)))))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fs.fs_cross_attn(q, k, v, bufs["out"], bufs["lse"], k_len=lens, bias=bias)
+        fs.fs_cross_attn_grad(q, k, v, bufs["out"], bufs["lse"], dout, bufs["dq"], bufs["dk"], bufs["dv"], k_len=lens,
+                              bias=bias)
+    for value in (None, -1e9, -math.inf, 1e6, None):
+        bias.copy_(ordinary)
+        if value is not None:
+            bias[1] = value
+        lens.copy_(k_len if value != 1e6 else k_len.flip(0))
+        graph.replay()
+        want = attn.run(q, k, v, dout, bias=bias.clone(), k_len=lens.clone())
+        for name in names:
+            assert torch.equal(bufs[name], want[name]), (value, name)
