@@ -25,9 +25,10 @@ constexpr float kBiasNear = 64.f;
 
 // A row's statistics over one part of the keys: what the part's biases are measured from, the reference (base 2) of its
 // scores beside them, and the sum.
-struct AttnPart {
+struct alignas(16) AttnPart {
     float top, m, l;
 };
+constexpr int kAttnParts = 128;  // parts of a row at most
 
 struct AttnParams {
     int batch, n, m, heads, kv_heads, group, d, dv;

@@ -207,7 +207,7 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, AttnKind kind, bool ragged,
             }
         };
         // (numbers of parts that give the same tiles a part are one choice)
-        for (int s = 1; s <= std::min(tiles, 128) && (s == 1 || units < 3ll * slots); ++s)
+        for (int s = 1; s <= std::min(tiles, fs::kAttnParts) && (s == 1 || units < 3ll * slots); ++s)
             if (s == 1 || up(tiles, s) != up(tiles, s - 1)) consider(units, s);
         if (!ragged && units > slots && rest)
             for (int s = 2; s <= std::min(tiles, 16); ++s)

@@ -462,27 +462,40 @@ __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParam
     const int b = p.k_len ? attn_problem<true>(p, place) : place;
     if (r >= p.n * p.group) return;
     grid_dependency_wait();
-    // the largest bias reference, and the largest score reference measured from it
-    float from = -INFINITY;
-    for (int s = lane; s < p.splits; s += 32) {
-        const AttnPart ml = p.part_ml[s * all + at];
-        if (ml.l != 0.f) from = fmaxf(from, ml.top);
+    // a lane's parts, one in every 32
+    AttnPart ml[kAttnParts / 32];
+#pragma unroll
+    for (int c32 = 0; c32 < kAttnParts / 32; ++c32) {
+        ml[c32] = AttnPart{0.f, -INFINITY, 0.f};
+        if (32 * c32 < p.splits && 32 * c32 + lane < p.splits) ml[c32] = p.part_ml[(32 * c32 + lane) * all + at];
     }
-    for (int w = 16; w; w >>= 1) from = fmaxf(from, __shfl_xor_sync(~0u, from, w));
-    auto reference = [&](const AttnPart &ml) { return ml.l == 0.f ? -INFINITY : (ml.top - from) * kLog2e + ml.m; };
-    float mx = -INFINITY;
-    for (int s = lane; s < p.splits; s += 32) mx = fmaxf(mx, reference(p.part_ml[s * all + at]));
+    // the largest bias reference (of parts with a key), and the largest score reference measured from it
+    float from = 0.f, mx = -INFINITY;
+    if (p.bias) {
+        from = -INFINITY;
+#pragma unroll
+        for (int c32 = 0; c32 < kAttnParts / 32; ++c32)
+            if (ml[c32].l != 0.f) from = fmaxf(from, ml[c32].top);
+        for (int w = 16; w; w >>= 1) from = fmaxf(from, __shfl_xor_sync(~0u, from, w));
+    }
+#pragma unroll
+    for (int c32 = 0; c32 < kAttnParts / 32; ++c32) {
+        if (ml[c32].l != 0.f) ml[c32].m += (ml[c32].top - from) * kLog2e;
+        mx = fmaxf(mx, ml[c32].m);
+    }
     for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, w));
     const float ref = mx == -INFINITY ? 0.f : mx;
     float l = 0.f, o[kMaxD / 32];
 #pragma unroll
     for (int k = 0; k < kMaxD / 32; ++k) o[k] = 0.f;
-    for (int s0 = 0; s0 < p.splits; s0 += 32) {
+#pragma unroll
+    for (int c32 = 0; c32 < kAttnParts / 32; ++c32) {
+        const int s0 = 32 * c32;
+        if (s0 >= p.splits) break;
         // a lane's part: its weight; 0 where it has no key (its sums were not written)
-        const AttnPart ml = s0 + lane < p.splits ? p.part_ml[(s0 + lane) * all + at] : AttnPart{0.f, -INFINITY, 0.f};
-        const float f = ml.l == 0.f ? 0.f : exp2f(reference(ml) - ref);
-        const unsigned has = __ballot_sync(~0u, ml.l != 0.f);
-        float lw = ml.l * f;
+        const float f = ml[c32].l == 0.f ? 0.f : exp2f(ml[c32].m - ref);
+        const unsigned has = __ballot_sync(~0u, ml[c32].l != 0.f);
+        float lw = ml[c32].l * f;
         for (int w = 16; w; w >>= 1) lw += __shfl_xor_sync(~0u, lw, w);
         l += lw;
         const int cnt = min(32, p.splits - s0);
@@ -536,6 +549,8 @@ __global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p,
     const int sub = threadIdx.x % per, b = blockIdx.y;
     const bool live = at < rows;
     const int h = (int)(at % (unsigned)p.heads), i = (int)(at / (unsigned)p.heads);
+    const size_t to = ((size_t)b * p.heads + h) * p.n + i;
+    const float lse = live && sub == 0 ? p.lse[to] : 0.f;
     float s = 0.f;
     if (live) {
         const T *o = (const T *)p.out + p.os.batch * b + p.os.token * i + p.os.head * h;
@@ -553,9 +568,8 @@ __global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p,
     for (int w = per / 2; w; w >>= 1) s += __shfl_xor_sync(~0u, s, w);
     grid_dependency_wait();
     if (!live || sub) return;
-    const size_t to = ((size_t)b * p.heads + h) * p.n + i;
     p.dot[to] = s;
-    if (!p.top || p.top[b] == 0.f || p.top[b] == -INFINITY) p.lse2[to] = p.lse[to] * kLog2e;
+    if (!p.top || p.top[b] == 0.f || p.top[b] == -INFINITY) p.lse2[to] = lse * kLog2e;
 }
 
 // KEYS: one CTA keeps 16 U keys of a key head (K, V) and streams its packed rows (Q, dO) in tiles of 32: dk and dv.

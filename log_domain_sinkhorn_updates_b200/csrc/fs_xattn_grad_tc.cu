@@ -304,7 +304,8 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
         // the sums over tile t's streamed rows, once its P and dS are written
         auto sums = [&](int t) {
             const int u = bp.slot, xs = sp.slot;
-            if (!warp_all(mbar_wait_near(pready + u, bp.phase, p.timeout_ns) && !*abort_flag)) return false;
+            const bool aborted = *abort_flag;  // read under the wait
+            if (!warp_all(mbar_wait_near(pready + u, bp.phase, p.timeout_ns) && !aborted)) return false;
             tc_fence_after();
             if (lead) {
                 const uint64_t m1 = c1 + (uint64_t)(xs * slot16), m2 = c2 + (uint64_t)(xs * slot16);
@@ -375,8 +376,9 @@ __device__ void grad_pass(const CUtensorMap &map_q, const CUtensorMap &map_g, co
         for (int t = grp; t < nt; t += 2) {
             const int j = t % kColSlots, u = bp.slot;
             const uint32_t ts = tmem_base + lanes + 128u * u, td = ts + 64u;
+            const bool aborted = *abort_flag;  // read under the waits
             if (!warp_all(mbar_wait_near(sfull + u, bp.phase, p.timeout_ns) &&
-                          mbar_wait_near(cfull + j, (uint32_t)(t / kColSlots) & 1u, p.timeout_ns) && !*abort_flag)) {
+                          mbar_wait_near(cfull + j, (uint32_t)(t / kColSlots) & 1u, p.timeout_ns) && !aborted)) {
                 ok = false;
                 break;
             }

@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                 const uint32_t dt = tmem_base + (uint32_t)(b * 256);
                 for (int kb = 0; ok && kb < blocks; ++kb) {
-                    if (!warp_all(mbar_wait_near(full + rp.slot, rp.phase, p.timeout_ns) && !*abort_flag)) {
+                    const bool aborted = *abort_flag;  // read under the wait
+                    if (!warp_all(mbar_wait_near(full + rp.slot, rp.phase, p.timeout_ns) && !aborted)) {
                         ok = false;
                         break;
                     }
@@ -268,7 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (ign) target = -1;
                 }
             }
-            if (!warp_all(mbar_wait_near(sfull + grp, (uint32_t)(n >> 1) & 1u, p.timeout_ns) && !*abort_flag)) {
+            const bool aborted = *abort_flag;  // read under the wait
+            if (!warp_all(mbar_wait_near(sfull + grp, (uint32_t)(n >> 1) & 1u, p.timeout_ns) && !aborted)) {
                 ok = false;
                 break;
             }
