@@ -353,3 +353,51 @@ def test_a_captured_masked_step_replayed_on_other_masks(dtype, n):
         want = attn.run(q, k, v, dout, bias=bias.clone(), k_len=lens.clone())
         for name in names:
             assert torch.equal(bufs[name], want[name]), (value, name)
+
+
+def test_calls_from_several_threads():
+    """Threads with streams of their own, first calls of new geometries among them: the same bits as one after the other."""
+    import threading
+    fs = _fs()
+    jobs = []
+    for i, (n, m, d, dtype) in enumerate([(1, 2100, 64, BF16), (70, 300, 136, F32), (33, 500, 200, BF16), (5, 90, 24, F32)]):
+        q, k, v, dout = attn.make(2, n, m, 4, 2, d, d, dtype, seed=i)
+        x, w, target, dloss = xent.make(50 + i, 300 + i, 64, dtype, seed=i)
+        bias = torch.randn(2, m, device="cuda")
+        bias[1] = -1e9
+        jobs.append((q, k, v, dout, bias, x, w, target, dloss))
+
+    def work(q, k, v, dout, bias, x, w, target, dloss):
+        out, lse = torch.empty_like(q), torch.empty(2, 4, q.shape[1], device="cuda")
+        grads = [torch.empty_like(t) for t in (q, k, v, x, w)]
+        fs.fs_cross_attn(q, k, v, out, lse, bias=bias)
+        fs.fs_cross_attn_grad(q, k, v, out, lse, dout, *grads[:3], bias=bias)
+        loss, z = torch.empty(x.shape[0], device="cuda"), torch.empty(x.shape[0], device="cuda")
+        fs.fs_cross_entropy(x, w, target, loss, z)
+        fs.fs_cross_entropy_grad(x, w, target, z, dloss, *grads[3:])
+        return [out, lse, loss, z, *grads]
+
+    got, errors = [[] for _ in jobs], []
+    torch.cuda.synchronize()
+
+    def thread(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    got[i].append(work(*jobs[i]))
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001 - reported by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for job, runs in zip(jobs, got):
+        want = work(*job)
+        for run in runs:
+            assert all(torch.equal(a, b) for a, b in zip(run, want))
+    fs.fs_check()
