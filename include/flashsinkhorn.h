@@ -459,6 +459,9 @@ FS_API size_t fs_cross_attn_workspace(const fs_attn_desc *desc, int grad);
  * sizes where they have one sign (a bf16 step, 2^-8, at half a million keys).
  * A score of NaN or +inf makes its row NaN; one of -inf weighs nothing.
  * Asynchronous.
+ * bf16 runs on the tensor cores where d and dv are multiples of 8 up to 128 and
+ * every base and stride is a multiple of 16 bytes; elsewhere, and in fp32, on CUDA
+ * cores, at a fortieth to a fiftieth of the rate for long sequences.
  * Errors: FS_ERR_INVALID_ARG (sizes, scale, strides, null pointers, output
  * strides that overlap, a workspace that is too small), FS_ERR_UNSUPPORTED
  * (device not compute capability 10.x; batch * heads over 65535; n * heads of
@@ -473,11 +476,11 @@ FS_API fs_status fs_cross_attn(const fs_attn_desc *desc, const void *q, const vo
  *   P_ij = e^{S_ij - lse_i},  D_i = dout_i.out_i,  dS_ij = P_ij (dout_i.v_j - D_i)
  *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
  * (dk and dv summed over the heads that share a key head).  Keys that take no
- * part get zeros, also beside a query or a dout that is not finite.  k_len and bias as in the forward; no gradient of bias.  On
- * the tensor cores P and dS are rounded to bf16 for their products.  P comes from
- * the scores and the fp32 lse: its relative error is at least 2^-24 of |lse| (from
- * scores alone: where the largest bias is over 64 in size, the row's sum is taken
- * again beside it).
+ * part get zeros, also beside a query or a dout that is not finite.  k_len and
+ * bias as in the forward; no gradient of bias.  On the tensor cores P and dS are
+ * rounded to bf16 for their products.  P comes from the scores and the fp32 lse:
+ * its relative error can be 2^-24 of |lse| (from scores alone: where the largest
+ * bias is over 64 in size, the row's sum is taken again beside it).
  * Asynchronous.  Errors as fs_cross_attn.
  */
 FS_API fs_status fs_cross_attn_grad(const fs_attn_desc *desc, const void *q, const void *k, const void *v,

@@ -504,7 +504,8 @@ def fs_cross_attn(q, k, v, out, lse=None, k_len=None, bias=None, scale=None, str
 
     q [batch, n, heads, d], k [batch, m, kv_heads, d], v [batch, m, kv_heads, dv], out [batch, n,
     heads, dv]: CUDA float32 or bfloat16 with any strides whose last one is 1 (slices of a fused
-    projection, inputs expanded over the batch).  heads is a multiple of kv_heads.  lse (written
+    projection, inputs expanded over the batch); bfloat16 widths that are not multiples of 8 up to 128,
+    or rows off 16 bytes, leave the tensor cores.  heads is a multiple of kv_heads.  lse (written
     if given): float32 [batch, heads, n].  k_len: int32 [batch] valid keys, or None for all; bias:
     float32 [batch, m] added to the scores, -1e30 or less masking the key.  Masked keys may hold
     anything; a row without a key gives 0 and lse -inf.  scale: 1/sqrt(d) if None.  stream: the

@@ -143,7 +143,7 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, AttnKind kind, bool ragged,
         // It has to save more than the joining pass costs, and the sums written and read back at 4 TB/s.  Tensor
         // cores, 2000 queries of 8 heads on one key head, 64 keys of 128: 232 us whole, 43 split; 1000 x 1000, 4 heads:
         // 21 whole, 24 split.  CUDA cores, fp32, 2 x 200 x 300, 4 on 2 heads of 40: 75 whole, 45 split; 4 heads: 44
-        // whole, 47 split.
+        // whole, 47 split.  (Shares take the work as divisible: that whole waves may end with few CTAs is not counted.)
         const size_t side = tc ? 128 : 16;
         const double slots = dev.sms * (tc ? 1.0 : wide <= 64 ? 4.0 : 2.0);
         const size_t key_blocks = (D.m + side - 1) / side, row_blocks = (rows + side - 1) / side;
@@ -171,7 +171,8 @@ AttnPlan plan_attn(const fs_attn_desc &D, bool grad, AttnKind kind, bool ragged,
     }
     if (rows == 0 || heads == 0) return L;
     // Rows of a unit (tensor cores: 128, or 256 in two blocks that share every tile), and which units are split over
-    // their keys: what costs least, in tiles of 128 keys.  A CTA takes its tiles (two blocks: 1.28 times as long each,
+    // their keys: what costs least, in tiles of 128 keys.  All of it was measured at width 128 on the tensor cores and
+    // serves the other widths and kernels too.  A CTA takes its tiles (two blocks: 1.28 times as long each,
     // 2.3 us against 1.8 at width 128) and 1.5 tiles' time to start and end; waves of CTAs, one an SM (CUDA cores:
     // two).  With lengths, the longest problems come first and short ones fill in, so that the waves need not be whole,
     // and parts of unequal problems cost more (32 requests of up to 4096 keys: 66 us in one part, 89 in two; 8: 52 in

@@ -12,14 +12,14 @@
 // of each product in registers; where shared memory allows it the next tile
 // arrives under this one's arithmetic (fp32: asynchronous copies).  Products go
 // two to an instruction (forward, 4 x 1024 x 1024, 8 heads of 64: 348 -> 338 us).
-// What bounds it is shared memory's latency: 2 of 6 cycles between a warp's
-// instructions wait for it, the FMA pipe is 35 to 40 % active (2 x 1024 x 1024, 8
-// heads of 64: forward 24 TFLOP/s, gradient 25).  Where few CTAs stream for long
-// (4 queries of 8 heads against 5000 keys: 892 -> 49 us) the gradient's streamed
-// tiles are split into parts, whose sums a second kernel adds.  Up to 8 rows a
-// key head (single tokens) have a kernel that streams K and V through
-// registers alone: what bounds it is memory (fp32, 65536 keys of 8 heads of 128:
-// 124 us).
+// What bounds it is shared memory's latency: the FMA pipe is 34 to 37 % active,
+// the schedulers issue every other cycle (2 x 1024 x 1024, 8 heads of 64: forward
+// 25 TFLOP/s, gradient 25).  Where few CTAs stream for long (4 queries of 8 heads
+// against 5000 keys: 892 -> 49 us) the gradient's streamed tiles are split into
+// parts, whose sums a second kernel adds.  Up to 8 rows a key head (single tokens)
+// have a kernel that streams K and V through registers alone: what bounds it is
+// the loads that two warps a scheduler keep in flight (fp32, 65536 keys of 8 heads
+// of 128: 108 us and the join, 131 back to back; DRAM 61 % of its peak).
 //
 // The heads that share a key head are rows of one problem: row r = i group + h.
 // Keys past the length or masked by the bias are staged as zeros, so nothing
@@ -541,7 +541,8 @@ __global__ void __launch_bounds__(kThreads) xattn_combine_kernel(const AttnParam
         p.lse[row_stat(p, b, c, r)] = l == 0.f ? -INFINITY : (float)(((double)mx + log2((double)l)) * kLn2d + from);
 }
 
-// D_i = dout_i.out_i of every (query, head) of a problem: `per` lanes take a row, eight elements each at a time.  And
+// D_i = dout_i.out_i of every (query, head) of a problem: `per` lanes take a row, eight elements each at a time.  out is
+// the stored one, in bf16 off by 2^-8 at most: a gradient then needs no fp32 copy of it.  And
 // its base-2 LSE, unless the forward kernels have taken that (AttnParams::stats).
 template <class T>
 __global__ void __launch_bounds__(kThreads) xattn_dot_kernel(const AttnParams p, int per, bool vec) {

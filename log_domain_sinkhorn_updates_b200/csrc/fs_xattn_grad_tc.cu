@@ -10,11 +10,12 @@
 //
 // In both the kept side is the left factor, so S, dP and with them P and dS
 // come out with the kept rows in TMEM's lanes: they are written back as bf16
-// over the scores they came from and are the left factor of the next products
-// there.  The streamed tile is the right factor of both kinds of product, once
-// with its width and once with its rows as the K axis: the same shared-memory
-// tile under two descriptors.  Seven products instead of the five of one
-// combined pass, in exchange for sums that never leave the SM.
+// (the type of the other operand, as in the forward) over the scores they came
+// from and are the left factor of the next products there.  The streamed tile is
+// the right factor of both kinds of product, once with its width and once with its
+// rows as the K axis: the same shared-memory tile under two descriptors.  Seven
+// products instead of the five of one combined pass, in exchange for sums that
+// never leave the SM.
 //
 // Where there are fewer CTAs than SMs the streamed tiles are split into parts,
 // whose raw sums a second kernel adds in their order.

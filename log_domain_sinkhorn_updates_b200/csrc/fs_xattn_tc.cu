@@ -13,9 +13,10 @@
 // [128 g + 64 h, +64), O_g behind them in [256 + 128 g, ...).  While a group
 // turns one buffer into weights, the products of the other and its next scores
 // run: with one 128-key buffer, softmax, P V and the next S were a chain.
-// P (bf16) is written over the S it came from and is the A operand of the P V
-// product there; V is its right factor as it lies in memory (width contiguous),
-// by the descriptor.
+// P is written over the S it came from and is the A operand of the P V product
+// there, in bf16 as V is (both operands of the product have one type; rounding
+// either to more bits would take tf32, at half the rate and twice the bytes); V
+// is its right factor as it lies in memory (width contiguous), by the descriptor.
 //
 // The maximum is lazy: the weights of 64 keys are taken against the running
 // reference as it stands, and only where their sum passes 2^12 (which any score

@@ -5,7 +5,8 @@
 // classes (gradient).
 //
 //   LSE  C = x w^T          rows: (max, sum 2^(z - max)) per 256 columns, the target's logit
-//   DL   C = x w^T          dz = scale (e^{z - lse} (dloss + dlse) - onehot dloss) -> bf16
+//   DL   C = x w^T          dz = scale (e^{z - lse} (dloss + dlse) - onehot dloss) -> bf16,
+//                           the type of x and w, with which it is multiplied next
 //   ACC  C = dz w           fp32 partial sums of dx (per part of the classes)
 //   OUT  C = dz^T x or dz w  rows of dw, or of dx where one product is all of it
 //
