@@ -539,7 +539,8 @@ FS_API fs_status fs_cross_entropy(const fs_xent_desc *desc, const void *x, const
  *   dx_i = scale sum_j dz_ij w_j,   dw_j = scale sum_i dz_ij x_i
  * dx [n][d] and dw [v][d] of `dtype`.  dloss of ignored rows is not used.
  * Taken in pieces of the classes: the logits of a piece again, dz of the piece
- * (rounded to bf16 for bf16 inputs, in three planes for fp32), its share of dx
+ * (rounded to bf16 for bf16 inputs, but for the significands of scale and of a
+ * dloss that all rows share; in three planes for fp32), its share of dx
  * (summed in fp32) and its rows of dw.
  * A target outside 0..v-1 that is not ignore_index makes the gradients NaN.
  * Asynchronous.  Errors as fs_cross_entropy.

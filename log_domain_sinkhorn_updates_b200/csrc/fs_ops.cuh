@@ -223,7 +223,9 @@ cudaError_t launch_xattn_grad_simt(const AttnParams &p, bool bf16, int sms, cuda
 // Softmax cross entropy: rows x [n][d] against classes w [v][d].
 struct XentParams {
     int n, v, d;
+    int n_all;                     // rows of the call (n: of the product)
     float scale, scale2;           // logit scale, and times log2(e)
+    float scale_pow, scale_m;      // scale = scale_pow scale_m: a power of two, and 1 <= scale_m < 2
     // The operands as the products read them: bf16 rows of `planes` planes (1 for bf16, 3 for fp32), plane_x and
     // plane_w elements apart.
     const void *x, *w;             // w: of the classes from c0 on
@@ -239,7 +241,7 @@ struct XentParams {
     int c0, c1;                    // classes of the piece
     float2 *part;                  // [column tiles][n]: (max, sum) in base 2
     float *hit;                    // [n] scaled logit of the target
-    void *dl;                      // [n][planes][ld_dl] gradient of the logits of classes c0..c1
+    void *dl;                      // [n][planes][ld_dl] gradient of the logits of classes c0..c1, over scale_m xent_unit
     long long ld_dl;
     float *acc;                    // [parts][n][ld_acc] partial sums of dx
     long long ld_acc;
@@ -248,6 +250,30 @@ struct XentParams {
     unsigned long long timeout_ns;
     int *err;
 };
+
+// A factor 1 <= u < 2 that stays out of the logit gradients, with scale_m, until the products' sums: the significand of
+// dloss of the first counted row that has any.  Of a mean's gradient dloss is the same everywhere, and bf16 would round
+// dloss (1 - p) of every target the same way, by up to 2^-8 of the whole gradient (2^-9 in the mean); without it a target
+// gives p - 1, and the roundings are even in sign (8192 rows, 131072 classes of 2048: 0.0030 -> 0.0018 beside 64 bits).
+// Only exponents stay in dz, so no range is lost.  By whole warps; rows past the first 16384 are not looked at.
+__device__ __forceinline__ float xent_unit(const XentParams &p) {
+    const int lane = threadIdx.x & 31, rows = min(p.n_all, 16384);
+    for (int i0 = 0; i0 < rows; i0 += 256) {
+        float g[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + 32 * u + lane;
+            g[u] = i < rows && p.target[i] != p.ignore ? fabsf(p.dloss[i]) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const unsigned has = __ballot_sync(~0u, g[u] > 0.f && g[u] < INFINITY);
+            if (has)
+                return __uint_as_float((__float_as_uint(__shfl_sync(~0u, g[u], __ffs(has) - 1)) & 0x7fffffu) | 0x3f800000u);
+        }
+    }
+    return 1.f;
+}
 
 // Columns of the products' tiles, one partial statistic of a row each.
 constexpr int kXentCols = 256;

@@ -376,10 +376,13 @@ XentPlan plan_xent(const fs_xent_desc &D, const void *x, const void *w, bool gra
 fs::XentParams xent_params(const fs_xent_desc &D, const XentPlan &L, const Device &dev, void *ws, const void *x) {
     fs::XentParams p{};
     char *base = static_cast<char *>(ws);
-    p.n = D.n;
+    p.n = p.n_all = D.n;
     p.v = D.v;
     p.d = D.d;
     p.scale = D.scale;
+    int exponent = 0;
+    p.scale_m = 2.f * std::frexp(D.scale, &exponent);
+    p.scale_pow = std::ldexp(1.f, exponent - 1);
     p.scale2 = (float)((double)D.scale * fs::kLog2ed);
     p.planes = L.planes;
     p.plane_x = p.plane_w = L.dp;

@@ -98,11 +98,12 @@ __global__ void __launch_bounds__(256) xent_finish_kernel(const XentParams p, in
 template <class T>
 __global__ void __launch_bounds__(256) xent_reduce_kernel(const XentParams p) {
     const size_t all = (size_t)p.n * p.d;
+    const float mul = p.scale_m * xent_unit(p);
     for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < all; e += (size_t)gridDim.x * 256) {
         float s = 0.f;
         const size_t i = e / p.d, j = e % p.d;
         for (int k = 0; k < p.parts; ++k) s += p.acc[((size_t)k * p.n + i) * p.ld_acc + j];
-        from_f(s, (T *)p.dx + p.lddx * (long long)i + (long long)j);
+        from_f(s * mul, (T *)p.dx + p.lddx * (long long)i + (long long)j);
     }
 }
 

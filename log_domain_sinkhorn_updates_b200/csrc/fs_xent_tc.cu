@@ -6,7 +6,8 @@
 //
 //   LSE  C = x w^T          rows: (max, sum 2^(z - max)) per 256 columns, the target's logit
 //   DL   C = x w^T          dz = scale (e^{z - lse} (dloss + dlse) - onehot dloss) -> bf16,
-//                           the type of x and w, with which it is multiplied next
+//                           the type of x and w, with which it is multiplied next; a
+//                           factor common to all rows stays out of it (xent_unit)
 //   ACC  C = dz w           fp32 partial sums of dx (per part of the classes)
 //   OUT  C = dz^T x or dz w  rows of dw, or of dx where one product is all of it
 //
@@ -248,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rl = (int)rank * 128 + q * 32 + lane;
         const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(grp * 256);
         const uint32_t sempty0 = cluster_addr(saddr(sempty + grp), 0);
+        const float unit = EPI == kDl || EPI == kOut ? xent_unit(p) : 1.f, mul = p.scale_m * unit;
         bool ok = true;
         int n = grp;
         for (int t = pair + grp * pairs; t < tiles; t += 2 * pairs, n += 2) {
@@ -262,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (EPI == kDl) {
                     const bool ign = target == p.ignore;
                     gl = ign ? 0.f : (target < 0 || target >= p.v ? NAN : __ldg(p.dloss + row));
-                    gs = gl + (p.dlse ? __ldg(p.dlse + row) : 0.f);
+                    gs = (gl + (p.dlse ? __ldg(p.dlse + row) : 0.f)) / unit;
+                    gl /= unit;  // exact where dloss is the common one
                     const float lse = __ldg(p.lse + row);
                     l2 = lse * kLog2e;
                     if (F32)  // what the product's rounding lost, and log2(e)'s own tail
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (F32) z -= l2lo;
                             v[u] = gs == 0.f ? 0.f : ex2_approx(z) * gs;
                             if (any && at == k + u) v[u] -= gl;
-                            v[u] *= p.scale;
+                            v[u] *= p.scale_pow;
                         }
                         // a row's padding beyond the last class (ld_dl is a multiple of 256) is written too: zeros
                         // where a next plane follows it, which the dx product reads
@@ -383,6 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         st_v8(dst + k, &r[k]);
                     }
                 } else if constexpr (F32) {
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * mul);
                     float *dst = (float *)g.out + g.ldo * row + c0;
 #pragma unroll
                     for (int k = 0; k < 128; k += 4) {
@@ -403,6 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 } else {
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * mul);
                     __nv_bfloat16 *dst = (__nv_bfloat16 *)g.out + g.ldo * row + c0;
                     if (live) {
 #pragma unroll

@@ -401,3 +401,36 @@ def test_calls_from_several_threads():
         for run in runs:
             assert all(torch.equal(a, b) for a, b in zip(run, want))
     fs.fs_check()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,v,ignored", [(1000, 8192, 0), (300, 9000, 200), (2, 8192, 1), (5000, 8200, 1500)])
+def test_a_factor_common_to_all_rows_is_not_rounded_with_the_logit_gradients(dtype, n, v, ignored):
+    """The gradient of a mean: 1 / n, and the scale, here with significands that bf16 rounds by 0.45 of 2^-7, stay out of
+    dz.  What is left of an error along the gradient: a target's dz is 1 - p short of 1, rounded to it (p < 2^-12 here), the
+    other classes' sum is a hundredth of a gradient's size and rounds by 2^-8 at most, and where the outputs' roundings are
+    even in sign, 2^-8 / sqrt(elements) x 4.  They are not altogether: a target's row of dw is x_i times one number, and of
+    x_i's 8 bits times 1.0035 more round down than up.  The exact result's own rounding has that share too, and it is
+    allowed for, with the 2^-12 / 2^-8 of the values that an error of 2^-12 before it makes round the other way, 2^-8 each.
+    With the factors inside it is 0.45 x 2^-7 (14 x 2^-12)."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    d = 64
+    x = torch.randn(n, d, device="cuda", generator=g).to(dtype)
+    w = torch.randn(v, d, device="cuda", generator=g).to(dtype)
+    target = torch.randint(0, v, (n,), device="cuda", generator=g)
+    dloss = torch.full((n,), (1 + 0.45 * 2.0 ** -7) * 2.0 ** -10, device="cuda")
+    target[:ignored], dloss[:ignored] = -100, math.nan  # rows before the first counted one; their dloss is not used
+    for scale in (2.0 ** -7, (1 + 0.45 * 2.0 ** -7) * 2.0 ** -7):
+        got = xent.run(x, w, target, dloss, scale=scale)
+        z = scale * (x.double() @ w.double().t())
+        dz = torch.softmax(z, 1)
+        assert dz.max() < 2.0 ** -12
+        dz[torch.arange(n), target.clamp(min=0)] -= 1
+        dz = scale * dz * torch.where(target == -100, 0.0, dloss.double())[:, None]
+        for name, want in (("dx", dz @ w.double()), ("dw", dz.t() @ x.double())):
+            def along(t):
+                return (((t.double() - want) * want).sum() / (want * want).sum()).abs().item()
+
+            count = (n - ignored) * d  # the rows of dw that targets give, and those of dx
+            most = 2 * 2.0 ** -12 + 2.0 ** -8 / 50 + 4 * 2.0 ** -8 / count ** 0.5 + along(want.to(dtype))
+            assert along(got[name]) <= most, (name, along(got[name]) * 2 ** 12, most * 2 ** 12)
